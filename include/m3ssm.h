@@ -391,6 +391,182 @@ m3_status m3_block_prepass(const m3_dims* dims, m3_dtype dtype, const void* x, c
 m3_status m3_block_postpass(const m3_dims* dims, m3_dtype dtype, const void* y,
                             const float* down, void* y_out, void* stream);
 
+/*
+ * Gated linear recurrence: the diagonal recurrence of gated linear layers,
+ * one state a channel instead of a state matrix a head.  Per sequence b and
+ * channel d, t = 0..T-1:
+ *
+ *   a_t = sigmoid(f_t)                         (forget gate, f its pre-activation)
+ *   h_t = a_t h_{t-1} + (1 - a_t) x_t          h_{-1} = h0
+ *   y_t = h_t * silu(g_t)                      (output gate; y_t = h_t without g)
+ *
+ * Masks are gate values: f = +inf passes the state on and x is not looked at
+ * (padding: x may hold anything, NaN included), f = -inf starts afresh from
+ * x and the state before is not looked at (the first token of a document
+ * packed behind another).  A finite f beyond float's range of the sigmoid
+ * acts as the infinity it rounds to.
+ *
+ * Layouts: x, f, g, y and their gradients [batch, T, D], token t of sequence
+ * b at (b T + t) ld with D contiguous channels; each array has its own ld in
+ * m3_scan_dims, so that a slice of a wider projection is read in place.  T
+ * (the type) is the storage type of dtype; states are float whatever it is:
+ *   h0, h_last, dh_last, dh0   [batch, D]          float, dense
+ *   states                     [batch, nC, D]      float, dense, nC = ceil(T / 256)
+ * `states` holds the state entering each chunk of M3_SCAN_CHUNK tokens (the
+ * first is h0): what the backward pass needs besides the inputs.
+ */
+#define M3_SCAN_CHUNK 256 /* tokens between two kept states */
+
+typedef struct {
+  int64_t batch;    /* sequences (>= 0) */
+  int64_t seqlen;   /* T (>= 0; ignored by m3_gated_scan_step) */
+  int64_t channels; /* D (>= 1) */
+  /* elements from one token to the next, >= channels; 0 means channels */
+  int64_t ld_x, ld_f, ld_g, ld_y;    /* ld_y also of dy */
+  int64_t ld_dx, ld_df, ld_dg;       /* backward only */
+} m3_scan_dims;
+
+/*
+ * Bytes of device workspace m3_gated_scan and m3_gated_scan_backward need (0:
+ * none, or an unsupported shape).  Host only.
+ */
+size_t m3_gated_scan_workspace_size(const m3_scan_dims* dims, m3_dtype dtype);
+
+/*
+ * The whole sequence: y for every token, h_last if not NULL, states if not
+ * NULL.  g, h0 (zeros) may be NULL.  Pointers need element alignment only;
+ * arrays whose base and ld are multiples of 16 bytes are read in 16-byte
+ * vectors.  y must not overlap an input.  seqlen == 0 writes h_last = h0
+ * (zeros when NULL); batch == 0 enqueues nothing.
+ */
+m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x, const void* f,
+                        const void* g, const float* h0, void* y, float* h_last, float* states,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum <y, dy> + <h_last, dh_last> for the same inputs and the
+ * `states` that m3_gated_scan wrote for them.  With G_t = dL/dh_t,
+ * G_t = dy_t silu(g_t) + a_{t+1} G_{t+1}:
+ *
+ *   dx_t = G_t (1 - a_t)        df_t = G_t (h_{t-1} - x_t) a_t (1 - a_t)
+ *   dg_t = dy_t h_t silu'(g_t)  dh0  = a_0 G_0
+ *
+ * dx, df, dg in the storage type, dh0 float.  Where the gate is a mask (a is
+ * 0 or 1 in float) df is 0; where it passes the state, dx is 0.  dh_last and
+ * dh0 may be NULL; dg is required exactly when g is given.  The outputs must
+ * not overlap the inputs or each other.  seqlen == 0 writes dh0 = dh_last.
+ */
+m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const void* dy,
+                                 const void* x, const void* f, const void* g,
+                                 const float* states, const float* dh_last, void* dx, void* df,
+                                 void* dg, float* dh0, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * One token for `batch` sequences (dims->seqlen ignored; row b of x, f, g, y
+ * at b ld): h_out = a h_in + (1 - a) x, y = h_out * silu(g).  h_in, h_out
+ * [batch, D] float, dense; h_out may be h_in but must not partially overlap
+ * it.  g may be NULL.
+ */
+m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const float* h_in,
+                             float* h_out, const void* x, const void* f, const void* g, void* y,
+                             void* stream);
+
+/*
+ * Layer norm over the model width, with the block's residual sum fused:
+ *
+ *   s = x + residual        (rounded to the storage type; s = x without it)
+ *   y = (s - mean) rstd * weight + bias,  rstd = 1 / sqrt(var + eps)
+ *
+ * mean and var (biased) over the `channels` values of a row, taken in float
+ * from the values as stored in s: the variance from the centred values, not
+ * from a difference of sums.  weight, bias [channels] float; bias may be NULL.
+ * sum_out receives s (NULL: not kept; it may be x itself or residual itself,
+ * with the same ld); y may be x or residual too, but not sum_out.  mean and
+ * rstd [rows] float, or NULL, are what the backward pass needs.  channels is
+ * at most 16384.  Row r of an array is at r ld; every pointer needs element
+ * alignment, and 16-byte aligned rows are read in vectors.
+ */
+typedef struct {
+  int64_t rows;     /* (>= 0) */
+  int64_t channels; /* 1..16384 */
+  /* elements from one row to the next, >= channels; 0 means channels */
+  int64_t ld_x, ld_residual, ld_sum, ld_y;
+  int64_t ld_dy, ld_dsum, ld_dx; /* backward only */
+} m3_norm_dims;
+
+m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
+                        const void* residual, const float* weight, const float* bias, float eps,
+                        void* y, void* sum_out, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of layer norm from s (the norm's input, ld_sum), its mean and
+ * rstd, dy and the gradient dsum that reaches s past the norm (NULL: none):
+ * with q = (s - mean) rstd and p = dy * weight, per row
+ *
+ *   dx = rstd (p - mean(p) - q mean(p q)) + dsum    (storage type; the
+ *        gradient of x and of residual alike)
+ *   dweight = sum over rows of dy q,  dbias = sum over rows of dy    (float)
+ *
+ * dbias may be NULL.  dx may be dy or dsum (same ld).  The sums over rows are
+ * taken in a fixed order: a call repeats bit for bit.  rows == 0 writes
+ * zeros to dweight and dbias.  The workspace needs 16-byte alignment.
+ */
+size_t m3_layer_norm_backward_workspace_size(const m3_norm_dims* dims, m3_dtype dtype);
+
+m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const void* dy,
+                                 const void* s, const float* weight, const float* mean,
+                                 const float* rstd, const void* dsum, void* dx, float* dweight,
+                                 float* dbias, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * State cache in 8 bits.  A pool of n_slots states, each [H, N, P] codes and
+ * [H, N] float scales (dense): element = code * scale of its row.  A row of P
+ * values is quantised as
+ *
+ *   amax = max |h|,  scale = amax / Q,  code = round(h * (Q / amax))
+ *
+ * (quotients and product rounded to float, the code to the nearest, ties to
+ * even), Q = 127 for int8 codes and 448 for e4m3 ones (the OCP 8-bit float:
+ * 4 exponent and 3 mantissa bits).  A row whose amax is below 2^-100 is held
+ * as zeros (scale 0).  A row that holds an infinity or NaN gets codes 0 and
+ * scale NaN, so that it reads back as NaN.
+ *
+ * slots [batch] int32 (device) names the slot of each state; NULL: state i in
+ * slot i (batch <= n_slots then).  An entry that is negative or >= n_slots is
+ * idle: a padded row of a batch.  store and decode skip it (codes, scales and
+ * y are left as they are), load writes zeros.  Where a slot is named more than
+ * once, store and decode take its first entry and treat the others as idle.
+ *
+ * codes need 16-byte alignment, h of store 16, other pointers element
+ * alignment (decode: as m3_decode_step).  P is 16, 32, 64 or 128; N even, as
+ * m3_decode_step.
+ */
+typedef enum { M3_CODE_INT8 = 0, M3_CODE_E4M3 = 1 } m3_code;
+
+/* h [batch, H, N, P] float into the slots (dims: batch, nheads, P, N). */
+m3_status m3_state_store(const m3_dims* dims, m3_code code, const float* h, void* codes,
+                         float* scales, const int32_t* slots, int64_t n_slots, void* stream);
+
+/* The slots' values into h [batch, H, N, P] of type dtype (rounded to nearest). */
+m3_status m3_state_load(const m3_dims* dims, m3_code code, m3_dtype dtype, const void* codes,
+                        const float* scales, const int32_t* slots, int64_t n_slots, void* h,
+                        void* stream);
+
+/*
+ * m3_decode_step on cached states: reads each slot's codes, takes one step of
+ * the recurrence in float, writes y from the new state before it is rounded,
+ * and the new state's codes and scales into the slot.  The other arguments
+ * and the reduced forms (lam, theta NULL) are those of m3_decode_step.
+ */
+m3_status m3_decode_step_cached(const m3_dims* dims, m3_dtype dtype, m3_code code, void* codes,
+                                float* scales, const int32_t* slots, int64_t n_slots,
+                                const void* x_t, const void* x_prev, const void* B_t,
+                                const void* B_prev, const void* C_t, const float* dt,
+                                const float* A, const float* lam, const float* theta, void* y_t,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

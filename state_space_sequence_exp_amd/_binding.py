@@ -22,11 +22,18 @@ M3_ERR_HIP = 4
 M3_ERR_CHAIN = 5
 M3_F32 = 0
 M3_BF16 = 1
+M3_CODE_INT8 = 0
+M3_CODE_E4M3 = 1
+SCAN_CHUNK = 256
 
 # every function declared in include/m3ssm.h
 ABI_SYMBOLS = ("m3_version", "m3_status_string", "m3_prefill_workspace_size", "m3_prefill",
                "m3_prefill_workspace_error", "m3_prefill_noalloc", "m3_prefill_from_state", "m3_decode_step", "m3_decode_step_mfma", "m3_block_prepass", "m3_block_postpass",
-               "m3_backward_workspace_size", "m3_backward")
+               "m3_backward_workspace_size", "m3_backward",
+               "m3_gated_scan_workspace_size", "m3_gated_scan", "m3_gated_scan_backward",
+               "m3_gated_scan_step", "m3_layer_norm", "m3_layer_norm_backward_workspace_size",
+               "m3_layer_norm_backward", "m3_state_store", "m3_state_load",
+               "m3_decode_step_cached")
 
 
 class M3Error(RuntimeError):
@@ -39,6 +46,16 @@ class M3Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("nheads", ctypes.c_int64), ("headdim_p", ctypes.c_int64),
                 ("dstate_n", ctypes.c_int64), ("rank_r", ctypes.c_int64)]
+
+
+class M3ScanDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("batch", "seqlen", "channels", "ld_x", "ld_f", "ld_g",
+                                              "ld_y", "ld_dx", "ld_df", "ld_dg")]
+
+
+class M3NormDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "channels", "ld_x", "ld_residual", "ld_sum",
+                                              "ld_y", "ld_dy", "ld_dsum", "ld_dx")]
 
 
 _lib = None
@@ -93,6 +110,28 @@ def load_library(path: Optional[str] = None):
                                      ctypes.c_float, vp, vp, vp, vp]
     lib.m3_block_postpass.restype = ctypes.c_int
     lib.m3_block_postpass.argtypes = [dp, ctypes.c_int, vp, vp, vp, vp]
+    sp, np_ = ctypes.POINTER(M3ScanDims), ctypes.POINTER(M3NormDims)
+    i, sz, i64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
+    lib.m3_gated_scan_workspace_size.restype = sz
+    lib.m3_gated_scan_workspace_size.argtypes = [sp, i]
+    lib.m3_gated_scan.restype = i
+    lib.m3_gated_scan.argtypes = [sp, i] + [vp] * 8 + [sz, vp]
+    lib.m3_gated_scan_backward.restype = i
+    lib.m3_gated_scan_backward.argtypes = [sp, i] + [vp] * 11 + [sz, vp]
+    lib.m3_gated_scan_step.restype = i
+    lib.m3_gated_scan_step.argtypes = [sp, i] + [vp] * 7
+    lib.m3_layer_norm.restype = i
+    lib.m3_layer_norm.argtypes = [np_, i] + [vp] * 4 + [ctypes.c_float] + [vp] * 5
+    lib.m3_layer_norm_backward_workspace_size.restype = sz
+    lib.m3_layer_norm_backward_workspace_size.argtypes = [np_, i]
+    lib.m3_layer_norm_backward.restype = i
+    lib.m3_layer_norm_backward.argtypes = [np_, i] + [vp] * 10 + [sz, vp]
+    lib.m3_state_store.restype = i
+    lib.m3_state_store.argtypes = [dp, i, vp, vp, vp, vp, i64, vp]
+    lib.m3_state_load.restype = i
+    lib.m3_state_load.argtypes = [dp, i, i, vp, vp, vp, i64, vp, vp]
+    lib.m3_decode_step_cached.restype = i
+    lib.m3_decode_step_cached.argtypes = [dp, i, i, vp, vp, vp, i64] + [vp] * 11
     if path is None:
         _lib = lib
     return lib
@@ -454,3 +493,375 @@ def backward(x, dt, A, lam, theta, B, C, dy, *, dh_final=None, workspace=None, s
     if squeeze:
         g["x"] = g["x"].squeeze(3)
     return g
+
+
+# ---- operators beside the recurrence ------------------------------------------
+# A call's device is its first tensor's.  Where that is not the current device
+# the call is made with it current, on that device's current stream.
+
+def _launch(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current; raises M3Error."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % dev)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    if st != M3_SUCCESS:
+        raise M3Error(st, fn.__name__)
+
+
+def _code_of(codes) -> int:
+    import torch
+    if codes.dtype == torch.int8:
+        return M3_CODE_INT8
+    if codes.dtype == torch.float8_e4m3fn:
+        return M3_CODE_E4M3
+    raise TypeError("codes must be int8 or float8_e4m3fn, got %s" % codes.dtype)
+
+
+def _rows(t, name, dtype, shape, dev) -> int:
+    """Checks an array of rows [..., D] whose channels are contiguous and whose
+    rows follow each other at one distance (a dense array, or a slice of wider
+    rows); returns that distance in elements."""
+    if t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != dev:
+        raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
+    if t.is_contiguous():
+        return shape[-1]
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: its last dimension must be contiguous" % name)
+    ld = step = None
+    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = step = st
+        if st != step or st < shape[-1]:
+            raise ValueError("%s: its rows must follow each other at one distance" % name)
+        step *= n
+    return shape[-1] if ld is None else ld
+
+
+def gated_scan_workspace_size(batch, seqlen, channels, dtype) -> int:
+    """Bytes of workspace gated_scan and gated_scan_backward need (0: none)."""
+    import torch
+    code = dtype if isinstance(dtype, int) else (M3_BF16 if dtype == torch.bfloat16 else M3_F32)
+    d = M3ScanDims(int(batch), int(seqlen), int(channels))
+    return int(load_library().m3_gated_scan_workspace_size(ctypes.byref(d), code))
+
+
+def _scan_workspace(lib, d, code, workspace, dev):
+    import torch
+    need = int(lib.m3_gated_scan_workspace_size(ctypes.byref(d), code))
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool = False,
+               states=None, workspace=None, stream=None) -> Tuple:
+    """Gated linear recurrence over a sequence (m3_gated_scan):
+    h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(f), y = h * silu(g)
+    (y = h without g).
+
+    x, f, g [B,T,D] float32 or bfloat16 (one type), channels contiguous and
+    tokens at one distance (a slice of a wider projection is read in place).
+    h0 [B,D] float32 or None (zeros).  f = +inf passes the state on without
+    looking at x (padding), f = -inf starts afresh (a packed document).
+    want_states keeps the state entering every 256 tokens, for the backward.
+    A workspace (gated_scan_workspace_size bytes, zero-filled once) may be
+    kept for later calls; calls that overlap need distinct ones.
+    Returns (y, h_last [B,D] float32, states [B,ceil(T/256),D] float32 or None).
+    """
+    import torch
+    lib = load_library()
+    shape, dev, dt = x.shape, x.device, x.dtype
+    if len(shape) != 3:
+        raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
+    nb, nt, nd = shape
+    code = _dtype_code(x)
+    d = M3ScanDims(nb, nt, nd, _rows(x, "x", dt, shape, dev), _rows(f, "f", dt, shape, dev),
+                   0 if g is None else _rows(g, "g", dt, shape, dev))
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, (nb, nd), dev)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        d.ld_y = _rows(y, "y", dt, shape, dev)
+    if h_last is None:
+        h_last = torch.empty((nb, nd), dtype=torch.float32, device=dev)
+    else:
+        _check(h_last, "h_last", torch.float32, (nb, nd), dev)
+    nc = -(-nt // SCAN_CHUNK)
+    if states is not None:
+        _check(states, "states", torch.float32, (nb, nc, nd), dev)
+    elif want_states:
+        states = torch.empty((nb, nc, nd), dtype=torch.float32, device=dev)
+    workspace, ws_bytes = _scan_workspace(lib, d, code, workspace, dev)
+    _launch(dev, stream, lib.m3_gated_scan, ctypes.byref(d), code, _ptr(x), _ptr(f), _ptr(g),
+            _ptr(h0), _ptr(y), _ptr(h_last), _ptr(states), _ptr(workspace), ws_bytes)
+    return y, h_last, states
+
+
+def gated_scan_backward(dy, x, f, g, states, *, dh_last=None, dx=None, df=None, dg=None,
+                        workspace=None, stream=None):
+    """Gradients of sum(y * dy) (+ sum(h_last * dh_last)) for gated_scan's
+    inputs (m3_gated_scan_backward).  `states` is what gated_scan kept for the
+    same inputs; g None when it had none.  dx, df, dg may be given (slices of
+    a wider gradient).  Returns a dict: x, f, g (absent without g) in the
+    inputs' type, h0 [B,D] float32."""
+    import torch
+    lib = load_library()
+    shape, dev, dt = x.shape, x.device, x.dtype
+    if len(shape) != 3:
+        raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
+    nb, nt, nd = shape
+    code = _dtype_code(x)
+    _check(states, "states", torch.float32, (nb, -(-nt // SCAN_CHUNK), nd), dev)
+    if dh_last is not None:
+        _check(dh_last, "dh_last", torch.float32, (nb, nd), dev)
+    if g is None and dg is not None:
+        raise ValueError("dg without g")
+    new = lambda t: torch.empty(shape, dtype=dt, device=dev) if t is None else t
+    dx, df, dg = new(dx), new(df), None if g is None else new(dg)
+    d = M3ScanDims(nb, nt, nd, _rows(x, "x", dt, shape, dev), _rows(f, "f", dt, shape, dev),
+                   0 if g is None else _rows(g, "g", dt, shape, dev),
+                   _rows(dy, "dy", dt, shape, dev), _rows(dx, "dx", dt, shape, dev),
+                   _rows(df, "df", dt, shape, dev),
+                   0 if g is None else _rows(dg, "dg", dt, shape, dev))
+    dh0 = torch.empty((nb, nd), dtype=torch.float32, device=dev)
+    workspace, ws_bytes = _scan_workspace(lib, d, code, workspace, dev)
+    _launch(dev, stream, lib.m3_gated_scan_backward, ctypes.byref(d), code, _ptr(dy), _ptr(x),
+            _ptr(f), _ptr(g), _ptr(states), _ptr(dh_last), _ptr(dx), _ptr(df), _ptr(dg),
+            _ptr(dh0), _ptr(workspace), ws_bytes)
+    out = {"x": dx, "f": df, "h0": dh0}
+    if g is not None:
+        out["g"] = dg
+    return out
+
+
+def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None, stream=None) -> Tuple:
+    """One token of the gated linear recurrence (m3_gated_scan_step).
+
+    h [B,D] float32; x, f, g [B,D] float32 or bfloat16.  h_out defaults to h
+    itself (in-place update).  Returns (y [B,D], h_out)."""
+    import torch
+    lib = load_library()
+    shape, dev, dt = x.shape, x.device, x.dtype
+    if len(shape) != 2:
+        raise ValueError("x: expected [B, D], got %s" % (tuple(shape),))
+    code = _dtype_code(x)
+    d = M3ScanDims(shape[0], 1, shape[1], _rows(x, "x", dt, shape, dev),
+                   _rows(f, "f", dt, shape, dev), 0 if g is None else _rows(g, "g", dt, shape, dev))
+    _check(h, "h", torch.float32, shape, dev)
+    if h_out is None:
+        h_out = h
+    else:
+        _check(h_out, "h_out", torch.float32, shape, dev)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        d.ld_y = _rows(y, "y", dt, shape, dev)
+    _launch(dev, stream, lib.m3_gated_scan_step, ctypes.byref(d), code, _ptr(h), _ptr(h_out),
+            _ptr(x), _ptr(f), _ptr(g), _ptr(y))
+    return y, h_out
+
+
+def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None, sum_out=None,
+               want_stats: bool = True, stream=None) -> Tuple:
+    """Layer norm over the last dimension with the residual sum fused
+    (m3_layer_norm): s = x + residual, y = (s - mean) rstd weight + bias.
+
+    x, residual [..., D] float32 or bfloat16, D <= 16384, rows at one
+    distance; weight, bias [D] float32.  sum_out may be x or residual (in
+    place).  Returns (y, s, mean, rstd): s is x itself without a residual,
+    mean and rstd [...] float32 (None without want_stats)."""
+    import torch
+    lib = load_library()
+    shape, dev, dt = x.shape, x.device, x.dtype
+    if len(shape) < 1:
+        raise ValueError("x: expected [..., D]")
+    code = _dtype_code(x)
+    nd = shape[-1]
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    d = M3NormDims(rows, nd, _rows(x, "x", dt, shape, dev))
+    _check(weight, "weight", torch.float32, (nd,), dev)
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (nd,), dev)
+    s = x
+    if residual is not None:
+        d.ld_residual = _rows(residual, "residual", dt, shape, dev)
+        if sum_out is None:
+            sum_out = torch.empty(shape, dtype=dt, device=dev)
+        s = sum_out
+    if sum_out is not None:
+        d.ld_sum = _rows(sum_out, "sum_out", dt, shape, dev)
+        s = sum_out
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        d.ld_y = _rows(y, "y", dt, shape, dev)
+    mean = rstd = None
+    if want_stats:
+        mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev).unbind(0)
+    _launch(dev, stream, lib.m3_layer_norm, ctypes.byref(d), code, _ptr(x), _ptr(residual),
+            _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(sum_out), _ptr(mean), _ptr(rstd))
+    return y, s, mean, rstd
+
+
+def layer_norm_backward(dy, s, weight, mean, rstd, *, dsum=None, dx=None, want_bias: bool = True,
+                        workspace=None, stream=None):
+    """Gradients of layer_norm (m3_layer_norm_backward): s, mean and rstd as
+    layer_norm returned them, dsum the gradient that reaches s past the norm
+    (the residual stream's).  dx may be dy or dsum (in place).  Returns a
+    dict: x (the gradient of x and of residual) in s's type, weight and bias
+    [D] float32 (bias absent without want_bias)."""
+    import torch
+    lib = load_library()
+    shape, dev, dt = s.shape, s.device, s.dtype
+    if len(shape) < 1:
+        raise ValueError("s: expected [..., D]")
+    code = _dtype_code(s)
+    nd = shape[-1]
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    d = M3NormDims(rows, nd)
+    d.ld_sum = _rows(s, "s", dt, shape, dev)
+    d.ld_dy = _rows(dy, "dy", dt, shape, dev)
+    _check(weight, "weight", torch.float32, (nd,), dev)
+    _check(mean, "mean", torch.float32, shape[:-1], dev)
+    _check(rstd, "rstd", torch.float32, shape[:-1], dev)
+    if dsum is not None:
+        d.ld_dsum = _rows(dsum, "dsum", dt, shape, dev)
+    if dx is None:
+        dx = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        d.ld_dx = _rows(dx, "dx", dt, shape, dev)
+    dwb = torch.empty((2 if want_bias else 1, nd), dtype=torch.float32, device=dev)
+    need = int(lib.m3_layer_norm_backward_workspace_size(ctypes.byref(d), code))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch(dev, stream, lib.m3_layer_norm_backward, ctypes.byref(d), code, _ptr(dy), _ptr(s),
+            _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dwb[0]),
+            _ptr(dwb[1]) if want_bias else None, _ptr(workspace), ws_bytes)
+    out = {"x": dx, "weight": dwb[0]}
+    if want_bias:
+        out["bias"] = dwb[1]
+    return out
+
+
+def state_cache(n_slots, nheads, N, P, dtype=None, device="cuda") -> Tuple:
+    """An empty 8-bit state cache: codes [n_slots,H,N,P] (int8, or
+    float8_e4m3fn by dtype) and scales [n_slots,H,N] float32, all zero states."""
+    import torch
+    if dtype not in (None, torch.int8, torch.float8_e4m3fn):
+        raise TypeError("codes must be int8 or float8_e4m3fn, got %s" % dtype)
+    codes = torch.zeros((n_slots, nheads, N, P), dtype=torch.int8, device=device)
+    scales = torch.zeros((n_slots, nheads, N), dtype=torch.float32, device=device)
+    return codes.view(dtype or torch.int8), scales
+
+
+def _cache_check(codes, scales, slots, dev):
+    import torch
+    if codes.dim() != 4:
+        raise ValueError("codes: expected [slots, H, N, P], got %s" % (tuple(codes.shape),))
+    code = _code_of(codes)
+    _check(codes, "codes", codes.dtype, codes.shape, dev)
+    _check(scales, "scales", torch.float32, codes.shape[:3], dev)
+    if slots is not None:
+        if slots.dim() != 1:
+            raise ValueError("slots: expected [batch], got %s" % (tuple(slots.shape),))
+        _check(slots, "slots", torch.int32, slots.shape, dev)
+    return code
+
+
+def state_store(h, codes, scales, slots=None, *, stream=None) -> None:
+    """Quantises states h [S,H,N,P] float32 into the cache's slots
+    (m3_state_store).  slots [S] int32, negative or past the pool: idle; None:
+    state i into slot i."""
+    import torch
+    lib = load_library()
+    dev = codes.device
+    code = _cache_check(codes, scales, slots, dev)
+    ns = h.shape[0] if slots is None else slots.shape[0]
+    _check(h, "h", torch.float32, (ns,) + codes.shape[1:], dev)
+    n, nh, nn, npd = codes.shape
+    d = _dims(ns, 1, nh, npd, nn, 1)
+    _launch(dev, stream, lib.m3_state_store, ctypes.byref(d), code, _ptr(h), _ptr(codes),
+            _ptr(scales), _ptr(slots), n)
+
+
+def state_load(codes, scales, slots=None, *, dtype=None, h=None, stream=None):
+    """The states of the cache's slots [S,H,N,P] as float32 (or bfloat16 by
+    dtype) (m3_state_load); zeros for idle slots; slots None: the whole pool."""
+    import torch
+    lib = load_library()
+    dev = codes.device
+    code = _cache_check(codes, scales, slots, dev)
+    n, nh, nn, npd = codes.shape
+    ns = n if slots is None else slots.shape[0]
+    if h is None:
+        h = torch.empty((ns, nh, nn, npd), dtype=dtype or torch.float32, device=dev)
+    else:
+        _check(h, "h", dtype or h.dtype, (ns, nh, nn, npd), dev)
+    d = _dims(ns, 1, nh, npd, nn, 1)
+    _launch(dev, stream, lib.m3_state_load, ctypes.byref(d), code, _dtype_code(h), _ptr(codes),
+            _ptr(scales), _ptr(slots), n, _ptr(h))
+    return h
+
+
+def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, A, lam, theta, *,
+                       y=None, stream=None):
+    """One decode step on states in an 8-bit cache, in place
+    (m3_decode_step_cached).
+
+    codes [slots,H,N,P] int8 or float8_e4m3fn with scales [slots,H,N]
+    float32; slots [S] int32 (idle where negative or past the pool; None:
+    sequence i in slot i); the rest as for decode_step.  Returns y [S,H,R,P],
+    whose rows of idle entries are left as they were (zeros when y is not
+    given)."""
+    import torch
+    lib = load_library()
+    dev = codes.device
+    code = _cache_check(codes, scales, slots, dev)
+    n, nh, nn, npd = codes.shape
+    ns, nr = x_t.shape[0], x_t.shape[2]
+    xs, bs = (ns, nh, nr, npd), (ns, nh, nr, nn)
+    tcode = _dtype_code(x_t)
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (ns,), dev)
+    if lam is not None and (x_prev is None or B_prev is None):
+        raise ValueError("x_prev and B_prev are required with lam")
+    for name, t, shape in (("x_t", x_t, xs), ("x_prev", x_prev, xs), ("B_t", B_t, bs),
+                           ("B_prev", B_prev, bs), ("C_t", C_t, bs)):
+        if t is not None:
+            _check(t, name, x_t.dtype, shape, dev)
+    _check(dt, "dt", torch.float32, (ns, nh), dev)
+    if lam is not None:
+        _check(lam, "lam", torch.float32, (ns, nh), dev)
+    if theta is not None:
+        _check(theta, "theta", torch.float32, (ns, nh, nn // 2), dev)
+    _check(A, "A", torch.float32, (nh,), dev)
+    if y is None:
+        y = (torch.empty if slots is None else torch.zeros)(xs, dtype=x_t.dtype, device=dev)
+    else:
+        _check(y, "y", x_t.dtype, xs, dev)
+    d = _dims(ns, 1, nh, npd, nn, nr)
+    _launch(dev, stream, lib.m3_decode_step_cached, ctypes.byref(d), tcode, code, _ptr(codes),
+            _ptr(scales), _ptr(slots), n, _ptr(x_t), _ptr(x_prev), _ptr(B_t), _ptr(B_prev),
+            _ptr(C_t), _ptr(dt), _ptr(A), _ptr(lam), _ptr(theta), _ptr(y))
+    return y

@@ -1,0 +1,328 @@
+// state_cache.hip -- recurrent states held in 8 bits: quantised as they are
+// written, read back, and the decode step on them.
+//
+// A row of P values has one scale: amax = max |h|, scale = amax / Q, code =
+// round(h (Q / amax)), Q = 127 (int8) or 448 (e4m3); rows below 2^-100 are
+// zeros, rows with an infinity or NaN get scale NaN.
+//
+// The decode step is decode.hip's: a workgroup owns one (sequence, head),
+// builds the per-row coefficients of the recurrence in the LDS
+//   rot[k] = (cos, sin)(dt theta_k),  u_r[n] = alpha (1-lam) dt (R B_prev[r])[n],
+//   v_r[n] = lam dt B_t[r][n],  c_r[n] = C_t[r][n]
+// and every thread updates 8 columns of row pairs in registers; the row
+// maxima of the new state come from the lanes that share the row.
+#include "layer_internal.h"
+#include "m3_device.h"
+
+namespace m3 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kTinyRow = 7.8886090522101181e-31f;  // 2^-100
+
+// The 8 codes of a lane as two words, and back.
+template <int kCode>
+struct Code;
+template <>
+struct Code<M3_CODE_INT8> {
+  static constexpr float kMax = 127.f;
+  __device__ __forceinline__ static void unpack4(uint32_t w, float* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
+  }
+  __device__ __forceinline__ static uint32_t pack4(const float* v) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = (int)__builtin_rintf(v[i]);
+      w |= ((uint32_t)(q < -127 ? -127 : q > 127 ? 127 : q) & 0xffu) << (8 * i);
+    }
+    return w;
+  }
+};
+template <>
+struct Code<M3_CODE_E4M3> {
+  static constexpr float kMax = 448.f;
+  __device__ __forceinline__ static void unpack4(uint32_t w, float* v) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
+  }
+  __device__ __forceinline__ static uint32_t pack4(const float* v) {
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(v[i], -448.f), 448.f);
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    return (uint32_t)w;
+  }
+};
+
+// |v| as ordered bits, so that a maximum keeps NaN (above infinity).
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// A row's scale and the factor that takes it to codes, from its largest
+// magnitude's bits.
+template <int kCode>
+__device__ __forceinline__ void row_scale(uint32_t top, float* scale, float* inv) {
+  const float amax = __uint_as_float(top);
+  if (top >= 0x7f800000u) {
+    *scale = __uint_as_float(0x7fc00000u);
+    *inv = 0.f;
+  } else if (amax < kTinyRow) {
+    *scale = *inv = 0.f;
+  } else {
+    *scale = amax / Code<kCode>::kMax;
+    *inv = Code<kCode>::kMax / amax;
+  }
+}
+
+// Codes of 8 values of a row whose top is `top`.
+template <int kCode>
+__device__ __forceinline__ uint2 quantise8(const float (&h)[8], float inv, bool finite) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = finite ? h[e] * inv : 0.f;
+  return make_uint2(Code<kCode>::pack4(v), Code<kCode>::pack4(v + 4));
+}
+
+__device__ __forceinline__ uint32_t top8(const float (&h)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = abs_bits(h[e]);
+    top = b > top ? b : top;
+  }
+  return top;
+}
+// Maximum over the `lanes` (a power of two) consecutive lanes of a row.
+__device__ __forceinline__ uint32_t row_top(uint32_t top, int lanes) {
+  for (int off = lanes >> 1; off > 0; off >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, off, kWave);
+    top = o > top ? o : top;
+  }
+  return top;
+}
+
+// The slot of entry i, or -1 when it is idle.
+__device__ __forceinline__ int slot_of(const CacheArgs& a, int i) {
+  const int s = a.slots ? a.slots[i] : i;
+  return (s < 0 || s >= a.n_slots) ? -1 : s;
+}
+// Whether an entry before i names the same slot (every thread of the
+// workgroup calls it and gets the same answer).
+__device__ __forceinline__ bool named_before(const CacheArgs& a, int i, int slot) {
+  if (!a.slots) return false;
+  int same = 0;
+  for (int j = threadIdx.x; j < i; j += kThreads) same |= a.slots[j] == slot ? 1 : 0;
+  return __syncthreads_or(same) != 0;
+}
+
+template <int kCode>
+__global__ void __launch_bounds__(kThreads) store_kernel(CacheArgs a) {
+  const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
+  const int slot = slot_of(a, i);
+  if (slot < 0 || named_before(a, i, slot)) return;
+  const int lanes = a.P / 8;
+  const float* h = a.h_in + ((size_t)i * a.H + head) * a.N * a.P;
+  const size_t unit = (size_t)slot * a.H + head;
+  uint2* codes = reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.codes) + unit * a.N * a.P);
+  for (int p0 = 0; p0 < a.N * lanes; p0 += kThreads) {  // every lane of a row together
+    const int p = p0 + threadIdx.x;
+    const bool in = p < a.N * lanes;
+    float v[8];
+    const float4 lo = in ? reinterpret_cast<const float4*>(h)[2 * p] : make_float4(0, 0, 0, 0);
+    const float4 hi = in ? reinterpret_cast<const float4*>(h)[2 * p + 1] : make_float4(0, 0, 0, 0);
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    const uint32_t top = row_top(top8(v), lanes);
+    float scale, inv;
+    row_scale<kCode>(top, &scale, &inv);
+    if (in) {
+      codes[p] = quantise8<kCode>(v, inv, top < 0x7f800000u);
+      if (p % lanes == 0) a.scales[unit * a.N + p / lanes] = scale;
+    }
+  }
+}
+
+template <int kCode, typename T>
+__global__ void __launch_bounds__(kThreads) load_kernel(CacheArgs a) {
+  const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
+  const int slot = slot_of(a, i);
+  const int lanes = a.P / 8;
+  T* h = static_cast<T*>(a.h_out) + ((size_t)i * a.H + head) * a.N * a.P;
+  const size_t unit = (size_t)(slot < 0 ? 0 : slot) * a.H + head;
+  const uint2* codes =
+      reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(a.codes) + unit * a.N * a.P);
+  for (int p = threadIdx.x; p < a.N * lanes; p += kThreads) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot >= 0) {
+      const uint2 w = codes[p];
+      const float scale = a.scales[unit * a.N + p / lanes];
+      Code<kCode>::unpack4(w.x, v);
+      Code<kCode>::unpack4(w.y, v + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= scale;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[(size_t)p * 8 + e] = from_f32<T>(v[e]);
+  }
+}
+
+template <typename T, int R, int kCode>
+__global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
+  extern __shared__ __align__(16) float dsm[];
+  const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
+  const int slot = slot_of(a, i);
+  if (slot < 0 || named_before(a, i, slot)) return;
+  const int N = a.N, P = a.P, npair = N / 2, lanes = P / 8;
+  const int tid = threadIdx.x, c8 = tid % lanes, rg = tid / lanes, groups = kThreads / lanes;
+  const size_t in = (size_t)i * a.H + head;       // this token's inputs
+  const size_t unit = (size_t)slot * a.H + head;  // its state
+  float2* s_rot = reinterpret_cast<float2*>(dsm);
+  float* s_u = dsm + 2 * npair;
+  float* s_v = s_u + R * N;
+  float* s_c = s_v + R * N;
+  float* s_y = s_c + R * N;  // [groups][R][P]
+
+  const float d = a.dt[in], la = a.lam ? a.lam[in] : 1.f;
+  const float alpha = expf(d * a.A[head]);
+  const float cu = alpha * (1.f - la) * d, cv = la * d;
+  for (int kp = tid; kp < npair; kp += kThreads) {
+    float sn = 0.f, cn = 1.f;
+    if (a.theta) sincosf(d * a.theta[in * npair + kp], &sn, &cn);
+    s_rot[kp] = make_float2(cn, sn);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const size_t at = (in * R + r) * N + 2 * kp;
+      const float2 bt = load_pair(static_cast<const T*>(a.B_t) + at);
+      const float2 bp = a.lam ? load_pair(static_cast<const T*>(a.B_prev) + at) : make_float2(0, 0);
+      const float2 ct = load_pair(static_cast<const T*>(a.C_t) + at);
+      *reinterpret_cast<float2*>(s_u + r * N + 2 * kp) =
+          make_float2(cu * (cn * bp.x - sn * bp.y), cu * (sn * bp.x + cn * bp.y));
+      *reinterpret_cast<float2*>(s_v + r * N + 2 * kp) = make_float2(cv * bt.x, cv * bt.y);
+      *reinterpret_cast<float2*>(s_c + r * N + 2 * kp) = ct;
+    }
+  }
+  float xc[R][8], xq[R][8], yp[R][8];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const size_t at = (in * R + r) * P + 8 * c8 + e;
+      xc[r][e] = to_f32(static_cast<const T*>(a.x_t)[at]);
+      xq[r][e] = a.lam ? to_f32(static_cast<const T*>(a.x_prev)[at]) : 0.f;
+      yp[r][e] = 0.f;
+    }
+  __syncthreads();
+  uint2* codes = reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.codes) + unit * N * P);
+  float* scales = a.scales + unit * N;
+  for (int k0 = 0; k0 < npair; k0 += groups) {  // every lane of a row together
+    const int kp = k0 + rg;
+    const bool on = kp < npair;
+    const int row = on ? 2 * kp : 0;
+    const uint2 w0 = codes[(size_t)row * lanes + c8], w1 = codes[(size_t)(row + 1) * lanes + c8];
+    const float s0 = scales[row], s1 = scales[row + 1];
+    float v0[8], v1[8], n0[8], n1[8];
+    Code<kCode>::unpack4(w0.x, v0);
+    Code<kCode>::unpack4(w0.y, v0 + 4);
+    Code<kCode>::unpack4(w1.x, v1);
+    Code<kCode>::unpack4(w1.y, v1 + 4);
+    const float2 rc = s_rot[row / 2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float h0 = v0[e] * s0, h1 = v1[e] * s1;
+      n0[e] = alpha * (rc.x * h0 - rc.y * h1);
+      n1[e] = alpha * (rc.y * h0 + rc.x * h1);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        n0[e] += s_u[r * N + row] * xq[r][e] + s_v[r * N + row] * xc[r][e];
+        n1[e] += s_u[r * N + row + 1] * xq[r][e] + s_v[r * N + row + 1] * xc[r][e];
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (on) yp[r][e] += s_c[r * N + row] * n0[e] + s_c[r * N + row + 1] * n1[e];
+    }
+    const uint32_t t0 = row_top(top8(n0), lanes), t1 = row_top(top8(n1), lanes);
+    float sc0, sc1, i0, i1;
+    row_scale<kCode>(t0, &sc0, &i0);
+    row_scale<kCode>(t1, &sc1, &i1);
+    if (on) {
+      codes[(size_t)row * lanes + c8] = quantise8<kCode>(n0, i0, t0 < 0x7f800000u);
+      codes[(size_t)(row + 1) * lanes + c8] = quantise8<kCode>(n1, i1, t1 < 0x7f800000u);
+      if (c8 == 0) {
+        scales[row] = sc0;
+        scales[row + 1] = sc1;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_y[(rg * R + r) * P + 8 * c8 + e] = yp[r][e];
+  __syncthreads();
+  T* y = static_cast<T*>(a.y) + in * R * P;
+  for (int o = tid; o < R * P; o += kThreads) {
+    float sum = 0.f;
+    for (int g = 0; g < groups; ++g) sum += s_y[g * R * P + o];
+    y[o] = from_f32<T>(sum);
+  }
+}
+
+template <typename T, int R, int kCode>
+hipError_t launch_decode_r(const CacheArgs& a, hipStream_t stream) {
+  const int groups = kThreads / (a.P / 8);
+  const size_t lds = sizeof(float) * (a.N + 3 * (size_t)R * a.N + (size_t)groups * R * a.P);
+  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&decode_kernel<T, R, kCode>), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((decode_kernel<T, R, kCode>), dim3(a.S * a.H), dim3(kThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T, int kCode>
+hipError_t launch_decode_t(const CacheArgs& a, hipStream_t stream) {
+  switch (a.R) {
+    case 1: return launch_decode_r<T, 1, kCode>(a, stream);
+    case 2: return launch_decode_r<T, 2, kCode>(a, stream);
+    case 4: return launch_decode_r<T, 4, kCode>(a, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+template <int kCode>
+hipError_t launch_load_t(const CacheArgs& a, m3_dtype dtype, hipStream_t stream) {
+  if (dtype == M3_BF16)
+    hipLaunchKernelGGL((load_kernel<kCode, bf16>), dim3(a.S * a.H), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((load_kernel<kCode, float>), dim3(a.S * a.H), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_state_store(const CacheArgs& a, m3_code code, hipStream_t stream) {
+  if (code == M3_CODE_INT8)
+    hipLaunchKernelGGL(store_kernel<M3_CODE_INT8>, dim3(a.S * a.H), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL(store_kernel<M3_CODE_E4M3>, dim3(a.S * a.H), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_state_load(const CacheArgs& a, m3_code code, m3_dtype dtype,
+                             hipStream_t stream) {
+  return code == M3_CODE_INT8 ? launch_load_t<M3_CODE_INT8>(a, dtype, stream)
+                              : launch_load_t<M3_CODE_E4M3>(a, dtype, stream);
+}
+
+hipError_t launch_decode_cached(const CacheArgs& a, m3_code code, m3_dtype dtype,
+                                hipStream_t stream) {
+  if (dtype == M3_BF16)
+    return code == M3_CODE_INT8 ? launch_decode_t<bf16, M3_CODE_INT8>(a, stream)
+                                : launch_decode_t<bf16, M3_CODE_E4M3>(a, stream);
+  return code == M3_CODE_INT8 ? launch_decode_t<float, M3_CODE_INT8>(a, stream)
+                              : launch_decode_t<float, M3_CODE_E4M3>(a, stream);
+}
+
+}  // namespace m3
