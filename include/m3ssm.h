@@ -525,9 +525,9 @@ m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const
  * [H, N] float scales (dense): element = code * scale of its row.  A row of P
  * values is quantised as
  *
- *   amax = max |h|,  scale = amax / Q,  code = round(h * (Q / amax))
+ *   amax = max |h|,  scale = amax * (1 / Q),  code = round(h * (Q / amax))
  *
- * (quotients and product rounded to float, the code to the nearest, ties to
+ * (quotients and products rounded to float, the code to the nearest, ties to
  * even), Q = 127 for int8 codes and 448 for e4m3 ones (the OCP 8-bit float:
  * 4 exponent and 3 mantissa bits).  A row whose amax is below 2^-100 is held
  * as zeros (scale 0).  A row that holds an infinity or NaN gets codes 0 and
@@ -559,6 +559,16 @@ m3_status m3_state_load(const m3_dims* dims, m3_code code, m3_dtype dtype, const
  * the recurrence in float, writes y from the new state before it is rounded,
  * and the new state's codes and scales into the slot.  The other arguments
  * and the reduced forms (lam, theta NULL) are those of m3_decode_step.
+ *
+ * The codes are defined by float operations, each rounded, none fused, so
+ * that every evaluation writes the same cache (a last bit can decide a code):
+ *
+ *   h = code * scale
+ *   h = h + ((1 - lam) * dt) * (sum_r B_prev[r] * x_prev[r])
+ *   (h_0, h_1) = (cos * h_0 - sin * h_1, sin * h_0 + cos * h_1)   angle dt * theta
+ *   h = alpha * h + (lam * dt) * (sum_r B_t[r] * x_t[r]),  alpha = exp(dt * A)
+ *
+ * (r in order) and the rows of h are quantised as above.
  */
 m3_status m3_decode_step_cached(const m3_dims* dims, m3_dtype dtype, m3_code code, void* codes,
                                 float* scales, const int32_t* slots, int64_t n_slots,

@@ -162,7 +162,7 @@ def to_e4m3(v):
 
 def quantise(h, fmt):
     """Rows (last axis) of float32 values -> (codes uint8, scales float32), as
-    the format is defined: quotients and the product rounded to float32."""
+    the format is defined: quotients and products rounded to float32."""
     h = h.astype(np.float32)
     q = CODE_MAX[fmt]
     with np.errstate(all="ignore"):
@@ -170,7 +170,7 @@ def quantise(h, fmt):
         bad = ~np.isfinite(h).all(-1)
         held = ~bad & (amax >= TINY_ROW)
         safe = np.where(held, amax, np.float32(1))
-        scale = np.where(held, safe / q, np.float32(0)).astype(np.float32)
+        scale = np.where(held, safe * (np.float32(1) / q), np.float32(0)).astype(np.float32)
         inv = np.where(held, q / safe, np.float32(0)).astype(np.float32)
         v = np.where(bad[..., None], np.float32(0), h) * inv[..., None]
     v = np.clip(v.astype(np.float32), -q, q)

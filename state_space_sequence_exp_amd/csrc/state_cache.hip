@@ -1,16 +1,25 @@
 // state_cache.hip -- recurrent states held in 8 bits: quantised as they are
 // written, read back, and the decode step on them.
 //
-// A row of P values has one scale: amax = max |h|, scale = amax / Q, code =
-// round(h (Q / amax)), Q = 127 (int8) or 448 (e4m3); rows below 2^-100 are
+// A row of P values has one scale: amax = max |h|, scale = amax (1 / Q), code
+// = round(h (Q / amax)), Q = 127 (int8) or 448 (e4m3); rows below 2^-100 are
 // zeros, rows with an infinity or NaN get scale NaN.
 //
-// The decode step is decode.hip's: a workgroup owns one (sequence, head),
-// builds the per-row coefficients of the recurrence in the LDS
-//   rot[k] = (cos, sin)(dt theta_k),  u_r[n] = alpha (1-lam) dt (R B_prev[r])[n],
-//   v_r[n] = lam dt B_t[r][n],  c_r[n] = C_t[r][n]
-// and every thread updates 8 columns of row pairs in registers; the row
-// maxima of the new state come from the lanes that share the row.
+// A code is a whole number, and a difference in the last bit of a state value
+// that lies next to a border changes it for good.  So the decode step is
+// defined operation by operation, each rounded to float, none fused:
+//   h  = code scale
+//   h += ((1 - lam) dt) (sum_r B_prev[r] x_prev[r])
+//   h  = (cos h_0 - sin h_1, sin h_0 + cos h_1)           per row pair
+//   h  = alpha h + (lam dt) (sum_r B[r] x[r])             r in order
+// and any evaluation of these gets the same cache.  That takes about 30 vector
+// operations an element at R = 4 against 18 with fused ones; the sums of y,
+// which is rounded once and not kept, are fused.
+//
+// A workgroup owns one (sequence, head).  Its threads request their codes,
+// then put the coefficients of the row pairs into the LDS, a pair's together;
+// a thread updates 8 columns of its row pairs in registers; a row's largest
+// magnitude comes from the lanes that share the row.
 #include "layer_internal.h"
 #include "m3_device.h"
 
@@ -74,7 +83,7 @@ __device__ __forceinline__ void row_scale(uint32_t top, float* scale, float* inv
   } else if (amax < kTinyRow) {
     *scale = *inv = 0.f;
   } else {
-    *scale = amax / Code<kCode>::kMax;
+    *scale = amax * (1.f / Code<kCode>::kMax);
     *inv = Code<kCode>::kMax / amax;
   }
 }
@@ -171,97 +180,162 @@ __global__ void __launch_bounds__(kThreads) load_kernel(CacheArgs a) {
   }
 }
 
-template <typename T, int R, int kCode>
+// 8 consecutive inputs as floats.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
+  // the pointers are aligned to four elements
+  const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
+  const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// A row pair's coefficients in the LDS: cos, sin, 2 unused, then B_prev, B
+// and C of row 0 (R each) and of row 1.
+template <int R>
+struct PairCoef {
+  float cs, sn, pad[2];
+  float bp[2][R], b[2][R], c[2][R];
+};
+
+template <typename T, int R, int kCode, bool kTrap, bool kRot, int NPT>
 __global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
+#pragma clang fp contract(off)
   extern __shared__ __align__(16) float dsm[];
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
   const int slot = slot_of(a, i);
-  if (slot < 0 || named_before(a, i, slot)) return;
+  if (slot < 0) return;
   const int N = a.N, P = a.P, npair = N / 2, lanes = P / 8;
   const int tid = threadIdx.x, c8 = tid % lanes, rg = tid / lanes, groups = kThreads / lanes;
   const size_t in = (size_t)i * a.H + head;       // this token's inputs
   const size_t unit = (size_t)slot * a.H + head;  // its state
-  float2* s_rot = reinterpret_cast<float2*>(dsm);
-  float* s_u = dsm + 2 * npair;
-  float* s_v = s_u + R * N;
-  float* s_c = s_v + R * N;
-  float* s_y = s_c + R * N;  // [groups][R][P]
+  PairCoef<R>* s_pair = reinterpret_cast<PairCoef<R>*>(dsm);
+  float* s_y = dsm + (size_t)npair * (sizeof(PairCoef<R>) / 4);  // [groups][R][P]
 
-  const float d = a.dt[in], la = a.lam ? a.lam[in] : 1.f;
-  const float alpha = expf(d * a.A[head]);
-  const float cu = alpha * (1.f - la) * d, cv = la * d;
-  for (int kp = tid; kp < npair; kp += kThreads) {
-    float sn = 0.f, cn = 1.f;
-    if (a.theta) sincosf(d * a.theta[in * npair + kp], &sn, &cn);
-    s_rot[kp] = make_float2(cn, sn);
+  // everything this thread reads, requested before it is used
+  uint2* codes = reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.codes) + unit * N * P);
+  float* scales = a.scales + unit * N;
+  uint2 w0[NPT], w1[NPT];
+  float2 sc[NPT];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const size_t at = (in * R + r) * N + 2 * kp;
-      const float2 bt = load_pair(static_cast<const T*>(a.B_t) + at);
-      const float2 bp = a.lam ? load_pair(static_cast<const T*>(a.B_prev) + at) : make_float2(0, 0);
-      const float2 ct = load_pair(static_cast<const T*>(a.C_t) + at);
-      *reinterpret_cast<float2*>(s_u + r * N + 2 * kp) =
-          make_float2(cu * (cn * bp.x - sn * bp.y), cu * (sn * bp.x + cn * bp.y));
-      *reinterpret_cast<float2*>(s_v + r * N + 2 * kp) = make_float2(cv * bt.x, cv * bt.y);
-      *reinterpret_cast<float2*>(s_c + r * N + 2 * kp) = ct;
+  for (int k = 0; k < NPT; ++k) {
+    const int kp = rg + k * groups;
+    w0[k] = w1[k] = make_uint2(0u, 0u);
+    sc[k] = make_float2(0.f, 0.f);
+    if (kp < npair) {
+      w0[k] = codes[(size_t)(2 * kp) * lanes + c8];
+      w1[k] = codes[(size_t)(2 * kp + 1) * lanes + c8];
+      sc[k] = make_float2(scales[2 * kp], scales[2 * kp + 1]);
     }
   }
   float xc[R][8], xq[R][8], yp[R][8];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
+    const size_t at = (in * R + r) * P + 8 * c8;
+    load8(static_cast<const T*>(a.x_t) + at, xc[r]);
+    if constexpr (kTrap) load8(static_cast<const T*>(a.x_prev) + at, xq[r]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const size_t at = (in * R + r) * P + 8 * c8 + e;
-      xc[r][e] = to_f32(static_cast<const T*>(a.x_t)[at]);
-      xq[r][e] = a.lam ? to_f32(static_cast<const T*>(a.x_prev)[at]) : 0.f;
-      yp[r][e] = 0.f;
+    for (int e = 0; e < 8; ++e) yp[r][e] = 0.f;
+  }
+  const float d = a.dt[in], la = kTrap ? a.lam[in] : 1.f;
+  const float alpha = expf(d * a.A[head]);
+  const float cu = (1.f - la) * d, cv = la * d;
+  for (int kp = tid; kp < npair; kp += kThreads) {
+    PairCoef<R>& q = s_pair[kp];
+    if constexpr (kRot) {
+      const float psi = d * a.theta[in * npair + kp];
+      q.cs = cosf(psi);
+      q.sn = sinf(psi);
     }
-  __syncthreads();
-  uint2* codes = reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.codes) + unit * N * P);
-  float* scales = a.scales + unit * N;
-  for (int k0 = 0; k0 < npair; k0 += groups) {  // every lane of a row together
-    const int kp = k0 + rg;
-    const bool on = kp < npair;
-    const int row = on ? 2 * kp : 0;
-    const uint2 w0 = codes[(size_t)row * lanes + c8], w1 = codes[(size_t)(row + 1) * lanes + c8];
-    const float s0 = scales[row], s1 = scales[row + 1];
-    float v0[8], v1[8], n0[8], n1[8];
-    Code<kCode>::unpack4(w0.x, v0);
-    Code<kCode>::unpack4(w0.y, v0 + 4);
-    Code<kCode>::unpack4(w1.x, v1);
-    Code<kCode>::unpack4(w1.y, v1 + 4);
-    const float2 rc = s_rot[row / 2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float h0 = v0[e] * s0, h1 = v1[e] * s1;
-      n0[e] = alpha * (rc.x * h0 - rc.y * h1);
-      n1[e] = alpha * (rc.y * h0 + rc.x * h1);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        n0[e] += s_u[r * N + row] * xq[r][e] + s_v[r * N + row] * xc[r][e];
-        n1[e] += s_u[r * N + row + 1] * xq[r][e] + s_v[r * N + row + 1] * xc[r][e];
+    for (int r = 0; r < R; ++r) {
+      const size_t at = (in * R + r) * N + 2 * kp;
+      const float2 b = load_pair(static_cast<const T*>(a.B_t) + at);
+      const float2 c = load_pair(static_cast<const T*>(a.C_t) + at);
+      q.b[0][r] = b.x; q.b[1][r] = b.y;
+      q.c[0][r] = c.x; q.c[1][r] = c.y;
+      if constexpr (kTrap) {
+        const float2 p = load_pair(static_cast<const T*>(a.B_prev) + at);
+        q.bp[0][r] = p.x; q.bp[1][r] = p.y;
       }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (on) yp[r][e] += s_c[r * N + row] * n0[e] + s_c[r * N + row + 1] * n1[e];
     }
-    const uint32_t t0 = row_top(top8(n0), lanes), t1 = row_top(top8(n1), lanes);
+  }
+  // of entries with one slot the first takes it; also the barrier before the
+  // coefficients are read
+  int same = 0;
+  if (a.slots)
+    for (int j = tid; j < i; j += kThreads) same |= a.slots[j] == slot ? 1 : 0;
+  if (__syncthreads_or(same)) return;
+
+#pragma unroll
+  for (int k = 0; k < NPT; ++k) {
+    const int kp = rg + k * groups;
+    if (k * groups >= npair) break;  // for the whole workgroup
+    const bool on = kp < npair;
+    const PairCoef<R>& q = s_pair[on ? kp : 0];
+    float v0[8], v1[8];
+    Code<kCode>::unpack4(w0[k].x, v0);
+    Code<kCode>::unpack4(w0[k].y, v0 + 4);
+    Code<kCode>::unpack4(w1[k].x, v1);
+    Code<kCode>::unpack4(w1[k].y, v1 + 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float h0 = v0[e] * sc[k].x, h1 = v1[e] * sc[k].y;
+      if constexpr (kTrap) {
+        float t0 = q.bp[0][0] * xq[0][e], t1 = q.bp[1][0] * xq[0][e];
+#pragma unroll
+        for (int r = 1; r < R; ++r) {
+          t0 = t0 + q.bp[0][r] * xq[r][e];
+          t1 = t1 + q.bp[1][r] * xq[r][e];
+        }
+        h0 = h0 + cu * t0;
+        h1 = h1 + cu * t1;
+      }
+      if constexpr (kRot) {
+        const float n0 = q.cs * h0 - q.sn * h1, n1 = q.sn * h0 + q.cs * h1;
+        h0 = n0;
+        h1 = n1;
+      }
+      float t0 = q.b[0][0] * xc[0][e], t1 = q.b[1][0] * xc[0][e];
+#pragma unroll
+      for (int r = 1; r < R; ++r) {
+        t0 = t0 + q.b[0][r] * xc[r][e];
+        t1 = t1 + q.b[1][r] * xc[r][e];
+      }
+      v0[e] = alpha * h0 + cv * t0;
+      v1[e] = alpha * h1 + cv * t1;
+      if (on) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          yp[r][e] = __builtin_fmaf(q.c[0][r], v0[e], __builtin_fmaf(q.c[1][r], v1[e], yp[r][e]));
+      }
+    }
+    const uint32_t t0 = row_top(top8(v0), lanes), t1 = row_top(top8(v1), lanes);
     float sc0, sc1, i0, i1;
     row_scale<kCode>(t0, &sc0, &i0);
     row_scale<kCode>(t1, &sc1, &i1);
     if (on) {
-      codes[(size_t)row * lanes + c8] = quantise8<kCode>(n0, i0, t0 < 0x7f800000u);
-      codes[(size_t)(row + 1) * lanes + c8] = quantise8<kCode>(n1, i1, t1 < 0x7f800000u);
+      codes[(size_t)(2 * kp) * lanes + c8] = quantise8<kCode>(v0, i0, t0 < 0x7f800000u);
+      codes[(size_t)(2 * kp + 1) * lanes + c8] = quantise8<kCode>(v1, i1, t1 < 0x7f800000u);
       if (c8 == 0) {
-        scales[row] = sc0;
-        scales[row + 1] = sc1;
+        scales[2 * kp] = sc0;
+        scales[2 * kp + 1] = sc1;
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s_y[(rg * R + r) * P + 8 * c8 + e] = yp[r][e];
+  for (int r = 0; r < R; ++r) {
+    float4* o = reinterpret_cast<float4*>(s_y + (rg * R + r) * P + 8 * c8);
+    o[0] = make_float4(yp[r][0], yp[r][1], yp[r][2], yp[r][3]);
+    o[1] = make_float4(yp[r][4], yp[r][5], yp[r][6], yp[r][7]);
+  }
   __syncthreads();
   T* y = static_cast<T*>(a.y) + in * R * P;
   for (int o = tid; o < R * P; o += kThreads) {
@@ -271,14 +345,37 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
   }
 }
 
+template <typename T, int R, int kCode, bool kTrap, bool kRot, int NPT>
+hipError_t launch_decode_npt(const CacheArgs& a, hipStream_t stream) {
+  const int groups = kThreads / (a.P / 8);
+  const size_t lds =
+      sizeof(PairCoef<R>) * (a.N / 2) + sizeof(float) * (size_t)groups * R * a.P;
+  const hipError_t e = lds_limit(
+      reinterpret_cast<const void*>(&decode_kernel<T, R, kCode, kTrap, kRot, NPT>), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((decode_kernel<T, R, kCode, kTrap, kRot, NPT>), dim3(a.S * a.H),
+                     dim3(kThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+// Row pairs a thread: N / 2 over 256 / (P / 8) groups of lanes, at most 4
+// where decode_max_n allows N.
+template <typename T, int R, int kCode, bool kTrap, bool kRot>
+hipError_t launch_decode_form(const CacheArgs& a, hipStream_t stream) {
+  const int groups = kThreads / (a.P / 8), npt = (a.N / 2 + groups - 1) / groups;
+  if (npt <= 1) return launch_decode_npt<T, R, kCode, kTrap, kRot, 1>(a, stream);
+  if (npt <= 2) return launch_decode_npt<T, R, kCode, kTrap, kRot, 2>(a, stream);
+  if (npt <= 4) return launch_decode_npt<T, R, kCode, kTrap, kRot, 4>(a, stream);
+  return hipErrorInvalidValue;
+}
+
 template <typename T, int R, int kCode>
 hipError_t launch_decode_r(const CacheArgs& a, hipStream_t stream) {
-  const int groups = kThreads / (a.P / 8);
-  const size_t lds = sizeof(float) * (a.N + 3 * (size_t)R * a.N + (size_t)groups * R * a.P);
-  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&decode_kernel<T, R, kCode>), lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decode_kernel<T, R, kCode>), dim3(a.S * a.H), dim3(kThreads), lds, stream, a);
-  return hipGetLastError();
+  if (a.lam)
+    return a.theta ? launch_decode_form<T, R, kCode, true, true>(a, stream)
+                   : launch_decode_form<T, R, kCode, true, false>(a, stream);
+  return a.theta ? launch_decode_form<T, R, kCode, false, true>(a, stream)
+                 : launch_decode_form<T, R, kCode, false, false>(a, stream);
 }
 
 template <typename T, int kCode>
