@@ -421,22 +421,32 @@ typedef struct {
   int64_t batch;    /* sequences (>= 0) */
   int64_t seqlen;   /* T (>= 0; ignored by m3_gated_scan_step) */
   int64_t channels; /* D (>= 1) */
-  /* elements from one token to the next, >= channels; 0 means channels */
+  /* elements from one token to the next, >= channels and < 2^22 - 1024; 0
+     means channels */
   int64_t ld_x, ld_f, ld_g, ld_y;    /* ld_y also of dy */
   int64_t ld_dx, ld_df, ld_dg;       /* backward only */
 } m3_scan_dims;
 
 /*
  * Bytes of device workspace m3_gated_scan and m3_gated_scan_backward need (0:
- * none, or an unsupported shape).  Host only.
+ * none, as with up to 256 tokens, or an unsupported shape).  Host only.
+ *
+ * The workspace (256-byte aligned) holds the counters and words by which the
+ * chunks of a sequence hand on their states.  They are zero on entry and left
+ * zero, so a buffer zero-filled once serves every later call of any shape;
+ * calls that overlap need distinct ones.  Word 1 is an error word, read and
+ * cleared by m3_prefill_workspace_error: 1 when a chunk waited beyond its
+ * bounded spin for another (its outputs, and those of the chunks after it,
+ * are then NaN), 2 when the counters were not zero on entry (the workgroups
+ * that see it compute nothing).  After either, zero-fill the workspace.
  */
 size_t m3_gated_scan_workspace_size(const m3_scan_dims* dims, m3_dtype dtype);
 
 /*
  * The whole sequence: y for every token, h_last if not NULL, states if not
  * NULL.  g, h0 (zeros) may be NULL.  Pointers need element alignment only;
- * arrays whose base and ld are multiples of 16 bytes are read in 16-byte
- * vectors.  y must not overlap an input.  seqlen == 0 writes h_last = h0
+ * where every array's rows start at a multiple of four elements and channels
+ * is one, they are moved as such vectors.  y must not overlap an input.  seqlen == 0 writes h_last = h0
  * (zeros when NULL); batch == 0 enqueues nothing.
  */
 m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x, const void* f,

@@ -5,14 +5,20 @@ rows.  Plain NumPy from the formulas; shares no code with the HIP path.
 The recurrence and the norm also return how far a float32 evaluation may be
 from the exact values, by carrying each step's rounding through the same
 formulas (running error analysis): with u = 2^-24, a gate's two values within
-DELTA = 16 u relative (a hardware exponential and reciprocal, two ulps each,
-and the products around them), every state update within C = 8 roundings of
-its terms (a state composed from partial products takes up to that many)."""
+delta(f) = (8 + 2 |f|) u relative (the hardware exponential's argument f
+log2(e) is rounded, |f| u, and its constant is, 0.3 |f| u; the exponential and
+the reciprocal are within an ulp, 2 u, each; the sum and the product add 2 u),
+every state update within C = 8 roundings of its terms (a state composed from
+partial products takes up to that many)."""
 import numpy as np
 
 U = 2.0 ** -24
-DELTA = 16 * U
 C = 8
+
+
+def delta(f):
+    """Relative error of a float sigmoid of f, and of one minus it."""
+    return (8 + 2 * np.minimum(np.abs(f), 128)) * U
 
 
 def sigmoid(v):
@@ -24,7 +30,7 @@ def gated_scan(x, f, g=None, h0=None):
     """x, f, g [B,T,D] float64.  Returns dict: y, h (every token), before (the
     state each token meets), h_last, and the bounds e_h, e_y, e_last."""
     B, T, D = x.shape
-    a, w = sigmoid(f), sigmoid(-f)
+    a, w, df = sigmoid(f), sigmoid(-f), delta(f)
     h = np.zeros((B, D)) if h0 is None else h0.astype(np.float64)
     e = np.zeros((B, D))
     hs, es, before, e_before = (np.empty((B, T, D)) for _ in range(4))
@@ -33,8 +39,8 @@ def gated_scan(x, f, g=None, h0=None):
         # masks: w = 0 does not look at x, a = 0 not at the state
         xt = np.where(w[:, t] == 0, 0.0, x[:, t])
         ht, et = np.where(a[:, t] == 0, 0.0, h), np.where(a[:, t] == 0, 0.0, e)
-        e = a[:, t] * et + DELTA * w[:, t] * np.abs(xt) + \
-            DELTA * np.minimum(a[:, t], w[:, t]) * np.abs(ht) + \
+        e = a[:, t] * et + df[:, t] * w[:, t] * np.abs(xt) + \
+            df[:, t] * np.minimum(a[:, t], w[:, t]) * np.abs(ht) + \
             C * U * (w[:, t] * np.abs(xt) + a[:, t] * np.abs(ht))
         h = a[:, t] * ht + w[:, t] * xt
         hs[:, t], es[:, t] = h, e
@@ -43,7 +49,7 @@ def gated_scan(x, f, g=None, h0=None):
         out.update(y=hs, e_y=es)
     else:
         s = g * sigmoid(g)
-        out.update(y=hs * s, e_y=es * np.abs(s) + (DELTA + 4 * U) * np.abs(hs * s))
+        out.update(y=hs * s, e_y=es * np.abs(s) + (delta(g) + 4 * U) * np.abs(hs * s))
     return out
 
 
@@ -59,30 +65,30 @@ def gated_scan_backward(dy, x, f, g=None, h0=None, dh_last=None):
         sg = sigmoid(g)
         slope = sg * (1 + g * (1 - sg))
         out["dg"] = dy * s["h"] * slope
-        # the slope's two terms may cancel: bound by their magnitudes
-        mag = sg * (1 + np.abs(g) * (1 - sg))
-        out["e_dg"] = np.abs(dy) * (s["e_h"] * mag + np.abs(s["h"]) * mag * (2 * DELTA + 8 * U))
+        # d slope = d sg (1 + g (1 - sg)) + sg g d(1 - sg), both within delta sg
+        mag = sg * (1 + np.abs(g))
+        out["e_dg"] = np.abs(dy) * (s["e_h"] * mag + np.abs(s["h"]) * mag * (2 * delta(g) + 8 * U))
         dh = dy * g * sg
-        e_dh = (DELTA + 4 * U) * np.abs(dh)
+        e_dh = (delta(g) + 4 * U) * np.abs(dh)
     u = np.zeros((B, D)) if dh_last is None else dh_last.astype(np.float64)
     e = np.zeros((B, D))
     out["dx"], out["df"], out["e_dx"], out["e_df"] = (np.empty((B, T, D)) for _ in range(4))
     for t in range(T - 1, -1, -1):
         G = dh[:, t] + u
         eG = e_dh[:, t] + e + C * U * (np.abs(dh[:, t]) + np.abs(u))
-        at, wt = a[:, t], w[:, t]
+        at, wt, dt = a[:, t], w[:, t], delta(f[:, t])
         slope = at * wt
         diff = np.where(slope == 0, 0.0, before[:, t] - x[:, t])
         e_diff = s["e_before"][:, t] + 2 * U * (np.abs(before[:, t]) + np.abs(x[:, t]))
         e_diff = np.where(slope == 0, 0.0, e_diff)
         out["dx"][:, t] = G * wt
-        out["e_dx"][:, t] = eG * wt + (DELTA + 4 * U) * np.abs(G * wt)
+        out["e_dx"][:, t] = eG * wt + (dt + 4 * U) * np.abs(G * wt)
         out["df"][:, t] = G * diff * slope
         out["e_df"][:, t] = slope * (eG * np.abs(diff) + np.abs(G) * e_diff) + \
-            (2 * DELTA + 8 * U) * np.abs(G * diff * slope)
+            (2 * dt + 8 * U) * np.abs(G * diff * slope)
         G, eG = np.where(at == 0, 0.0, G), np.where(at == 0, 0.0, eG)
         u = at * G
-        e = at * eG + DELTA * np.minimum(at, wt) * np.abs(G) + C * U * np.abs(u)
+        e = at * eG + dt * np.minimum(at, wt) * np.abs(G) + C * U * np.abs(u)
     out["dh0"], out["e_dh0"] = u, e
     return out
 

@@ -1,10 +1,12 @@
 // gate.h -- the gate of the gated linear recurrence on the device.
 //
-//   a = sigmoid(f),  w = 1 - a = sigmoid(-f):  e = exp(-f), a = 1 / (1 + e),
-//   w = e a (1 where e overflows)
+//   a = sigmoid(f) = 1 / (1 + e),  w = 1 - a = e / (1 + e),  e = exp(-f)
 //
-// so that both keep their relative precision, and a product with a is taken
-// from the smaller of the two: a near 1 (long memory) as 1 - w.
+// A gate is kept as one float z, the smaller of a and w with a's sign bit
+// set: z = w where e <= 1, z = -a where e > 1.  Either value follows from it
+// with its relative precision (a long memory is its distance w from 1, a
+// short one a itself), so does the slope a w = |z| (1 - |z|), and the masks
+// are exact: +0 passes the state on, -0 drops it.
 #pragma once
 
 #include "m3_device.h"
@@ -13,38 +15,50 @@ namespace m3 {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// exp(-v) on the hardware exponential: v log2(e) in two floats, the second
-// applied to first order, so the result's error does not grow with |v|.
-__device__ __forceinline__ float exp_neg(float v) {
-  const float hi = -v * kLog2e;
-  // what the rounded product left out, in units of the exponent
-  const float lo = __builtin_fmaf(-v, kLog2e, -hi) + -v * 1.925963033500e-8f;
-  const float e = __builtin_amdgcn_exp2f(hi);
-  const float c = e * (lo * 0.6931471805599453f);
-  // an infinite v leaves no correction (inf - inf)
-  return (c == c && e < 3.0e38f) ? e + c : e;
+// exp(-v) on the hardware exponential; the rounding of v log2(e) makes its
+// relative error up to (2 + 1.3 |v|) 2^-24.
+__device__ __forceinline__ float exp_neg(float v) { return __builtin_amdgcn_exp2f(v * -kLog2e); }
+
+__device__ __forceinline__ float sigmoid_of(float v) {
+  return __builtin_amdgcn_rcpf(1.f + exp_neg(v));
 }
 
-struct Gate {
-  float a, w;
+__device__ __forceinline__ float gate_of(float f) {
+  const float e = exp_neg(f), a = __builtin_amdgcn_rcpf(1.f + e);
+  return e > 1.f ? -a : e * a;
+}
+
+__device__ __forceinline__ bool gate_cut(float z) { return __float_as_int(z) < 0; }
+__device__ __forceinline__ bool gate_drops(float z) { return __float_as_uint(z) == 0x80000000u; }
+__device__ __forceinline__ bool gate_passes(float z) { return __float_as_uint(z) == 0u; }
+
+// w
+__device__ __forceinline__ float gate_w(float z) { return z + (gate_cut(z) ? 1.f : 0.f); }
+// a v, for a finite v
+__device__ __forceinline__ float gate_keep(float z, float v) {
+  return __builtin_fmaf(-z, v, gate_cut(z) ? 0.f : v);
+}
+// a h + w x: a gate that drops the state does not look at h, one that passes
+// it not at x.
+__device__ __forceinline__ float gate_step(float z, float h, float x) {
+  const float hs = gate_drops(z) ? 0.f : h, xs = gate_passes(z) ? 0.f : x;
+  return __builtin_fmaf(gate_w(z), xs, gate_keep(z, hs));
+}
+
+// A run of steps as a map of the state before it: h -> A h + B.  A is 0 only
+// where a gate of the run dropped the state (then h is not looked at): a
+// product that underflows stays at the smallest normal float.
+struct Run {
+  float A, B;
 };
-__device__ __forceinline__ Gate gate_of(float f) {
-  const float e = exp_neg(f);
-  const float a = 1.f / (1.f + e);
-  return Gate{a, e > 3.0e38f ? 1.f : e * a};
+__device__ __forceinline__ float run_apply(Run r, float h) {
+  return __builtin_fmaf(r.A, r.A == 0.f ? 0.f : h, r.B);
 }
-
-// a v: from the smaller of a and w, so that neither a long memory (a near 1,
-// held as w) nor a short one loses digits.  a = 0 does not look at v.
-__device__ __forceinline__ float gate_decay(Gate q, float v) {
-  const float s = q.w < 0.5f ? __builtin_fmaf(-q.w, v, v) : q.a * v;
-  return q.a == 0.f ? 0.f : s;
+// `first`, then `then`.
+__device__ __forceinline__ Run run_join(Run first, Run then) {
+  const float p = first.A * then.A;
+  const bool none = first.A == 0.f || then.A == 0.f;
+  return Run{none ? 0.f : (p < 1.17549435e-38f ? 1.17549435e-38f : p), run_apply(then, first.B)};
 }
-// a h + w x; w = 0 does not look at x.
-__device__ __forceinline__ float gate_step(Gate q, float h, float x) {
-  return __builtin_fmaf(q.w, q.w == 0.f ? 0.f : x, gate_decay(q, h));
-}
-
-__device__ __forceinline__ float sigmoid_of(float v) { return 1.f / (1.f + exp_neg(v)); }
 
 }  // namespace m3

@@ -1,136 +1,256 @@
 // gated_scan.hip -- the gated linear recurrence, per channel
 //
-//   h_t = a_t h_{t-1} + (1 - a_t) x_t,  a = sigmoid(f),  y = h * silu(g)
+//   h_t = a_t h_{t-1} + w_t x_t,  a = sigmoid(f),  w = 1 - a,  y = h * silu(g)
 //
-// and its gradients: with G_t = dL/dh_t = dy_t silu(g_t) + a_{t+1} G_{t+1},
-//   dx = G w,  df = G (h_{t-1} - x) a w,  dg = dy h silu'(g),  dh0 = a_0 G_0.
+// over whole sequences (one pass: see scan_tile.h) and for one token.
 //
-// One lane per channel walks the tokens.  The backward pass goes from the
-// last chunk to the first: it walks a chunk forward from its kept entry
-// state, its states in the LDS, then back.
-#include "gate.h"
-#include "layer_internal.h"
+// A workgroup requests its chunk of x and f, forms its threads' maps, joins
+// and publishes them, requests g, looks back for the state that enters the
+// chunk, and walks each thread's tokens again from the state before them.
+#include "scan_tile.h"
 
 namespace m3 {
 namespace {
 
-constexpr int kLanes = 64;
+template <typename T, bool kGate, bool kVec>
+__global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, ChainWs ws, int nTiles) {
+  constexpr int C = kC, W = kPerWord<T>, K = kTok<T>, NT = kScanThreads<T>, NW = kScanWaves<T>;
+  __shared__ Run s_wave[NW][C];           // each wave's map, then the join of those before
+  __shared__ Run s_run[kV][NT];                   // the join of the maps before a thread's in its wave
+  __shared__ Run s_part[NW][C];  // the look-back's parts
+  __shared__ float s_entry[C];                    // the state entering the chunk
+  __shared__ int s_word;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nC = (int)a.nC;
+  const int units = (int)a.B * nTiles, unit = blockIdx.x % units;
+  const int64_t b = unit / nTiles;
+  const int d0 = unit % nTiles * C;
+  const int cl = (lane % kLanesAcross) * kV;       // this lane's first channel in the tile
+  const int n = (int)a.D - d0 - cl;               // channels from there to the row's end
+  const int k0 = nC > 1 ? chain_ticket(ws, unit, nC, &s_word) : 0;
+  if (k0 >= nC) return;
+  const int tok = (tid / kLanesAcross) * K;    // this thread's first token in the chunk
+  const int nt = (int)(a.T - (int64_t)k0 * M3_SCAN_CHUNK) - tok;  // tokens from there on
+  const int64_t row0 = b * a.T + (int64_t)k0 * M3_SCAN_CHUNK;
+  const Rows<T> rf(a.f, row0 * a.ld_f + d0, a.ld_f, tok, cl), rx(a.x, row0 * a.ld_x + d0, a.ld_x, tok, cl);
 
-template <typename T, bool kGate>
-__global__ void __launch_bounds__(kLanes) scan_kernel(ScanArgs a) {
-  const int64_t d = (int64_t)blockIdx.x * kLanes + threadIdx.x, b = blockIdx.y;
-  if (d >= a.D) return;
-  float h = a.h0 ? a.h0[b * a.D + d] : 0.f;
-  for (int64_t t = 0; t < a.T; ++t) {
-    const int64_t row = b * a.T + t;
-    if (a.states && t % M3_SCAN_CHUNK == 0)
-      a.states[(b * a.nC + t / M3_SCAN_CHUNK) * a.D + d] = h;
-    const float x = to_f32(static_cast<const T*>(a.x)[row * a.ld_x + d]);
-    const Gate q = gate_of(to_f32(static_cast<const T*>(a.f)[row * a.ld_f + d]));
-    h = gate_step(q, h, x);
-    float y = h;
-    if constexpr (kGate) {
-      const float g = to_f32(static_cast<const T*>(a.g)[row * a.ld_g + d]);
-      y = h * (g * sigmoid_of(g));
-    }
-    static_cast<T*>(a.y)[row * a.ld_y + d] = from_f32<T>(y);
-  }
-  if (a.h_last) a.h_last[b * a.D + d] = h;
-}
-
-template <typename T, bool kGate>
-__global__ void __launch_bounds__(kLanes) scan_backward_kernel(ScanArgs a) {
-  __shared__ float s_h[M3_SCAN_CHUNK][kLanes];  // the state before each token
-  const int lane = threadIdx.x;
-  const int64_t d = (int64_t)blockIdx.x * kLanes + lane, b = blockIdx.y;
-  if (d >= a.D) return;
-  float u = a.dh_last ? a.dh_last[b * a.D + d] : 0.f;  // a_{t+1} G_{t+1}
-  for (int64_t c = a.nC - 1; c >= 0; --c) {
-    const int64_t t0 = c * M3_SCAN_CHUNK;
-    const int n = (int)(a.T - t0 < M3_SCAN_CHUNK ? a.T - t0 : M3_SCAN_CHUNK);
-    float h = a.states[(b * a.nC + c) * a.D + d];
-    for (int i = 0; i < n; ++i) {
-      const int64_t row = b * a.T + t0 + i;
-      s_h[i][lane] = h;
-      h = gate_step(gate_of(to_f32(static_cast<const T*>(a.f)[row * a.ld_f + d])), h,
-                    to_f32(static_cast<const T*>(a.x)[row * a.ld_x + d]));
-    }
-    for (int i = n - 1; i >= 0; --i) {
-      const int64_t row = b * a.T + t0 + i;
-      const float x = to_f32(static_cast<const T*>(a.x)[row * a.ld_x + d]);
-      const Gate q = gate_of(to_f32(static_cast<const T*>(a.f)[row * a.ld_f + d]));
-      const float dy = to_f32(static_cast<const T*>(a.dy)[row * a.ld_y + d]);
-      const float before = s_h[i][lane];
-      float dh = dy;
-      if constexpr (kGate) {
-        const float g = to_f32(static_cast<const T*>(a.g)[row * a.ld_g + d]);
-        const float sg = sigmoid_of(g), after = gate_step(q, before, x);
-        static_cast<T*>(a.dg)[row * a.ld_dg + d] =
-            from_f32<T>(dy * after * (sg * __builtin_fmaf(g, 1.f - sg, 1.f)));
-        dh = dy * (g * sg);
+  Pack<T> x[K], f[K], g[K];
+  const bool full = nt >= K && n >= kV;
+  load_rows<T, kVec>(f, rf, full, nt, n, kPassGate<T>);
+  load_rows<T, kVec>(x, rx, full, nt, n, 0u);
+  float z[K][kV];
+#pragma unroll
+  for (int i = 0; i < kWords<T>; ++i) {
+    Run r[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) r[e] = Run{1.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float xv[W], fv[W];
+      unpack_word(x[k].w[i], xv);
+      unpack_word(f[k].w[i], fv);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float q = gate_of(fv[e]);
+        z[k][i * W + e] = q;
+        r[e].A = gate_keep(q, r[e].A);
+        r[e].B = gate_step(q, r[e].B, xv[e]);
       }
-      const float G = dh + u, slope = q.a * q.w;
-      static_cast<T*>(a.dx)[row * a.ld_dx + d] = from_f32<T>(q.w == 0.f ? 0.f : G * q.w);
-      static_cast<T*>(a.df)[row * a.ld_df + d] =
-          from_f32<T>(slope == 0.f ? 0.f : G * (before - x) * slope);
-      u = gate_decay(q, G);
+    }
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int v = i * W + e;
+      Run before;
+      wave_join<false>(r[e], before);
+      s_run[v][tid] = before;
+      if (lane / kLanesAcross == 3) s_wave[wave][cl + v] = r[e];
     }
   }
-  if (a.dh0) a.dh0[b * a.D + d] = u;
+  renew(x);
+  renew(z);
+  if constexpr (kGate) {
+    const Rows<T> rg(a.g, row0 * a.ld_g + d0, a.ld_g, tok, cl);
+    load_rows<T, kVec>(g, rg, full, nt, n, 0u);
+  }
+  __syncthreads();
+  Run total = Run{1.f, 0.f};
+  if (tid < C) {
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const Run m = s_wave[w][tid];
+      s_wave[w][tid] = total;
+      total = run_join(total, m);
+    }
+    if (k0 + 1 < nC && k0 % kScanGroup != kScanGroup - 1)
+      publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
+  }
+  const int ch = tid % C, part = tid / C;
+  const float h0 = a.h0 && d0 + ch < a.D ? a.h0[b * a.D + d0 + ch] : 0.f;
+  s_part[part][ch] = chain_part<NW>(ws, unit, nC, k0, part, ch, h0);
+  __syncthreads();
+  if (tid < C) {
+    float h = 0.f;
+#pragma unroll
+    for (int p = 0; p < NW; ++p) h = run_apply(s_part[p][tid], h);
+    s_entry[tid] = h;
+    const float out = run_apply(total, h);
+    if (k0 + 1 < nC && k0 % kScanGroup == kScanGroup - 1)
+      publish(ws.exits + ((size_t)unit * ((nC + kScanGroup - 1) / kScanGroup) + k0 / kScanGroup) * C +
+                  tid,
+              word_of(0.f, out));
+    if (d0 + tid < a.D) {
+      if (a.states) a.states[(b * nC + k0) * a.D + d0 + tid] = h;
+      if (a.h_last && k0 == nC - 1) a.h_last[b * a.D + d0 + tid] = out;
+    }
+  }
+  __syncthreads();
+  if (nC > 1 && tid == 0) s_word = chain_count(ws, unit, nC) ? 1 : 0;
+
+#pragma unroll
+  for (int i = 0; i < kWords<T>; ++i) {
+    float h[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int v = i * W + e;
+      h[e] = run_apply(s_run[v][tid], run_apply(s_wave[wave][cl + v], s_entry[cl + v]));
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float xv[W], gv[W], y[W];
+      unpack_word(x[k].w[i], xv);
+      if constexpr (kGate) unpack_word(g[k].w[i], gv);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        h[e] = gate_step(z[k][i * W + e], h[e], xv[e]);
+        y[e] = h[e];
+        if constexpr (kGate) y[e] = h[e] * (gv[e] * sigmoid_of(gv[e]));
+      }
+      x[k].w[i] = pack_word(y);
+      renew(x[k].w[i]);
+    }
+  }
+  const Rows<T> ry(a.y, row0 * a.ld_y + d0, a.ld_y, tok, cl);
+  store_rows<T, kVec>(x, ry, full, nt, n);
+  if (nC > 1) {
+    __syncthreads();
+    if (s_word) chain_clear(ws, unit, nC);
+  }
 }
 
-template <typename T, bool kGate>
-__global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a) {
-  const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
-  if (d >= a.D) return;
-  const float x = to_f32(static_cast<const T*>(a.x)[b * a.ld_x + d]);
-  const Gate q = gate_of(to_f32(static_cast<const T*>(a.f)[b * a.ld_f + d]));
-  const float h = gate_step(q, a.h_in[b * a.D + d], x);
-  a.h_out[b * a.D + d] = h;
-  float y = h;
-  if constexpr (kGate) {
-    const float g = to_f32(static_cast<const T*>(a.g)[b * a.ld_g + d]);
-    y = h * (g * sigmoid_of(g));
+// h_last of an empty sequence.
+__global__ void __launch_bounds__(256) scan_empty_kernel(const float* h0, float* h_last, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) h_last[i] = h0 ? h0[i] : 0.f;
+}
+
+// One token: a lane takes V channels of a sequence.
+template <typename T, bool kGate, bool kVec>
+__global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a, int64_t packs) {
+  constexpr int W = kPerWord<T>;
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= a.B * packs) return;
+  const int64_t b = j / packs, d = j % packs * kV;
+  const int n = (int)(a.D - d);
+  Pack<T> g;
+  const Pack<T> f = load_pack<T, kVec>(static_cast<const T*>(a.f) + b * a.ld_f + d, n);
+  Pack<T> x = load_pack<T, kVec>(static_cast<const T*>(a.x) + b * a.ld_x + d, n);
+  if constexpr (kGate) g = load_pack<T, kVec>(static_cast<const T*>(a.g) + b * a.ld_g + d, n);
+  Pack<float> h = load_pack<float, kVec>(a.h_in + b * a.D + d, n);
+#pragma unroll
+  for (int i = 0; i < kWords<T>; ++i) {
+    float xv[W], fv[W], gv[W], y[W];
+    unpack_word(x.w[i], xv);
+    unpack_word(f.w[i], fv);
+    if constexpr (kGate) unpack_word(g.w[i], gv);
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int v = i * W + e;
+      y[e] = gate_step(gate_of(fv[e]), __uint_as_float(h.w[v]), xv[e]);
+      h.w[v] = __float_as_uint(y[e]);
+      if constexpr (kGate) y[e] = y[e] * (gv[e] * sigmoid_of(gv[e]));
+    }
+    x.w[i] = pack_word(y);
   }
-  static_cast<T*>(a.y)[b * a.ld_y + d] = from_f32<T>(y);
+  store_pack<float, kVec>(a.h_out + b * a.D + d, n, h);
+  store_pack<T, kVec>(static_cast<T*>(a.y) + b * a.ld_y + d, n, x);
+}
+
+
+template <typename T>
+hipError_t launch_scan_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
+  constexpr size_t es = sizeof(T);
+  const int tiles = (int)scan_tiles(a.D);
+  const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
+                   vec_rows(a.g, a.ld_g, es) && vec_rows(a.y, a.ld_y, es);
+  const dim3 grid((unsigned)(a.B * tiles * a.nC));
+#define M3_SCAN_LAUNCH(G, VEC)                                                             \
+  hipLaunchKernelGGL((scan_kernel<T, G, VEC>), grid, dim3(kScanThreads<T>), 0, stream, a, ws, tiles)
+  if (a.g) {
+    if (vec) M3_SCAN_LAUNCH(true, true);
+    else M3_SCAN_LAUNCH(true, false);
+  } else {
+    if (vec) M3_SCAN_LAUNCH(false, true);
+    else M3_SCAN_LAUNCH(false, false);
+  }
+#undef M3_SCAN_LAUNCH
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_step_t(const ScanStepArgs& a, hipStream_t stream) {
+  constexpr size_t es = sizeof(T);
+  const int64_t packs = (a.D + kV - 1) / kV;
+  const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
+                   vec_rows(a.g, a.ld_g, es) && vec_rows(a.y, a.ld_y, es) && vec_rows(a.h_in, a.D, 4) &&
+                   vec_rows(a.h_out, a.D, 4);
+  const dim3 grid((unsigned)((a.B * packs + 255) / 256));
+#define M3_STEP_LAUNCH(G, VEC) \
+  hipLaunchKernelGGL((scan_step_kernel<T, G, VEC>), grid, dim3(256), 0, stream, a, packs)
+  if (a.g) {
+    if (vec) M3_STEP_LAUNCH(true, true);
+    else M3_STEP_LAUNCH(true, false);
+  } else {
+    if (vec) M3_STEP_LAUNCH(false, true);
+    else M3_STEP_LAUNCH(false, false);
+  }
+#undef M3_STEP_LAUNCH
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_scan(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.D + kLanes - 1) / kLanes), (unsigned)a.B);
-  if (dtype == M3_BF16) {
-    if (a.g) hipLaunchKernelGGL((scan_kernel<bf16, true>), grid, dim3(kLanes), 0, stream, a);
-    else hipLaunchKernelGGL((scan_kernel<bf16, false>), grid, dim3(kLanes), 0, stream, a);
-  } else {
-    if (a.g) hipLaunchKernelGGL((scan_kernel<float, true>), grid, dim3(kLanes), 0, stream, a);
-    else hipLaunchKernelGGL((scan_kernel<float, false>), grid, dim3(kLanes), 0, stream, a);
-  }
+int64_t scan_tiles(int64_t D) { return (D + kC - 1) / kC; }
+
+size_t scan_workspace(int64_t B, int64_t D, int64_t nC) {
+  if (nC <= 1) return 0;
+  const size_t units = (size_t)(B * scan_tiles(D)), nG = (nC + kScanGroup - 1) / kScanGroup;
+  return 256 + (units * 8 + 255) / 256 * 256 + units * (nC + nG) * kC * 8;
+}
+
+ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC) {
+  ChainWs w = {};
+  if (!workspace) return w;
+  const size_t units = (size_t)(B * scan_tiles(D));
+  unsigned char* p = static_cast<unsigned char*>(workspace);
+  w.err = reinterpret_cast<int*>(p) + 1;
+  w.counters = reinterpret_cast<int*>(p + 256);
+  w.maps = reinterpret_cast<unsigned long long*>(p + 256 + (units * 8 + 255) / 256 * 256);
+  w.exits = w.maps + units * nC * kC;
+  return w;
+}
+
+hipError_t launch_scan_empty(const float* h0, float* h_last, int64_t n, hipStream_t stream) {
+  hipLaunchKernelGGL(scan_empty_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, h0,
+                     h_last, n);
   return hipGetLastError();
 }
 
-hipError_t launch_scan_backward(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.D + kLanes - 1) / kLanes), (unsigned)a.B);
-  if (dtype == M3_BF16) {
-    if (a.g) hipLaunchKernelGGL((scan_backward_kernel<bf16, true>), grid, dim3(kLanes), 0, stream, a);
-    else hipLaunchKernelGGL((scan_backward_kernel<bf16, false>), grid, dim3(kLanes), 0, stream, a);
-  } else {
-    if (a.g) hipLaunchKernelGGL((scan_backward_kernel<float, true>), grid, dim3(kLanes), 0, stream, a);
-    else hipLaunchKernelGGL((scan_backward_kernel<float, false>), grid, dim3(kLanes), 0, stream, a);
-  }
-  return hipGetLastError();
+hipError_t launch_scan(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
+  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC);
+  return dtype == M3_BF16 ? launch_scan_t<bf16>(a, ws, stream) : launch_scan_t<float>(a, ws, stream);
 }
 
 hipError_t launch_scan_step(const ScanStepArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.D + 255) / 256), (unsigned)a.B);
-  if (dtype == M3_BF16) {
-    if (a.g) hipLaunchKernelGGL((scan_step_kernel<bf16, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((scan_step_kernel<bf16, false>), grid, dim3(256), 0, stream, a);
-  } else {
-    if (a.g) hipLaunchKernelGGL((scan_step_kernel<float, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((scan_step_kernel<float, false>), grid, dim3(256), 0, stream, a);
-  }
-  return hipGetLastError();
+  return dtype == M3_BF16 ? launch_step_t<bf16>(a, stream) : launch_step_t<float>(a, stream);
 }
 
 }  // namespace m3

@@ -1,0 +1,226 @@
+// gated_scan_backward.hip -- gradients of the gated linear recurrence:
+//
+//   G_t = dy_t silu(g_t) + u_t,  u_{t-1} = a_t G_t  (u_{T-1} = dh_last)
+//   dx = G w,  df = G (h_{t-1} - x) a w,  dg = dy h silu'(g),  dh0 = u_{-1}
+//
+// The tile and the chain are scan_tile.h's, the chain from the last chunk to
+// the first.  The state that enters a chunk was kept by the forward pass, so
+// only u has to come from another workgroup.  A thread's tokens make a map of
+// the state before them and one of the u behind them; both have the same A.
+#include "scan_tile.h"
+
+namespace m3 {
+namespace {
+
+template <typename T, bool kGate, bool kVec>
+__global__ void __launch_bounds__(kScanThreads<T>, 4)
+    scan_backward_kernel(ScanArgs a, ChainWs ws, int nTiles) {
+  constexpr int C = kC, W = kPerWord<T>, K = kTok<T>, NT = kScanThreads<T>, NW = kScanWaves<T>;
+  __shared__ Run s_fore[NW][C];           // each wave's map of h, then the state entering it
+  __shared__ Run s_back[NW][C];           // each wave's map of u, then the join of those behind
+  __shared__ Run s_run[kV][NT], s_behind[kV][NT];  // the joins before / behind a thread in its wave
+  __shared__ Run s_part[NW][C];  // the look-back's parts
+  __shared__ float s_entry[C];                    // the u entering the chunk from behind
+  __shared__ int s_word;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nC = (int)a.nC;
+  const int units = (int)a.B * nTiles, unit = blockIdx.x % units;
+  const int64_t b = unit / nTiles;
+  const int d0 = unit % nTiles * C;
+  const int cl = (lane % kLanesAcross) * kV;
+  const int n = (int)a.D - d0 - cl;
+  const int k0 = nC > 1 ? chain_ticket(ws, unit, nC, &s_word) : 0;  // place in the chain
+  if (k0 >= nC) return;
+  const int c0 = nC - 1 - k0;                                       // the chunk
+  const int tok = (tid / kLanesAcross) * K;
+  const int nt = (int)(a.T - (int64_t)c0 * M3_SCAN_CHUNK) - tok;
+  const int64_t row0 = b * a.T + (int64_t)c0 * M3_SCAN_CHUNK;
+  const Rows<T> rf(a.f, row0 * a.ld_f + d0, a.ld_f, tok, cl), rx(a.x, row0 * a.ld_x + d0, a.ld_x, tok, cl);
+  const Rows<T> rd(a.dy, row0 * a.ld_y + d0, a.ld_y, tok, cl), rg(a.g, row0 * a.ld_g + d0, a.ld_g, tok, cl);
+
+  Pack<T> x[K], f[K], dy[K], g[K];
+  const bool full = nt >= K && n >= kV;
+  load_rows<T, kVec>(f, rf, full, nt, n, kPassGate<T>);
+  load_rows<T, kVec>(x, rx, full, nt, n, 0u);
+  load_rows<T, kVec>(dy, rd, full, nt, n, 0u);
+  if constexpr (kGate) load_rows<T, kVec>(g, rg, full, nt, n, 0u);
+  float z[K][kV];
+#pragma unroll
+  for (int i = 0; i < kWords<T>; ++i) {
+    Run r[W], u[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) r[e] = u[e] = Run{1.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float xv[W], fv[W];
+      unpack_word(x[k].w[i], xv);
+      unpack_word(f[k].w[i], fv);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float q = gate_of(fv[e]);
+        z[k][i * W + e] = q;
+        r[e].A = gate_keep(q, r[e].A);
+        r[e].B = gate_step(q, r[e].B, xv[e]);
+      }
+    }
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      float dv[W], gv[W];
+      unpack_word(dy[k].w[i], dv);
+      if constexpr (kGate) unpack_word(g[k].w[i], gv);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        if constexpr (kGate) dv[e] *= gv[e] * sigmoid_of(gv[e]);
+        const float q = z[k][i * W + e], G = dv[e] + u[e].B;
+        u[e].B = gate_keep(q, gate_drops(q) ? 0.f : G);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int v = i * W + e;
+      Run o;
+      u[e].A = r[e].A;
+      wave_join<false>(r[e], o);
+      s_run[v][tid] = o;
+      if (lane / kLanesAcross == 3) s_fore[wave][cl + v] = r[e];
+      wave_join<true>(u[e], o);
+      s_behind[v][tid] = o;
+      if (lane / kLanesAcross == 0) s_back[wave][cl + v] = u[e];
+    }
+  }
+  renew(x);
+  renew(z);
+  renew(dy);
+  if constexpr (kGate) renew(g);
+  __syncthreads();
+  Run total = Run{1.f, 0.f};
+  if (tid < C) {
+#pragma unroll
+    for (int w = NW - 1; w >= 0; --w) {
+      const Run m = s_back[w][tid];
+      s_back[w][tid] = total;
+      total = run_join(total, m);
+    }
+    if (k0 + 1 < nC && k0 % kScanGroup != kScanGroup - 1)
+      publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
+  } else if (tid >= 64 && tid < 64 + C) {
+    const int c = tid - 64;
+    float h = d0 + c < a.D ? a.states[(b * nC + c0) * a.D + d0 + c] : 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const Run m = s_fore[w][c];
+      s_fore[w][c].B = h;
+      h = run_apply(m, h);
+    }
+  }
+  const int ch = tid % C, part = tid / C;
+  const float last = a.dh_last && d0 + ch < a.D ? a.dh_last[b * a.D + d0 + ch] : 0.f;
+  s_part[part][ch] = chain_part<NW>(ws, unit, nC, k0, part, ch, last);
+  __syncthreads();
+  if (tid < C) {
+    float v = 0.f;
+#pragma unroll
+    for (int p = 0; p < NW; ++p) v = run_apply(s_part[p][tid], v);
+    s_entry[tid] = v;
+    const float out = run_apply(total, v);
+    if (k0 + 1 < nC && k0 % kScanGroup == kScanGroup - 1)
+      publish(ws.exits + ((size_t)unit * ((nC + kScanGroup - 1) / kScanGroup) + k0 / kScanGroup) * C +
+                  tid,
+              word_of(0.f, out));
+    if (a.dh0 && k0 == nC - 1 && d0 + tid < a.D) a.dh0[b * a.D + d0 + tid] = out;
+  }
+  __syncthreads();
+  if (nC > 1 && tid == 0) s_word = chain_count(ws, unit, nC) ? 1 : 0;
+
+#pragma unroll
+  for (int i = 0; i < kWords<T>; ++i) {
+    float h[K][W], hk[W], u[W];  // the state before each token; u from behind
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const int v = i * W + e;
+      hk[e] = run_apply(s_run[v][tid], s_fore[wave][cl + v].B);
+      u[e] = run_apply(s_behind[v][tid], run_apply(s_back[wave][cl + v], s_entry[cl + v]));
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float xv[W];
+      unpack_word(x[k].w[i], xv);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        h[k][e] = hk[e];
+        hk[e] = gate_step(z[k][i * W + e], hk[e], xv[e]);
+      }
+    }
+    renew(x);
+    renew(z);
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      float xv[W], dv[W], gv[W], dx[W], df[W], dg[W];
+      unpack_word(x[k].w[i], xv);
+      unpack_word(dy[k].w[i], dv);
+      if constexpr (kGate) unpack_word(g[k].w[i], gv);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float q = z[k][i * W + e];
+        float dh = dv[e];
+        if constexpr (kGate) {
+          const float sg = sigmoid_of(gv[e]), after = k + 1 < K ? h[k + 1][e] : hk[e];
+          dg[e] = dv[e] * after * (sg * __builtin_fmaf(gv[e], 1.f - sg, 1.f));
+          dh = dv[e] * (gv[e] * sg);
+        }
+        const float G = dh + u[e], s = __builtin_fabsf(q);
+        const float slope = s * (1.f - s);
+        dx[e] = gate_passes(q) ? 0.f : G * gate_w(q);
+        df[e] = slope == 0.f ? 0.f : G * (h[k][e] - xv[e]) * slope;
+        u[e] = gate_keep(q, gate_drops(q) ? 0.f : G);
+      }
+      x[k].w[i] = pack_word(dx);
+      dy[k].w[i] = pack_word(df);
+      renew(x[k].w[i]);
+      renew(dy[k].w[i]);
+      if constexpr (kGate) {
+        g[k].w[i] = pack_word(dg);
+        renew(g[k].w[i]);
+      }
+    }
+  }
+  const Rows<T> wx(a.dx, row0 * a.ld_dx + d0, a.ld_dx, tok, cl), wf(a.df, row0 * a.ld_df + d0, a.ld_df, tok, cl);
+  const Rows<T> wg(a.dg, row0 * a.ld_dg + d0, a.ld_dg, tok, cl);
+  store_rows<T, kVec>(x, wx, full, nt, n);
+  store_rows<T, kVec>(dy, wf, full, nt, n);
+  if constexpr (kGate) store_rows<T, kVec>(g, wg, full, nt, n);
+  if (nC > 1) {
+    __syncthreads();
+    if (s_word) chain_clear(ws, unit, nC);
+  }
+}
+
+template <typename T>
+hipError_t launch_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
+  constexpr size_t es = sizeof(T);
+  const int tiles = (int)scan_tiles(a.D);
+  const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
+                   vec_rows(a.g, a.ld_g, es) && vec_rows(a.dy, a.ld_y, es) && vec_rows(a.dx, a.ld_dx, es) &&
+                   vec_rows(a.df, a.ld_df, es) && vec_rows(a.dg, a.ld_dg, es);
+  const dim3 grid((unsigned)(a.B * tiles * a.nC));
+#define M3_SCAN_LAUNCH(G, VEC)                                                                   \
+  hipLaunchKernelGGL((scan_backward_kernel<T, G, VEC>), grid, dim3(kScanThreads<T>), 0, stream, a,  \
+                     ws, tiles)
+  if (a.g) {
+    if (vec) M3_SCAN_LAUNCH(true, true);
+    else M3_SCAN_LAUNCH(true, false);
+  } else {
+    if (vec) M3_SCAN_LAUNCH(false, true);
+    else M3_SCAN_LAUNCH(false, false);
+  }
+#undef M3_SCAN_LAUNCH
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_scan_backward(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
+  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC);
+  return dtype == M3_BF16 ? launch_t<bf16>(a, ws, stream) : launch_t<float>(a, ws, stream);
+}
+
+}  // namespace m3

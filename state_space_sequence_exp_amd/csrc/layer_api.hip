@@ -40,6 +40,8 @@ m3_status done(hipError_t e) { return e == hipSuccess ? M3_SUCCESS : M3_ERR_HIP;
 // Elements of the largest array, kept where byte offsets fit 63 bits.
 constexpr double kMaxElements = 1.0e18;
 
+constexpr int64_t kMaxScanLd = (1 << 22) - 1024;
+
 m3_status check_scan(const m3_scan_dims* d, bool backward) {
   if (!d) return M3_ERR_INVALID_VALUE;
   if (d->batch < 0 || d->seqlen < 0 || d->channels < 1) return M3_ERR_INVALID_VALUE;
@@ -48,10 +50,25 @@ m3_status check_scan(const m3_scan_dims* d, bool backward) {
     if (!ld_ok(lds[i], d->channels)) return M3_ERR_INVALID_VALUE;
     if ((double)d->batch * (double)d->seqlen * (double)ld_of(lds[i], d->channels) > kMaxElements)
       return M3_ERR_NOT_SUPPORTED;
+    // a chunk's rows are addressed by 32-bit byte offsets
+    if (ld_of(lds[i], d->channels) > kMaxScanLd) return M3_ERR_NOT_SUPPORTED;
   }
-  if (d->batch > 65535 || d->channels > INT_MAX || d->seqlen > INT_MAX)
+  // one workgroup a chunk and channel tile; 64-bit words for each in the
+  // workspace
+  if (d->batch > INT_MAX || d->channels > INT_MAX / 2 || d->seqlen > INT_MAX - M3_SCAN_CHUNK ||
+      (double)d->batch * (double)m3::scan_tiles(d->channels) *
+              (double)(d->seqlen / M3_SCAN_CHUNK + 1) > 2147483647.0)
     return M3_ERR_NOT_SUPPORTED;
   return M3_SUCCESS;
+}
+
+// The workspace of a call: M3_SUCCESS, or why it is refused.
+m3_status check_scan_workspace(const m3_scan_dims* d, m3_dtype dtype, const void* workspace,
+                               size_t bytes) {
+  const size_t need_bytes = m3_gated_scan_workspace_size(d, dtype);
+  if (need_bytes == 0) return M3_SUCCESS;
+  if (!workspace || bytes < need_bytes) return M3_ERR_WORKSPACE;
+  return aligned(workspace, 256) ? M3_SUCCESS : M3_ERR_INVALID_VALUE;
 }
 
 m3::ScanArgs scan_args(const m3_scan_dims* d) {
@@ -82,7 +99,8 @@ extern "C" {
 
 size_t m3_gated_scan_workspace_size(const m3_scan_dims* dims, m3_dtype dtype) {
   if (!dtype_ok(&dtype) || check_scan(dims, false) != M3_SUCCESS) return 0;
-  return 0;
+  return m3::scan_workspace(dims->batch, dims->channels,
+                            (dims->seqlen + M3_SCAN_CHUNK - 1) / M3_SCAN_CHUNK);
 }
 
 m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x, const void* f,
@@ -97,6 +115,12 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
       (!need(x, es) || !need(f, es) || !maybe(g, es) || !need(y, es)))
     return M3_ERR_INVALID_VALUE;
   if (dims->batch == 0) return M3_SUCCESS;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dims->seqlen == 0)
+    return h_last ? done(m3::launch_scan_empty(h0, h_last, dims->batch * dims->channels, s))
+                  : M3_SUCCESS;
+  const m3_status wst = check_scan_workspace(dims, dtype, workspace, workspace_bytes);
+  if (wst != M3_SUCCESS) return wst;
   m3::ScanArgs a = scan_args(dims);
   a.x = x;
   a.f = f;
@@ -105,9 +129,8 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
   a.y = y;
   a.h_last = h_last;
   a.states = states;
-  (void)workspace;
-  (void)workspace_bytes;
-  return done(m3::launch_scan(a, dtype, static_cast<hipStream_t>(stream)));
+  a.workspace = a.nC > 1 ? workspace : nullptr;
+  return done(m3::launch_scan(a, dtype, s));
 }
 
 m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const void* dy,
@@ -126,6 +149,12 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
       return M3_ERR_INVALID_VALUE;
   }
   if (dims->batch == 0) return M3_SUCCESS;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dims->seqlen == 0)
+    return dh0 ? done(m3::launch_scan_empty(dh_last, dh0, dims->batch * dims->channels, s))
+               : M3_SUCCESS;
+  const m3_status wst = check_scan_workspace(dims, dtype, workspace, workspace_bytes);
+  if (wst != M3_SUCCESS) return wst;
   m3::ScanArgs a = scan_args(dims);
   a.dy = dy;
   a.x = x;
@@ -137,9 +166,8 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
   a.df = df;
   a.dg = dg;
   a.dh0 = dh0;
-  (void)workspace;
-  (void)workspace_bytes;
-  return done(m3::launch_scan_backward(a, dtype, static_cast<hipStream_t>(stream)));
+  a.workspace = a.nC > 1 ? workspace : nullptr;
+  return done(m3::launch_scan_backward(a, dtype, s));
 }
 
 m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const float* h_in,

@@ -1,0 +1,326 @@
+// scan_tile.h -- what the gated recurrence's forward and backward kernels
+// share: the tile a workgroup owns and the chain between workgroups.
+//
+// A workgroup owns one chunk of 256 tokens of 64 channels: 16 lanes side by
+// side read whole lines of a token, 4 channels a lane, and each thread holds 8
+// (bfloat16, 512 threads) or 4 (float, 1024 threads) consecutive tokens of its
+// lane's channels in registers: 64 bytes of each array either way.  So each
+// input is read once and each output written once.  (8 channels a lane, in
+// 16-byte bfloat16 vectors, take 32 registers more for the maps and spill.)  A
+// thread's steps make one map h -> A h + B a channel; the maps of the 4
+// threads of a wave that share channels are joined by lane moves, those of the
+// waves in the LDS, those of the chunks through the workspace.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "gate.h"
+#include "layer_internal.h"
+
+namespace m3 {
+
+constexpr int kV = 4;                                   // channels a lane
+constexpr int kLanesAcross = 16;                        // lanes side by side in the channels
+constexpr int kC = kV * kLanesAcross;                   // channels of a tile
+constexpr int kScanGroup = 32;                          // chunks of a group (see the chain)
+static_assert(kC == kWave, "one wave joins a tile's channels");
+template <typename T>
+constexpr int kTok = 16 / (int)sizeof(T);               // tokens a thread
+template <typename T>
+constexpr int kScanThreads = M3_SCAN_CHUNK / kTok<T> * kLanesAcross;
+template <typename T>
+constexpr int kScanWaves = kScanThreads<T> / kWave;     // also the parts of a look-back
+
+// The kV channels of a lane as they are stored.  The kernels go through them
+// word by word, so that a word of an output takes the registers of an input's
+// that has been used.
+template <typename T>
+constexpr int kWords = kV * (int)sizeof(T) / 4;
+template <typename T>
+constexpr int kPerWord = 4 / (int)sizeof(T);  // channels of a word
+template <typename T>
+struct Pack {
+  uint32_t w[kWords<T>];
+};
+
+__device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[2]) {
+  v[0] = __uint_as_float(w << 16);
+  v[1] = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[1]) {
+  v[0] = __uint_as_float(w);
+}
+__device__ __forceinline__ uint32_t pack_word(const float (&v)[2]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[0], v[1]}), bf16x2));
+}
+__device__ __forceinline__ uint32_t pack_word(const float (&v)[1]) { return __float_as_uint(v[0]); }
+
+// n of kV channels from p (n <= 0: none, zeros).  kVec: p is aligned to kV
+// elements and n is kV or <= 0; else p has element alignment and the last
+// lane of a row may hold fewer.
+template <typename T, bool kVec>
+__device__ __forceinline__ Pack<T> load_pack(const void* p, int n) {
+  Pack<T> r;
+  if (n >= kV) {
+    if constexpr (kVec)
+      r = *static_cast<const Pack<T>*>(__builtin_assume_aligned(p, kV * sizeof(T)));
+    else
+      __builtin_memcpy(r.w, p, sizeof r.w);
+    return r;
+  }
+#pragma unroll
+  for (int i = 0; i < kWords<T>; ++i) r.w[i] = 0u;
+  if constexpr (!kVec) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          r.w[i / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+        else
+          r.w[i] = static_cast<const uint32_t*>(p)[i];
+      }
+  }
+  return r;
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_pack(void* p, int n, const Pack<T>& r) {
+  if (n >= kV) {
+    if constexpr (kVec)
+      *static_cast<Pack<T>*>(__builtin_assume_aligned(p, kV * sizeof(T))) = r;
+    else
+      __builtin_memcpy(p, r.w, sizeof r.w);
+  } else if constexpr (!kVec) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          static_cast<uint16_t*>(p)[i] = (uint16_t)(r.w[i / 2] >> (16 * (i & 1)));
+        else
+          static_cast<uint32_t*>(p)[i] = r.w[i];
+      }
+  }
+}
+
+// Hides a register's value from the compiler.  What was computed from it is
+// then computed again, not kept (an unpacked copy of every value kept between
+// the two walks of a tile would spill), and a result is computed here, not
+// where it is stored (the values it comes from would be kept until then).
+__device__ __forceinline__ void renew(uint32_t& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void renew(float& v) { asm volatile("" : "+v"(v)); }
+template <typename T, int K>
+__device__ __forceinline__ void renew(Pack<T> (&p)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < kWords<T>; ++i) renew(p[k].w[i]);
+}
+template <int K>
+__device__ __forceinline__ void renew(float (&z)[K][kV]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int v = 0; v < kV; ++v) renew(z[k][v]);
+}
+
+// A thread's rows of an array in the tile whose first element is at `first`:
+// row k at a 32-bit byte offset from a base that the workgroup shares
+// (M3_SCAN_CHUNK rows of an array span less than 4 GiB).
+template <typename T>
+struct Rows {
+  char* base;
+  uint32_t at, step;
+  __device__ __forceinline__ Rows(const void* p, int64_t first, int64_t ld, int tok, int cl)
+      : base(static_cast<char*>(const_cast<void*>(p)) + first * (int64_t)sizeof(T)),
+        at((uint32_t)((tok * (uint32_t)ld + cl) * sizeof(T))),
+        step((uint32_t)(ld * sizeof(T))) {}
+  __device__ __forceinline__ void* operator[](int k) const { return base + (at + k * step); }
+};
+
+// ---- the chain -----------------------------------------------------------------
+// A unit is one (sequence, channel tile); its chunks form a chain.  The
+// workgroup takes its place in the chain from the unit's ticket counter, so
+// it only ever waits for workgroups that already run, whatever the order of
+// their start.
+//
+// What a chunk hands on are 64-bit words, one a channel, that validate
+// themselves: the high half is A with its sign bit set (A is never negative),
+// the low half B; an empty word is 0.  They are written and read by relaxed
+// device-scope atomics, and no order between words is needed.  A chunk
+// publishes its map as soon as it has it.  Chunks form groups of 32: a
+// chunk's entry is the state that left the group before (the last chunk of a
+// group publishes it as a word with A = 0) through the maps of its
+// predecessors in its group, joined in a fixed order, so results do not
+// depend on timing.  Counters and words are zero between calls: the unit's
+// last workgroup to finish looking back clears them.
+//
+// Workspace, in 32-bit words: [0] unused, [1] error word (1: a wait ran out;
+// 2: the counters were not zero), then from byte 256 two counters a unit,
+// then (256-byte aligned) the 64-bit words: [unit][chunk][C] maps,
+// [unit][chunk / 32][C] states.
+struct ChainWs {
+  int* err;
+  int* counters;                 // [units][2]: ticket, finished
+  unsigned long long* maps;      // [units][nC][C]
+  unsigned long long* exits;     // [units][nG][C]
+};
+
+__device__ __forceinline__ unsigned long long word_of(float A, float B) {
+  return ((unsigned long long)(__float_as_uint(A) | 0x80000000u) << 32) | __float_as_uint(B);
+}
+__device__ __forceinline__ Run run_of(unsigned long long w) {
+  return Run{__uint_as_float((uint32_t)(w >> 32) & 0x7fffffffu), __uint_as_float((uint32_t)w)};
+}
+__device__ __forceinline__ void publish(unsigned long long* p, unsigned long long w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned long long peek(const unsigned long long* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// About a quarter of a second of sleeps.
+constexpr int kScanSpins = 1 << 18;
+
+// The word at p once it is there; a NaN state and error word 1 if it never is.
+__device__ __forceinline__ unsigned long long await(const unsigned long long* p, int* err) {
+  unsigned long long w = peek(p);
+  for (int i = 0; w == 0 && i < kScanSpins; ++i) {
+    __builtin_amdgcn_s_sleep(1);
+    w = peek(p);
+  }
+  if (w == 0) {
+    __hip_atomic_store(err, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    w = word_of(0.f, __uint_as_float(0x7fc00000u));
+  }
+  return w;
+}
+
+// A thread's K tokens of an array: `nt` of them inside the sequence and `n` of
+// the lane's channels inside the row (`full`: all); what lies outside is
+// filled with `fill` words.
+template <typename T, bool kVec, int K>
+__device__ __forceinline__ void load_rows(Pack<T> (&v)[K], const Rows<T>& r, bool full, int nt, int n,
+                                          uint32_t fill) {
+  if (full) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = load_pack<T, kVec>(r[k], kV);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k] = load_pack<T, kVec>(r[k], k < nt ? n : 0);
+#pragma unroll
+      for (int i = 0; i < kWords<T>; ++i) v[k].w[i] = k < nt ? v[k].w[i] : fill;
+    }
+  }
+}
+template <typename T, bool kVec, int K>
+__device__ __forceinline__ void store_rows(const Pack<T> (&v)[K], const Rows<T>& r, bool full, int nt,
+                                           int n) {
+  if (full) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) store_pack<T, kVec>(r[k], kV, v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < nt) store_pack<T, kVec>(r[k], n, v[k]);
+  }
+}
+// Gates behind the sequence pass the state on: f = +inf.
+template <typename T>
+constexpr uint32_t kPassGate = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
+
+// Whether every row of an array starts at a multiple of kV elements.
+inline bool vec_rows(const void* p, int64_t ld, size_t es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (kV * es) == 0 && ld % kV == 0);
+}
+
+// This workgroup's place in its unit's chain, the same in every thread; nC
+// when the counters were not zero (error word 2; the workgroup leaves).
+__device__ __forceinline__ int chain_ticket(const ChainWs& ws, int unit, int nC, int* s_word) {
+  if (threadIdx.x == 0) {
+    const int k = __hip_atomic_fetch_add(ws.counters + 2 * unit, 1, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    if (k < 0 || k >= nC)
+      __hip_atomic_store(ws.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *s_word = k < 0 || k >= nC ? nC : k;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(*s_word);  // in a scalar register, as the addresses from it
+}
+
+// The maps of this channel's predecessors in the group that fall to this
+// part, joined; part 0 starts from the state that left the group before
+// (`start` for the first group).
+template <int kParts>
+__device__ __forceinline__ Run chain_part(const ChainWs& ws, int unit, int nC, int k, int part,
+                                          int ch, float start) {
+  constexpr int C = kC, kPer = kScanGroup / kParts;
+  const int g0 = k / kScanGroup * kScanGroup, n = k - g0;
+  Run r = Run{1.f, 0.f};
+  unsigned long long w[kPer], exit = 0;
+  const unsigned long long* maps = ws.maps + ((size_t)unit * nC + g0) * C + ch;
+  const unsigned long long* from =
+      ws.exits + ((size_t)unit * ((nC + kScanGroup - 1) / kScanGroup) + k / kScanGroup) * C + ch;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    w[j] = 0;
+    if (part * kPer + j < n) w[j] = peek(maps + (size_t)(part * kPer + j) * C);
+  }
+  if (part == 0) {
+    r = Run{0.f, start};
+    if (g0 > 0) {
+      exit = peek(from - C);
+      if (exit == 0) exit = await(from - C, ws.err);
+      r = run_of(exit);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (part * kPer + j < n) {
+      if (w[j] == 0) w[j] = await(maps + (size_t)(part * kPer + j) * C, ws.err);
+      r = run_join(r, run_of(w[j]));
+    }
+  return r;
+}
+
+// Counts this workgroup as done with the unit's words; thread 0 calls it after
+// a barrier behind the look-back, from the wave that published.  True for the
+// unit's last.
+__device__ __forceinline__ bool chain_count(const ChainWs& ws, int unit, int nC) {
+  // what this wave published has arrived before the count does
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  return __hip_atomic_fetch_add(ws.counters + 2 * unit + 1, 1, __ATOMIC_RELAXED,
+                                __HIP_MEMORY_SCOPE_AGENT) == nC - 1;
+}
+// The unit's last workgroup leaves its counters and words zero.
+__device__ __forceinline__ void chain_clear(const ChainWs& ws, int unit, int nC) {
+  constexpr int C = kC;
+  const size_t nG = (nC + kScanGroup - 1) / kScanGroup;
+  for (size_t i = threadIdx.x; i < (size_t)nC * C; i += blockDim.x)
+    publish(ws.maps + (size_t)unit * nC * C + i, 0);
+  for (size_t i = threadIdx.x; i < nG * C; i += blockDim.x)
+    publish(ws.exits + (size_t)unit * nG * C + i, 0);
+  if (threadIdx.x < 2)
+    __hip_atomic_store(ws.counters + 2 * unit + threadIdx.x, 0, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The thread maps of a wave joined over the 4 threads that share a channel
+// (kBack: from the last token to the first): r becomes the join up to and
+// with this thread, `before` the join of those before it.
+template <bool kBack>
+__device__ __forceinline__ void wave_join(Run& r, Run& before) {
+  const int g = (threadIdx.x & 63) / kLanesAcross, place = kBack ? 3 - g : g;
+#pragma unroll
+  for (int s = 1; s < 4; s *= 2) {
+    Run o;
+    o.A = kBack ? __shfl_down(r.A, s * kLanesAcross, kWave) : __shfl_up(r.A, s * kLanesAcross, kWave);
+    o.B = kBack ? __shfl_down(r.B, s * kLanesAcross, kWave) : __shfl_up(r.B, s * kLanesAcross, kWave);
+    if (place >= s) r = run_join(o, r);
+  }
+  before.A = kBack ? __shfl_down(r.A, kLanesAcross, kWave) : __shfl_up(r.A, kLanesAcross, kWave);
+  before.B = kBack ? __shfl_down(r.B, kLanesAcross, kWave) : __shfl_up(r.B, kLanesAcross, kWave);
+  if (place == 0) before = Run{1.f, 0.f};
+}
+
+}  // namespace m3

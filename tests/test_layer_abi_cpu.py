@@ -32,7 +32,7 @@ def scan_dims(b=2, t=300, d=64, **ld):
 
 BAD_SCAN = [(dict(b=-1), INV), (dict(t=-1), INV), (dict(d=0), INV), (dict(ld_x=63), INV), (dict(ld_f=-1), INV),
             (dict(ld_g=1), INV), (dict(ld_y=63), INV), (dict(t=1 << 40), UNS), (dict(d=1 << 40), UNS),
-            (dict(b=1 << 20), UNS), (dict(ld_x=1 << 62), UNS)]
+            (dict(b=1 << 33), UNS), (dict(b=1 << 30), UNS), (dict(ld_x=1 << 62), UNS), (dict(ld_y=1 << 22), UNS)]
 
 
 @pytest.mark.parametrize("bad,code", BAD_SCAN)
@@ -59,6 +59,13 @@ def test_scan_pointers(lib):
         if i in (0, 1, 4):
             p[i] = None
             assert call(p) == INV
+    need = lib.m3_gated_scan_workspace_size(ctypes.byref(d), 0)
+    # 2 sequences x 1 tile: 256 bytes, their counters (256), 2 chunks and 1 group of 64 words each
+    assert need == 256 + 256 + 2 * (2 + 1) * 64 * 8
+    assert call([OK] * 7, w=[None, need, None]) == WS and call([OK] * 7, w=[OK, need - 1, None]) == WS
+    assert call([OK] * 7, w=[HALF, need, None]) == INV
+    for t in (0, 1, 256):                 # one chunk hands nothing on
+        assert lib.m3_gated_scan_workspace_size(ctypes.byref(scan_dims(t=t)), 0) == 0
     bw = lambda p, dd=d: lib.m3_gated_scan_backward(ctypes.byref(dd), 1, *p, *ws)
     for i in range(10):                   # dy x f g states dh_last dx df dg dh0
         p = [OK] * 10
@@ -68,6 +75,7 @@ def test_scan_pointers(lib):
             p[i] = None
             assert bw(p) == INV
     assert bw([OK] * 10, scan_dims(ld_dx=63)) == INV
+    assert lib.m3_gated_scan_backward(ctypes.byref(d), 1, *[OK] * 10, OK, need - 1, None) == WS
     assert call([None] * 7, dd=scan_dims(b=0)) == m3.M3_SUCCESS
     assert bw([None] * 10, scan_dims(b=0)) == m3.M3_SUCCESS
     st = lambda p, dd=d: lib.m3_gated_scan_step(ctypes.byref(dd), 0, *p, None)
