@@ -96,9 +96,9 @@ def gated_scan_backward(dy, x, f, g=None, h0=None, dh_last=None):
 def layer_norm(s, weight, bias, eps):
     """s [M,D] float64 (the stored sum).  Returns y, q, mean, rstd and bounds.
     A float32 mean of D values summed in pieces is within K u of the mean
-    magnitude, K = 32 roundings (up to 16 in a lane, 6 in a wave, 4 between
-    waves, the division, and the centring)."""
-    K = 32
+    magnitude, K = 48 roundings (up to 16 in a lane, 6 in a wave, 16 between
+    waves, and the division)."""
+    K = 48
     mean = s.mean(-1, keepdims=True)
     c = s - mean
     var = (c * c).mean(-1, keepdims=True)
@@ -118,7 +118,7 @@ def layer_norm(s, weight, bias, eps):
 
 def layer_norm_backward(dy, s, weight, eps, dsum=None):
     """Gradients dx, dw, db of layer norm and their bounds."""
-    K = 32
+    K = 48
     n = layer_norm(s, weight, np.zeros_like(weight), eps)
     q, rstd = n["q"], n["rstd"][:, None]
     p = dy * weight

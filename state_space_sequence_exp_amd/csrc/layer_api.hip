@@ -270,7 +270,8 @@ m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
 
 size_t m3_layer_norm_backward_workspace_size(const m3_norm_dims* dims, m3_dtype dtype) {
   if (!dtype_ok(&dtype) || check_norm(dims, true) != M3_SUCCESS) return 0;
-  return (size_t)m3::norm_backward_groups(dims->rows, (int)dims->channels) * 2 *
+  return (size_t)m3::norm_backward_groups(dims->rows, (int)dims->channels,
+                                          (int)esize_of(dtype)) * 2 *
          (size_t)dims->channels * sizeof(float);
 }
 

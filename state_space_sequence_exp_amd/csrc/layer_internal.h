@@ -64,7 +64,7 @@ struct NormArgs {
   float* partial;  // backward workspace
 };
 // Row groups whose weight-gradient partials the backward keeps.
-int norm_backward_groups(int64_t rows, int D);
+int norm_backward_groups(int64_t rows, int D, int esize);
 hipError_t launch_norm(const NormArgs& a, m3_dtype dtype, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs& a, m3_dtype dtype, hipStream_t stream);
 

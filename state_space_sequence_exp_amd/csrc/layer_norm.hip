@@ -4,9 +4,16 @@
 //   dx = rstd (p - mean(p) - q mean(p q)) + dsum,  p = dy weight
 //   dweight = sum_rows dy q,  dbias = sum_rows dy
 //
-// One workgroup a row; the row stays in the LDS as floats between the passes
-// (sum, centred squares, output).  The weight gradients are summed by row
-// groups into the workspace, then over the groups, in a fixed order.
+// Bound by memory: each array is read or written once.  A row belongs to a
+// team of 64 to 1024 threads that keeps it in registers, NV 16-byte
+// vectors a thread, between the sum, the centred squares and the output; the
+// threads keep their columns of the weights while their team walks rows.  The
+// sums go by lane moves in a wave and by the LDS between waves.
+//
+// The backward pass keeps each column's dweight and dbias in the registers of
+// the thread that owns it, over all rows of its workgroup (up to 256 groups of
+// rows); the teams of a workgroup are joined in the LDS, the groups by a
+// second kernel, both in a fixed order.
 #include <algorithm>
 
 #include "layer_internal.h"
@@ -15,133 +22,429 @@
 namespace m3 {
 namespace {
 
-constexpr int kThreads = 256;
+template <typename T>
+constexpr int kE = 16 / (int)sizeof(T);  // elements of a vector
 
-// Sum over the workgroup, the same in every thread.
-__device__ __forceinline__ float block_sum(float v, float* s_part) {
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < kThreads / kWave; ++i) v += s_part[i];
+struct Vec {
+  uint32_t w[4];
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Vec& p, float (&v)[kE<T>]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      v[2 * i] = __uint_as_float(p.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(p.w[i] & 0xffff0000u);
+    } else {
+      v[i] = __uint_as_float(p.w[i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ Vec pack(const float (&v)[kE<T>]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  Vec p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2)
+      p.w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2 * i], v[2 * i + 1]}), bf16x2));
+    else
+      p.w[i] = __float_as_uint(v[i]);
+  }
+  return p;
+}
+
+// n of a vector's elements at p (n <= 0: none; the rest zeros).  kVec: rows
+// are 16-byte aligned and n is a whole vector or <= 0; else elements are
+// aligned and the last vector of a row may be cut.
+template <typename T, bool kVec>
+__device__ __forceinline__ Vec load_vec(const T* p, int n) {
+  Vec r = {{0u, 0u, 0u, 0u}};
+  if (n >= kE<T>) {
+    if constexpr (kVec) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+    } else {
+      __builtin_memcpy(r.w, p, 16);
+    }
+  } else if constexpr (!kVec) {
+#pragma unroll
+    for (int i = 0; i < kE<T>; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          r.w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i & 1));
+        else
+          r.w[i] = __builtin_bit_cast(uint32_t, p[i]);
+      }
+  }
+  return r;
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_vec(T* p, int n, const Vec& r) {
+  if (n >= kE<T>) {
+    if constexpr (kVec)
+      *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else
+      __builtin_memcpy(p, r.w, 16);
+  } else if constexpr (!kVec) {
+#pragma unroll
+    for (int i = 0; i < kE<T>; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          p[i] = __builtin_bit_cast(T, (uint16_t)(r.w[i / 2] >> (16 * (i & 1))));
+        else
+          p[i] = __builtin_bit_cast(T, r.w[i]);
+      }
+  }
+}
+// A vector's weights (zeros without p or past the row).
+template <int E>
+__device__ __forceinline__ void load_weights(const float* p, int n, float (&w)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) w[i] = p && i < n ? p[i] : 0.f;
+}
+
+__device__ __forceinline__ float wave_sum(float v) { return wave_read_lane(wave_incl_scan(v), 63); }
+
+// Sum of v over the TPR threads of a team, the same in each.  `s` holds one
+// float a wave; teams of several waves must not use the same `s` in two sums
+// one after the other.
+template <int TPR>
+__device__ __forceinline__ float team_sum(float v, float* s) {
+  v = wave_sum(v);
+  if constexpr (TPR > kWave) {
+    const int wave = threadIdx.x / kWave, w0 = wave / (TPR / kWave) * (TPR / kWave);
+    if ((threadIdx.x & 63) == 0) s[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / kWave; ++i) v += s[w0 + i];
+  }
   return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs a) {
-  extern __shared__ float s_row[];
-  __shared__ float s_part[kThreads / kWave];
-  const int64_t r = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + r * a.ld_x;
-  const T* res = static_cast<const T*>(a.residual) + r * a.ld_res;
-  float sum = 0.f;
-  for (int d = threadIdx.x; d < a.D; d += kThreads) {
-    float v = to_f32(x[d]);
-    if (a.residual) v = to_f32(from_f32<T>(v + to_f32(res[d])));
-    if (a.sum) static_cast<T*>(a.sum)[r * a.ld_sum + d] = from_f32<T>(v);
-    s_row[d] = v;
-    sum += v;
+template <typename T, int TPR, int NV, bool kVec>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs a) {
+  constexpr int E = kE<T>, NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
+  __shared__ float s_sum[2][NT / kWave];
+  const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+  const float inv = 1.f / (float)a.D;
+  float w[NV][E], b[NV][E];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (j * TPR + t) * E;
+    load_weights<E>(a.weight + e0, a.D - e0, w[j]);
+    load_weights<E>(a.bias ? a.bias + e0 : nullptr, a.D - e0, b[j]);
   }
-  const float mean = block_sum(sum, s_part) / (float)a.D;
-  float sq = 0.f;
-  for (int d = threadIdx.x; d < a.D; d += kThreads) {
-    const float c = s_row[d] - mean;
-    sq = __builtin_fmaf(c, c, sq);
-  }
-  const float rstd = 1.f / sqrtf(block_sum(sq, s_part) / (float)a.D + a.eps);
-  for (int d = threadIdx.x; d < a.D; d += kThreads) {
-    const float q = (s_row[d] - mean) * rstd;
-    static_cast<T*>(a.y)[r * a.ld_y + d] =
-        from_f32<T>(__builtin_fmaf(q, a.weight[d], a.bias ? a.bias[d] : 0.f));
-  }
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[r] = mean;
-    if (a.rstd) a.rstd[r] = rstd;
+  for (int64_t r = (int64_t)blockIdx.x * kTeams + team; r < a.rows; r += (int64_t)gridDim.x * kTeams) {
+    Vec x[NV], res[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (j * TPR + t) * E;
+      x[j] = load_vec<T, kVec>(static_cast<const T*>(a.x) + r * a.ld_x + e0, a.D - e0);
+      if (a.residual)
+        res[j] = load_vec<T, kVec>(static_cast<const T*>(a.residual) + r * a.ld_res + e0, a.D - e0);
+    }
+    float v[NV][E], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack<T>(x[j], v[j]);
+      if (a.residual) {
+        float q[E];
+        unpack<T>(res[j], q);
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[j][i] += q[i];
+        x[j] = pack<T>(v[j]);
+        unpack<T>(x[j], v[j]);  // the statistics are those of the stored sum
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum += v[j][i];
+    }
+    const float mean = team_sum<TPR>(sum, s_sum[0]) * inv;
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int n = a.D - (j * TPR + t) * E;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float c = v[j][i] - mean;
+        v[j][i] = c;
+        if (kVec ? n > 0 : i < n) sq = __builtin_fmaf(c, c, sq);
+      }
+    }
+    const float rstd = 1.f / sqrtf(team_sum<TPR>(sq, s_sum[1]) * inv + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (j * TPR + t) * E;
+      if (a.sum) store_vec<T, kVec>(static_cast<T*>(a.sum) + r * a.ld_sum + e0, a.D - e0, x[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[j][i] = __builtin_fmaf(v[j][i] * rstd, w[j][i], b[j][i]);
+      store_vec<T, kVec>(static_cast<T*>(a.y) + r * a.ld_y + e0, a.D - e0, pack<T>(v[j]));
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
   }
 }
 
-// Workgroup i: the rows of group i, one after another.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(NormArgs a) {
-  extern __shared__ float s_acc[];  // this group's dweight and dbias
-  __shared__ float s_part[kThreads / kWave];
-  float *s_dw = s_acc, *s_db = s_acc + a.D;
-  for (int d = threadIdx.x; d < a.D; d += kThreads) s_dw[d] = s_db[d] = 0.f;
-  const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
-  const int64_t r0 = blockIdx.x * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
-  for (int64_t r = r0; r < r1; ++r) {
-    const T* s = static_cast<const T*>(a.sum) + r * a.ld_sum;
-    const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
-    const float mean = a.mean[r], rstd = a.rstd[r];
-    float sp = 0.f, spq = 0.f;
-    for (int d = threadIdx.x; d < a.D; d += kThreads) {
-      const float q = (to_f32(s[d]) - mean) * rstd, g = to_f32(dy[d]), p = g * a.weight[d];
-      sp += p;
-      spq = __builtin_fmaf(p, q, spq);
-      s_dw[d] = __builtin_fmaf(g, q, s_dw[d]);
-      s_db[d] += g;
+constexpr int kBwThreads = 1024;
+constexpr int kMaxGroups = 256;
+
+// A row's inputs in the backward pass.
+template <typename T, int NV>
+struct BwRow {
+  Vec s[NV], dy[NV], ds[NV];
+  float mean, rstd;
+};
+template <typename T, int TPR, int NV, bool kVec>
+__device__ __forceinline__ void load_bw(const NormArgs& a, int64_t r, int t, BwRow<T, NV>& q) {
+  if (r >= a.rows) {  // a row of zeros adds nothing
+#pragma unroll
+    for (int j = 0; j < NV; ++j) q.s[j] = q.dy[j] = q.ds[j] = Vec{{0u, 0u, 0u, 0u}};
+    q.mean = q.rstd = 0.f;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (j * TPR + t) * kE<T>, n = a.D - e0;
+    q.s[j] = load_vec<T, kVec>(static_cast<const T*>(a.sum) + r * a.ld_sum + e0, n);
+    q.dy[j] = load_vec<T, kVec>(static_cast<const T*>(a.dy) + r * a.ld_dy + e0, n);
+    q.ds[j] = a.dsum ? load_vec<T, kVec>(static_cast<const T*>(a.dsum) + r * a.ld_dsum + e0, n)
+                     : Vec{{0u, 0u, 0u, 0u}};
+  }
+  q.mean = a.mean[r];
+  q.rstd = a.rstd[r];
+}
+
+template <typename T, int TPR, int NV, bool kVec>
+__global__ void __launch_bounds__(kBwThreads) norm_backward_kernel(NormArgs a, int rounds) {
+  constexpr int E = kE<T>, kTeams = kBwThreads / TPR, C = TPR * NV * E;  // columns of a team
+  __shared__ float s_p[2][kBwThreads / kWave], s_pq[2][kBwThreads / kWave];
+  extern __shared__ __align__(16) float s_acc[];  // [teams][2][C] at the end
+  const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+  const float inv = 1.f / (float)a.D;
+  float w[NV][E], dw[NV][E], db[NV][E];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e0 = (j * TPR + t) * E;
+    load_weights<E>(a.weight + e0, a.D - e0, w[j]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) dw[j][i] = db[j][i] = 0.f;
+  }
+  // every team makes the same number of rounds (they share the barriers)
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  int64_t r = (int64_t)blockIdx.x * kTeams + team;
+  // the next row is requested while this one is worked on, where the
+  // registers hold both
+  constexpr bool kAhead = NV == 1;
+  BwRow<T, NV> cur, next;
+  if constexpr (kAhead) load_bw<T, TPR, NV, kVec>(a, r, t, next);
+  for (int k = 0; k < rounds; ++k, r += step) {
+    if constexpr (kAhead) {
+      cur = next;
+      load_bw<T, TPR, NV, kVec>(a, k + 1 < rounds ? r + step : a.rows, t, next);
+    } else {
+      load_bw<T, TPR, NV, kVec>(a, r, t, cur);
     }
-    const float mp = block_sum(sp, s_part) / (float)a.D;
-    const float mpq = block_sum(spq, s_part) / (float)a.D;
-    for (int d = threadIdx.x; d < a.D; d += kThreads) {
-      const float q = (to_f32(s[d]) - mean) * rstd, p = to_f32(dy[d]) * a.weight[d];
-      float v = rstd * (p - mp - q * mpq);
-      if (a.dsum) v += to_f32(static_cast<const T*>(a.dsum)[r * a.ld_dsum + d]);
-      static_cast<T*>(a.dx)[r * a.ld_dx + d] = from_f32<T>(v);
+    float q[NV][E], g[NV][E], sp = 0.f, spq = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack<T>(cur.s[j], q[j]);
+      unpack<T>(cur.dy[j], g[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        q[j][i] = (q[j][i] - cur.mean) * cur.rstd;  // past the row dy and the weight are 0
+        dw[j][i] = __builtin_fmaf(g[j][i], q[j][i], dw[j][i]);
+        db[j][i] += g[j][i];
+        g[j][i] *= w[j][i];
+        sp += g[j][i];
+        spq = __builtin_fmaf(g[j][i], q[j][i], spq);
+      }
+    }
+    sp = wave_sum(sp);
+    spq = wave_sum(spq);
+    if constexpr (TPR > kWave) {
+      const int wave = threadIdx.x / kWave, w0 = wave / (TPR / kWave) * (TPR / kWave);
+      if ((threadIdx.x & 63) == 0) {
+        s_p[k & 1][wave] = sp;
+        s_pq[k & 1][wave] = spq;
+      }
+      __syncthreads();
+      sp = spq = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / kWave; ++i) {
+        sp += s_p[k & 1][w0 + i];
+        spq += s_pq[k & 1][w0 + i];
+      }
+    }
+    const float mp = sp * inv, mpq = spq * inv;
+    if (r < a.rows) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e0 = (j * TPR + t) * E;
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          v[i] = cur.rstd * (g[j][i] - mp - q[j][i] * mpq);
+        if (a.dsum) {
+          float d[E];
+          unpack<T>(cur.ds[j], d);
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[i] += d[i];
+        }
+        store_vec<T, kVec>(static_cast<T*>(a.dx) + r * a.ld_dx + e0, a.D - e0, pack<T>(v));
+      }
     }
   }
-  for (int d = threadIdx.x; d < a.D; d += kThreads) {
-    a.partial[((int64_t)blockIdx.x * 2) * a.D + d] = s_dw[d];
-    a.partial[((int64_t)blockIdx.x * 2 + 1) * a.D + d] = s_db[d];
+  // the teams' sums, in the order of the teams
+  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.D;
+  if constexpr (kTeams > 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        s_acc[(team * 2) * C + (j * TPR + t) * E + i] = dw[j][i];
+        s_acc[(team * 2 + 1) * C + (j * TPR + t) * E + i] = db[j][i];
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * C; c += kBwThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int m = 0; m < kTeams; ++m) v += s_acc[m * 2 * C + c];
+      if (c % C < a.D) out[c / C * a.D + c % C] = v;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = (j * TPR + t) * E + i;
+        if (c < a.D) {
+          out[c] = dw[j][i];
+          out[a.D + c] = db[j][i];
+        }
+      }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) norm_weights_kernel(NormArgs a, int groups) {
-  const int d = (int)(blockIdx.x * kThreads + threadIdx.x);
-  if (d >= a.D) return;
-  float dw = 0.f, db = 0.f;
-  for (int i = 0; i < groups; ++i) {
-    dw += a.partial[((int64_t)i * 2) * a.D + d];
-    db += a.partial[((int64_t)i * 2 + 1) * a.D + d];
+// dweight and dbias from the groups' partials: 64 columns a workgroup, the
+// groups split over its 16 waves and joined in their order.
+__global__ void __launch_bounds__(1024) norm_weights_kernel(NormArgs a, int groups) {
+  __shared__ float s_part[16][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
+  const int64_t c = (int64_t)blockIdx.x * kWave + lane;  // of 2 D
+  const int per = (groups + 15) / 16;
+  float v = 0.f;
+  if (c < 2 * (int64_t)a.D)
+    for (int i = wave * per; i < (wave + 1) * per && i < groups; ++i)
+      v += a.partial[(int64_t)i * 2 * a.D + c];
+  s_part[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && c < 2 * (int64_t)a.D) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += s_part[i][lane];
+    if (c < a.D) a.dweight[c] = v;
+    else if (a.dbias) a.dbias[c - a.D] = v;
   }
-  a.dweight[d] = dw;
-  if (a.dbias) a.dbias[d] = db;
+}
+
+bool vec16(const void* p, int64_t ld, size_t es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)ld * es % 16 == 0);
+}
+
+template <typename T, int TPR, int NV>
+hipError_t launch_fwd(const NormArgs& a, bool vec, hipStream_t stream) {
+  constexpr int NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
+  // up to 2048 threads a compute unit, each team walking its rows
+  const int64_t most = 256 * (2048 / NT);
+  const dim3 grid((unsigned)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, most));
+  if (vec)
+    hipLaunchKernelGGL((norm_kernel<T, TPR, NV, true>), grid, dim3(NT), 0, stream, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<T, TPR, NV, false>), grid, dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
+
+// The team for a row of `vecs` vectors.
+template <typename T>
+hipError_t launch_fwd_t(const NormArgs& a, hipStream_t stream) {
+  constexpr size_t es = sizeof(T);
+  const bool vec = a.D % kE<T> == 0 && vec16(a.x, a.ld_x, es) && vec16(a.residual, a.ld_res, es) &&
+                   vec16(a.sum, a.ld_sum, es) && vec16(a.y, a.ld_y, es);
+  const int vecs = (a.D + kE<T> - 1) / kE<T>;
+  if (vecs <= 64) return launch_fwd<T, 64, 1>(a, vec, stream);
+  if (vecs <= 128) return launch_fwd<T, 64, 2>(a, vec, stream);
+  if (vecs <= 256) return launch_fwd<T, 256, 1>(a, vec, stream);
+  if (vecs <= 512) return launch_fwd<T, 256, 2>(a, vec, stream);
+  if (vecs <= 1024) return launch_fwd<T, 256, 4>(a, vec, stream);
+  if (vecs <= 2048) return launch_fwd<T, 1024, 2>(a, vec, stream);
+  if constexpr (sizeof(T) == 4) return launch_fwd<T, 1024, 4>(a, vec, stream);
+  return hipErrorInvalidValue;
+}
+
+template <typename T, int TPR, int NV, bool kVec>
+hipError_t launch_bw_v(const NormArgs& a, int groups, hipStream_t stream) {
+  constexpr int kTeams = kBwThreads / TPR;
+  const size_t lds = kTeams > 1 ? sizeof(float) * (size_t)kTeams * 2 * TPR * NV * kE<T> : 0;
+  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&norm_backward_kernel<T, TPR, NV, kVec>), lds);
+  if (e != hipSuccess) return e;
+  const int64_t step = (int64_t)groups * kTeams;
+  const int rounds = (int)((a.rows + step - 1) / step);
+  hipLaunchKernelGGL((norm_backward_kernel<T, TPR, NV, kVec>), dim3(groups), dim3(kBwThreads), lds,
+                     stream, a, rounds);
+  return hipGetLastError();
+}
+template <typename T, int TPR, int NV>
+hipError_t launch_bw(const NormArgs& a, bool vec, int groups, hipStream_t stream) {
+  return vec ? launch_bw_v<T, TPR, NV, true>(a, groups, stream)
+             : launch_bw_v<T, TPR, NV, false>(a, groups, stream);
+}
+
+template <typename T>
+hipError_t launch_bw_t(const NormArgs& a, int groups, hipStream_t stream) {
+  constexpr size_t es = sizeof(T);
+  const bool vec = a.D % kE<T> == 0 && vec16(a.sum, a.ld_sum, es) && vec16(a.dy, a.ld_dy, es) &&
+                   vec16(a.dsum, a.ld_dsum, es) && vec16(a.dx, a.ld_dx, es);
+  const int vecs = (a.D + kE<T> - 1) / kE<T>;
+  if (vecs <= 64) return launch_bw<T, 64, 1>(a, vec, groups, stream);
+  if (vecs <= 128) return launch_bw<T, 128, 1>(a, vec, groups, stream);
+  if (vecs <= 256) return launch_bw<T, 256, 1>(a, vec, groups, stream);
+  if (vecs <= 512) return launch_bw<T, 512, 1>(a, vec, groups, stream);
+  if (vecs <= 1024) return launch_bw<T, 1024, 1>(a, vec, groups, stream);
+  if (vecs <= 2048) return launch_bw<T, 1024, 2>(a, vec, groups, stream);
+  if constexpr (sizeof(T) == 4) return launch_bw<T, 1024, 4>(a, vec, groups, stream);
+  return hipErrorInvalidValue;
+}
+
+// Teams of a backward workgroup for rows of D channels (the table above).
+int bw_teams(int D, int esize) {
+  const int e = 16 / esize, vecs = (D + e - 1) / e;
+  return vecs <= 64 ? 16 : vecs <= 128 ? 8 : vecs <= 256 ? 4 : vecs <= 512 ? 2 : 1;
 }
 
 }  // namespace
 
-int norm_backward_groups(int64_t rows, int) { return (int)std::min<int64_t>(rows, 256); }
+int norm_backward_groups(int64_t rows, int D, int esize) {
+  const int teams = bw_teams(D, esize);
+  return (int)std::min<int64_t>((rows + teams - 1) / teams, kMaxGroups);
+}
 
 hipError_t launch_norm(const NormArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const size_t lds = sizeof(float) * (size_t)a.D;
-  const dim3 grid((unsigned)a.rows);
-  const void* k = dtype == M3_BF16 ? reinterpret_cast<const void*>(&norm_kernel<bf16>)
-                                   : reinterpret_cast<const void*>(&norm_kernel<float>);
-  const hipError_t e = lds_limit(k, lds);
-  if (e != hipSuccess) return e;
-  if (dtype == M3_BF16)
-    hipLaunchKernelGGL(norm_kernel<bf16>, grid, dim3(kThreads), lds, stream, a);
-  else
-    hipLaunchKernelGGL(norm_kernel<float>, grid, dim3(kThreads), lds, stream, a);
-  return hipGetLastError();
+  return dtype == M3_BF16 ? launch_fwd_t<bf16>(a, stream) : launch_fwd_t<float>(a, stream);
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const int groups = norm_backward_groups(a.rows, a.D);
+  const int groups = norm_backward_groups(a.rows, a.D, dtype == M3_BF16 ? 2 : 4);
   if (groups > 0) {
-    const size_t lds = 2 * sizeof(float) * (size_t)a.D;
-    const void* k = dtype == M3_BF16 ? reinterpret_cast<const void*>(&norm_backward_kernel<bf16>)
-                                     : reinterpret_cast<const void*>(&norm_backward_kernel<float>);
-    const hipError_t e = lds_limit(k, lds);
+    const hipError_t e = dtype == M3_BF16 ? launch_bw_t<bf16>(a, groups, stream)
+                                          : launch_bw_t<float>(a, groups, stream);
     if (e != hipSuccess) return e;
-    if (dtype == M3_BF16)
-      hipLaunchKernelGGL(norm_backward_kernel<bf16>, dim3(groups), dim3(kThreads), lds, stream, a);
-    else
-      hipLaunchKernelGGL(norm_backward_kernel<float>, dim3(groups), dim3(kThreads), lds, stream, a);
   }
-  hipLaunchKernelGGL(norm_weights_kernel, dim3((a.D + kThreads - 1) / kThreads), dim3(kThreads), 0,
-                     stream, a, groups);
+  hipLaunchKernelGGL(norm_weights_kernel, dim3((2 * a.D + kWave - 1) / kWave), dim3(1024), 0, stream,
+                     a, groups);
   return hipGetLastError();
 }
 
