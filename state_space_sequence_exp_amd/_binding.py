@@ -8,6 +8,7 @@ is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -498,42 +499,72 @@ def backward(x, dt, A, lam, theta, B, C, dy, *, dh_final=None, workspace=None, s
 # ---- operators beside the recurrence ------------------------------------------
 # A call's device is its first tensor's.  Where that is not the current device
 # the call is made with it current, on that device's current stream.
+#
+# Several of these run for a few microseconds, less than a careless wrapper
+# takes, so the checks of a call ask each tensor for as little as they can.
 
-def _launch(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current; raises M3Error."""
+_types = None
+
+
+def _type_code(t) -> int:
+    """M3_F32 or M3_BF16 of a tensor's type."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: M3_F32, torch.bfloat16: M3_BF16}
+    code = _types.get(t.dtype)
+    if code is None:
+        raise TypeError("expected float32 or bfloat16, got %s" % t.dtype)
+    return code
+
+
+def _launch(dev: int, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current; raises M3Error."""
     import torch
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a GPU, got %s" % dev)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, _raw_stream(dev, stream))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
+            st = fn(*args, _raw_stream(dev, stream))
     if st != M3_SUCCESS:
         raise M3Error(st, fn.__name__)
 
 
-def _code_of(codes) -> int:
+def _raw_stream(dev: int, stream) -> int:
     import torch
-    if codes.dtype == torch.int8:
-        return M3_CODE_INT8
-    if codes.dtype == torch.float8_e4m3fn:
-        return M3_CODE_E4M3
-    raise TypeError("codes must be int8 or float8_e4m3fn, got %s" % codes.dtype)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _rows(t, name, dtype, shape, dev) -> int:
-    """Checks an array of rows [..., D] whose channels are contiguous and whose
-    rows follow each other at one distance (a dense array, or a slice of wider
-    rows); returns that distance in elements."""
-    if t.dtype != dtype:
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same(t, name, dtype, shape, dev: int):
+    """A dense array of this type and shape on device `dev`."""
+    if t.dtype is not dtype:
         raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != dev:
-        raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
+    if t.get_device() != dev:
+        raise ValueError("%s: on %s, expected the first tensor's device" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _rows(t, name, dtype, shape, dev: int) -> int:
+    """Checks an array of rows [..., D] whose channels are contiguous and whose
+    rows follow each other at one distance (a dense array, or a slice of wider
+    rows); returns that distance in elements."""
+    if t.dtype is not dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s: on %s, expected the first tensor's device" % (name, t.device))
     if t.is_contiguous():
-        return shape[-1]
+        return 0
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError("%s: its last dimension must be contiguous" % name)
     ld = step = None
@@ -545,7 +576,27 @@ def _rows(t, name, dtype, shape, dev) -> int:
         if st != step or st < shape[-1]:
             raise ValueError("%s: its rows must follow each other at one distance" % name)
         step *= n
-    return shape[-1] if ld is None else ld
+    return 0 if ld is None else ld
+
+
+def _gpu(dev: int):
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+
+
+def _like(x, dense: bool):
+    """A new dense array of x's shape and type."""
+    import torch
+    return torch.empty_like(x) if dense else x.new_empty(x.shape)
+
+
+def _code_of(codes) -> int:
+    import torch
+    if codes.dtype == torch.int8:
+        return M3_CODE_INT8
+    if codes.dtype == torch.float8_e4m3fn:
+        return M3_CODE_E4M3
+    raise TypeError("codes must be int8 or float8_e4m3fn, got %s" % codes.dtype)
 
 
 def gated_scan_workspace_size(batch, seqlen, channels, dtype) -> int:
@@ -563,9 +614,9 @@ def _scan_workspace(lib, d, code, workspace, dev):
         return None, 0
     if workspace is None:
         workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and on %s" % dev)
-    return workspace, workspace.numel() * workspace.element_size()
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the first tensor's device")
+    return workspace, workspace.nbytes
 
 
 def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool = False,
@@ -584,32 +635,34 @@ def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool 
     Returns (y, h_last [B,D] float32, states [B,ceil(T/256),D] float32 or None).
     """
     import torch
-    lib = load_library()
-    shape, dev, dt = x.shape, x.device, x.dtype
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) != 3:
         raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
     nb, nt, nd = shape
-    code = _dtype_code(x)
-    d = M3ScanDims(nb, nt, nd, _rows(x, "x", dt, shape, dev), _rows(f, "f", dt, shape, dev),
+    code = _type_code(x)
+    ld = _rows(x, "x", dt, shape, dev)
+    d = M3ScanDims(nb, nt, nd, ld, _rows(f, "f", dt, shape, dev),
                    0 if g is None else _rows(g, "g", dt, shape, dev))
-    if h0 is not None:
-        _check(h0, "h0", torch.float32, (nb, nd), dev)
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
-    else:
-        d.ld_y = _rows(y, "y", dt, shape, dev)
-    if h_last is None:
-        h_last = torch.empty((nb, nd), dtype=torch.float32, device=dev)
-    else:
-        _check(h_last, "h_last", torch.float32, (nb, nd), dev)
     nc = -(-nt // SCAN_CHUNK)
+    if h0 is not None:
+        _same(h0, "h0", torch.float32, (nb, nd), dev)
+    if h_last is not None:
+        _same(h_last, "h_last", torch.float32, (nb, nd), dev)
     if states is not None:
-        _check(states, "states", torch.float32, (nb, nc, nd), dev)
-    elif want_states:
-        states = torch.empty((nb, nc, nd), dtype=torch.float32, device=dev)
+        _same(states, "states", torch.float32, (nb, nc, nd), dev)
+    if y is not None:
+        d.ld_y = _rows(y, "y", dt, shape, dev)
+    _gpu(dev)
+    if y is None:
+        y = _like(x, ld == 0)
+    if h_last is None:
+        h_last = x.new_empty((nb, nd), dtype=torch.float32)
+    if states is None and want_states:
+        states = x.new_empty((nb, nc, nd), dtype=torch.float32)
     workspace, ws_bytes = _scan_workspace(lib, d, code, workspace, dev)
-    _launch(dev, stream, lib.m3_gated_scan, ctypes.byref(d), code, _ptr(x), _ptr(f), _ptr(g),
-            _ptr(h0), _ptr(y), _ptr(h_last), _ptr(states), _ptr(workspace), ws_bytes)
+    _launch(dev, stream, lib.m3_gated_scan, ctypes.byref(d), code, _at(x), _at(f), _at(g),
+            _at(h0), _at(y), _at(h_last), _at(states), _at(workspace), ws_bytes)
     return y, h_last, states
 
 
@@ -621,29 +674,28 @@ def gated_scan_backward(dy, x, f, g, states, *, dh_last=None, dx=None, df=None, 
     a wider gradient).  Returns a dict: x, f, g (absent without g) in the
     inputs' type, h0 [B,D] float32."""
     import torch
-    lib = load_library()
-    shape, dev, dt = x.shape, x.device, x.dtype
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) != 3:
         raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
     nb, nt, nd = shape
-    code = _dtype_code(x)
-    _check(states, "states", torch.float32, (nb, -(-nt // SCAN_CHUNK), nd), dev)
+    code = _type_code(x)
+    _same(states, "states", torch.float32, (nb, -(-nt // SCAN_CHUNK), nd), dev)
     if dh_last is not None:
-        _check(dh_last, "dh_last", torch.float32, (nb, nd), dev)
+        _same(dh_last, "dh_last", torch.float32, (nb, nd), dev)
     if g is None and dg is not None:
         raise ValueError("dg without g")
-    new = lambda t: torch.empty(shape, dtype=dt, device=dev) if t is None else t
+    rows = lambda t, name: 0 if t is None else _rows(t, name, dt, shape, dev)
+    d = M3ScanDims(nb, nt, nd, rows(x, "x"), rows(f, "f"), rows(g, "g"),
+                   _rows(dy, "dy", dt, shape, dev), rows(dx, "dx"), rows(df, "df"), rows(dg, "dg"))
+    _gpu(dev)
+    new = lambda t: _like(x, d.ld_x == 0) if t is None else t
     dx, df, dg = new(dx), new(df), None if g is None else new(dg)
-    d = M3ScanDims(nb, nt, nd, _rows(x, "x", dt, shape, dev), _rows(f, "f", dt, shape, dev),
-                   0 if g is None else _rows(g, "g", dt, shape, dev),
-                   _rows(dy, "dy", dt, shape, dev), _rows(dx, "dx", dt, shape, dev),
-                   _rows(df, "df", dt, shape, dev),
-                   0 if g is None else _rows(dg, "dg", dt, shape, dev))
-    dh0 = torch.empty((nb, nd), dtype=torch.float32, device=dev)
+    dh0 = states.new_empty((nb, nd))
     workspace, ws_bytes = _scan_workspace(lib, d, code, workspace, dev)
-    _launch(dev, stream, lib.m3_gated_scan_backward, ctypes.byref(d), code, _ptr(dy), _ptr(x),
-            _ptr(f), _ptr(g), _ptr(states), _ptr(dh_last), _ptr(dx), _ptr(df), _ptr(dg),
-            _ptr(dh0), _ptr(workspace), ws_bytes)
+    _launch(dev, stream, lib.m3_gated_scan_backward, ctypes.byref(d), code, _at(dy), _at(x),
+            _at(f), _at(g), _at(states), _at(dh_last), _at(dx), _at(df), _at(dg),
+            _at(dh0), _at(workspace), ws_bytes)
     out = {"x": dx, "f": df, "h0": dh0}
     if g is not None:
         out["g"] = dg
@@ -656,24 +708,26 @@ def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None, stream=None) -> Tupl
     h [B,D] float32; x, f, g [B,D] float32 or bfloat16.  h_out defaults to h
     itself (in-place update).  Returns (y [B,D], h_out)."""
     import torch
-    lib = load_library()
-    shape, dev, dt = x.shape, x.device, x.dtype
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) != 2:
         raise ValueError("x: expected [B, D], got %s" % (tuple(shape),))
-    code = _dtype_code(x)
-    d = M3ScanDims(shape[0], 1, shape[1], _rows(x, "x", dt, shape, dev),
-                   _rows(f, "f", dt, shape, dev), 0 if g is None else _rows(g, "g", dt, shape, dev))
-    _check(h, "h", torch.float32, shape, dev)
+    code = _type_code(x)
+    ld = _rows(x, "x", dt, shape, dev)
+    d = M3ScanDims(shape[0], 1, shape[1], ld, _rows(f, "f", dt, shape, dev),
+                   0 if g is None else _rows(g, "g", dt, shape, dev))
+    _same(h, "h", torch.float32, shape, dev)
     if h_out is None:
         h_out = h
     else:
-        _check(h_out, "h_out", torch.float32, shape, dev)
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
-    else:
+        _same(h_out, "h_out", torch.float32, shape, dev)
+    if y is not None:
         d.ld_y = _rows(y, "y", dt, shape, dev)
-    _launch(dev, stream, lib.m3_gated_scan_step, ctypes.byref(d), code, _ptr(h), _ptr(h_out),
-            _ptr(x), _ptr(f), _ptr(g), _ptr(y))
+    _gpu(dev)
+    if y is None:
+        y = _like(x, ld == 0)
+    _launch(dev, stream, lib.m3_gated_scan_step, ctypes.byref(d), code, _at(h), _at(h_out),
+            _at(x), _at(f), _at(g), _at(y))
     return y, h_out
 
 
@@ -687,37 +741,35 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None
     place).  Returns (y, s, mean, rstd): s is x itself without a residual,
     mean and rstd [...] float32 (None without want_stats)."""
     import torch
-    lib = load_library()
-    shape, dev, dt = x.shape, x.device, x.dtype
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) < 1:
         raise ValueError("x: expected [..., D]")
-    code = _dtype_code(x)
+    code = _type_code(x)
     nd = shape[-1]
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    d = M3NormDims(rows, nd, _rows(x, "x", dt, shape, dev))
-    _check(weight, "weight", torch.float32, (nd,), dev)
+    rows = math.prod(shape[:-1])
+    ld = _rows(x, "x", dt, shape, dev)
+    d = M3NormDims(rows, nd, ld)
+    _same(weight, "weight", torch.float32, (nd,), dev)
     if bias is not None:
-        _check(bias, "bias", torch.float32, (nd,), dev)
-    s = x
+        _same(bias, "bias", torch.float32, (nd,), dev)
     if residual is not None:
         d.ld_residual = _rows(residual, "residual", dt, shape, dev)
-        if sum_out is None:
-            sum_out = torch.empty(shape, dtype=dt, device=dev)
-        s = sum_out
     if sum_out is not None:
         d.ld_sum = _rows(sum_out, "sum_out", dt, shape, dev)
-        s = sum_out
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
-    else:
+    if y is not None:
         d.ld_y = _rows(y, "y", dt, shape, dev)
+    _gpu(dev)
+    if residual is not None and sum_out is None:
+        sum_out = _like(x, ld == 0)
+    s = x if sum_out is None else sum_out
+    if y is None:
+        y = _like(x, ld == 0)
     mean = rstd = None
     if want_stats:
-        mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev).unbind(0)
-    _launch(dev, stream, lib.m3_layer_norm, ctypes.byref(d), code, _ptr(x), _ptr(residual),
-            _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(sum_out), _ptr(mean), _ptr(rstd))
+        mean, rstd = weight.new_empty(shape[:-1]), weight.new_empty(shape[:-1])
+    _launch(dev, stream, lib.m3_layer_norm, ctypes.byref(d), code, _at(x), _at(residual),
+            _at(weight), _at(bias), float(eps), _at(y), _at(sum_out), _at(mean), _at(rstd))
     return y, s, mean, rstd
 
 
@@ -729,38 +781,39 @@ def layer_norm_backward(dy, s, weight, mean, rstd, *, dsum=None, dx=None, want_b
     dict: x (the gradient of x and of residual) in s's type, weight and bias
     [D] float32 (bias absent without want_bias)."""
     import torch
-    lib = load_library()
-    shape, dev, dt = s.shape, s.device, s.dtype
+    lib = _lib or load_library()
+    shape, dev, dt = s.shape, s.get_device(), s.dtype
     if len(shape) < 1:
         raise ValueError("s: expected [..., D]")
-    code = _dtype_code(s)
+    code = _type_code(s)
     nd = shape[-1]
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    d = M3NormDims(rows, nd)
+    d = M3NormDims(math.prod(shape[:-1]), nd)
     d.ld_sum = _rows(s, "s", dt, shape, dev)
     d.ld_dy = _rows(dy, "dy", dt, shape, dev)
-    _check(weight, "weight", torch.float32, (nd,), dev)
-    _check(mean, "mean", torch.float32, shape[:-1], dev)
-    _check(rstd, "rstd", torch.float32, shape[:-1], dev)
+    _same(weight, "weight", torch.float32, (nd,), dev)
+    _same(mean, "mean", torch.float32, shape[:-1], dev)
+    _same(rstd, "rstd", torch.float32, shape[:-1], dev)
     if dsum is not None:
         d.ld_dsum = _rows(dsum, "dsum", dt, shape, dev)
-    if dx is None:
-        dx = torch.empty(shape, dtype=dt, device=dev)
-    else:
+    if dx is not None:
         d.ld_dx = _rows(dx, "dx", dt, shape, dev)
-    dwb = torch.empty((2 if want_bias else 1, nd), dtype=torch.float32, device=dev)
+    _gpu(dev)
+    if dx is None:
+        dx = _like(s, d.ld_sum == 0)
+    dw = weight.new_empty((nd,))
+    db = weight.new_empty((nd,)) if want_bias else None
     need = int(lib.m3_layer_norm_backward_workspace_size(ctypes.byref(d), code))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch(dev, stream, lib.m3_layer_norm_backward, ctypes.byref(d), code, _ptr(dy), _ptr(s),
-            _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dwb[0]),
-            _ptr(dwb[1]) if want_bias else None, _ptr(workspace), ws_bytes)
-    out = {"x": dx, "weight": dwb[0]}
+        workspace = weight.new_empty((need,), dtype=torch.uint8)
+    elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the first tensor's device")
+    ws_bytes = 0 if workspace is None else workspace.nbytes
+    _launch(dev, stream, lib.m3_layer_norm_backward, ctypes.byref(d), code, _at(dy), _at(s),
+            _at(weight), _at(mean), _at(rstd), _at(dsum), _at(dx), _at(dw),
+            _at(db), _at(workspace), ws_bytes)
+    out = {"x": dx, "weight": dw}
     if want_bias:
-        out["bias"] = dwb[1]
+        out["bias"] = db
     return out
 
 
@@ -775,17 +828,17 @@ def state_cache(n_slots, nheads, N, P, dtype=None, device="cuda") -> Tuple:
     return codes.view(dtype or torch.int8), scales
 
 
-def _cache_check(codes, scales, slots, dev):
+def _cache_same(codes, scales, slots, dev):
     import torch
     if codes.dim() != 4:
         raise ValueError("codes: expected [slots, H, N, P], got %s" % (tuple(codes.shape),))
     code = _code_of(codes)
-    _check(codes, "codes", codes.dtype, codes.shape, dev)
-    _check(scales, "scales", torch.float32, codes.shape[:3], dev)
+    _same(codes, "codes", codes.dtype, codes.shape, dev)
+    _same(scales, "scales", torch.float32, codes.shape[:3], dev)
     if slots is not None:
         if slots.dim() != 1:
             raise ValueError("slots: expected [batch], got %s" % (tuple(slots.shape),))
-        _check(slots, "slots", torch.int32, slots.shape, dev)
+        _same(slots, "slots", torch.int32, slots.shape, dev)
     return code
 
 
@@ -794,33 +847,37 @@ def state_store(h, codes, scales, slots=None, *, stream=None) -> None:
     (m3_state_store).  slots [S] int32, negative or past the pool: idle; None:
     state i into slot i."""
     import torch
-    lib = load_library()
-    dev = codes.device
-    code = _cache_check(codes, scales, slots, dev)
+    lib = _lib or load_library()
+    dev = codes.get_device()
+    code = _cache_same(codes, scales, slots, dev)
     ns = h.shape[0] if slots is None else slots.shape[0]
-    _check(h, "h", torch.float32, (ns,) + codes.shape[1:], dev)
+    _same(h, "h", torch.float32, (ns,) + codes.shape[1:], dev)
+    _gpu(dev)
     n, nh, nn, npd = codes.shape
-    d = _dims(ns, 1, nh, npd, nn, 1)
-    _launch(dev, stream, lib.m3_state_store, ctypes.byref(d), code, _ptr(h), _ptr(codes),
-            _ptr(scales), _ptr(slots), n)
+    d = M3Dims(ns, 1, nh, npd, nn, 1)
+    _launch(dev, stream, lib.m3_state_store, ctypes.byref(d), code, _at(h), _at(codes),
+            _at(scales), _at(slots), n)
 
 
 def state_load(codes, scales, slots=None, *, dtype=None, h=None, stream=None):
     """The states of the cache's slots [S,H,N,P] as float32 (or bfloat16 by
     dtype) (m3_state_load); zeros for idle slots; slots None: the whole pool."""
     import torch
-    lib = load_library()
-    dev = codes.device
-    code = _cache_check(codes, scales, slots, dev)
+    lib = _lib or load_library()
+    dev = codes.get_device()
+    code = _cache_same(codes, scales, slots, dev)
     n, nh, nn, npd = codes.shape
     ns = n if slots is None else slots.shape[0]
+    if h is not None:
+        _same(h, "h", dtype or h.dtype, (ns, nh, nn, npd), dev)
+    elif dtype not in (None, torch.float32, torch.bfloat16):
+        raise TypeError("expected float32 or bfloat16, got %s" % dtype)
+    _gpu(dev)
     if h is None:
-        h = torch.empty((ns, nh, nn, npd), dtype=dtype or torch.float32, device=dev)
-    else:
-        _check(h, "h", dtype or h.dtype, (ns, nh, nn, npd), dev)
-    d = _dims(ns, 1, nh, npd, nn, 1)
-    _launch(dev, stream, lib.m3_state_load, ctypes.byref(d), code, _dtype_code(h), _ptr(codes),
-            _ptr(scales), _ptr(slots), n, _ptr(h))
+        h = scales.new_empty((ns, nh, nn, npd), dtype=dtype or torch.float32)
+    d = M3Dims(ns, 1, nh, npd, nn, 1)
+    _launch(dev, stream, lib.m3_state_load, ctypes.byref(d), code, _type_code(h), _at(codes),
+            _at(scales), _at(slots), n, _at(h))
     return h
 
 
@@ -835,33 +892,34 @@ def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, 
     whose rows of idle entries are left as they were (zeros when y is not
     given)."""
     import torch
-    lib = load_library()
-    dev = codes.device
-    code = _cache_check(codes, scales, slots, dev)
+    lib = _lib or load_library()
+    dev = codes.get_device()
+    code = _cache_same(codes, scales, slots, dev)
     n, nh, nn, npd = codes.shape
     ns, nr = x_t.shape[0], x_t.shape[2]
     xs, bs = (ns, nh, nr, npd), (ns, nh, nr, nn)
-    tcode = _dtype_code(x_t)
-    if slots is not None:
-        _check(slots, "slots", torch.int32, (ns,), dev)
+    tcode = _type_code(x_t)
+    if slots is not None and slots.shape[0] != ns:
+        raise ValueError("slots: expected shape %s, got %s" % ((ns,), tuple(slots.shape)))
     if lam is not None and (x_prev is None or B_prev is None):
         raise ValueError("x_prev and B_prev are required with lam")
     for name, t, shape in (("x_t", x_t, xs), ("x_prev", x_prev, xs), ("B_t", B_t, bs),
                            ("B_prev", B_prev, bs), ("C_t", C_t, bs)):
         if t is not None:
-            _check(t, name, x_t.dtype, shape, dev)
-    _check(dt, "dt", torch.float32, (ns, nh), dev)
+            _same(t, name, x_t.dtype, shape, dev)
+    _same(dt, "dt", torch.float32, (ns, nh), dev)
     if lam is not None:
-        _check(lam, "lam", torch.float32, (ns, nh), dev)
+        _same(lam, "lam", torch.float32, (ns, nh), dev)
     if theta is not None:
-        _check(theta, "theta", torch.float32, (ns, nh, nn // 2), dev)
-    _check(A, "A", torch.float32, (nh,), dev)
+        _same(theta, "theta", torch.float32, (ns, nh, nn // 2), dev)
+    _same(A, "A", torch.float32, (nh,), dev)
+    if y is not None:
+        _same(y, "y", x_t.dtype, xs, dev)
+    _gpu(dev)
     if y is None:
         y = (torch.empty if slots is None else torch.zeros)(xs, dtype=x_t.dtype, device=dev)
-    else:
-        _check(y, "y", x_t.dtype, xs, dev)
-    d = _dims(ns, 1, nh, npd, nn, nr)
-    _launch(dev, stream, lib.m3_decode_step_cached, ctypes.byref(d), tcode, code, _ptr(codes),
-            _ptr(scales), _ptr(slots), n, _ptr(x_t), _ptr(x_prev), _ptr(B_t), _ptr(B_prev),
-            _ptr(C_t), _ptr(dt), _ptr(A), _ptr(lam), _ptr(theta), _ptr(y))
+    d = M3Dims(ns, 1, nh, npd, nn, nr)
+    _launch(dev, stream, lib.m3_decode_step_cached, ctypes.byref(d), tcode, code, _at(codes),
+            _at(scales), _at(slots), n, _at(x_t), _at(x_prev), _at(B_t), _at(B_prev),
+            _at(C_t), _at(dt), _at(A), _at(lam), _at(theta), _at(y))
     return y
