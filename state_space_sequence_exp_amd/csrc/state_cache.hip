@@ -12,9 +12,10 @@
 //   h += ((1 - lam) dt) (sum_r B_prev[r] x_prev[r])
 //   h  = (cos h_0 - sin h_1, sin h_0 + cos h_1)           per row pair
 //   h  = alpha h + (lam dt) (sum_r B[r] x[r])             r in order
-// and any evaluation of these gets the same cache.  That takes about 30 vector
-// operations an element at R = 4 against 18 with fused ones; the sums of y,
-// which is rounded once and not kept, are fused.
+// and any evaluation of these gets the same cache.  A product of two bfloat16
+// values is a float, so that in bfloat16 the sums over r are fused all the
+// same (4 operations at R = 4 instead of 7, twice an element); the sums of y,
+// which is rounded once and not kept, are fused in either type.
 //
 // A workgroup owns one (sequence, head).  Its threads request their codes,
 // then put the coefficients of the row pairs into the LDS, a pair's together;
@@ -39,14 +40,15 @@ struct Code<M3_CODE_INT8> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
   }
+  // |v| <= 127 (1 + 2^-23): beside 1.5 x 2^23 a float's last place is one, so
+  // the sum's low byte is v rounded to even, in two's complement
   __device__ __forceinline__ static uint32_t pack4(const float* v) {
-    uint32_t w = 0;
+    uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = (int)__builtin_rintf(v[i]);
-      w |= ((uint32_t)(q < -127 ? -127 : q > 127 ? 127 : q) & 0xffu) << (8 * i);
-    }
-    return w;
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[i] + 12582912.f);
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    return lo | hi;
   }
 };
 template <>
@@ -58,60 +60,55 @@ struct Code<M3_CODE_E4M3> {
     const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
     v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
   }
+  // |v| <= 448 (1 + 2^-23), which rounds to 448: nothing to clamp
   __device__ __forceinline__ static uint32_t pack4(const float* v) {
-    float c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(v[i], -448.f), 448.f);
     int w = 0;
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], w, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
     return (uint32_t)w;
   }
 };
 
-// |v| as ordered bits, so that a maximum keeps NaN (above infinity).
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 // A row's scale and the factor that takes it to codes, from its largest
-// magnitude's bits.
+// magnitude (NaN where the row holds one).
 template <int kCode>
-__device__ __forceinline__ void row_scale(uint32_t top, float* scale, float* inv) {
-  const float amax = __uint_as_float(top);
-  if (top >= 0x7f800000u) {
-    *scale = __uint_as_float(0x7fc00000u);
-    *inv = 0.f;
-  } else if (amax < kTinyRow) {
-    *scale = *inv = 0.f;
-  } else {
-    *scale = amax * (1.f / Code<kCode>::kMax);
-    *inv = Code<kCode>::kMax / amax;
-  }
+__device__ __forceinline__ void row_scale(float amax, float* scale, float* inv) {
+  const bool held = amax >= kTinyRow && amax < __builtin_inff();
+  *inv = held ? Code<kCode>::kMax / amax : 0.f;
+  *scale = held ? amax * (1.f / Code<kCode>::kMax) : amax < kTinyRow ? 0.f : __uint_as_float(0x7fc00000u);
 }
 
-// Codes of 8 values of a row whose top is `top`.
+// Codes of 8 values of a row.
 template <int kCode>
-__device__ __forceinline__ uint2 quantise8(const float (&h)[8], float inv, bool finite) {
+__device__ __forceinline__ uint2 quantise8(const float (&h)[8], float amax, float inv) {
   float v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = finite ? h[e] * inv : 0.f;
+  for (int e = 0; e < 8; ++e) v[e] = h[e] * inv;
+  // rare, so a branch of the whole wave: 0 x infinity is no code
+  const bool bad = !(amax < __builtin_inff());
+  if (__builtin_expect(__any(bad), 0)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = bad ? 0.f : v[e];
+  }
   return make_uint2(Code<kCode>::pack4(v), Code<kCode>::pack4(v + 4));
 }
 
-__device__ __forceinline__ uint32_t top8(const float (&h)[8]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = abs_bits(h[e]);
-    top = b > top ? b : top;
-  }
-  return top;
+// The larger of two magnitudes; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
 }
-// Maximum over the `lanes` (a power of two) consecutive lanes of a row.
-__device__ __forceinline__ uint32_t row_top(uint32_t top, int lanes) {
-  for (int off = lanes >> 1; off > 0; off >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, off, kWave);
-    top = o > top ? o : top;
-  }
+__device__ __forceinline__ float top8(const float (&h)[8]) {
+  const float a = max_abs(max_abs(h[0], h[1]), h[2]), b = max_abs(max_abs(h[3], h[4]), h[5]);
+  return max_abs(max_abs(a, b), max_abs(h[6], h[7]));
+}
+// Maximum over the `lanes` (2, 4, 8 or 16) consecutive lanes of a row, by lane
+// moves inside the 16 lanes of a DPP row: lane xor 1, xor 2, then (all four of
+// a quad being equal) the mirrored half row and row.
+__device__ __forceinline__ float row_top(float top, int lanes) {
+  top = max_abs(top, dpp_move<0xb1>(top));
+  if (lanes > 2) top = max_abs(top, dpp_move<0x4e>(top));
+  if (lanes > 4) top = max_abs(top, dpp_move<0x141>(top));
+  if (lanes > 8) top = max_abs(top, dpp_move<0x140>(top));
   return top;
 }
 
@@ -146,11 +143,11 @@ __global__ void __launch_bounds__(kThreads) store_kernel(CacheArgs a) {
     const float4 hi = in ? reinterpret_cast<const float4*>(h)[2 * p + 1] : make_float4(0, 0, 0, 0);
     v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-    const uint32_t top = row_top(top8(v), lanes);
+    const float top = row_top(top8(v), lanes);
     float scale, inv;
     row_scale<kCode>(top, &scale, &inv);
     if (in) {
-      codes[p] = quantise8<kCode>(v, inv, top < 0x7f800000u);
+      codes[p] = quantise8<kCode>(v, top, inv);
       if (p % lanes == 0) a.scales[unit * a.N + p / lanes] = scale;
     }
   }
@@ -205,36 +202,56 @@ struct PairCoef {
   float bp[2][R], b[2][R], c[2][R];
 };
 
-template <typename T, int R, int kCode, bool kTrap, bool kRot, int NPT>
-__global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
+// sum_r b[r] x[r][e] in order, each product and sum rounded (a product of two
+// bfloat16 values is exact, so there the fused form is the same).
+template <typename T, int R>
+__device__ __forceinline__ float rank_sum(const float (&b)[R], const float (&x)[R][8], int e) {
+#pragma clang fp contract(off)
+  float t = b[0] * x[0][e];
+#pragma unroll
+  for (int r = 1; r < R; ++r) {
+    if constexpr (sizeof(T) == 2)
+      t = __builtin_fmaf(b[r], x[r][e], t);
+    else
+      t = t + b[r] * x[r][e];
+  }
+  return t;
+}
+
+// What a thread reads of one row pair.
+struct PairIn {
+  uint2 w0, w1;
+  float s0, s1;
+};
+
+// NT threads own a unit: row pair rg + k NT / lanes is the k-th of the thread
+// in lane group rg.  The next pair is requested before the present one is
+// worked on.
+template <typename T, int R, int kCode, bool kTrap, bool kRot, int NT>
+__global__ void __launch_bounds__(NT) decode_kernel(CacheArgs a) {
 #pragma clang fp contract(off)
   extern __shared__ __align__(16) float dsm[];
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
   const int slot = slot_of(a, i);
   if (slot < 0) return;
   const int N = a.N, P = a.P, npair = N / 2, lanes = P / 8;
-  const int tid = threadIdx.x, c8 = tid % lanes, rg = tid / lanes, groups = kThreads / lanes;
+  const int tid = threadIdx.x, c8 = tid % lanes, rg = tid / lanes, groups = NT / lanes;
   const size_t in = (size_t)i * a.H + head;       // this token's inputs
   const size_t unit = (size_t)slot * a.H + head;  // its state
   PairCoef<R>* s_pair = reinterpret_cast<PairCoef<R>*>(dsm);
-  float* s_y = dsm + (size_t)npair * (sizeof(PairCoef<R>) / 4);  // [groups][R][P]
+  float* s_y = dsm;  // [groups][R][P], in the coefficients' place at the end
 
-  // everything this thread reads, requested before it is used
-  uint2* codes = reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.codes) + unit * N * P);
+  char* codes = static_cast<char*>(a.codes) + unit * N * P;
   float* scales = a.scales + unit * N;
-  uint2 w0[NPT], w1[NPT];
-  float2 sc[NPT];
-#pragma unroll
-  for (int k = 0; k < NPT; ++k) {
-    const int kp = rg + k * groups;
-    w0[k] = w1[k] = make_uint2(0u, 0u);
-    sc[k] = make_float2(0.f, 0.f);
-    if (kp < npair) {
-      w0[k] = codes[(size_t)(2 * kp) * lanes + c8];
-      w1[k] = codes[(size_t)(2 * kp + 1) * lanes + c8];
-      sc[k] = make_float2(scales[2 * kp], scales[2 * kp + 1]);
-    }
-  }
+  // pair kp's codes: row 2 kp at byte 2 kp P, its second row P bytes on
+  // (past the last pair: the last pair's, unused)
+  const auto request = [&](int kp) {
+    kp = kp < npair ? kp : npair - 1;
+    const uint32_t at = 2 * kp * P + 8 * c8;
+    return PairIn{*reinterpret_cast<const uint2*>(codes + at),
+                  *reinterpret_cast<const uint2*>(codes + at + P), scales[2 * kp], scales[2 * kp + 1]};
+  };
+  PairIn cur = request(rg);
   float xc[R][8], xq[R][8], yp[R][8];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -247,12 +264,11 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
   const float d = a.dt[in], la = kTrap ? a.lam[in] : 1.f;
   const float alpha = expf(d * a.A[head]);
   const float cu = (1.f - la) * d, cv = la * d;
-  for (int kp = tid; kp < npair; kp += kThreads) {
+  for (int kp = tid; kp < npair; kp += NT) {
     PairCoef<R>& q = s_pair[kp];
     if constexpr (kRot) {
       const float psi = d * a.theta[in * npair + kp];
-      q.cs = cosf(psi);
-      q.sn = sinf(psi);
+      sincosf(psi, &q.sn, &q.cs);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -271,65 +287,52 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
   // coefficients are read
   int same = 0;
   if (a.slots)
-    for (int j = tid; j < i; j += kThreads) same |= a.slots[j] == slot ? 1 : 0;
+    for (int j = tid; j < i; j += NT) same |= a.slots[j] == slot ? 1 : 0;
   if (__syncthreads_or(same)) return;
 
-#pragma unroll
-  for (int k = 0; k < NPT; ++k) {
-    const int kp = rg + k * groups;
-    if (k * groups >= npair) break;  // for the whole workgroup
-    const bool on = kp < npair;
-    const PairCoef<R>& q = s_pair[on ? kp : 0];
+  for (int kp = rg; kp < npair; kp += groups) {  // the lanes of a row together
+    const PairCoef<R>& q = s_pair[kp];
     float v0[8], v1[8];
-    Code<kCode>::unpack4(w0[k].x, v0);
-    Code<kCode>::unpack4(w0[k].y, v0 + 4);
-    Code<kCode>::unpack4(w1[k].x, v1);
-    Code<kCode>::unpack4(w1[k].y, v1 + 4);
+    Code<kCode>::unpack4(cur.w0.x, v0);
+    Code<kCode>::unpack4(cur.w0.y, v0 + 4);
+    Code<kCode>::unpack4(cur.w1.x, v1);
+    Code<kCode>::unpack4(cur.w1.y, v1 + 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float h0 = v0[e] * sc[k].x, h1 = v1[e] * sc[k].y;
-      if constexpr (kTrap) {
-        float t0 = q.bp[0][0] * xq[0][e], t1 = q.bp[1][0] * xq[0][e];
+      v0[e] = v0[e] * cur.s0;
+      v1[e] = v1[e] * cur.s1;
+    }
+    cur = request(kp + groups);
 #pragma unroll
-        for (int r = 1; r < R; ++r) {
-          t0 = t0 + q.bp[0][r] * xq[r][e];
-          t1 = t1 + q.bp[1][r] * xq[r][e];
-        }
-        h0 = h0 + cu * t0;
-        h1 = h1 + cu * t1;
+    for (int e = 0; e < 8; ++e) {
+      float h0 = v0[e], h1 = v1[e];
+      if constexpr (kTrap) {
+        h0 = h0 + cu * rank_sum<T, R>(q.bp[0], xq, e);
+        h1 = h1 + cu * rank_sum<T, R>(q.bp[1], xq, e);
       }
       if constexpr (kRot) {
         const float n0 = q.cs * h0 - q.sn * h1, n1 = q.sn * h0 + q.cs * h1;
         h0 = n0;
         h1 = n1;
       }
-      float t0 = q.b[0][0] * xc[0][e], t1 = q.b[1][0] * xc[0][e];
+      v0[e] = alpha * h0 + cv * rank_sum<T, R>(q.b[0], xc, e);
+      v1[e] = alpha * h1 + cv * rank_sum<T, R>(q.b[1], xc, e);
 #pragma unroll
-      for (int r = 1; r < R; ++r) {
-        t0 = t0 + q.b[0][r] * xc[r][e];
-        t1 = t1 + q.b[1][r] * xc[r][e];
-      }
-      v0[e] = alpha * h0 + cv * t0;
-      v1[e] = alpha * h1 + cv * t1;
-      if (on) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          yp[r][e] = __builtin_fmaf(q.c[0][r], v0[e], __builtin_fmaf(q.c[1][r], v1[e], yp[r][e]));
-      }
+      for (int r = 0; r < R; ++r)
+        yp[r][e] = __builtin_fmaf(q.c[0][r], v0[e], __builtin_fmaf(q.c[1][r], v1[e], yp[r][e]));
     }
-    const uint32_t t0 = row_top(top8(v0), lanes), t1 = row_top(top8(v1), lanes);
-    float sc0, sc1, i0, i1;
-    row_scale<kCode>(t0, &sc0, &i0);
-    row_scale<kCode>(t1, &sc1, &i1);
-    if (on) {
-      codes[(size_t)(2 * kp) * lanes + c8] = quantise8<kCode>(v0, i0, t0 < 0x7f800000u);
-      codes[(size_t)(2 * kp + 1) * lanes + c8] = quantise8<kCode>(v1, i1, t1 < 0x7f800000u);
-      if (c8 == 0) {
-        scales[2 * kp] = sc0;
-        scales[2 * kp + 1] = sc1;
-      }
-    }
+    // the even lanes of a row pair take the first row's scale, the odd ones
+    // the second's: one division for both
+    const float t0 = row_top(top8(v0), lanes), t1 = row_top(top8(v1), lanes);
+    float scale, inv;
+    row_scale<kCode>(c8 & 1 ? t1 : t0, &scale, &inv);
+    const float i0 = dpp_move<0xa0>(inv), i1 = dpp_move<0xf5>(inv);  // of lanes 0, 0, 2, 2 / 1, 1, 3, 3
+    const uint32_t at = 2 * kp * P + 8 * c8;
+    *reinterpret_cast<uint2*>(codes + at) = quantise8<kCode>(v0, t0, i0);
+    *reinterpret_cast<uint2*>(codes + at + P) = quantise8<kCode>(v1, t1, i1);
+    if (c8 < 2) scales[2 * kp + c8] = scale;
   }
+  __syncthreads();  // the coefficients are read
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float4* o = reinterpret_cast<float4*>(s_y + (rg * R + r) * P + 8 * c8);
@@ -338,35 +341,34 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(CacheArgs a) {
   }
   __syncthreads();
   T* y = static_cast<T*>(a.y) + in * R * P;
-  for (int o = tid; o < R * P; o += kThreads) {
+  for (int o = tid; o < R * P; o += NT) {
     float sum = 0.f;
     for (int g = 0; g < groups; ++g) sum += s_y[g * R * P + o];
     y[o] = from_f32<T>(sum);
   }
 }
 
-template <typename T, int R, int kCode, bool kTrap, bool kRot, int NPT>
-hipError_t launch_decode_npt(const CacheArgs& a, hipStream_t stream) {
-  const int groups = kThreads / (a.P / 8);
-  const size_t lds =
-      sizeof(PairCoef<R>) * (a.N / 2) + sizeof(float) * (size_t)groups * R * a.P;
+template <typename T, int R, int kCode, bool kTrap, bool kRot, int NT>
+hipError_t launch_decode_nt(const CacheArgs& a, hipStream_t stream) {
+  const size_t coef = sizeof(PairCoef<R>) * (a.N / 2);
+  const size_t part = sizeof(float) * (size_t)(NT / (a.P / 8)) * R * a.P;
+  const size_t lds = coef > part ? coef : part;
   const hipError_t e = lds_limit(
-      reinterpret_cast<const void*>(&decode_kernel<T, R, kCode, kTrap, kRot, NPT>), lds);
+      reinterpret_cast<const void*>(&decode_kernel<T, R, kCode, kTrap, kRot, NT>), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decode_kernel<T, R, kCode, kTrap, kRot, NPT>), dim3(a.S * a.H),
-                     dim3(kThreads), lds, stream, a);
+  hipLaunchKernelGGL((decode_kernel<T, R, kCode, kTrap, kRot, NT>), dim3(a.S * a.H), dim3(NT), lds,
+                     stream, a);
   return hipGetLastError();
 }
 
-// Row pairs a thread: N / 2 over 256 / (P / 8) groups of lanes, at most 4
-// where decode_max_n allows N.
+#ifndef M3_DECODE_WAVE_UNITS
+#define M3_DECODE_WAVE_UNITS 1024
+#endif
 template <typename T, int R, int kCode, bool kTrap, bool kRot>
 hipError_t launch_decode_form(const CacheArgs& a, hipStream_t stream) {
-  const int groups = kThreads / (a.P / 8), npt = (a.N / 2 + groups - 1) / groups;
-  if (npt <= 1) return launch_decode_npt<T, R, kCode, kTrap, kRot, 1>(a, stream);
-  if (npt <= 2) return launch_decode_npt<T, R, kCode, kTrap, kRot, 2>(a, stream);
-  if (npt <= 4) return launch_decode_npt<T, R, kCode, kTrap, kRot, 4>(a, stream);
-  return hipErrorInvalidValue;
+  if (a.S * a.H >= M3_DECODE_WAVE_UNITS)
+    return launch_decode_nt<T, R, kCode, kTrap, kRot, 64>(a, stream);
+  return launch_decode_nt<T, R, kCode, kTrap, kRot, 256>(a, stream);
 }
 
 template <typename T, int R, int kCode>
