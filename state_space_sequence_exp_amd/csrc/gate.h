@@ -6,7 +6,9 @@
 // set: z = w where e <= 1, z = -a where e > 1.  Either value follows from it
 // with its relative precision (a long memory is its distance w from 1, a
 // short one a itself), so does the slope a w = |z| (1 - |z|), and the masks
-// are exact: +0 passes the state on, -0 drops it.
+// are exact: +0 passes the state on, -0 drops it.  Not looking at what a mask
+// hides (it may be NaN) takes some selects a step, which the waves that hold
+// no mask leave out (kMask).
 #pragma once
 
 #include "m3_device.h"
@@ -32,18 +34,25 @@ __device__ __forceinline__ bool gate_cut(float z) { return __float_as_int(z) < 0
 __device__ __forceinline__ bool gate_drops(float z) { return __float_as_uint(z) == 0x80000000u; }
 __device__ __forceinline__ bool gate_passes(float z) { return __float_as_uint(z) == 0u; }
 
+// Whether some gate may be a mask, from the smallest |z|.
+__device__ __forceinline__ bool gate_masks(float least) { return least < 1e-30f; }
+
 // w
 __device__ __forceinline__ float gate_w(float z) { return z + (gate_cut(z) ? 1.f : 0.f); }
-// a v, for a finite v
+// a v.  kMask: a gate that drops the state does not look at v.
+template <bool kMask>
 __device__ __forceinline__ float gate_keep(float z, float v) {
+  if constexpr (kMask) v = gate_drops(z) ? 0.f : v;
   return __builtin_fmaf(-z, v, gate_cut(z) ? 0.f : v);
 }
-// a h + w x: a gate that drops the state does not look at h, one that passes
-// it not at x.
+// a h + w x.  kMask: nor does one that passes it look at x.
+template <bool kMask>
 __device__ __forceinline__ float gate_step(float z, float h, float x) {
-  const float hs = gate_drops(z) ? 0.f : h, xs = gate_passes(z) ? 0.f : x;
-  return __builtin_fmaf(gate_w(z), xs, gate_keep(z, hs));
+  if constexpr (kMask) x = gate_passes(z) ? 0.f : x;
+  return __builtin_fmaf(gate_w(z), x, gate_keep<kMask>(z, h));
 }
+
+constexpr float kLeastA = 1.17549435e-38f;
 
 // A run of steps as a map of the state before it: h -> A h + B.  A is 0 only
 // where a gate of the run dropped the state (then h is not looked at): a
@@ -58,7 +67,7 @@ __device__ __forceinline__ float run_apply(Run r, float h) {
 __device__ __forceinline__ Run run_join(Run first, Run then) {
   const float p = first.A * then.A;
   const bool none = first.A == 0.f || then.A == 0.f;
-  return Run{none ? 0.f : (p < 1.17549435e-38f ? 1.17549435e-38f : p), run_apply(then, first.B)};
+  return Run{none ? 0.f : (p < kLeastA ? kLeastA : p), run_apply(then, first.B)};
 }
 
 }  // namespace m3

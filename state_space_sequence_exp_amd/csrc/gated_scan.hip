@@ -4,9 +4,15 @@
 //
 // over whole sequences (one pass: see scan_tile.h) and for one token.
 //
-// A workgroup requests its chunk of x and f, forms its threads' maps, joins
-// and publishes them, requests g, looks back for the state that enters the
-// chunk, and walks each thread's tokens again from the state before them.
+// A workgroup requests its chunk of x and f and walks each thread's tokens
+// once, keeping for every token the map from the state before the thread's
+// first (A and B, where x and f were); the threads' maps are joined and
+// published, g is requested, and once the state that enters the chunk is known
+// every state is A h + B.  (Walking the tokens a second time instead keeps
+// one float a token less and takes 63 vector operations an element with the
+// output gate, against 37: 139 us for B1 T16384 D4096 bf16 and bound by them.)
+#include <type_traits>
+
 #include "scan_tile.h"
 
 namespace m3 {
@@ -37,36 +43,52 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, Ch
   const bool full = nt >= K && n >= kV;
   load_rows<T, kVec>(f, rf, full, nt, n, kPassGate<T>);
   load_rows<T, kVec>(x, rx, full, nt, n, 0u);
-  float z[K][kV];
+  // per token the map from the state before the thread's first
+  float A[K][kV], B[K][kV];
+  bool masks = false;  // in this wave
 #pragma unroll
   for (int i = 0; i < kWords<T>; ++i) {
-    Run r[W];
-#pragma unroll
-    for (int e = 0; e < W; ++e) r[e] = Run{1.f, 0.f};
+    float z[K][W], least = 1.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float xv[W], fv[W];
-      unpack_word(x[k].w[i], xv);
+      float fv[W];
       unpack_word(f[k].w[i], fv);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        const float q = gate_of(fv[e]);
-        z[k][i * W + e] = q;
-        r[e].A = gate_keep(q, r[e].A);
-        r[e].B = gate_step(q, r[e].B, xv[e]);
+        z[k][e] = gate_of(fv[e]);
+        least = fminf(least, __builtin_fabsf(z[k][e]));
       }
     }
+    const auto walk = [&](auto mask) {
+      constexpr bool kMask = decltype(mask)::value;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        Run r = Run{1.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float xv[W];
+          unpack_word(x[k].w[i], xv);
+          r.A = gate_keep<false>(z[k][e], r.A);
+          r.B = gate_step<kMask>(z[k][e], r.B, xv[e]);
+          A[k][i * W + e] = r.A;
+          B[k][i * W + e] = r.B;
+        }
+      }
+    };
+    const bool some = __any(gate_masks(least));
+    masks |= some;
+    if (some) walk(std::true_type{});
+    else walk(std::false_type{});
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const int v = i * W + e;
-      Run before;
-      wave_join<false>(r[e], before);
+      Run r = Run{A[K - 1][v], B[K - 1][v]}, before;
+      if (!some) r.A = fmaxf(r.A, kLeastA);
+      wave_join<false>(r, before);
       s_run[v][tid] = before;
-      if (lane / kLanesAcross == 3) s_wave[wave][cl + v] = r[e];
+      if (lane / kLanesAcross == 3) s_wave[wave][cl + v] = r;
     }
   }
-  renew(x);
-  renew(z);
   if constexpr (kGate) {
     const Rows<T> rg(a.g, row0 * a.ld_g + d0, a.ld_g, tok, cl);
     load_rows<T, kVec>(g, rg, full, nt, n, 0u);
@@ -115,14 +137,13 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, Ch
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float xv[W], gv[W], y[W];
-      unpack_word(x[k].w[i], xv);
+      float gv[W], y[W];
       if constexpr (kGate) unpack_word(g[k].w[i], gv);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        h[e] = gate_step(z[k][i * W + e], h[e], xv[e]);
-        y[e] = h[e];
-        if constexpr (kGate) y[e] = h[e] * (gv[e] * sigmoid_of(gv[e]));
+        const float p = A[k][i * W + e];
+        y[e] = __builtin_fmaf(p, masks && p == 0.f ? 0.f : h[e], B[k][i * W + e]);
+        if constexpr (kGate) y[e] *= gv[e] * sigmoid_of(gv[e]);
       }
       x[k].w[i] = pack_word(y);
       renew(x[k].w[i]);
@@ -164,7 +185,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a, int64_t 
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const int v = i * W + e;
-      y[e] = gate_step(gate_of(fv[e]), __uint_as_float(h.w[v]), xv[e]);
+      y[e] = gate_step<true>(gate_of(fv[e]), __uint_as_float(h.w[v]), xv[e]);
       h.w[v] = __float_as_uint(y[e]);
       if constexpr (kGate) y[e] = y[e] * (gv[e] * sigmoid_of(gv[e]));
     }

@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
       for (int e = 0; e < W; ++e) {
         const float q = gate_of(fv[e]);
         z[k][i * W + e] = q;
-        r[e].A = gate_keep(q, r[e].A);
-        r[e].B = gate_step(q, r[e].B, xv[e]);
+        r[e].A = gate_keep<false>(q, r[e].A);
+        r[e].B = gate_step<true>(q, r[e].B, xv[e]);
       }
     }
 #pragma unroll
@@ -70,8 +70,7 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         if constexpr (kGate) dv[e] *= gv[e] * sigmoid_of(gv[e]);
-        const float q = z[k][i * W + e], G = dv[e] + u[e].B;
-        u[e].B = gate_keep(q, gate_drops(q) ? 0.f : G);
+        u[e].B = gate_keep<true>(z[k][i * W + e], dv[e] + u[e].B);
       }
     }
 #pragma unroll
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         h[k][e] = hk[e];
-        hk[e] = gate_step(z[k][i * W + e], hk[e], xv[e]);
+        hk[e] = gate_step<true>(z[k][i * W + e], hk[e], xv[e]);
       }
     }
     renew(x);
@@ -167,11 +166,10 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
           dg[e] = dv[e] * after * (sg * __builtin_fmaf(gv[e], 1.f - sg, 1.f));
           dh = dv[e] * (gv[e] * sg);
         }
-        const float G = dh + u[e], s = __builtin_fabsf(q);
-        const float slope = s * (1.f - s);
+        const float G = dh + u[e], s = __builtin_fabsf(q), slope = s * (1.f - s);
         dx[e] = gate_passes(q) ? 0.f : G * gate_w(q);
         df[e] = slope == 0.f ? 0.f : G * (h[k][e] - xv[e]) * slope;
-        u[e] = gate_keep(q, gate_drops(q) ? 0.f : G);
+        u[e] = gate_keep<true>(q, G);
       }
       x[k].w[i] = pack_word(dx);
       dy[k].w[i] = pack_word(df);
