@@ -19,22 +19,22 @@ namespace m3 {
 namespace {
 
 template <typename T, bool kGate, bool kVec>
-__global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, ChainWs ws, int nTiles) {
-  constexpr int C = kC, W = kPerWord<T>, K = kTok<T>, NT = kScanThreads<T>, NW = kScanWaves<T>;
+__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, ChainWs ws, int nTiles) {
+  constexpr int C = kC<T>, W = kPerWord<T>, K = kTok<T>, NW = kScanWaves;
   __shared__ Run s_wave[NW][C];           // each wave's map, then the join of those before
-  __shared__ Run s_run[kV][NT];                   // the join of the maps before a thread's in its wave
-  __shared__ Run s_part[NW][C];  // the look-back's parts
+  __shared__ Run s_run[kV][kScanThreads];                   // the join of the maps before a thread's in its wave
+  __shared__ Run s_part[kParts<T>][C];  // the look-back's parts
   __shared__ float s_entry[C];                    // the state entering the chunk
   __shared__ int s_word;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nC = (int)a.nC;
-  const int units = (int)a.B * nTiles, unit = blockIdx.x % units;
+  const int units = (int)a.B * nTiles, unit = (blockIdx.x + blockIdx.x / units) % units;
   const int64_t b = unit / nTiles;
   const int d0 = unit % nTiles * C;
-  const int cl = (lane % kLanesAcross) * kV;       // this lane's first channel in the tile
+  const int cl = (lane % kAcross<T>) * kV;       // this lane's first channel in the tile
   const int n = (int)a.D - d0 - cl;               // channels from there to the row's end
   const int k0 = nC > 1 ? chain_ticket(ws, unit, nC, &s_word) : 0;
   if (k0 >= nC) return;
-  const int tok = (tid / kLanesAcross) * K;    // this thread's first token in the chunk
+  const int tok = (tid / kAcross<T>) * K;    // this thread's first token in the chunk
   const int nt = (int)(a.T - (int64_t)k0 * M3_SCAN_CHUNK) - tok;  // tokens from there on
   const int64_t row0 = b * a.T + (int64_t)k0 * M3_SCAN_CHUNK;
   const Rows<T> rf(a.f, row0 * a.ld_f + d0, a.ld_f, tok, cl), rx(a.x, row0 * a.ld_x + d0, a.ld_x, tok, cl);
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, Ch
       const int v = i * W + e;
       Run r = Run{A[K - 1][v], B[K - 1][v]}, before;
       if (!some) r.A = fmaxf(r.A, kLeastA);
-      wave_join<false>(r, before);
+      wave_join<T, false>(r, before);
       s_run[v][tid] = before;
-      if (lane / kLanesAcross == 3) s_wave[wave][cl + v] = r;
+      if (lane / kAcross<T> == kShare<T> - 1) s_wave[wave][cl + v] = r;
     }
   }
   if constexpr (kGate) {
@@ -102,30 +102,28 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, Ch
       s_wave[w][tid] = total;
       total = run_join(total, m);
     }
-    if (k0 + 1 < nC && k0 % kScanGroup != kScanGroup - 1)
+    if (k0 + 1 < nC)
       publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
   }
   const int ch = tid % C, part = tid / C;
   const float h0 = a.h0 && d0 + ch < a.D ? a.h0[b * a.D + d0 + ch] : 0.f;
-  s_part[part][ch] = chain_part<NW>(ws, unit, nC, k0, part, ch, h0);
+  s_part[part][ch] = chain_part<T>(ws, unit, nC, k0, part, ch, h0);
   __syncthreads();
   if (tid < C) {
     float h = 0.f;
 #pragma unroll
-    for (int p = 0; p < NW; ++p) h = run_apply(s_part[p][tid], h);
+    for (int p = 0; p < kParts<T>; ++p) h = run_apply(s_part[p][tid], h);
     s_entry[tid] = h;
     const float out = run_apply(total, h);
-    if (k0 + 1 < nC && k0 % kScanGroup == kScanGroup - 1)
-      publish(ws.exits + ((size_t)unit * ((nC + kScanGroup - 1) / kScanGroup) + k0 / kScanGroup) * C +
-                  tid,
-              word_of(0.f, out));
+    if (k0 + kWindow < nC)
+      publish(ws.exits + ((size_t)unit * nC + k0) * C + tid, word_of(0.f, out));
     if (d0 + tid < a.D) {
       if (a.states) a.states[(b * nC + k0) * a.D + d0 + tid] = h;
       if (a.h_last && k0 == nC - 1) a.h_last[b * a.D + d0 + tid] = out;
     }
   }
   __syncthreads();
-  if (nC > 1 && tid == 0) s_word = chain_count(ws, unit, nC) ? 1 : 0;
+  const bool final = nC > 1 && wave < kHeads<T> && chain_count<T>(ws, unit, nC);
 
 #pragma unroll
   for (int i = 0; i < kWords<T>; ++i) {
@@ -151,10 +149,7 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4) scan_kernel(ScanArgs a, Ch
   }
   const Rows<T> ry(a.y, row0 * a.ld_y + d0, a.ld_y, tok, cl);
   store_rows<T, kVec>(x, ry, full, nt, n);
-  if (nC > 1) {
-    __syncthreads();
-    if (s_word) chain_clear(ws, unit, nC);
-  }
+  if (nC > 1 && __syncthreads_or(final)) chain_clear<T>(ws, unit, nC);
 }
 
 // h_last of an empty sequence.
@@ -199,12 +194,12 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a, int64_t 
 template <typename T>
 hipError_t launch_scan_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
   constexpr size_t es = sizeof(T);
-  const int tiles = (int)scan_tiles(a.D);
+  const int tiles = (int)scan_tiles(a.D, kC<T>);
   const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
                    vec_rows(a.g, a.ld_g, es) && vec_rows(a.y, a.ld_y, es);
   const dim3 grid((unsigned)(a.B * tiles * a.nC));
 #define M3_SCAN_LAUNCH(G, VEC)                                                             \
-  hipLaunchKernelGGL((scan_kernel<T, G, VEC>), grid, dim3(kScanThreads<T>), 0, stream, a, ws, tiles)
+  hipLaunchKernelGGL((scan_kernel<T, G, VEC>), grid, dim3(kScanThreads), 0, stream, a, ws, tiles)
   if (a.g) {
     if (vec) M3_SCAN_LAUNCH(true, true);
     else M3_SCAN_LAUNCH(true, false);
@@ -239,23 +234,24 @@ hipError_t launch_step_t(const ScanStepArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t scan_tiles(int64_t D) { return (D + kC - 1) / kC; }
+int64_t scan_tiles(int64_t D, int tile) { return (D + tile - 1) / tile; }
+int scan_tile(m3_dtype dtype) { return dtype == M3_BF16 ? kC<bf16> : kC<float>; }
 
-size_t scan_workspace(int64_t B, int64_t D, int64_t nC) {
+size_t scan_workspace(int64_t B, int64_t D, int64_t nC, int tile) {
   if (nC <= 1) return 0;
-  const size_t units = (size_t)(B * scan_tiles(D)), nG = (nC + kScanGroup - 1) / kScanGroup;
-  return 256 + (units * 8 + 255) / 256 * 256 + units * (nC + nG) * kC * 8;
+  const size_t units = (size_t)(B * scan_tiles(D, tile));
+  return 256 + (units * 8 + 255) / 256 * 256 + units * nC * 2 * tile * 8;
 }
 
-ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC) {
+ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC, int tile) {
   ChainWs w = {};
   if (!workspace) return w;
-  const size_t units = (size_t)(B * scan_tiles(D));
+  const size_t units = (size_t)(B * scan_tiles(D, tile));
   unsigned char* p = static_cast<unsigned char*>(workspace);
   w.err = reinterpret_cast<int*>(p) + 1;
   w.counters = reinterpret_cast<int*>(p + 256);
   w.maps = reinterpret_cast<unsigned long long*>(p + 256 + (units * 8 + 255) / 256 * 256);
-  w.exits = w.maps + units * nC * kC;
+  w.exits = w.maps + units * nC * tile;
   return w;
 }
 
@@ -266,7 +262,7 @@ hipError_t launch_scan_empty(const float* h0, float* h_last, int64_t n, hipStrea
 }
 
 hipError_t launch_scan(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC);
+  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC, scan_tile(dtype));
   return dtype == M3_BF16 ? launch_scan_t<bf16>(a, ws, stream) : launch_scan_t<float>(a, ws, stream);
 }
 

@@ -13,25 +13,25 @@ namespace m3 {
 namespace {
 
 template <typename T, bool kGate, bool kVec>
-__global__ void __launch_bounds__(kScanThreads<T>, 4)
+__global__ void __launch_bounds__(kScanThreads, 4)
     scan_backward_kernel(ScanArgs a, ChainWs ws, int nTiles) {
-  constexpr int C = kC, W = kPerWord<T>, K = kTok<T>, NT = kScanThreads<T>, NW = kScanWaves<T>;
+  constexpr int C = kC<T>, W = kPerWord<T>, K = kTok<T>, NW = kScanWaves;
   __shared__ Run s_fore[NW][C];           // each wave's map of h, then the state entering it
   __shared__ Run s_back[NW][C];           // each wave's map of u, then the join of those behind
-  __shared__ Run s_run[kV][NT], s_behind[kV][NT];  // the joins before / behind a thread in its wave
-  __shared__ Run s_part[NW][C];  // the look-back's parts
+  __shared__ Run s_run[kV][kScanThreads], s_behind[kV][kScanThreads];  // the joins before / behind a thread in its wave
+  __shared__ Run s_part[kParts<T>][C];  // the look-back's parts
   __shared__ float s_entry[C];                    // the u entering the chunk from behind
   __shared__ int s_word;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nC = (int)a.nC;
-  const int units = (int)a.B * nTiles, unit = blockIdx.x % units;
+  const int units = (int)a.B * nTiles, unit = (blockIdx.x + blockIdx.x / units) % units;
   const int64_t b = unit / nTiles;
   const int d0 = unit % nTiles * C;
-  const int cl = (lane % kLanesAcross) * kV;
+  const int cl = (lane % kAcross<T>) * kV;
   const int n = (int)a.D - d0 - cl;
   const int k0 = nC > 1 ? chain_ticket(ws, unit, nC, &s_word) : 0;  // place in the chain
   if (k0 >= nC) return;
   const int c0 = nC - 1 - k0;                                       // the chunk
-  const int tok = (tid / kLanesAcross) * K;
+  const int tok = (tid / kAcross<T>) * K;
   const int nt = (int)(a.T - (int64_t)c0 * M3_SCAN_CHUNK) - tok;
   const int64_t row0 = b * a.T + (int64_t)c0 * M3_SCAN_CHUNK;
   const Rows<T> rf(a.f, row0 * a.ld_f + d0, a.ld_f, tok, cl), rx(a.x, row0 * a.ld_x + d0, a.ld_x, tok, cl);
@@ -78,12 +78,12 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
       const int v = i * W + e;
       Run o;
       u[e].A = r[e].A;
-      wave_join<false>(r[e], o);
+      wave_join<T, false>(r[e], o);
       s_run[v][tid] = o;
-      if (lane / kLanesAcross == 3) s_fore[wave][cl + v] = r[e];
-      wave_join<true>(u[e], o);
+      if (lane / kAcross<T> == kShare<T> - 1) s_fore[wave][cl + v] = r[e];
+      wave_join<T, true>(u[e], o);
       s_behind[v][tid] = o;
-      if (lane / kLanesAcross == 0) s_back[wave][cl + v] = u[e];
+      if (lane / kAcross<T> == 0) s_back[wave][cl + v] = u[e];
     }
   }
   renew(x);
@@ -99,10 +99,10 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
       s_back[w][tid] = total;
       total = run_join(total, m);
     }
-    if (k0 + 1 < nC && k0 % kScanGroup != kScanGroup - 1)
+    if (k0 + 1 < nC)
       publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
-  } else if (tid >= 64 && tid < 64 + C) {
-    const int c = tid - 64;
+  } else if (tid < 2 * C) {
+    const int c = tid - C;
     float h = d0 + c < a.D ? a.states[(b * nC + c0) * a.D + d0 + c] : 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -113,22 +113,20 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
   }
   const int ch = tid % C, part = tid / C;
   const float last = a.dh_last && d0 + ch < a.D ? a.dh_last[b * a.D + d0 + ch] : 0.f;
-  s_part[part][ch] = chain_part<NW>(ws, unit, nC, k0, part, ch, last);
+  s_part[part][ch] = chain_part<T>(ws, unit, nC, k0, part, ch, last);
   __syncthreads();
   if (tid < C) {
     float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < NW; ++p) v = run_apply(s_part[p][tid], v);
+    for (int p = 0; p < kParts<T>; ++p) v = run_apply(s_part[p][tid], v);
     s_entry[tid] = v;
     const float out = run_apply(total, v);
-    if (k0 + 1 < nC && k0 % kScanGroup == kScanGroup - 1)
-      publish(ws.exits + ((size_t)unit * ((nC + kScanGroup - 1) / kScanGroup) + k0 / kScanGroup) * C +
-                  tid,
-              word_of(0.f, out));
+    if (k0 + kWindow < nC)
+      publish(ws.exits + ((size_t)unit * nC + k0) * C + tid, word_of(0.f, out));
     if (a.dh0 && k0 == nC - 1 && d0 + tid < a.D) a.dh0[b * a.D + d0 + tid] = out;
   }
   __syncthreads();
-  if (nC > 1 && tid == 0) s_word = chain_count(ws, unit, nC) ? 1 : 0;
+  const bool final = nC > 1 && wave < kHeads<T> && chain_count<T>(ws, unit, nC);
 
 #pragma unroll
   for (int i = 0; i < kWords<T>; ++i) {
@@ -186,22 +184,19 @@ __global__ void __launch_bounds__(kScanThreads<T>, 4)
   store_rows<T, kVec>(x, wx, full, nt, n);
   store_rows<T, kVec>(dy, wf, full, nt, n);
   if constexpr (kGate) store_rows<T, kVec>(g, wg, full, nt, n);
-  if (nC > 1) {
-    __syncthreads();
-    if (s_word) chain_clear(ws, unit, nC);
-  }
+  if (nC > 1 && __syncthreads_or(final)) chain_clear<T>(ws, unit, nC);
 }
 
 template <typename T>
 hipError_t launch_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
   constexpr size_t es = sizeof(T);
-  const int tiles = (int)scan_tiles(a.D);
+  const int tiles = (int)scan_tiles(a.D, kC<T>);
   const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
                    vec_rows(a.g, a.ld_g, es) && vec_rows(a.dy, a.ld_y, es) && vec_rows(a.dx, a.ld_dx, es) &&
                    vec_rows(a.df, a.ld_df, es) && vec_rows(a.dg, a.ld_dg, es);
   const dim3 grid((unsigned)(a.B * tiles * a.nC));
 #define M3_SCAN_LAUNCH(G, VEC)                                                                   \
-  hipLaunchKernelGGL((scan_backward_kernel<T, G, VEC>), grid, dim3(kScanThreads<T>), 0, stream, a,  \
+  hipLaunchKernelGGL((scan_backward_kernel<T, G, VEC>), grid, dim3(kScanThreads), 0, stream, a,  \
                      ws, tiles)
   if (a.g) {
     if (vec) M3_SCAN_LAUNCH(true, true);
@@ -217,7 +212,7 @@ hipError_t launch_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_scan_backward(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC);
+  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC, scan_tile(dtype));
   return dtype == M3_BF16 ? launch_t<bf16>(a, ws, stream) : launch_t<float>(a, ws, stream);
 }
 

@@ -28,11 +28,12 @@ struct ScanArgs {
   void* workspace;         // the chain's counters and words; null with one chunk
 };
 struct ChainWs;            // scan_tile.h
-// Channel tiles of a row of D channels; the chain's workspace, its bytes (0
-// with one chunk) and its parts.
-int64_t scan_tiles(int64_t D);
-size_t scan_workspace(int64_t B, int64_t D, int64_t nC);
-ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC);
+// Channels of a tile, tiles of a row of D channels; the chain's workspace,
+// its bytes (0 with one chunk) and its parts.
+int scan_tile(m3_dtype dtype);
+int64_t scan_tiles(int64_t D, int tile);
+size_t scan_workspace(int64_t B, int64_t D, int64_t nC, int tile);
+ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC, int tile);
 // h_last of sequences without tokens (n states; zeros without h0).
 hipError_t launch_scan_empty(const float* h0, float* h_last, int64_t n, hipStream_t stream);
 hipError_t launch_scan(const ScanArgs& a, m3_dtype dtype, hipStream_t stream);

@@ -1,15 +1,17 @@
 // scan_tile.h -- what the gated recurrence's forward and backward kernels
 // share: the tile a workgroup owns and the chain between workgroups.
 //
-// A workgroup owns one chunk of 256 tokens of 64 channels: 16 lanes side by
-// side read whole lines of a token, 4 channels a lane, and each thread holds 8
-// (bfloat16, 512 threads) or 4 (float, 1024 threads) consecutive tokens of its
-// lane's channels in registers: 64 bytes of each array either way.  So each
-// input is read once and each output written once.  (8 channels a lane, in
-// 16-byte bfloat16 vectors, take 32 registers more for the maps and spill.)  A
-// thread's steps make one map h -> A h + B a channel; the maps of the 4
-// threads of a wave that share channels are joined by lane moves, those of the
-// waves in the LDS, those of the chunks through the workspace.
+// A workgroup of 512 threads owns one chunk of 128 tokens of 256 bytes of
+// channels (128 bfloat16, 64 float): lanes side by side read whole lines of a
+// token, 4 channels a lane, and each thread holds 8 (bfloat16) or 4 (float)
+// consecutive tokens of its lane's channels in registers: 64 bytes of each
+// array.  So each input is read once and each output written once.  (Tiles of
+// 128 bytes of channels and 256 tokens reach 4.1 TB/s where these reach 4.6;
+// 8 channels a lane, in 16-byte bfloat16 vectors, take 32 registers more for
+// the maps and spill.)  A thread's steps make one map h -> A h + B a channel;
+// the maps of the threads of a wave that share channels are joined by lane
+// moves, those of the waves in the LDS, those of the chunks through the
+// workspace.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -20,16 +22,24 @@
 namespace m3 {
 
 constexpr int kV = 4;                                   // channels a lane
-constexpr int kLanesAcross = 16;                        // lanes side by side in the channels
-constexpr int kC = kV * kLanesAcross;                   // channels of a tile
-constexpr int kScanGroup = 32;                          // chunks of a group (see the chain)
-static_assert(kC == kWave, "one wave joins a tile's channels");
+template <typename T>
+constexpr int kAcross = 64 / (int)sizeof(T);            // lanes side by side in the channels
+template <typename T>
+constexpr int kC = kV * kAcross<T>;                     // channels of a tile
+constexpr int kWindow = 8;                              // chunks a look-back spans (see the chain)
 template <typename T>
 constexpr int kTok = 16 / (int)sizeof(T);               // tokens a thread
+constexpr int kScanThreads = 512;
+constexpr int kScanWaves = kScanThreads / kWave;
+static_assert(kScanThreads / kAcross<bf16> * kTok<bf16> == M3_SCAN_CHUNK &&
+              kScanThreads / kAcross<float> * kTok<float> == M3_SCAN_CHUNK,
+              "a workgroup owns one chunk");
 template <typename T>
-constexpr int kScanThreads = M3_SCAN_CHUNK / kTok<T> * kLanesAcross;
+constexpr int kShare = kWave / kAcross<T>;              // threads of a wave that share a channel
 template <typename T>
-constexpr int kScanWaves = kScanThreads<T> / kWave;     // also the parts of a look-back
+constexpr int kParts = kScanThreads / kC<T>;            // threads that look back for one channel
+template <typename T>
+constexpr int kHeads = kC<T> / kWave;                   // waves that join a tile's channels
 
 // The kV channels of a lane as they are stored.  The kernels go through them
 // word by word, so that a word of an output takes the registers of an input's
@@ -147,22 +157,24 @@ struct Rows {
 // themselves: the high half is A with its sign bit set (A is never negative),
 // the low half B; an empty word is 0.  They are written and read by relaxed
 // device-scope atomics, and no order between words is needed.  A chunk
-// publishes its map as soon as it has it.  Chunks form groups of 32: a
-// chunk's entry is the state that left the group before (the last chunk of a
-// group publishes it as a word with A = 0) through the maps of its
-// predecessors in its group, joined in a fixed order, so results do not
-// depend on timing.  Counters and words are zero between calls: the unit's
-// last workgroup to finish looking back clears them.
+// publishes its map as soon as it has it, and the state that leaves it (a word
+// with A = 0) once it knows its entry.  Chunk k's entry is the state that left
+// chunk k - 8 through the maps of chunks k - 7 .. k - 1, joined in this order,
+// so that results do not depend on timing.  About as many chunks of a unit
+// run at once, so the state waited for is there by then; a window that slides
+// has no place where all have to wait for their neighbour's state, as groups
+// have at their borders.  Counters and words are zero between calls: the
+// unit's last workgroup to finish looking back clears them.
 //
 // Workspace, in 32-bit words: [0] unused, [1] error word (1: a wait ran out;
 // 2: the counters were not zero), then from byte 256 two counters a unit,
-// then (256-byte aligned) the 64-bit words: [unit][chunk][C] maps,
-// [unit][chunk / 32][C] states.
+// then (256-byte aligned) the 64-bit words: [unit][chunk][C] maps, then
+// [unit][chunk][C] states.
 struct ChainWs {
   int* err;
   int* counters;                 // [units][2]: ticket, finished
   unsigned long long* maps;      // [units][nC][C]
-  unsigned long long* exits;     // [units][nG][C]
+  unsigned long long* exits;     // [units][nC][C]
 };
 
 __device__ __forceinline__ unsigned long long word_of(float A, float B) {
@@ -248,78 +260,79 @@ __device__ __forceinline__ int chain_ticket(const ChainWs& ws, int unit, int nC,
   return __builtin_amdgcn_readfirstlane(*s_word);  // in a scalar register, as the addresses from it
 }
 
-// The maps of this channel's predecessors in the group that fall to this
-// part, joined; part 0 starts from the state that left the group before
-// (`start` for the first group).
-template <int kParts>
+// This part's share of the window of chunk k, joined: the state that left
+// chunk k - kWindow (`start` where there is none) and the maps behind it.
+template <typename T>
 __device__ __forceinline__ Run chain_part(const ChainWs& ws, int unit, int nC, int k, int part,
                                           int ch, float start) {
-  constexpr int C = kC, kPer = kScanGroup / kParts;
-  const int g0 = k / kScanGroup * kScanGroup, n = k - g0;
-  Run r = Run{1.f, 0.f};
-  unsigned long long w[kPer], exit = 0;
-  const unsigned long long* maps = ws.maps + ((size_t)unit * nC + g0) * C + ch;
-  const unsigned long long* from =
-      ws.exits + ((size_t)unit * ((nC + kScanGroup - 1) / kScanGroup) + k / kScanGroup) * C + ch;
+  constexpr int C = kC<T>, kPer = kWindow / kParts<T>;
+  const size_t base = ((size_t)unit * nC) * C + ch;
+  unsigned long long w[kPer];
+  const unsigned long long* from[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    w[j] = 0;
-    if (part * kPer + j < n) w[j] = peek(maps + (size_t)(part * kPer + j) * C);
+    const int i = part * kPer + j, c = k - kWindow + i;
+    from[j] = (i == 0 ? ws.exits : ws.maps) + base + (int64_t)(c < 0 ? 0 : c) * C;
+    w[j] = c >= 0 ? peek(from[j]) : 0;
   }
-  if (part == 0) {
-    r = Run{0.f, start};
-    if (g0 > 0) {
-      exit = peek(from - C);
-      if (exit == 0) exit = await(from - C, ws.err);
-      r = run_of(exit);
-    }
-  }
+  Run r = Run{1.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (part * kPer + j < n) {
-      if (w[j] == 0) w[j] = await(maps + (size_t)(part * kPer + j) * C, ws.err);
+  for (int j = 0; j < kPer; ++j) {
+    const int i = part * kPer + j, c = k - kWindow + i;
+    if (c >= 0) {
+      if (w[j] == 0) w[j] = await(from[j], ws.err);
       r = run_join(r, run_of(w[j]));
+    } else if (i == 0) {
+      r = Run{0.f, start};
     }
+  }
   return r;
 }
 
-// Counts this workgroup as done with the unit's words; thread 0 calls it after
-// a barrier behind the look-back, from the wave that published.  True for the
+// Counts this wave as done with the unit's words: each wave that publishes
+// (the first kHeads), after a barrier behind the look-back.  True in the
 // unit's last.
+template <typename T>
 __device__ __forceinline__ bool chain_count(const ChainWs& ws, int unit, int nC) {
   // what this wave published has arrived before the count does
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  return __hip_atomic_fetch_add(ws.counters + 2 * unit + 1, 1, __ATOMIC_RELAXED,
-                                __HIP_MEMORY_SCOPE_AGENT) == nC - 1;
+  int old = 0;
+  if ((threadIdx.x & 63) == 0)
+    old = __hip_atomic_fetch_add(ws.counters + 2 * unit + 1, 1, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_amdgcn_readfirstlane(old) == nC * kHeads<T> - 1;
 }
 // The unit's last workgroup leaves its counters and words zero.
+template <typename T>
 __device__ __forceinline__ void chain_clear(const ChainWs& ws, int unit, int nC) {
-  constexpr int C = kC;
-  const size_t nG = (nC + kScanGroup - 1) / kScanGroup;
-  for (size_t i = threadIdx.x; i < (size_t)nC * C; i += blockDim.x)
-    publish(ws.maps + (size_t)unit * nC * C + i, 0);
-  for (size_t i = threadIdx.x; i < nG * C; i += blockDim.x)
-    publish(ws.exits + (size_t)unit * nG * C + i, 0);
+  for (size_t i = threadIdx.x; i < (size_t)nC * kC<T>; i += kScanThreads) {
+    publish(ws.maps + (size_t)unit * nC * kC<T> + i, 0);
+    publish(ws.exits + (size_t)unit * nC * kC<T> + i, 0);
+  }
   if (threadIdx.x < 2)
     __hip_atomic_store(ws.counters + 2 * unit + threadIdx.x, 0, __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The thread maps of a wave joined over the 4 threads that share a channel
+// The thread maps of a wave joined over the threads that share a channel
 // (kBack: from the last token to the first): r becomes the join up to and
 // with this thread, `before` the join of those before it.
-template <bool kBack>
+template <typename T, bool kBack>
 __device__ __forceinline__ void wave_join(Run& r, Run& before) {
-  const int g = (threadIdx.x & 63) / kLanesAcross, place = kBack ? 3 - g : g;
+  constexpr int kStep = kAcross<T>;
+  const int g = (threadIdx.x & 63) / kStep, place = kBack ? kShare<T> - 1 - g : g;
 #pragma unroll
-  for (int s = 1; s < 4; s *= 2) {
+  for (int s = 1; s < kShare<T>; s *= 2) {
     Run o;
-    o.A = kBack ? __shfl_down(r.A, s * kLanesAcross, kWave) : __shfl_up(r.A, s * kLanesAcross, kWave);
-    o.B = kBack ? __shfl_down(r.B, s * kLanesAcross, kWave) : __shfl_up(r.B, s * kLanesAcross, kWave);
+    o.A = kBack ? __shfl_down(r.A, s * kStep, kWave) : __shfl_up(r.A, s * kStep, kWave);
+    o.B = kBack ? __shfl_down(r.B, s * kStep, kWave) : __shfl_up(r.B, s * kStep, kWave);
+    if (s == 1) before = o;
     if (place >= s) r = run_join(o, r);
   }
-  before.A = kBack ? __shfl_down(r.A, kLanesAcross, kWave) : __shfl_up(r.A, kLanesAcross, kWave);
-  before.B = kBack ? __shfl_down(r.B, kLanesAcross, kWave) : __shfl_up(r.B, kLanesAcross, kWave);
+  if constexpr (kShare<T> > 2) {
+    before.A = kBack ? __shfl_down(r.A, kStep, kWave) : __shfl_up(r.A, kStep, kWave);
+    before.B = kBack ? __shfl_down(r.B, kStep, kWave) : __shfl_up(r.B, kStep, kWave);
+  }
   if (place == 0) before = Run{1.f, 0.f};
 }
 
