@@ -105,6 +105,24 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, Chain
     if (k0 + 1 < nC)
       publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
   }
+  if constexpr (kGate) {
+    // the output gate goes into the maps while the neighbours publish theirs
+#pragma unroll
+    for (int i = 0; i < kWords<T>; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float gv[W];
+        unpack_word(g[k].w[i], gv);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float s = gv[e] * sigmoid_of(gv[e]);
+          A[k][i * W + e] *= s;
+          B[k][i * W + e] *= s;
+          renew(A[k][i * W + e]);
+          renew(B[k][i * W + e]);
+        }
+      }
+  }
   const int ch = tid % C, part = tid / C;
   const float h0 = a.h0 && d0 + ch < a.D ? a.h0[b * a.D + d0 + ch] : 0.f;
   s_part[part][ch] = chain_part<T>(ws, unit, nC, k0, part, ch, h0);
@@ -135,13 +153,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, Chain
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float gv[W], y[W];
-      if constexpr (kGate) unpack_word(g[k].w[i], gv);
+      float y[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         const float p = A[k][i * W + e];
         y[e] = __builtin_fmaf(p, masks && p == 0.f ? 0.f : h[e], B[k][i * W + e]);
-        if constexpr (kGate) y[e] *= gv[e] * sigmoid_of(gv[e]);
       }
       x[k].w[i] = pack_word(y);
       renew(x[k].w[i]);

@@ -134,17 +134,19 @@ __device__ __forceinline__ void renew(float (&z)[K][kV]) {
 }
 
 // A thread's rows of an array in the tile whose first element is at `first`:
-// row k at a 32-bit byte offset from a base that the workgroup shares
-// (M3_SCAN_CHUNK rows of an array span less than 4 GiB).
+// row k is k rows on from a base that the workgroup shares (scalar), plus a
+// 32-bit byte offset of the thread (M3_SCAN_CHUNK rows of an array span less
+// than 4 GiB).
 template <typename T>
 struct Rows {
   char* base;
-  uint32_t at, step;
+  int64_t step;
+  uint32_t at;
   __device__ __forceinline__ Rows(const void* p, int64_t first, int64_t ld, int tok, int cl)
       : base(static_cast<char*>(const_cast<void*>(p)) + first * (int64_t)sizeof(T)),
-        at((uint32_t)((tok * (uint32_t)ld + cl) * sizeof(T))),
-        step((uint32_t)(ld * sizeof(T))) {}
-  __device__ __forceinline__ void* operator[](int k) const { return base + (at + k * step); }
+        step(ld * (int64_t)sizeof(T)),
+        at((uint32_t)((tok * (uint32_t)ld + cl) * sizeof(T))) {}
+  __device__ __forceinline__ void* operator[](int k) const { return base + k * step + at; }
 };
 
 // ---- the chain -----------------------------------------------------------------
@@ -302,16 +304,19 @@ __device__ __forceinline__ bool chain_count(const ChainWs& ws, int unit, int nC)
                                  __HIP_MEMORY_SCOPE_AGENT);
   return __builtin_amdgcn_readfirstlane(old) == nC * kHeads<T> - 1;
 }
-// The unit's last workgroup leaves its counters and words zero.
+// The unit's last workgroup leaves its counters and words zero.  Nobody reads
+// them any more in this launch, so ordinary 16-byte stores do: they are out
+// by the end of the kernel.
 template <typename T>
 __device__ __forceinline__ void chain_clear(const ChainWs& ws, int unit, int nC) {
-  for (size_t i = threadIdx.x; i < (size_t)nC * kC<T>; i += kScanThreads) {
-    publish(ws.maps + (size_t)unit * nC * kC<T> + i, 0);
-    publish(ws.exits + (size_t)unit * nC * kC<T> + i, 0);
+  const size_t n = (size_t)nC * kC<T> / 2;  // 16-byte vectors
+  uint4* maps = reinterpret_cast<uint4*>(ws.maps) + unit * n;
+  uint4* exits = reinterpret_cast<uint4*>(ws.exits) + unit * n;
+  for (size_t i = threadIdx.x; i < n; i += kScanThreads) {
+    maps[i] = make_uint4(0u, 0u, 0u, 0u);
+    exits[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (threadIdx.x < 2)
-    __hip_atomic_store(ws.counters + 2 * unit + threadIdx.x, 0, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x < 2) ws.counters[2 * unit + threadIdx.x] = 0;
 }
 
 // The thread maps of a wave joined over the threads that share a channel
