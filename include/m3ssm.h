@@ -411,11 +411,11 @@ m3_status m3_block_postpass(const m3_dims* dims, m3_dtype dtype, const void* y,
  * m3_scan_dims, so that a slice of a wider projection is read in place.  T
  * (the type) is the storage type of dtype; states are float whatever it is:
  *   h0, h_last, dh_last, dh0   [batch, D]          float, dense
- *   states                     [batch, nC, D]      float, dense, nC = ceil(T / 128)
+ *   states                     [batch, nC, D]      float, dense, nC = ceil(T / 64)
  * `states` holds the state entering each chunk of M3_SCAN_CHUNK tokens (the
  * first is h0): what the backward pass needs besides the inputs.
  */
-#define M3_SCAN_CHUNK 128 /* tokens between two kept states */
+#define M3_SCAN_CHUNK 64 /* tokens between two kept states */
 
 typedef struct {
   int64_t batch;    /* sequences (>= 0) */
@@ -429,7 +429,7 @@ typedef struct {
 
 /*
  * Bytes of device workspace m3_gated_scan and m3_gated_scan_backward need (0:
- * none, as with up to 128 tokens, or an unsupported shape).  Host only.
+ * none, as with up to 64 tokens, or an unsupported shape).  Host only.
  *
  * The workspace (256-byte aligned) holds the counters and words by which the
  * chunks of a sequence hand on their states.  They are zero on entry and left

@@ -25,7 +25,7 @@ M3_F32 = 0
 M3_BF16 = 1
 M3_CODE_INT8 = 0
 M3_CODE_E4M3 = 1
-SCAN_CHUNK = 128
+SCAN_CHUNK = 64
 
 # every function declared in include/m3ssm.h
 ABI_SYMBOLS = ("m3_version", "m3_status_string", "m3_prefill_workspace_size", "m3_prefill",
@@ -629,10 +629,10 @@ def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool 
     tokens at one distance (a slice of a wider projection is read in place).
     h0 [B,D] float32 or None (zeros).  f = +inf passes the state on without
     looking at x (padding), f = -inf starts afresh (a packed document).
-    want_states keeps the state entering every 128 tokens, for the backward.
+    want_states keeps the state entering every 64 tokens, for the backward.
     A workspace (gated_scan_workspace_size bytes, zero-filled once) may be
     kept for later calls; calls that overlap need distinct ones.
-    Returns (y, h_last [B,D] float32, states [B,ceil(T/128),D] float32 or None).
+    Returns (y, h_last [B,D] float32, states [B,ceil(T/64),D] float32 or None).
     """
     import torch
     lib = _lib or load_library()

@@ -19,35 +19,37 @@ namespace m3 {
 namespace {
 
 template <typename T, bool kGate, bool kVec>
-__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, ChainWs ws, int nTiles) {
-  constexpr int C = kC<T>, W = kPerWord<T>, K = kTok<T>, NW = kScanWaves;
+__global__ void __launch_bounds__(ScanForward<T>::kThreads, 4) scan_kernel(ScanArgs a, ChainWs ws, int nTiles) {
+  typedef ScanForward<T> Cfg;
+  constexpr int C = Cfg::C, W = Cfg::kPerWord, K = Cfg::K, V = Cfg::V, NW = Cfg::kWaves;
   __shared__ Run s_wave[NW][C];           // each wave's map, then the join of those before
-  __shared__ Run s_run[kV][kScanThreads];                   // the join of the maps before a thread's in its wave
-  __shared__ Run s_part[kParts<T>][C];  // the look-back's parts
+  __shared__ Run s_run[V][Cfg::kThreads];                   // the join of the maps before a thread's in its wave
+  __shared__ Run s_part[Cfg::kParts][C];  // the look-back's parts
   __shared__ float s_entry[C];                    // the state entering the chunk
   __shared__ int s_word;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nC = (int)a.nC;
-  const int units = (int)a.B * nTiles, unit = (blockIdx.x + blockIdx.x / units) % units;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nP = (int)((a.T + Cfg::kTile - 1) / Cfg::kTile);
+  const int units = (int)a.B * nTiles, unit = chain_unit(units);
+  const size_t words = (size_t)unit * nP * C;     // of this unit
   const int64_t b = unit / nTiles;
   const int d0 = unit % nTiles * C;
-  const int cl = (lane % kAcross<T>) * kV;       // this lane's first channel in the tile
+  const int cl = (lane % Cfg::kAcross) * V;       // this lane's first channel in the tile
   const int n = (int)a.D - d0 - cl;               // channels from there to the row's end
-  const int k0 = nC > 1 ? chain_ticket(ws, unit, nC, &s_word) : 0;
-  if (k0 >= nC) return;
-  const int tok = (tid / kAcross<T>) * K;    // this thread's first token in the chunk
-  const int nt = (int)(a.T - (int64_t)k0 * M3_SCAN_CHUNK) - tok;  // tokens from there on
-  const int64_t row0 = b * a.T + (int64_t)k0 * M3_SCAN_CHUNK;
+  const int k0 = nP > 1 ? chain_ticket(ws, unit, nP, &s_word) : 0;
+  if (k0 >= nP) return;
+  const int tok = (tid / Cfg::kAcross) * K;    // this thread's first token in the chunk
+  const int nt = (int)(a.T - (int64_t)k0 * Cfg::kTile) - tok;  // tokens from there on
+  const int64_t row0 = b * a.T + (int64_t)k0 * Cfg::kTile;
   const Rows<T> rf(a.f, row0 * a.ld_f + d0, a.ld_f, tok, cl), rx(a.x, row0 * a.ld_x + d0, a.ld_x, tok, cl);
 
-  Pack<T> x[K], f[K], g[K];
-  const bool full = nt >= K && n >= kV;
-  load_rows<T, kVec>(f, rf, full, nt, n, kPassGate<T>);
-  load_rows<T, kVec>(x, rx, full, nt, n, 0u);
+  Pack<T, V> x[K], f[K], g[K];
+  const bool full = nt >= K && n >= V;
+  load_rows<kVec>(f, rf, full, nt, n, kPassGate<T>);
+  load_rows<kVec>(x, rx, full, nt, n, 0u);
   // per token the map from the state before the thread's first
-  float A[K][kV], B[K][kV];
+  float A[K][V], B[K][V];
   bool masks = false;  // in this wave
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) {
+  for (int i = 0; i < Cfg::kWords; ++i) {
     float z[K][W], least = 1.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -84,14 +86,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, Chain
       const int v = i * W + e;
       Run r = Run{A[K - 1][v], B[K - 1][v]}, before;
       if (!some) r.A = fmaxf(r.A, kLeastA);
-      wave_join<T, false>(r, before);
+      wave_join<Cfg, false>(r, before);
       s_run[v][tid] = before;
-      if (lane / kAcross<T> == kShare<T> - 1) s_wave[wave][cl + v] = r;
+      if (lane / Cfg::kAcross == Cfg::kShare - 1) s_wave[wave][cl + v] = r;
     }
   }
   if constexpr (kGate) {
     const Rows<T> rg(a.g, row0 * a.ld_g + d0, a.ld_g, tok, cl);
-    load_rows<T, kVec>(g, rg, full, nt, n, 0u);
+    load_rows<kVec>(g, rg, full, nt, n, 0u);
   }
   __syncthreads();
   Run total = Run{1.f, 0.f};
@@ -102,13 +104,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, Chain
       s_wave[w][tid] = total;
       total = run_join(total, m);
     }
-    if (k0 + 1 < nC)
-      publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
+    if (k0 + 1 < nP)
+      publish(ws.maps + words + (size_t)k0 * C + tid, word_of(total.A, total.B));
   }
   if constexpr (kGate) {
     // the output gate goes into the maps while the neighbours publish theirs
 #pragma unroll
-    for (int i = 0; i < kWords<T>; ++i)
+    for (int i = 0; i < Cfg::kWords; ++i)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float gv[W];
@@ -125,26 +127,39 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, Chain
   }
   const int ch = tid % C, part = tid / C;
   const float h0 = a.h0 && d0 + ch < a.D ? a.h0[b * a.D + d0 + ch] : 0.f;
-  s_part[part][ch] = chain_part<T>(ws, unit, nC, k0, part, ch, h0);
+  if (wave == NW - 1) chain_passed(ws, words, C, k0);
+  s_part[part][ch] = chain_part<Cfg>(ws, words, k0, part, ch, h0);
   __syncthreads();
   if (tid < C) {
     float h = 0.f;
 #pragma unroll
-    for (int p = 0; p < kParts<T>; ++p) h = run_apply(s_part[p][tid], h);
+    for (int p = 0; p < Cfg::kParts; ++p) h = run_apply(s_part[p][tid], h);
     s_entry[tid] = h;
     const float out = run_apply(total, h);
-    if (k0 + kWindow < nC)
-      publish(ws.exits + ((size_t)unit * nC + k0) * C + tid, word_of(0.f, out));
+    if (k0 + kWindow < nP)
+      publish(ws.exits + words + (size_t)k0 * C + tid, word_of(0.f, out));
     if (d0 + tid < a.D) {
-      if (a.states) a.states[(b * nC + k0) * a.D + d0 + tid] = h;
-      if (a.h_last && k0 == nC - 1) a.h_last[b * a.D + d0 + tid] = out;
+      if (a.states) {
+        // one state a chunk: that before the chunk's first wave
+        constexpr int kPerTile = Cfg::kTile / M3_SCAN_CHUNK, kStep = NW / kPerTile;
+#pragma unroll
+        for (int j = 0; j < kPerTile; ++j) {
+          const int64_t c = (int64_t)k0 * kPerTile + j;
+          if (c < a.nC) a.states[(b * a.nC + c) * a.D + d0 + tid] = run_apply(s_wave[j * kStep][tid], h);
+        }
+      }
+      if (a.h_last && k0 == nP - 1) a.h_last[b * a.D + d0 + tid] = out;
     }
   }
   __syncthreads();
-  const bool final = nC > 1 && wave < kHeads<T> && chain_count<T>(ws, unit, nC);
+  bool final = false;
+  if (nP > 1) {
+    chain_clear<Cfg>(ws, words, k0);
+    final = wave < Cfg::kHeads && chain_count<Cfg>(ws, unit, nP);
+  }
 
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) {
+  for (int i = 0; i < Cfg::kWords; ++i) {
     float h[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) {
@@ -164,8 +179,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(ScanArgs a, Chain
     }
   }
   const Rows<T> ry(a.y, row0 * a.ld_y + d0, a.ld_y, tok, cl);
-  store_rows<T, kVec>(x, ry, full, nt, n);
-  if (nC > 1 && __syncthreads_or(final)) chain_clear<T>(ws, unit, nC);
+  store_rows<kVec>(x, ry, full, nt, n);
+  if (nP > 1 && __syncthreads_or(final)) chain_clear_rest<Cfg>(ws, words, unit, nP);
 }
 
 // h_last of an empty sequence.
@@ -174,21 +189,21 @@ __global__ void __launch_bounds__(256) scan_empty_kernel(const float* h0, float*
   if (i < n) h_last[i] = h0 ? h0[i] : 0.f;
 }
 
-// One token: a lane takes V channels of a sequence.
+// One token: a lane takes 4 channels of a sequence.
 template <typename T, bool kGate, bool kVec>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a, int64_t packs) {
-  constexpr int W = kPerWord<T>;
+  constexpr int W = 4 / (int)sizeof(T), V = 4;
   const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (j >= a.B * packs) return;
-  const int64_t b = j / packs, d = j % packs * kV;
+  const int64_t b = j / packs, d = j % packs * V;
   const int n = (int)(a.D - d);
-  Pack<T> g;
-  const Pack<T> f = load_pack<T, kVec>(static_cast<const T*>(a.f) + b * a.ld_f + d, n);
-  Pack<T> x = load_pack<T, kVec>(static_cast<const T*>(a.x) + b * a.ld_x + d, n);
-  if constexpr (kGate) g = load_pack<T, kVec>(static_cast<const T*>(a.g) + b * a.ld_g + d, n);
-  Pack<float> h = load_pack<float, kVec>(a.h_in + b * a.D + d, n);
+  Pack<T, V> g;
+  const Pack<T, V> f = load_pack<T, V, kVec>(static_cast<const T*>(a.f) + b * a.ld_f + d, n);
+  Pack<T, V> x = load_pack<T, V, kVec>(static_cast<const T*>(a.x) + b * a.ld_x + d, n);
+  if constexpr (kGate) g = load_pack<T, V, kVec>(static_cast<const T*>(a.g) + b * a.ld_g + d, n);
+  Pack<float, V> h = load_pack<float, V, kVec>(a.h_in + b * a.D + d, n);
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) {
+  for (int i = 0; i < f.kWords; ++i) {
     float xv[W], fv[W], gv[W], y[W];
     unpack_word(x.w[i], xv);
     unpack_word(f.w[i], fv);
@@ -202,20 +217,22 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a, int64_t 
     }
     x.w[i] = pack_word(y);
   }
-  store_pack<float, kVec>(a.h_out + b * a.D + d, n, h);
-  store_pack<T, kVec>(static_cast<T*>(a.y) + b * a.ld_y + d, n, x);
+  store_pack<float, V, kVec>(a.h_out + b * a.D + d, n, h);
+  store_pack<T, V, kVec>(static_cast<T*>(a.y) + b * a.ld_y + d, n, x);
 }
 
 
 template <typename T>
 hipError_t launch_scan_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
+  typedef ScanForward<T> Cfg;
   constexpr size_t es = sizeof(T);
-  const int tiles = (int)scan_tiles(a.D, kC<T>);
-  const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
-                   vec_rows(a.g, a.ld_g, es) && vec_rows(a.y, a.ld_y, es);
-  const dim3 grid((unsigned)(a.B * tiles * a.nC));
+  constexpr int V = Cfg::V;
+  const int tiles = (int)scan_tiles(a.D, (int)es);
+  const bool vec = a.D % V == 0 && vec_rows(a.x, a.ld_x, es, V) && vec_rows(a.f, a.ld_f, es, V) &&
+                   vec_rows(a.g, a.ld_g, es, V) && vec_rows(a.y, a.ld_y, es, V);
+  const dim3 grid((unsigned)(a.B * tiles * ((a.T + Cfg::kTile - 1) / Cfg::kTile)));
 #define M3_SCAN_LAUNCH(G, VEC)                                                             \
-  hipLaunchKernelGGL((scan_kernel<T, G, VEC>), grid, dim3(kScanThreads), 0, stream, a, ws, tiles)
+  hipLaunchKernelGGL((scan_kernel<T, G, VEC>), grid, dim3(Cfg::kThreads), 0, stream, a, ws, tiles)
   if (a.g) {
     if (vec) M3_SCAN_LAUNCH(true, true);
     else M3_SCAN_LAUNCH(true, false);
@@ -230,10 +247,10 @@ hipError_t launch_scan_t(const ScanArgs& a, const ChainWs& ws, hipStream_t strea
 template <typename T>
 hipError_t launch_step_t(const ScanStepArgs& a, hipStream_t stream) {
   constexpr size_t es = sizeof(T);
-  const int64_t packs = (a.D + kV - 1) / kV;
-  const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
-                   vec_rows(a.g, a.ld_g, es) && vec_rows(a.y, a.ld_y, es) && vec_rows(a.h_in, a.D, 4) &&
-                   vec_rows(a.h_out, a.D, 4);
+  const int64_t packs = (a.D + 3) / 4;
+  const bool vec = a.D % 4 == 0 && vec_rows(a.x, a.ld_x, es, 4) && vec_rows(a.f, a.ld_f, es, 4) &&
+                   vec_rows(a.g, a.ld_g, es, 4) && vec_rows(a.y, a.ld_y, es, 4) && vec_rows(a.h_in, a.D, 4, 4) &&
+                   vec_rows(a.h_out, a.D, 4, 4);
   const dim3 grid((unsigned)((a.B * packs + 255) / 256));
 #define M3_STEP_LAUNCH(G, VEC) \
   hipLaunchKernelGGL((scan_step_kernel<T, G, VEC>), grid, dim3(256), 0, stream, a, packs)
@@ -250,24 +267,29 @@ hipError_t launch_step_t(const ScanStepArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t scan_tiles(int64_t D, int tile) { return (D + tile - 1) / tile; }
-int scan_tile(m3_dtype dtype) { return dtype == M3_BF16 ? kC<bf16> : kC<float>; }
+namespace {
+// Counters (rounded up), then the words' count.
+size_t chain_head(size_t units) { return 256 + (units * 8 + 255) / 256 * 256; }
+size_t chain_words(size_t units, int64_t T, int tile, int esize) {
+  return units * (size_t)((T + tile - 1) / tile) * (kScanTileBytes / esize);
+}
+}  // namespace
 
-size_t scan_workspace(int64_t B, int64_t D, int64_t nC, int tile) {
-  if (nC <= 1) return 0;
-  const size_t units = (size_t)(B * scan_tiles(D, tile));
-  return 256 + (units * 8 + 255) / 256 * 256 + units * nC * 2 * tile * 8;
+size_t scan_workspace(int64_t B, int64_t T, int64_t D, int tile, int esize) {
+  if (T <= tile) return 0;
+  const size_t units = (size_t)(B * scan_tiles(D, esize));
+  return chain_head(units) + 2 * 8 * chain_words(units, T, tile, esize);
 }
 
-ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC, int tile) {
+ChainWs scan_chain(void* workspace, int64_t B, int64_t T, int64_t D, int tile, int esize) {
   ChainWs w = {};
-  if (!workspace) return w;
-  const size_t units = (size_t)(B * scan_tiles(D, tile));
+  if (!workspace || T <= tile) return w;
+  const size_t units = (size_t)(B * scan_tiles(D, esize));
   unsigned char* p = static_cast<unsigned char*>(workspace);
   w.err = reinterpret_cast<int*>(p) + 1;
   w.counters = reinterpret_cast<int*>(p + 256);
-  w.maps = reinterpret_cast<unsigned long long*>(p + 256 + (units * 8 + 255) / 256 * 256);
-  w.exits = w.maps + units * nC * tile;
+  w.maps = reinterpret_cast<unsigned long long*>(p + chain_head(units));
+  w.exits = w.maps + chain_words(units, T, tile, esize);
   return w;
 }
 
@@ -278,7 +300,7 @@ hipError_t launch_scan_empty(const float* h0, float* h_last, int64_t n, hipStrea
 }
 
 hipError_t launch_scan(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC, scan_tile(dtype));
+  const ChainWs ws = scan_chain(a.workspace, a.B, a.T, a.D, kScanForwardTile, dtype == M3_BF16 ? 2 : 4);
   return dtype == M3_BF16 ? launch_scan_t<bf16>(a, ws, stream) : launch_scan_t<float>(a, ws, stream);
 }
 

@@ -13,39 +13,41 @@ namespace m3 {
 namespace {
 
 template <typename T, bool kGate, bool kVec>
-__global__ void __launch_bounds__(kScanThreads, 4)
+__global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
     scan_backward_kernel(ScanArgs a, ChainWs ws, int nTiles) {
-  constexpr int C = kC<T>, W = kPerWord<T>, K = kTok<T>, NW = kScanWaves;
+  typedef ScanBackward<T> Cfg;
+  constexpr int C = Cfg::C, W = Cfg::kPerWord, K = Cfg::K, V = Cfg::V, NW = Cfg::kWaves;
   __shared__ Run s_fore[NW][C];           // each wave's map of h, then the state entering it
   __shared__ Run s_back[NW][C];           // each wave's map of u, then the join of those behind
-  __shared__ Run s_run[kV][kScanThreads], s_behind[kV][kScanThreads];  // the joins before / behind a thread in its wave
-  __shared__ Run s_part[kParts<T>][C];  // the look-back's parts
+  __shared__ Run s_run[V][Cfg::kThreads], s_behind[V][Cfg::kThreads];  // the joins before / behind a thread in its wave
+  __shared__ Run s_part[Cfg::kParts][C];  // the look-back's parts
   __shared__ float s_entry[C];                    // the u entering the chunk from behind
   __shared__ int s_word;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nC = (int)a.nC;
-  const int units = (int)a.B * nTiles, unit = (blockIdx.x + blockIdx.x / units) % units;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nP = (int)((a.T + Cfg::kTile - 1) / Cfg::kTile);
+  const int units = (int)a.B * nTiles, unit = chain_unit(units);
+  const size_t words = (size_t)unit * nP * C;     // of this unit
   const int64_t b = unit / nTiles;
   const int d0 = unit % nTiles * C;
-  const int cl = (lane % kAcross<T>) * kV;
+  const int cl = (lane % Cfg::kAcross) * V;
   const int n = (int)a.D - d0 - cl;
-  const int k0 = nC > 1 ? chain_ticket(ws, unit, nC, &s_word) : 0;  // place in the chain
-  if (k0 >= nC) return;
-  const int c0 = nC - 1 - k0;                                       // the chunk
-  const int tok = (tid / kAcross<T>) * K;
-  const int nt = (int)(a.T - (int64_t)c0 * M3_SCAN_CHUNK) - tok;
-  const int64_t row0 = b * a.T + (int64_t)c0 * M3_SCAN_CHUNK;
+  const int k0 = nP > 1 ? chain_ticket(ws, unit, nP, &s_word) : 0;  // place in the chain
+  if (k0 >= nP) return;
+  const int c0 = nP - 1 - k0;                                       // the chunk
+  const int tok = (tid / Cfg::kAcross) * K;
+  const int nt = (int)(a.T - (int64_t)c0 * Cfg::kTile) - tok;
+  const int64_t row0 = b * a.T + (int64_t)c0 * Cfg::kTile;
   const Rows<T> rf(a.f, row0 * a.ld_f + d0, a.ld_f, tok, cl), rx(a.x, row0 * a.ld_x + d0, a.ld_x, tok, cl);
   const Rows<T> rd(a.dy, row0 * a.ld_y + d0, a.ld_y, tok, cl), rg(a.g, row0 * a.ld_g + d0, a.ld_g, tok, cl);
 
-  Pack<T> x[K], f[K], dy[K], g[K];
-  const bool full = nt >= K && n >= kV;
-  load_rows<T, kVec>(f, rf, full, nt, n, kPassGate<T>);
-  load_rows<T, kVec>(x, rx, full, nt, n, 0u);
-  load_rows<T, kVec>(dy, rd, full, nt, n, 0u);
-  if constexpr (kGate) load_rows<T, kVec>(g, rg, full, nt, n, 0u);
-  float z[K][kV];
+  Pack<T, V> x[K], f[K], dy[K], g[K];
+  const bool full = nt >= K && n >= V;
+  load_rows<kVec>(f, rf, full, nt, n, kPassGate<T>);
+  load_rows<kVec>(x, rx, full, nt, n, 0u);
+  load_rows<kVec>(dy, rd, full, nt, n, 0u);
+  if constexpr (kGate) load_rows<kVec>(g, rg, full, nt, n, 0u);
+  float z[K][V];
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) {
+  for (int i = 0; i < Cfg::kWords; ++i) {
     Run r[W], u[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) r[e] = u[e] = Run{1.f, 0.f};
@@ -78,12 +80,12 @@ __global__ void __launch_bounds__(kScanThreads, 4)
       const int v = i * W + e;
       Run o;
       u[e].A = r[e].A;
-      wave_join<T, false>(r[e], o);
+      wave_join<Cfg, false>(r[e], o);
       s_run[v][tid] = o;
-      if (lane / kAcross<T> == kShare<T> - 1) s_fore[wave][cl + v] = r[e];
-      wave_join<T, true>(u[e], o);
+      if (lane / Cfg::kAcross == Cfg::kShare - 1) s_fore[wave][cl + v] = r[e];
+      wave_join<Cfg, true>(u[e], o);
       s_behind[v][tid] = o;
-      if (lane / kAcross<T> == 0) s_back[wave][cl + v] = u[e];
+      if (lane / Cfg::kAcross == 0) s_back[wave][cl + v] = u[e];
     }
   }
   renew(x);
@@ -99,11 +101,11 @@ __global__ void __launch_bounds__(kScanThreads, 4)
       s_back[w][tid] = total;
       total = run_join(total, m);
     }
-    if (k0 + 1 < nC)
-      publish(ws.maps + ((size_t)unit * nC + k0) * C + tid, word_of(total.A, total.B));
+    if (k0 + 1 < nP)
+      publish(ws.maps + words + (size_t)k0 * C + tid, word_of(total.A, total.B));
   } else if (tid < 2 * C) {
     const int c = tid - C;
-    float h = d0 + c < a.D ? a.states[(b * nC + c0) * a.D + d0 + c] : 0.f;
+    float h = d0 + c < a.D ? a.states[(b * nP + c0) * a.D + d0 + c] : 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const Run m = s_fore[w][c];
@@ -113,23 +115,28 @@ __global__ void __launch_bounds__(kScanThreads, 4)
   }
   const int ch = tid % C, part = tid / C;
   const float last = a.dh_last && d0 + ch < a.D ? a.dh_last[b * a.D + d0 + ch] : 0.f;
-  s_part[part][ch] = chain_part<T>(ws, unit, nC, k0, part, ch, last);
+  if (wave == NW - 1) chain_passed(ws, words, C, k0);
+  s_part[part][ch] = chain_part<Cfg>(ws, words, k0, part, ch, last);
   __syncthreads();
   if (tid < C) {
     float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < kParts<T>; ++p) v = run_apply(s_part[p][tid], v);
+    for (int p = 0; p < Cfg::kParts; ++p) v = run_apply(s_part[p][tid], v);
     s_entry[tid] = v;
     const float out = run_apply(total, v);
-    if (k0 + kWindow < nC)
-      publish(ws.exits + ((size_t)unit * nC + k0) * C + tid, word_of(0.f, out));
-    if (a.dh0 && k0 == nC - 1 && d0 + tid < a.D) a.dh0[b * a.D + d0 + tid] = out;
+    if (k0 + kWindow < nP)
+      publish(ws.exits + words + (size_t)k0 * C + tid, word_of(0.f, out));
+    if (a.dh0 && k0 == nP - 1 && d0 + tid < a.D) a.dh0[b * a.D + d0 + tid] = out;
   }
   __syncthreads();
-  const bool final = nC > 1 && wave < kHeads<T> && chain_count<T>(ws, unit, nC);
+  bool final = false;
+  if (nP > 1) {
+    chain_clear<Cfg>(ws, words, k0);
+    final = wave < Cfg::kHeads && chain_count<Cfg>(ws, unit, nP);
+  }
 
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) {
+  for (int i = 0; i < Cfg::kWords; ++i) {
     float h[K][W], hk[W], u[W];  // the state before each token; u from behind
 #pragma unroll
     for (int e = 0; e < W; ++e) {
@@ -181,22 +188,24 @@ __global__ void __launch_bounds__(kScanThreads, 4)
   }
   const Rows<T> wx(a.dx, row0 * a.ld_dx + d0, a.ld_dx, tok, cl), wf(a.df, row0 * a.ld_df + d0, a.ld_df, tok, cl);
   const Rows<T> wg(a.dg, row0 * a.ld_dg + d0, a.ld_dg, tok, cl);
-  store_rows<T, kVec>(x, wx, full, nt, n);
-  store_rows<T, kVec>(dy, wf, full, nt, n);
-  if constexpr (kGate) store_rows<T, kVec>(g, wg, full, nt, n);
-  if (nC > 1 && __syncthreads_or(final)) chain_clear<T>(ws, unit, nC);
+  store_rows<kVec>(x, wx, full, nt, n);
+  store_rows<kVec>(dy, wf, full, nt, n);
+  if constexpr (kGate) store_rows<kVec>(g, wg, full, nt, n);
+  if (nP > 1 && __syncthreads_or(final)) chain_clear_rest<Cfg>(ws, words, unit, nP);
 }
 
 template <typename T>
 hipError_t launch_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
+  typedef ScanBackward<T> Cfg;
   constexpr size_t es = sizeof(T);
-  const int tiles = (int)scan_tiles(a.D, kC<T>);
-  const bool vec = a.D % kV == 0 && vec_rows(a.x, a.ld_x, es) && vec_rows(a.f, a.ld_f, es) &&
-                   vec_rows(a.g, a.ld_g, es) && vec_rows(a.dy, a.ld_y, es) && vec_rows(a.dx, a.ld_dx, es) &&
-                   vec_rows(a.df, a.ld_df, es) && vec_rows(a.dg, a.ld_dg, es);
-  const dim3 grid((unsigned)(a.B * tiles * a.nC));
+  constexpr int V = Cfg::V;
+  const int tiles = (int)scan_tiles(a.D, (int)es);
+  const bool vec = a.D % V == 0 && vec_rows(a.x, a.ld_x, es, V) && vec_rows(a.f, a.ld_f, es, V) &&
+                   vec_rows(a.g, a.ld_g, es, V) && vec_rows(a.dy, a.ld_y, es, V) && vec_rows(a.dx, a.ld_dx, es, V) &&
+                   vec_rows(a.df, a.ld_df, es, V) && vec_rows(a.dg, a.ld_dg, es, V);
+  const dim3 grid((unsigned)(a.B * tiles * ((a.T + Cfg::kTile - 1) / Cfg::kTile)));
 #define M3_SCAN_LAUNCH(G, VEC)                                                                   \
-  hipLaunchKernelGGL((scan_backward_kernel<T, G, VEC>), grid, dim3(kScanThreads), 0, stream, a,  \
+  hipLaunchKernelGGL((scan_backward_kernel<T, G, VEC>), grid, dim3(Cfg::kThreads), 0, stream, a,  \
                      ws, tiles)
   if (a.g) {
     if (vec) M3_SCAN_LAUNCH(true, true);
@@ -212,7 +221,7 @@ hipError_t launch_t(const ScanArgs& a, const ChainWs& ws, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_scan_backward(const ScanArgs& a, m3_dtype dtype, hipStream_t stream) {
-  const ChainWs ws = scan_chain(a.workspace, a.B, a.D, a.nC, scan_tile(dtype));
+  const ChainWs ws = scan_chain(a.workspace, a.B, a.T, a.D, kScanBackwardTile, dtype == M3_BF16 ? 2 : 4);
   return dtype == M3_BF16 ? launch_t<bf16>(a, ws, stream) : launch_t<float>(a, ws, stream);
 }
 

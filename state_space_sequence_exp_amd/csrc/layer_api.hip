@@ -56,7 +56,7 @@ m3_status check_scan(const m3_scan_dims* d, bool backward) {
   // one workgroup a chunk and channel tile; 64-bit words for each in the
   // workspace
   if (d->batch > INT_MAX || d->channels > INT_MAX / 2 || d->seqlen > INT_MAX - M3_SCAN_CHUNK ||
-      (double)d->batch * (double)m3::scan_tiles(d->channels, m3::scan_tile(M3_F32)) *
+      (double)d->batch * (double)m3::scan_tiles(d->channels, 4) *
               (double)(d->seqlen / M3_SCAN_CHUNK + 1) > 2147483647.0)
     return M3_ERR_NOT_SUPPORTED;
   return M3_SUCCESS;
@@ -99,9 +99,9 @@ extern "C" {
 
 size_t m3_gated_scan_workspace_size(const m3_scan_dims* dims, m3_dtype dtype) {
   if (!dtype_ok(&dtype) || check_scan(dims, false) != M3_SUCCESS) return 0;
-  return m3::scan_workspace(dims->batch, dims->channels,
-                            (dims->seqlen + M3_SCAN_CHUNK - 1) / M3_SCAN_CHUNK,
-                            m3::scan_tile(dtype));
+  // the backward pass has the smaller tiles
+  return m3::scan_workspace(dims->batch, dims->seqlen, dims->channels, m3::kScanBackwardTile,
+                            (int)esize_of(dtype));
 }
 
 m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x, const void* f,
@@ -130,7 +130,7 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
   a.y = y;
   a.h_last = h_last;
   a.states = states;
-  a.workspace = a.nC > 1 ? workspace : nullptr;
+  a.workspace = workspace;
   return done(m3::launch_scan(a, dtype, s));
 }
 
@@ -167,7 +167,7 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
   a.df = df;
   a.dg = dg;
   a.dh0 = dh0;
-  a.workspace = a.nC > 1 ? workspace : nullptr;
+  a.workspace = workspace;
   return done(m3::launch_scan_backward(a, dtype, s));
 }
 

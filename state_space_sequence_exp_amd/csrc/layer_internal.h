@@ -25,15 +25,19 @@ struct ScanArgs {
   const float* dh_last;    // may be null
   void *dx, *df, *dg;
   float* dh0;              // may be null
-  void* workspace;         // the chain's counters and words; null with one chunk
+  void* workspace;         // the chain's counters and words; null where none is needed
 };
 struct ChainWs;            // scan_tile.h
-// Channels of a tile, tiles of a row of D channels; the chain's workspace,
-// its bytes (0 with one chunk) and its parts.
-int scan_tile(m3_dtype dtype);
-int64_t scan_tiles(int64_t D, int tile);
-size_t scan_workspace(int64_t B, int64_t D, int64_t nC, int tile);
-ChainWs scan_chain(void* workspace, int64_t B, int64_t D, int64_t nC, int tile);
+// A workgroup's tile: tokens (forward, backward) x bytes of channels.
+constexpr int kScanForwardTile = 128, kScanBackwardTile = M3_SCAN_CHUNK, kScanTileBytes = 256;
+static_assert(kScanForwardTile % M3_SCAN_CHUNK == 0, "a tile holds whole chunks");
+inline int64_t scan_tiles(int64_t D, int esize) {
+  return (D + kScanTileBytes / esize - 1) / (kScanTileBytes / esize);
+}
+// The chain's workspace: its bytes (0 with one tile) and its parts, for tiles
+// of `tile` tokens.
+size_t scan_workspace(int64_t B, int64_t T, int64_t D, int tile, int esize);
+ChainWs scan_chain(void* workspace, int64_t B, int64_t T, int64_t D, int tile, int esize);
 // h_last of sequences without tokens (n states; zeros without h0).
 hipError_t launch_scan_empty(const float* h0, float* h_last, int64_t n, hipStream_t stream);
 hipError_t launch_scan(const ScanArgs& a, m3_dtype dtype, hipStream_t stream);

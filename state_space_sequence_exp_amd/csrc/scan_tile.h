@@ -1,17 +1,21 @@
 // scan_tile.h -- what the gated recurrence's forward and backward kernels
 // share: the tile a workgroup owns and the chain between workgroups.
 //
-// A workgroup of 512 threads owns one chunk of 128 tokens of 256 bytes of
-// channels (128 bfloat16, 64 float): lanes side by side read whole lines of a
-// token, 4 channels a lane, and each thread holds 8 (bfloat16) or 4 (float)
-// consecutive tokens of its lane's channels in registers: 64 bytes of each
-// array.  So each input is read once and each output written once.  (Tiles of
-// 128 bytes of channels and 256 tokens reach 4.1 TB/s where these reach 4.6;
-// 8 channels a lane, in 16-byte bfloat16 vectors, take 32 registers more for
-// the maps and spill.)  A thread's steps make one map h -> A h + B a channel;
-// the maps of the threads of a wave that share channels are joined by lane
-// moves, those of the waves in the LDS, those of the chunks through the
-// workspace.
+// A workgroup owns some tokens of 256 bytes of channels (128 bfloat16, 64
+// float): lanes side by side read whole lines of a token, V channels a lane,
+// and each thread holds K consecutive tokens of its lane's channels in
+// registers, so each input is read once and each output written once.  A
+// thread's steps make one map h -> A h + B a channel; the maps of the threads
+// of a wave that share channels are joined by lane moves, those of the waves
+// in the LDS, those of the tiles through the workspace.
+//
+// The kernels are bound by memory, and by how many of a compute unit's waves
+// the registers let run.  Measured on B1 T16384 and B4 T2048, D4096, bfloat16
+// with the output gate: tiles of 128 bytes of channels reach 4.1 TB/s where
+// these reach 4.7; the forward pass with V = 2 and 64 tokens runs three
+// workgroups a unit instead of two and is no faster (142 against 123 us), as a
+// long sequence then has twice the tiles to chain; the backward pass with V =
+// 4 and 128 tokens fills its registers and runs two (126 against 116 us).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,36 +25,42 @@
 
 namespace m3 {
 
-constexpr int kV = 4;                                   // channels a lane
+template <typename T_, int V_, int K_, int kTile_>
+struct ScanCfg {
+  typedef T_ T;
+  static constexpr int V = V_;                                // channels a lane
+  static constexpr int K = K_;                                // tokens a thread
+  static constexpr int kTile = kTile_;                        // tokens a workgroup
+  static constexpr int C = kScanTileBytes / (int)sizeof(T);   // channels of a tile
+  static constexpr int kAcross = C / V;                       // lanes side by side in the channels
+  static constexpr int kThreads = kTile / K * kAcross;
+  static constexpr int kWaves = kThreads / kWave;
+  static constexpr int kShare = kWave / kAcross;              // threads of a wave that share a channel
+  static constexpr int kParts = kThreads / C;                 // threads that look back for one channel
+  static constexpr int kHeads = C / kWave;                    // waves that join a tile's channels
+  static constexpr int kPerWord = 4 / (int)sizeof(T);         // channels of a word
+  static constexpr int kWords = V / kPerWord;                 // words of a lane's channels
+};
 template <typename T>
-constexpr int kAcross = 64 / (int)sizeof(T);            // lanes side by side in the channels
+struct ScanForward;
+template <>
+struct ScanForward<bf16> : ScanCfg<bf16, 4, 8, kScanForwardTile> {};
+template <>
+struct ScanForward<float> : ScanCfg<float, 4, 4, kScanForwardTile> {};
 template <typename T>
-constexpr int kC = kV * kAcross<T>;                     // channels of a tile
-constexpr int kWindow = 8;                              // chunks a look-back spans (see the chain)
-template <typename T>
-constexpr int kTok = 16 / (int)sizeof(T);               // tokens a thread
-constexpr int kScanThreads = 512;
-constexpr int kScanWaves = kScanThreads / kWave;
-static_assert(kScanThreads / kAcross<bf16> * kTok<bf16> == M3_SCAN_CHUNK &&
-              kScanThreads / kAcross<float> * kTok<float> == M3_SCAN_CHUNK,
-              "a workgroup owns one chunk");
-template <typename T>
-constexpr int kShare = kWave / kAcross<T>;              // threads of a wave that share a channel
-template <typename T>
-constexpr int kParts = kScanThreads / kC<T>;            // threads that look back for one channel
-template <typename T>
-constexpr int kHeads = kC<T> / kWave;                   // waves that join a tile's channels
+struct ScanBackward;
+template <>
+struct ScanBackward<bf16> : ScanCfg<bf16, 2, 8, kScanBackwardTile> {};
+template <>
+struct ScanBackward<float> : ScanCfg<float, 4, 4, kScanBackwardTile> {};
 
-// The kV channels of a lane as they are stored.  The kernels go through them
-// word by word, so that a word of an output takes the registers of an input's
-// that has been used.
-template <typename T>
-constexpr int kWords = kV * (int)sizeof(T) / 4;
-template <typename T>
-constexpr int kPerWord = 4 / (int)sizeof(T);  // channels of a word
-template <typename T>
+// V channels of a lane as they are stored.  The kernels go through them word
+// by word, so that a word of an output takes the registers of an input's that
+// has been used.
+template <typename T, int V>
 struct Pack {
-  uint32_t w[kWords<T>];
+  static constexpr int kWords = V * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
 };
 
 __device__ __forceinline__ void unpack_word(uint32_t w, float (&v)[2]) {
@@ -66,24 +76,24 @@ __device__ __forceinline__ uint32_t pack_word(const float (&v)[2]) {
 }
 __device__ __forceinline__ uint32_t pack_word(const float (&v)[1]) { return __float_as_uint(v[0]); }
 
-// n of kV channels from p (n <= 0: none, zeros).  kVec: p is aligned to kV
-// elements and n is kV or <= 0; else p has element alignment and the last
-// lane of a row may hold fewer.
-template <typename T, bool kVec>
-__device__ __forceinline__ Pack<T> load_pack(const void* p, int n) {
-  Pack<T> r;
-  if (n >= kV) {
+// n of V channels from p (n <= 0: none, zeros).  kVec: p is aligned to V
+// elements and n is V or <= 0; else p has element alignment and the last lane
+// of a row may hold fewer.
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ Pack<T, V> load_pack(const void* p, int n) {
+  Pack<T, V> r;
+  if (n >= V) {
     if constexpr (kVec)
-      r = *static_cast<const Pack<T>*>(__builtin_assume_aligned(p, kV * sizeof(T)));
+      r = *static_cast<const Pack<T, V>*>(__builtin_assume_aligned(p, V * sizeof(T)));
     else
       __builtin_memcpy(r.w, p, sizeof r.w);
     return r;
   }
 #pragma unroll
-  for (int i = 0; i < kWords<T>; ++i) r.w[i] = 0u;
+  for (int i = 0; i < r.kWords; ++i) r.w[i] = 0u;
   if constexpr (!kVec) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
+    for (int i = 0; i < V; ++i)
       if (i < n) {
         if constexpr (sizeof(T) == 2)
           r.w[i / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
@@ -93,16 +103,16 @@ __device__ __forceinline__ Pack<T> load_pack(const void* p, int n) {
   }
   return r;
 }
-template <typename T, bool kVec>
-__device__ __forceinline__ void store_pack(void* p, int n, const Pack<T>& r) {
-  if (n >= kV) {
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ void store_pack(void* p, int n, const Pack<T, V>& r) {
+  if (n >= V) {
     if constexpr (kVec)
-      *static_cast<Pack<T>*>(__builtin_assume_aligned(p, kV * sizeof(T))) = r;
+      *static_cast<Pack<T, V>*>(__builtin_assume_aligned(p, V * sizeof(T))) = r;
     else
       __builtin_memcpy(p, r.w, sizeof r.w);
   } else if constexpr (!kVec) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
+    for (int i = 0; i < V; ++i)
       if (i < n) {
         if constexpr (sizeof(T) == 2)
           static_cast<uint16_t*>(p)[i] = (uint16_t)(r.w[i / 2] >> (16 * (i & 1)));
@@ -118,25 +128,25 @@ __device__ __forceinline__ void store_pack(void* p, int n, const Pack<T>& r) {
 // where it is stored (the values it comes from would be kept until then).
 __device__ __forceinline__ void renew(uint32_t& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void renew(float& v) { asm volatile("" : "+v"(v)); }
-template <typename T, int K>
-__device__ __forceinline__ void renew(Pack<T> (&p)[K]) {
+template <typename T, int V, int K>
+__device__ __forceinline__ void renew(Pack<T, V> (&p)[K]) {
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < kWords<T>; ++i) renew(p[k].w[i]);
+    for (int i = 0; i < p[k].kWords; ++i) renew(p[k].w[i]);
 }
-template <int K>
-__device__ __forceinline__ void renew(float (&z)[K][kV]) {
+template <int V, int K>
+__device__ __forceinline__ void renew(float (&z)[K][V]) {
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int v = 0; v < kV; ++v) renew(z[k][v]);
+    for (int v = 0; v < V; ++v) renew(z[k][v]);
 }
 
 // A thread's rows of an array in the tile whose first element is at `first`:
 // row k is k rows on from a base that the workgroup shares (scalar), plus a
-// 32-bit byte offset of the thread (M3_SCAN_CHUNK rows of an array span less
-// than 4 GiB).
+// 32-bit byte offset of the thread (a tile's rows of an array span less than
+// 4 GiB).
 template <typename T>
 struct Rows {
   char* base;
@@ -149,35 +159,83 @@ struct Rows {
   __device__ __forceinline__ void* operator[](int k) const { return base + k * step + at; }
 };
 
+// A thread's K tokens of an array: `nt` of them inside the sequence and `n` of
+// the lane's channels inside the row (`full`: all); what lies outside is
+// filled with `fill` words.
+template <bool kVec, typename T, int V, int K>
+__device__ __forceinline__ void load_rows(Pack<T, V> (&v)[K], const Rows<T>& r, bool full, int nt,
+                                          int n, uint32_t fill) {
+  if (full) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = load_pack<T, V, kVec>(r[k], V);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k] = load_pack<T, V, kVec>(r[k], k < nt ? n : 0);
+#pragma unroll
+      for (int i = 0; i < v[k].kWords; ++i) v[k].w[i] = k < nt ? v[k].w[i] : fill;
+    }
+  }
+}
+template <bool kVec, typename T, int V, int K>
+__device__ __forceinline__ void store_rows(const Pack<T, V> (&v)[K], const Rows<T>& r, bool full,
+                                           int nt, int n) {
+  if (full) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) store_pack<T, V, kVec>(r[k], V, v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < nt) store_pack<T, V, kVec>(r[k], n, v[k]);
+  }
+}
+// Gates behind the sequence pass the state on: f = +inf.
+template <typename T>
+constexpr uint32_t kPassGate = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
+
+// Whether every row of an array starts at a multiple of V elements.
+inline bool vec_rows(const void* p, int64_t ld, size_t es, int V) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (V * es) == 0 && ld % V == 0);
+}
+
 // ---- the chain -----------------------------------------------------------------
-// A unit is one (sequence, channel tile); its chunks form a chain.  The
+// A unit is one (sequence, channel tile); its tiles in time form a chain.  The
 // workgroup takes its place in the chain from the unit's ticket counter, so
 // it only ever waits for workgroups that already run, whatever the order of
 // their start.
 //
-// What a chunk hands on are 64-bit words, one a channel, that validate
+// What a tile hands on are 64-bit words, one a channel, that validate
 // themselves: the high half is A with its sign bit set (A is never negative),
 // the low half B; an empty word is 0.  They are written and read by relaxed
-// device-scope atomics, and no order between words is needed.  A chunk
+// device-scope atomics, and no order between words is needed.  Place k
 // publishes its map as soon as it has it, and the state that leaves it (a word
-// with A = 0) once it knows its entry.  Chunk k's entry is the state that left
-// chunk k - 8 through the maps of chunks k - 7 .. k - 1, joined in this order,
-// so that results do not depend on timing.  About as many chunks of a unit
-// run at once, so the state waited for is there by then; a window that slides
+// with A = 0) once it knows its entry.  Its entry is the state that left place
+// k - W (W = kWindow) through the maps of places k - W + 1 .. k - 1, joined in
+// this order, so that results do not depend on timing.  A window that slides
 // has no place where all have to wait for their neighbour's state, as groups
-// have at their borders.  Counters and words are zero between calls: the
-// unit's last workgroup to finish looking back clears them.
+// have at their borders.
+//
+// Words are cleared as the chain moves on.  Besides the state it needs, place
+// k waits until the states that left places k - 2 W + 1 .. k - W are all there
+// (one lane looks at one word of each, and they are as good as always there):
+// a place publishes its state after its look-back, so the look-backs of all
+// places up to k - W are then over, by induction.  The map of place c is read
+// by places up to c + W - 1 and its state's words by places up to c + 2 W - 1,
+// so place k clears map k - 2 W + 1 and state k - 3 W + 1.  The rest, and the
+// counters, are left to the unit's last workgroup: all is zero between calls.
+// (All of it left to that one took 15 us of a B1 T16384 D4096 call.)
 //
 // Workspace, in 32-bit words: [0] unused, [1] error word (1: a wait ran out;
 // 2: the counters were not zero), then from byte 256 two counters a unit,
-// then (256-byte aligned) the 64-bit words: [unit][chunk][C] maps, then
-// [unit][chunk][C] states.
+// then (256-byte aligned) the 64-bit words: [unit][place][C] maps, then
+// [unit][place][C] states.
 struct ChainWs {
   int* err;
   int* counters;                 // [units][2]: ticket, finished
-  unsigned long long* maps;      // [units][nC][C]
-  unsigned long long* exits;     // [units][nC][C]
+  unsigned long long* maps;      // [units][nP][C]
+  unsigned long long* exits;     // [units][nP][C]
 };
+constexpr int kWindow = 8;
 
 __device__ __forceinline__ unsigned long long word_of(float A, float B) {
   return ((unsigned long long)(__float_as_uint(A) | 0x80000000u) << 32) | __float_as_uint(B);
@@ -209,72 +267,39 @@ __device__ __forceinline__ unsigned long long await(const unsigned long long* p,
   return w;
 }
 
-// A thread's K tokens of an array: `nt` of them inside the sequence and `n` of
-// the lane's channels inside the row (`full`: all); what lies outside is
-// filled with `fill` words.
-template <typename T, bool kVec, int K>
-__device__ __forceinline__ void load_rows(Pack<T> (&v)[K], const Rows<T>& r, bool full, int nt, int n,
-                                          uint32_t fill) {
-  if (full) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = load_pack<T, kVec>(r[k], kV);
-  } else {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      v[k] = load_pack<T, kVec>(r[k], k < nt ? n : 0);
-#pragma unroll
-      for (int i = 0; i < kWords<T>; ++i) v[k].w[i] = k < nt ? v[k].w[i] : fill;
-    }
-  }
-}
-template <typename T, bool kVec, int K>
-__device__ __forceinline__ void store_rows(const Pack<T> (&v)[K], const Rows<T>& r, bool full, int nt,
-                                           int n) {
-  if (full) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) store_pack<T, kVec>(r[k], kV, v[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (k < nt) store_pack<T, kVec>(r[k], n, v[k]);
-  }
-}
-// Gates behind the sequence pass the state on: f = +inf.
-template <typename T>
-constexpr uint32_t kPassGate = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
-
-// Whether every row of an array starts at a multiple of kV elements.
-inline bool vec_rows(const void* p, int64_t ld, size_t es) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % (kV * es) == 0 && ld % kV == 0);
+// A launch's unit of workgroup i: the units in turn, turned by one a round, so
+// that a compute die does not keep to the same columns.
+__device__ __forceinline__ int chain_unit(int units) {
+  return (int)((blockIdx.x + blockIdx.x / units) % units);
 }
 
-// This workgroup's place in its unit's chain, the same in every thread; nC
+// This workgroup's place in its unit's chain, the same in every thread; nP
 // when the counters were not zero (error word 2; the workgroup leaves).
-__device__ __forceinline__ int chain_ticket(const ChainWs& ws, int unit, int nC, int* s_word) {
+__device__ __forceinline__ int chain_ticket(const ChainWs& ws, int unit, int nP, int* s_word) {
   if (threadIdx.x == 0) {
     const int k = __hip_atomic_fetch_add(ws.counters + 2 * unit, 1, __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT);
-    if (k < 0 || k >= nC)
+    if (k < 0 || k >= nP)
       __hip_atomic_store(ws.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *s_word = k < 0 || k >= nC ? nC : k;
+    *s_word = k < 0 || k >= nP ? nP : k;
   }
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(*s_word);  // in a scalar register, as the addresses from it
 }
 
-// This part's share of the window of chunk k, joined: the state that left
-// chunk k - kWindow (`start` where there is none) and the maps behind it.
-template <typename T>
-__device__ __forceinline__ Run chain_part(const ChainWs& ws, int unit, int nC, int k, int part,
-                                          int ch, float start) {
-  constexpr int C = kC<T>, kPer = kWindow / kParts<T>;
-  const size_t base = ((size_t)unit * nC) * C + ch;
+// This part's share of the window of place k, joined: the state that left
+// place k - kWindow (`start` where there is none) and the maps behind it.
+// `base`: the unit's first word.
+template <typename Cfg>
+__device__ __forceinline__ Run chain_part(const ChainWs& ws, size_t base, int k, int part, int ch,
+                                          float start) {
+  constexpr int C = Cfg::C, kPer = kWindow / Cfg::kParts;
   unsigned long long w[kPer];
   const unsigned long long* from[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = part * kPer + j, c = k - kWindow + i;
-    from[j] = (i == 0 ? ws.exits : ws.maps) + base + (int64_t)(c < 0 ? 0 : c) * C;
+    from[j] = (i == 0 ? ws.exits : ws.maps) + base + (size_t)(c < 0 ? 0 : c) * C + ch;
     w[j] = c >= 0 ? peek(from[j]) : 0;
   }
   Run r = Run{1.f, 0.f};
@@ -291,54 +316,74 @@ __device__ __forceinline__ Run chain_part(const ChainWs& ws, int unit, int nC, i
   return r;
 }
 
+// One wave of a workgroup waits for the states that left the window before.
+__device__ __forceinline__ void chain_passed(const ChainWs& ws, size_t base, int C, int k) {
+  const int lane = threadIdx.x & 63, c = k - 2 * kWindow + 1 + lane;
+  if (lane < kWindow && c >= 0) {
+    const unsigned long long* from = ws.exits + base + (size_t)c * C;
+    if (peek(from) == 0) await(from, ws.err);
+  }
+}
+// Clears what place k is the last to need, behind its look-back.  Nobody reads
+// these words any more in this launch, so ordinary stores do: they are out by
+// the end of the kernel.
+template <typename Cfg>
+__device__ __forceinline__ void chain_clear(const ChainWs& ws, size_t base, int k) {
+  constexpr int C = Cfg::C;
+  const int tid = threadIdx.x, m = k - 2 * kWindow + 1, e = k - 3 * kWindow + 1;
+  if (tid < C) {
+    if (m >= 0) ws.maps[base + (size_t)m * C + tid] = 0;
+  } else if (tid < 2 * C) {
+    if (e >= 0) ws.exits[base + (size_t)e * C + tid - C] = 0;
+  }
+}
 // Counts this wave as done with the unit's words: each wave that publishes
 // (the first kHeads), after a barrier behind the look-back.  True in the
 // unit's last.
-template <typename T>
-__device__ __forceinline__ bool chain_count(const ChainWs& ws, int unit, int nC) {
+template <typename Cfg>
+__device__ __forceinline__ bool chain_count(const ChainWs& ws, int unit, int nP) {
   // what this wave published has arrived before the count does
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   int old = 0;
   if ((threadIdx.x & 63) == 0)
     old = __hip_atomic_fetch_add(ws.counters + 2 * unit + 1, 1, __ATOMIC_RELAXED,
                                  __HIP_MEMORY_SCOPE_AGENT);
-  return __builtin_amdgcn_readfirstlane(old) == nC * kHeads<T> - 1;
+  return __builtin_amdgcn_readfirstlane(old) == nP * Cfg::kHeads - 1;
 }
-// The unit's last workgroup leaves its counters and words zero.  Nobody reads
-// them any more in this launch, so ordinary 16-byte stores do: they are out
-// by the end of the kernel.
-template <typename T>
-__device__ __forceinline__ void chain_clear(const ChainWs& ws, int unit, int nC) {
-  const size_t n = (size_t)nC * kC<T> / 2;  // 16-byte vectors
-  uint4* maps = reinterpret_cast<uint4*>(ws.maps) + unit * n;
-  uint4* exits = reinterpret_cast<uint4*>(ws.exits) + unit * n;
-  for (size_t i = threadIdx.x; i < n; i += kScanThreads) {
-    maps[i] = make_uint4(0u, 0u, 0u, 0u);
-    exits[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
+template <typename Cfg>
+__device__ __forceinline__ void chain_clear_rest(const ChainWs& ws, size_t base, int unit, int nP) {
+  constexpr int C = Cfg::C;
+  const int m = nP - 2 * kWindow + 1, e = nP - 3 * kWindow + 1;
+  for (int i = (m < 0 ? 0 : m) * C + (int)threadIdx.x; i < nP * C; i += Cfg::kThreads)
+    ws.maps[base + i] = 0;
+  for (int i = (e < 0 ? 0 : e) * C + (int)threadIdx.x; i < (nP - kWindow) * C; i += Cfg::kThreads)
+    ws.exits[base + i] = 0;
   if (threadIdx.x < 2) ws.counters[2 * unit + threadIdx.x] = 0;
 }
 
 // The thread maps of a wave joined over the threads that share a channel
 // (kBack: from the last token to the first): r becomes the join up to and
 // with this thread, `before` the join of those before it.
-template <typename T, bool kBack>
+template <typename Cfg, bool kBack>
 __device__ __forceinline__ void wave_join(Run& r, Run& before) {
-  constexpr int kStep = kAcross<T>;
-  const int g = (threadIdx.x & 63) / kStep, place = kBack ? kShare<T> - 1 - g : g;
-#pragma unroll
-  for (int s = 1; s < kShare<T>; s *= 2) {
+  constexpr int kStep = Cfg::kAcross, kShare = Cfg::kShare;
+  before = Run{1.f, 0.f};
+  if constexpr (kShare > 1) {
+    const int g = (threadIdx.x & 63) / kStep, place = kBack ? kShare - 1 - g : g;
     Run o;
-    o.A = kBack ? __shfl_down(r.A, s * kStep, kWave) : __shfl_up(r.A, s * kStep, kWave);
-    o.B = kBack ? __shfl_down(r.B, s * kStep, kWave) : __shfl_up(r.B, s * kStep, kWave);
-    if (s == 1) before = o;
-    if (place >= s) r = run_join(o, r);
+#pragma unroll
+    for (int s = 1; s < kShare; s *= 2) {
+      o.A = kBack ? __shfl_down(r.A, s * kStep, kWave) : __shfl_up(r.A, s * kStep, kWave);
+      o.B = kBack ? __shfl_down(r.B, s * kStep, kWave) : __shfl_up(r.B, s * kStep, kWave);
+      if (kShare == 2 && place > 0) before = o;
+      if (place >= s) r = run_join(o, r);
+    }
+    if constexpr (kShare > 2) {
+      o.A = kBack ? __shfl_down(r.A, kStep, kWave) : __shfl_up(r.A, kStep, kWave);
+      o.B = kBack ? __shfl_down(r.B, kStep, kWave) : __shfl_up(r.B, kStep, kWave);
+      if (place > 0) before = o;
+    }
   }
-  if constexpr (kShare<T> > 2) {
-    before.A = kBack ? __shfl_down(r.A, kStep, kWave) : __shfl_up(r.A, kStep, kWave);
-    before.B = kBack ? __shfl_down(r.B, kStep, kWave) : __shfl_up(r.B, kStep, kWave);
-  }
-  if (place == 0) before = Run{1.f, 0.f};
 }
 
 }  // namespace m3

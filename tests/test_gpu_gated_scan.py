@@ -46,7 +46,7 @@ def check_all(v, t, dtype, workspace=None):
 CASES = [
     # B, T, D: one token, one chunk and its ends, ragged chunks, odd widths, several groups of chunks
     (1, 1, 8), (2, 1, 1), (3, 2, 65), (1, 7, 130), (2, 255, 64), (2, 256, 72), (1, 257, 200),
-    (2, 127, 64), (2, 128, 132), (1, 129, 200), (2, 513, 33), (3, 777, 129), (1, 2100, 16), (5, 300, 256), (1, 4500, 12),
+    (2, 63, 20), (1, 64, 64), (2, 65, 128), (2, 127, 64), (2, 128, 132), (1, 129, 200), (2, 513, 33), (3, 777, 129), (1, 2100, 16), (5, 300, 256), (1, 4500, 12),
 ]
 
 
@@ -94,7 +94,7 @@ def test_masks(T, D, dtype):
     x[0, T // 2:] = np.nan
     f[1] = np.inf                             # nothing but padding
     x[1, ::2] = np.inf
-    for s in (0, 5, T // 3, 127, 128, 255, 256, T - 1):
+    for s in (0, 5, 63, 64, T // 3, 127, 128, 255, 256, T - 1):
         if s < T:
             f[2, s] = -np.inf                 # documents
     big = -np.finfo(np.float32).max if dtype == "f32" else -3.3895e38

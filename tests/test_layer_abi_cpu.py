@@ -60,15 +60,15 @@ def test_scan_pointers(lib):
             p[i] = None
             assert call(p) == INV
     need = lib.m3_gated_scan_workspace_size(ctypes.byref(d), 0)
-    # 2 sequences x 1 tile of 64 floats: 256 bytes, their counters (256), 3
-    # chunks of 128 tokens with a map and a state each, 64 words of 8 bytes
-    assert need == 256 + 256 + 2 * 3 * 2 * 64 * 8
+    # 2 sequences x 1 tile of 64 floats: 256 bytes, their counters (256), 5
+    # tiles of 64 tokens with a map and a state each, 64 words of 8 bytes
+    assert need == 256 + 256 + 2 * 5 * 2 * 64 * 8
     # bfloat16 tiles are 128 channels wide
     assert lib.m3_gated_scan_workspace_size(ctypes.byref(scan_dims(t=4200, d=129)), 1) == \
-        256 + 256 + 4 * 33 * 2 * 128 * 8
+        256 + 256 + 4 * 66 * 2 * 128 * 8
     assert call([OK] * 7, w=[None, need, None]) == WS and call([OK] * 7, w=[OK, need - 1, None]) == WS
     assert call([OK] * 7, w=[HALF, need, None]) == INV
-    for t in (0, 1, 128):                 # one chunk hands nothing on
+    for t in (0, 1, 64):                  # one tile hands nothing on
         assert lib.m3_gated_scan_workspace_size(ctypes.byref(scan_dims(t=t)), 0) == 0
     bw = lambda p, dd=d: lib.m3_gated_scan_backward(ctypes.byref(dd), 1, *p, *ws)
     for i in range(10):                   # dy x f g states dh_last dx df dg dh0
