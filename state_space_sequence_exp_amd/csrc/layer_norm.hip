@@ -101,8 +101,12 @@ __device__ __forceinline__ void store_vec(T* p, int n, const Vec& r) {
 // A vector's weights (zeros without p or past the row).
 template <int E>
 __device__ __forceinline__ void load_weights(const float* p, int n, float (&w)[E]) {
+  if (p && n >= E) {
+    __builtin_memcpy(w, p, sizeof w);
+  } else {
 #pragma unroll
-  for (int i = 0; i < E; ++i) w[i] = p && i < n ? p[i] : 0.f;
+    for (int i = 0; i < E; ++i) w[i] = p && i < n ? p[i] : 0.f;
+  }
 }
 
 __device__ __forceinline__ float wave_sum(float v) { return wave_read_lane(wave_incl_scan(v), 63); }
@@ -137,14 +141,33 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs a)
     load_weights<E>(a.weight + e0, a.D - e0, w[j]);
     load_weights<E>(a.bias ? a.bias + e0 : nullptr, a.D - e0, b[j]);
   }
-  for (int64_t r = (int64_t)blockIdx.x * kTeams + team; r < a.rows; r += (int64_t)gridDim.x * kTeams) {
-    Vec x[NV], res[NV];
+  // the next row is requested while this one is worked on, where the
+  // registers hold both
+  constexpr bool kAhead = NV == 1;
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  int64_t r = (int64_t)blockIdx.x * kTeams + team;
+  Vec x[NV], res[NV], next_x[NV], next_res[NV];
+  const auto request = [&](int64_t row, Vec(&p)[NV], Vec(&q)[NV]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e0 = (j * TPR + t) * E;
-      x[j] = load_vec<T, kVec>(static_cast<const T*>(a.x) + r * a.ld_x + e0, a.D - e0);
+      const int e0 = (j * TPR + t) * E, n = row < a.rows ? a.D - e0 : 0;
+      p[j] = load_vec<T, kVec>(static_cast<const T*>(a.x) + row * a.ld_x + e0, n);
       if (a.residual)
-        res[j] = load_vec<T, kVec>(static_cast<const T*>(a.residual) + r * a.ld_res + e0, a.D - e0);
+        q[j] = load_vec<T, kVec>(static_cast<const T*>(a.residual) + row * a.ld_res + e0, n);
+    }
+  };
+  if constexpr (kAhead) request(r, next_x, next_res);
+  // every team makes the same number of rounds (they share the barriers)
+  for (int64_t r0 = (int64_t)blockIdx.x * kTeams; r0 < a.rows; r0 += step, r += step) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        x[j] = next_x[j];
+        res[j] = next_res[j];
+      }
+      request(r + step, next_x, next_res);
+    } else {
+      request(r, x, res);
     }
     float v[NV][E], sum = 0.f;
 #pragma unroll
@@ -174,6 +197,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs a)
       }
     }
     const float rstd = 1.f / sqrtf(team_sum<TPR>(sq, s_sum[1]) * inv + a.eps);
+    if (r >= a.rows) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e0 = (j * TPR + t) * E;
@@ -329,25 +353,30 @@ __global__ void __launch_bounds__(kBwThreads) norm_backward_kernel(NormArgs a, i
   }
 }
 
-// dweight and dbias from the groups' partials: 64 columns a workgroup, the
-// groups split over its 16 waves and joined in their order.
+// dweight and dbias from the groups' partials: 32 columns a workgroup, the
+// groups dealt to its 32 half waves, 8 in flight a thread, joined in a fixed
+// order.
 __global__ void __launch_bounds__(1024) norm_weights_kernel(NormArgs a, int groups) {
-  __shared__ float s_part[16][kWave];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
-  const int64_t c = (int64_t)blockIdx.x * kWave + lane;  // of 2 D
-  const int per = (groups + 15) / 16;
-  float v = 0.f;
-  if (c < 2 * (int64_t)a.D)
-    for (int i = wave * per; i < (wave + 1) * per && i < groups; ++i)
-      v += a.partial[(int64_t)i * 2 * a.D + c];
-  s_part[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && c < 2 * (int64_t)a.D) {
-    v = 0.f;
+  constexpr int kCols = 32, kParts = 1024 / kCols, kFly = kMaxGroups / kParts;
+  __shared__ float s_part[kParts][kCols];
+  const int col = threadIdx.x % kCols, part = threadIdx.x / kCols;
+  const int64_t c = (int64_t)blockIdx.x * kCols + col;  // of 2 D
+  float v[kFly], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += s_part[i][lane];
-    if (c < a.D) a.dweight[c] = v;
-    else if (a.dbias) a.dbias[c - a.D] = v;
+  for (int i = 0; i < kFly; ++i) {
+    const int g = i * kParts + part;
+    v[i] = c < 2 * (int64_t)a.D && g < groups ? a.partial[(int64_t)g * 2 * a.D + c] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kFly; ++i) sum += v[i];
+  s_part[part][col] = sum;
+  __syncthreads();
+  if (part == 0 && c < 2 * (int64_t)a.D) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) sum += s_part[i][col];
+    if (c < a.D) a.dweight[c] = sum;
+    else if (a.dbias) a.dbias[c - a.D] = sum;
   }
 }
 
@@ -376,10 +405,10 @@ hipError_t launch_fwd_t(const NormArgs& a, hipStream_t stream) {
                    vec16(a.sum, a.ld_sum, es) && vec16(a.y, a.ld_y, es);
   const int vecs = (a.D + kE<T> - 1) / kE<T>;
   if (vecs <= 64) return launch_fwd<T, 64, 1>(a, vec, stream);
-  if (vecs <= 128) return launch_fwd<T, 64, 2>(a, vec, stream);
+  if (vecs <= 128) return launch_fwd<T, 128, 1>(a, vec, stream);
   if (vecs <= 256) return launch_fwd<T, 256, 1>(a, vec, stream);
-  if (vecs <= 512) return launch_fwd<T, 256, 2>(a, vec, stream);
-  if (vecs <= 1024) return launch_fwd<T, 256, 4>(a, vec, stream);
+  if (vecs <= 512) return launch_fwd<T, 512, 1>(a, vec, stream);
+  if (vecs <= 1024) return launch_fwd<T, 1024, 1>(a, vec, stream);
   if (vecs <= 2048) return launch_fwd<T, 1024, 2>(a, vec, stream);
   if constexpr (sizeof(T) == 4) return launch_fwd<T, 1024, 4>(a, vec, stream);
   return hipErrorInvalidValue;
@@ -443,7 +472,7 @@ hipError_t launch_norm_backward(const NormArgs& a, m3_dtype dtype, hipStream_t s
                                           : launch_bw_t<float>(a, groups, stream);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_weights_kernel, dim3((2 * a.D + kWave - 1) / kWave), dim3(1024), 0, stream,
+  hipLaunchKernelGGL(norm_weights_kernel, dim3((2 * a.D + 31) / 32), dim3(1024), 0, stream,
                      a, groups);
   return hipGetLastError();
 }
