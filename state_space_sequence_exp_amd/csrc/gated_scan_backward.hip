@@ -45,7 +45,11 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
   load_rows<kVec>(x, rx, full, nt, n, 0u);
   load_rows<kVec>(dy, rd, full, nt, n, 0u);
   if constexpr (kGate) load_rows<kVec>(g, rg, full, nt, n, 0u);
-  float z[K][V];
+  // per token: the gate, the map from the state before the thread's first
+  // token to that before this one, dL/dh without what comes from behind, and
+  // dy silu'(g)
+  float z[K][V], A[K][V], B[K][V], dh[K][V], dsilu[kGate ? K : 1][V];
+  Run whole[V];  // of the thread's tokens
 #pragma unroll
   for (int i = 0; i < Cfg::kWords; ++i) {
     Run r[W], u[W];
@@ -58,8 +62,11 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
       unpack_word(f[k].w[i], fv);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
+        const int v = i * W + e;
         const float q = gate_of(fv[e]);
-        z[k][i * W + e] = q;
+        z[k][v] = q;
+        A[k][v] = r[e].A;
+        B[k][v] = r[e].B;
         r[e].A = gate_keep<false>(q, r[e].A);
         r[e].B = gate_step<true>(q, r[e].B, xv[e]);
       }
@@ -71,14 +78,21 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
       if constexpr (kGate) unpack_word(g[k].w[i], gv);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        if constexpr (kGate) dv[e] *= gv[e] * sigmoid_of(gv[e]);
-        u[e].B = gate_keep<true>(z[k][i * W + e], dv[e] + u[e].B);
+        const int v = i * W + e;
+        dh[k][v] = dv[e];
+        if constexpr (kGate) {
+          const float sg = sigmoid_of(gv[e]);
+          dh[k][v] = dv[e] * (gv[e] * sg);
+          dsilu[k][v] = dv[e] * (sg * __builtin_fmaf(gv[e], 1.f - sg, 1.f));
+        }
+        u[e].B = gate_keep<true>(z[k][v], dh[k][v] + u[e].B);
       }
     }
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const int v = i * W + e;
       Run o;
+      whole[v] = r[e];
       u[e].A = r[e].A;
       wave_join<Cfg, false>(r[e], o);
       s_run[v][tid] = o;
@@ -90,8 +104,8 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
   }
   renew(x);
   renew(z);
-  renew(dy);
-  if constexpr (kGate) renew(g);
+  renew(dh);
+  if constexpr (kGate) renew(dsilu);
   __syncthreads();
   Run total = Run{1.f, 0.f};
   if (tid < C) {
@@ -137,44 +151,28 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
 
 #pragma unroll
   for (int i = 0; i < Cfg::kWords; ++i) {
-    float h[K][W], hk[W], u[W];  // the state before each token; u from behind
+    float h[W], after[W], u[W];  // the state before the thread, after a token; u from behind
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const int v = i * W + e;
-      hk[e] = run_apply(s_run[v][tid], s_fore[wave][cl + v].B);
+      h[e] = run_apply(s_run[v][tid], s_fore[wave][cl + v].B);
+      after[e] = run_apply(whole[v], h[e]);
       u[e] = run_apply(s_behind[v][tid], run_apply(s_back[wave][cl + v], s_entry[cl + v]));
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float xv[W];
-      unpack_word(x[k].w[i], xv);
-#pragma unroll
-      for (int e = 0; e < W; ++e) {
-        h[k][e] = hk[e];
-        hk[e] = gate_step<true>(z[k][i * W + e], hk[e], xv[e]);
-      }
-    }
-    renew(x);
-    renew(z);
-#pragma unroll
     for (int k = K - 1; k >= 0; --k) {
-      float xv[W], dv[W], gv[W], dx[W], df[W], dg[W];
+      float xv[W], dx[W], df[W], dg[W];
       unpack_word(x[k].w[i], xv);
-      unpack_word(dy[k].w[i], dv);
-      if constexpr (kGate) unpack_word(g[k].w[i], gv);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        const float q = z[k][i * W + e];
-        float dh = dv[e];
-        if constexpr (kGate) {
-          const float sg = sigmoid_of(gv[e]), after = k + 1 < K ? h[k + 1][e] : hk[e];
-          dg[e] = dv[e] * after * (sg * __builtin_fmaf(gv[e], 1.f - sg, 1.f));
-          dh = dv[e] * (gv[e] * sg);
-        }
-        const float G = dh + u[e], s = __builtin_fabsf(q), slope = s * (1.f - s);
+        const int v = i * W + e;
+        const float q = z[k][v], before = run_apply(Run{A[k][v], B[k][v]}, h[e]);
+        if constexpr (kGate) dg[e] = dsilu[k][v] * after[e];
+        const float G = dh[k][v] + u[e], s = __builtin_fabsf(q), slope = s * (1.f - s);
         dx[e] = gate_passes(q) ? 0.f : G * gate_w(q);
-        df[e] = slope == 0.f ? 0.f : G * (h[k][e] - xv[e]) * slope;
+        df[e] = slope == 0.f ? 0.f : G * (before - xv[e]) * slope;
         u[e] = gate_keep<true>(q, G);
+        after[e] = before;
       }
       x[k].w[i] = pack_word(dx);
       dy[k].w[i] = pack_word(df);

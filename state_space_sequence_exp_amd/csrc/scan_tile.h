@@ -52,7 +52,7 @@ struct ScanBackward;
 template <>
 struct ScanBackward<bf16> : ScanCfg<bf16, 2, 8, kScanBackwardTile> {};
 template <>
-struct ScanBackward<float> : ScanCfg<float, 4, 4, kScanBackwardTile> {};
+struct ScanBackward<float> : ScanCfg<float, 2, 4, kScanBackwardTile> {};
 
 // V channels of a lane as they are stored.  The kernels go through them word
 // by word, so that a word of an output takes the registers of an input's that
