@@ -361,12 +361,19 @@ hipError_t launch_decode_nt(const CacheArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-#ifndef M3_DECODE_WAVE_UNITS
-#define M3_DECODE_WAVE_UNITS 1024
-#endif
+// One wave a unit once there is a wave for every SIMD, four before that; from
+// 2048 units on where a wave takes 16 turns or more (a workgroup of four then
+// pays longer), and always where a wave holds the whole unit.  Measured, us for
+// one wave / four: N = 128, P = 64, R = 4, bfloat16: 12.4 / 6.8 with 256 units,
+// 13.8 / 13.6 with 1024, 18.9 / 22.1 with 2048, 57.3 / 74.9 with 8192; N = P =
+// 64, R = 1: 6.1 / 4.4, 6.9 / 6.8, 9.0 / 10.2, 22.9 / 30.6; N = P = 128, R = 4,
+// float: 25.1 / 10.4, 28.5 / 21.8, 37.5 / 37.2, 114.6 / 130.2; N = 64, P = 16,
+// R = 2, a whole unit: 4.3 / 5.9, 4.5 / 6.8, 5.7 / 12.2, 13.2 / 38.0.
 template <typename T, int R, int kCode, bool kTrap, bool kRot>
 hipError_t launch_decode_form(const CacheArgs& a, hipStream_t stream) {
-  if (a.S * a.H >= M3_DECODE_WAVE_UNITS)
+  const int groups = kWave / (a.P / 8), turns = (a.N / 2 + groups - 1) / groups;
+  const int64_t units = (int64_t)a.S * a.H;
+  if (turns <= 1 || units >= (turns >= 16 ? 2048 : 1024))
     return launch_decode_nt<T, R, kCode, kTrap, kRot, 64>(a, stream);
   return launch_decode_nt<T, R, kCode, kTrap, kRot, 256>(a, stream);
 }

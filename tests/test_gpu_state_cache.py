@@ -173,6 +173,8 @@ CASES = [
     # S, H, N, P, R
     (1, 1, 2, 16, 1), (3, 2, 64, 64, 1), (2, 3, 34, 32, 2), (5, 2, 128, 64, 4), (2, 1, 128, 128, 1),
     (2, 1, 256, 16, 4), (1, 2, 22, 128, 2), (4, 3, 256, 64, 2),
+    # a wave a unit: a wave for every SIMD and more, whole units, ragged pairs
+    (37, 28, 66, 64, 1), (33, 32, 128, 64, 4), (130, 16, 98, 128, 2), (3, 5, 64, 16, 2), (1100, 1, 34, 32, 1),
 ]
 
 
