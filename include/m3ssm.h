@@ -414,6 +414,9 @@ m3_status m3_block_postpass(const m3_dims* dims, m3_dtype dtype, const void* y,
  *   states                     [batch, nC, D]      float, dense, nC = ceil(T / 64)
  * `states` holds the state entering each chunk of M3_SCAN_CHUNK tokens (the
  * first is h0): what the backward pass needs besides the inputs.
+ *
+ * batch * ceil(D / 64) * (seqlen / 64 + 1) is at most 2^23 - 1 (the step:
+ * with seqlen 1).
  */
 #define M3_SCAN_CHUNK 64 /* tokens between two kept states */
 
@@ -549,9 +552,9 @@ m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const
  * y are left as they are), load writes zeros.  Where a slot is named more than
  * once, store and decode take its first entry and treat the others as idle.
  *
- * codes need 16-byte alignment, h of store 16, other pointers element
- * alignment (decode: as m3_decode_step).  P is 16, 32, 64 or 128; N even, as
- * m3_decode_step.
+ * codes and h need 16-byte alignment, other pointers element alignment
+ * (decode: as m3_decode_step).  P is 16, 32, 64 or 128; N even, as
+ * m3_decode_step; batch * H at most 2^24 - 1.
  */
 typedef enum { M3_CODE_INT8 = 0, M3_CODE_E4M3 = 1 } m3_code;
 

@@ -40,6 +40,9 @@ m3_status done(hipError_t e) { return e == hipSuccess ? M3_SUCCESS : M3_ERR_HIP;
 // Elements of the largest array, kept where byte offsets fit 63 bits.
 constexpr double kMaxElements = 1.0e18;
 
+// A launch holds fewer than 2^32 threads: workgroups of 512 and of 256.
+constexpr double kMaxGroups512 = 8388607.0, kMaxGroups256 = 16777215.0;
+
 constexpr int64_t kMaxScanLd = (1 << 22) - 1024;
 
 m3_status check_scan(const m3_scan_dims* d, bool backward) {
@@ -53,11 +56,10 @@ m3_status check_scan(const m3_scan_dims* d, bool backward) {
     // a chunk's rows are addressed by 32-bit byte offsets
     if (ld_of(lds[i], d->channels) > kMaxScanLd) return M3_ERR_NOT_SUPPORTED;
   }
-  // one workgroup a chunk and channel tile; 64-bit words for each in the
-  // workspace
+  // one workgroup a chunk and channel tile, of 512 threads at most
   if (d->batch > INT_MAX || d->channels > INT_MAX / 2 || d->seqlen > INT_MAX - M3_SCAN_CHUNK ||
       (double)d->batch * (double)m3::scan_tiles(d->channels, 4) *
-              (double)(d->seqlen / M3_SCAN_CHUNK + 1) > 2147483647.0)
+              (double)(d->seqlen / M3_SCAN_CHUNK + 1) > kMaxGroups512)
     return M3_ERR_NOT_SUPPORTED;
   return M3_SUCCESS;
 }
@@ -174,8 +176,10 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
 m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const float* h_in,
                              float* h_out, const void* x, const void* f, const void* g, void* y,
                              void* stream) {
-  if (!dtype_ok(&dtype)) return M3_ERR_INVALID_VALUE;
-  const m3_status st = check_scan(dims, false);
+  if (!dtype_ok(&dtype) || !dims) return M3_ERR_INVALID_VALUE;
+  m3_scan_dims one = *dims;
+  one.seqlen = 1;
+  const m3_status st = check_scan(&one, false);
   if (st != M3_SUCCESS) return st;
   if (dims->batch == 0) return M3_SUCCESS;
   const uintptr_t es = esize_of(dtype);
@@ -325,7 +329,7 @@ m3_status check_cache(const m3_dims* d, const int32_t* slots, int64_t n_slots) {
   if (P != 16 && P != 32 && P != 64 && P != 128) return M3_ERR_NOT_SUPPORTED;
   if (d->dstate_n > 256 || d->dstate_n > m3::decode_max_n((int)P)) return M3_ERR_NOT_SUPPORTED;
   if (d->batch > INT_MAX || d->nheads > INT_MAX || n_slots > INT_MAX ||
-      d->batch * d->nheads > INT_MAX)
+      (double)d->batch * (double)d->nheads > kMaxGroups256)
     return M3_ERR_NOT_SUPPORTED;
   if (!slots && d->batch > n_slots) return M3_ERR_INVALID_VALUE;
   return M3_SUCCESS;

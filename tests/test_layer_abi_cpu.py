@@ -46,6 +46,26 @@ def test_scan_shapes(lib, bad, code):
         assert lib.m3_gated_scan_step(ctypes.byref(d), 0, *[OK] * 6, None) == code
 
 
+@pytest.mark.parametrize("b,t,d", [(1 << 23, 0, 64), (1 << 22, 64, 64), (1 << 17, 1, 1 << 12), (1, 1 << 29, 64)])
+def test_scan_launch_size(lib, b, t, d):
+    """No launch has 2^32 threads or more, whatever the memory would hold."""
+    dims = ctypes.byref(scan_dims(b, t, d))
+    assert lib.m3_gated_scan(dims, 1, *[OK] * 7, OK, 1 << 62, None) == UNS
+    assert lib.m3_gated_scan_backward(dims, 1, *[OK] * 10, OK, 1 << 62, None) == UNS
+    assert lib.m3_gated_scan_workspace_size(dims, 1) == 0
+    if b > 1:
+        assert lib.m3_gated_scan_step(ctypes.byref(scan_dims(1 << 23, 1, d)), 1, *[OK] * 6, None) == UNS
+
+
+@pytest.mark.parametrize("t", [-1, 0, 1 << 40])
+def test_step_ignores_the_length(lib, t):
+    """The single-token form does not look at seqlen: what it refuses here is
+    the pointer, and an empty batch passes."""
+    args = [OK] * 5 + [MIS, None]
+    assert lib.m3_gated_scan_step(ctypes.byref(scan_dims(t=t)), 0, *args) == INV
+    assert lib.m3_gated_scan_step(ctypes.byref(scan_dims(t=t, b=0)), 0, *args) == m3.M3_SUCCESS
+
+
 def test_scan_pointers(lib):
     d = scan_dims()
     ws = [OK, 1 << 40, None]
@@ -165,6 +185,13 @@ def test_cache_shapes(lib, bad, code):
     assert lib.m3_state_store(d, 0, OK, OK, OK, OK, 9, None) == code
     assert lib.m3_state_load(d, 0, 0, OK, OK, OK, 9, OK, None) == code
     assert lib.m3_decode_step_cached(d, 0, 0, OK, OK, OK, 9, *[OK] * 10, None) == code
+
+
+def test_cache_launch_size(lib):
+    d = ctypes.byref(cdims(b=1 << 12, h=1 << 12))
+    assert lib.m3_state_store(d, 0, OK, OK, OK, OK, 9, None) == UNS
+    assert lib.m3_state_load(d, 0, 0, OK, OK, OK, 9, OK, None) == UNS
+    assert lib.m3_decode_step_cached(d, 0, 0, OK, OK, OK, 9, *[OK] * 10, None) == UNS
 
 
 def test_cache_pointers(lib):
