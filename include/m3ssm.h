@@ -449,8 +449,10 @@ size_t m3_gated_scan_workspace_size(const m3_scan_dims* dims, m3_dtype dtype);
  * The whole sequence: y for every token, h_last if not NULL, states if not
  * NULL.  g, h0 (zeros) may be NULL.  Pointers need element alignment only;
  * where every array's rows start at a multiple of four elements and channels
- * is one, they are moved as such vectors.  y must not overlap an input.  seqlen == 0 writes h_last = h0
- * (zeros when NULL); batch == 0 enqueues nothing.
+ * is one, they are moved as such vectors.  y must not
+ * overlap x, f or g (slices of one wider array lie between each other's rows),
+ * nor h_last h0.  seqlen == 0 writes h_last = h0 (zeros when NULL; there it may
+ * be h0 itself); batch == 0 enqueues nothing.
  */
 m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x, const void* f,
                         const void* g, const float* h0, void* y, float* h_last, float* states,
@@ -467,7 +469,8 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
  * dx, df, dg in the storage type, dh0 float.  Where the gate is a mask (a is
  * 0 or 1 in float) df is 0; where it passes the state, dx is 0.  dh_last and
  * dh0 may be NULL; dg is required exactly when g is given.  The outputs must
- * not overlap the inputs or each other.  seqlen == 0 writes dh0 = dh_last.
+ * not overlap the inputs or each other, nor dh0 dh_last.  seqlen == 0 writes
+ * dh0 = dh_last.
  */
 m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const void* dy,
                                  const void* x, const void* f, const void* g,
@@ -479,7 +482,7 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
  * One token for `batch` sequences (dims->seqlen ignored; row b of x, f, g, y
  * at b ld): h_out = a h_in + (1 - a) x, y = h_out * silu(g).  h_in, h_out
  * [batch, D] float, dense; h_out may be h_in but must not partially overlap
- * it.  g may be NULL.
+ * it; y must not overlap x, f or g.  g may be NULL.
  */
 m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const float* h_in,
                              float* h_out, const void* x, const void* f, const void* g, void* y,
@@ -495,7 +498,8 @@ m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const flo
  * from the values as stored in s: the variance from the centred values, not
  * from a difference of sums.  weight, bias [channels] float; bias may be NULL.
  * sum_out receives s (NULL: not kept; it may be x itself or residual itself,
- * with the same ld); y may be x or residual too, but not sum_out.  mean and
+ * with the same ld); y may be x or residual too, but not sum_out.  Arrays that
+ * overlap otherwise are refused.  mean and
  * rstd [rows] float, or NULL, are what the backward pass needs.  channels is
  * at most 16384.  Row r of an array is at r ld; every pointer needs element
  * alignment, and 16-byte aligned rows are read in vectors.
@@ -521,7 +525,8 @@ m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
  *        gradient of x and of residual alike)
  *   dweight = sum over rows of dy q,  dbias = sum over rows of dy    (float)
  *
- * dbias may be NULL.  dx may be dy or dsum (same ld).  The sums over rows are
+ * dbias may be NULL.  dx may be dy or dsum (same ld) but must not
+ * overlap them otherwise, nor s.  The sums over rows are
  * taken in a fixed order: a call repeats bit for bit.  rows == 0 writes
  * zeros to dweight and dbias.  The workspace needs 16-byte alignment.
  */
@@ -571,7 +576,8 @@ m3_status m3_state_load(const m3_dims* dims, m3_code code, m3_dtype dtype, const
  * m3_decode_step on cached states: reads each slot's codes, takes one step of
  * the recurrence in float, writes y from the new state before it is rounded,
  * and the new state's codes and scales into the slot.  The other arguments
- * and the reduced forms (lam, theta NULL) are those of m3_decode_step.
+ * and the reduced forms (lam, theta NULL) are those of m3_decode_step; y_t must
+ * not overlap an input.
  *
  * The codes are defined by float operations, each rounded, none fused, so
  * that every evaluation writes the same cache (a last bit can decide a code):

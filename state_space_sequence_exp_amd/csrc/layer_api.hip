@@ -89,6 +89,34 @@ m3::ScanArgs scan_args(const m3_scan_dims* d) {
   return a;
 }
 
+// Whether two arrays share an element: `rows` rows of n elements of es bytes,
+// ld elements apart.  Slices of one wider array (the same ld) lie between each
+// other's rows; arrays of different ld whose extents meet are taken to share.
+bool rows_meet(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t n,
+               size_t es) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t extent_a = ((uintptr_t)(rows - 1) * (uintptr_t)lda + (uintptr_t)n) * es;
+  const uintptr_t extent_b = ((uintptr_t)(rows - 1) * (uintptr_t)ldb + (uintptr_t)n) * es;
+  if (x >= y ? x - y >= extent_b : y - x >= extent_a) return false;
+  if (lda != ldb) return true;
+  const uintptr_t apart = x >= y ? x - y : y - x, pitch = (uintptr_t)lda * es, row = (uintptr_t)n * es;
+  const uintptr_t k = apart / pitch, at = apart % pitch;
+  return at < row || (at + row > pitch && k + 1 < (uintptr_t)rows);
+}
+// The same, but one array in the place of the other is fine.
+bool rows_cross(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t n,
+                size_t es) {
+  return !(a == b && lda == ldb) && rows_meet(a, lda, b, ldb, rows, n, es);
+}
+
+// Whether [a, a + na) and [b, b + nb) meet.
+bool bytes_meet(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x >= y ? x - y < nb : y - x < na;
+}
+
 // Whether [a, a + n) and [b, b + n) overlap without being the same.
 bool partial_overlap(const void* a, const void* b, size_t n) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -119,9 +147,12 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
     return M3_ERR_INVALID_VALUE;
   if (dims->batch == 0) return M3_SUCCESS;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dims->seqlen == 0)
+  const size_t state_bytes = (size_t)dims->batch * dims->channels * sizeof(float);
+  if (dims->seqlen == 0) {
+    if (h0 && h_last && partial_overlap(h0, h_last, state_bytes)) return M3_ERR_INVALID_VALUE;
     return h_last ? done(m3::launch_scan_empty(h0, h_last, dims->batch * dims->channels, s))
                   : M3_SUCCESS;
+  }
   const m3_status wst = check_scan_workspace(dims, dtype, workspace, workspace_bytes);
   if (wst != M3_SUCCESS) return wst;
   m3::ScanArgs a = scan_args(dims);
@@ -133,6 +164,11 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
   a.h_last = h_last;
   a.states = states;
   a.workspace = workspace;
+  const int64_t rows = a.B * a.T;
+  // (a sequence's last tile writes h_last while others may still read h0)
+  if (bytes_meet(h0, state_bytes, h_last, state_bytes) || rows_meet(y, a.ld_y, x, a.ld_x, rows, a.D, es) ||
+      rows_meet(y, a.ld_y, f, a.ld_f, rows, a.D, es) || rows_meet(y, a.ld_y, g, a.ld_g, rows, a.D, es))
+    return M3_ERR_INVALID_VALUE;
   return done(m3::launch_scan(a, dtype, s));
 }
 
@@ -153,9 +189,12 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
   }
   if (dims->batch == 0) return M3_SUCCESS;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dims->seqlen == 0)
+  const size_t state_bytes = (size_t)dims->batch * dims->channels * sizeof(float);
+  if (dims->seqlen == 0) {
+    if (dh_last && dh0 && partial_overlap(dh_last, dh0, state_bytes)) return M3_ERR_INVALID_VALUE;
     return dh0 ? done(m3::launch_scan_empty(dh_last, dh0, dims->batch * dims->channels, s))
                : M3_SUCCESS;
+  }
   const m3_status wst = check_scan_workspace(dims, dtype, workspace, workspace_bytes);
   if (wst != M3_SUCCESS) return wst;
   m3::ScanArgs a = scan_args(dims);
@@ -170,6 +209,17 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
   a.dg = dg;
   a.dh0 = dh0;
   a.workspace = workspace;
+  const int64_t rows = a.B * a.T;
+  const void* const out[] = {dx, df, dg};
+  const void* const in[] = {dy, x, f, g};
+  const int64_t ld_out[] = {a.ld_dx, a.ld_df, a.ld_dg}, ld_in[] = {a.ld_y, a.ld_x, a.ld_f, a.ld_g};
+  if (bytes_meet(dh_last, state_bytes, dh0, state_bytes)) return M3_ERR_INVALID_VALUE;
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (rows_meet(out[i], ld_out[i], in[j], ld_in[j], rows, a.D, es)) return M3_ERR_INVALID_VALUE;
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(out[i], ld_out[i], out[j], ld_out[j], rows, a.D, es)) return M3_ERR_INVALID_VALUE;
+  }
   return done(m3::launch_scan_backward(a, dtype, s));
 }
 
@@ -201,6 +251,9 @@ m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const flo
   a.f = f;
   a.g = g;
   a.y = y;
+  if (rows_meet(y, a.ld_y, x, a.ld_x, a.B, a.D, es) || rows_meet(y, a.ld_y, f, a.ld_f, a.B, a.D, es) ||
+      rows_meet(y, a.ld_y, g, a.ld_g, a.B, a.D, es))
+    return M3_ERR_INVALID_VALUE;
   return done(m3::launch_scan_step(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -256,10 +309,12 @@ m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
       !need(y, es) || !maybe(sum_out, es) || !maybe(mean, 4) || !maybe(rstd, 4))
     return M3_ERR_INVALID_VALUE;
   m3::NormArgs a = norm_args(dims);
-  // an output that is an input has to lie as it does, and the outputs differ
-  if (y == sum_out || (y == x && a.ld_y != a.ld_x) || (y == residual && a.ld_y != a.ld_res) ||
-      (sum_out && sum_out == x && a.ld_sum != a.ld_x) ||
-      (sum_out && sum_out == residual && a.ld_sum != a.ld_res))
+  // an output takes an input's place whole or not at all, and the outputs differ
+  if (rows_meet(y, a.ld_y, sum_out, a.ld_sum, a.rows, a.D, es) ||
+      rows_cross(y, a.ld_y, x, a.ld_x, a.rows, a.D, es) ||
+      rows_cross(y, a.ld_y, residual, a.ld_res, a.rows, a.D, es) ||
+      rows_cross(sum_out, a.ld_sum, x, a.ld_x, a.rows, a.D, es) ||
+      rows_cross(sum_out, a.ld_sum, residual, a.ld_res, a.rows, a.D, es))
     return M3_ERR_INVALID_VALUE;
   a.eps = eps;
   a.x = x;
@@ -295,7 +350,9 @@ m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const
     if (!need(dy, es) || !need(s, es) || !need(weight, 4) || !need(mean, 4) || !need(rstd, 4) ||
         !maybe(dsum, es) || !need(dx, es))
       return M3_ERR_INVALID_VALUE;
-    if ((dx == dy && a.ld_dx != a.ld_dy) || (dx == dsum && a.ld_dx != a.ld_dsum))
+    if (rows_cross(dx, a.ld_dx, dy, a.ld_dy, a.rows, a.D, es) ||
+        rows_cross(dx, a.ld_dx, dsum, a.ld_dsum, a.rows, a.D, es) ||
+        rows_meet(dx, a.ld_dx, s, a.ld_sum, a.rows, a.D, es))
       return M3_ERR_INVALID_VALUE;
     if (!workspace || workspace_bytes < m3_layer_norm_backward_workspace_size(dims, dtype))
       return M3_ERR_WORKSPACE;
@@ -400,6 +457,11 @@ m3_status m3_decode_step_cached(const m3_dims* dims, m3_dtype dtype, m3_code cod
     return M3_ERR_INVALID_VALUE;
   if (!maybe(lam, 4) || !maybe(theta, 4) || !maybe(x_prev, 4 * es) || !maybe(B_prev, 2 * es) ||
       (lam && (!x_prev || !B_prev)))
+    return M3_ERR_INVALID_VALUE;
+  const size_t units = (size_t)dims->batch * dims->nheads * R;
+  const size_t xy = units * dims->headdim_p * es, bc = units * dims->dstate_n * es;
+  if (bytes_meet(y_t, xy, x_t, xy) || bytes_meet(y_t, xy, B_t, bc) || bytes_meet(y_t, xy, C_t, bc) ||
+      (lam && (bytes_meet(y_t, xy, x_prev, xy) || bytes_meet(y_t, xy, B_prev, bc))))
     return M3_ERR_INVALID_VALUE;
   m3::CacheArgs a = cache_args(dims, codes, scales, slots, n_slots);
   a.R = (int)R;

@@ -285,3 +285,66 @@ def test_binding_refuses():
         m3.decode_step_cached(c, s, None, t, None, t, None, t, z, torch.zeros(2), z, None)
     with pytest.raises(ValueError):
         m3.decode_step_cached(c, s, torch.zeros(3, dtype=torch.int32), t, t, t, t, t, z, torch.zeros(2), z, None)
+
+
+def at(address):
+    return ctypes.c_void_p(address)
+
+
+def apart(n, first=0x10000000):
+    """n addresses 16 MiB apart."""
+    return [first + (i << 24) for i in range(n)]
+
+
+def refused(call, args, i, j, shift, **dims):
+    p = list(args)
+    p[i] = args[j] + shift
+    return call([at(a) for a in p], **dims) == INV
+
+
+def test_scan_overlaps(lib):
+    """An output over an input or another output is refused before anything is
+    enqueued; slices of one wider array are told apart by the length of a row."""
+    B, T, D = 2, 300, 64
+    fwd = lambda p, **ld: lib.m3_gated_scan(ctypes.byref(scan_dims(B, T, D, **ld)), 0, *p, OK, 1 << 40, None)
+    p = apart(7)                          # x f g h0 y h_last states
+    for i, j in ((4, 0), (4, 1), (4, 2)):
+        for shift in (0, 4, -4, 4 * (B * T * D - 1), -4 * (B * T * D - 1)):
+            assert refused(fwd, p, i, j, shift)
+    for shift in (0, 4, 4 * (B * D - 1)):
+        assert refused(fwd, p, 5, 3, shift)
+    wide = dict(ld_x=3 * D, ld_y=3 * D)   # x, then y: D, 2 D elements on
+    for shift in (0, 4 * (D - 1), 4 * (2 * D + 1), 4 * (7 * 3 * D - 1), -4 * (D - 1), -4 * (2 * D + 1)):
+        assert refused(fwd, p, 4, 0, shift, **wide)
+    assert refused(fwd, p, 4, 0, 4 * D, ld_x=3 * D, ld_y=2 * D)
+    bwd = lambda p: lib.m3_gated_scan_backward(ctypes.byref(scan_dims(B, T, D)), 0, *p, OK, 1 << 40, None)
+    p = apart(10)                         # dy x f g states dh_last dx df dg dh0
+    for i in (6, 7, 8):
+        for j in (0, 1, 2, 3, 6, 7, 8):
+            if i != j:
+                assert refused(bwd, p, i, j, 0) and refused(bwd, p, i, j, 4 * (B * T * D - 1))
+    assert refused(bwd, p, 9, 5, 0) and refused(bwd, p, 9, 5, -4)
+    step = lambda p: lib.m3_gated_scan_step(ctypes.byref(scan_dims(B, 1, D)), 0, *p, None)
+    p = apart(6)                          # h_in h_out x f g y
+    for j in (2, 3, 4):
+        assert refused(step, p, 5, j, 0) and refused(step, p, 5, j, 4 * (2 * D - 1))
+
+
+def test_norm_and_cache_overlaps(lib):
+    M, D = 4, 64
+    fwd = lambda p, **ld: lib.m3_layer_norm(ctypes.byref(norm_dims(M, D, **ld)), 0, *p[:4], 1e-5, *p[4:], None)
+    p = apart(8)                          # x residual weight bias y sum mean rstd
+    for i, j in ((4, 0), (4, 1), (5, 0), (5, 1), (4, 5)):
+        for shift in (4, -4, 4 * (M * D - 1)):
+            assert refused(fwd, p, i, j, shift)
+    assert refused(fwd, p, 4, 5, 0)
+    assert refused(fwd, p, 4, 0, 4 * (D - 1), ld_x=2 * D, ld_y=2 * D)
+    need = lib.m3_layer_norm_backward_workspace_size(ctypes.byref(norm_dims(M, D)), 0)
+    bwd = lambda p: lib.m3_layer_norm_backward(ctypes.byref(norm_dims(M, D)), 0, *p, OK, need, None)
+    p = apart(9)                          # dy s weight mean rstd dsum dx dweight dbias
+    for j, shift in ((0, 4), (5, -4), (1, 0), (1, 4 * D)):
+        assert refused(bwd, p, 6, j, shift)
+    dec = lambda p: lib.m3_decode_step_cached(ctypes.byref(cdims()), 0, 0, *p[:3], 9, *p[3:], None)
+    p = apart(13)                         # codes scales slots | x_t x_prev B_t B_prev C_t dt A lam theta y_t
+    for j in (3, 4, 5, 6, 7):
+        assert refused(dec, p, 12, j, 0) and refused(dec, p, 12, j, 4 * (2 * 2 * 2 * 64 - 1))
