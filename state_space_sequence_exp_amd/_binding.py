@@ -8,6 +8,7 @@ is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -518,23 +519,37 @@ def _type_code(t) -> int:
     return code
 
 
-def _launch(dev: int, stream, fn, *args):
-    """fn(*args, stream) with device `dev` current; raises M3Error."""
+def _launch(dev: int, fn, *args):
+    """fn(*args, stream) with device `dev` and its current stream; raises M3Error."""
     import torch
     if dev == torch._C._cuda_getDevice():
-        st = fn(*args, _raw_stream(dev, stream))
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev, stream))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != M3_SUCCESS:
         raise M3Error(st, fn.__name__)
 
 
-def _raw_stream(dev: int, stream) -> int:
-    import torch
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _streamed(fn):
+    """A function that works on the current stream, with an argument `stream`
+    (a torch stream or its handle, of the first tensor's device) that makes
+    another one current for the call: what the call allocates and zero-fills
+    is then ordered with its kernels."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        dev = (args[0] if args else next(iter(kw.values()))).get_device()
+        _gpu(dev)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream.device.index != dev:
+            raise ValueError("stream: of %s, expected the first tensor's device" % stream.device)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _at(t):
@@ -619,8 +634,9 @@ def _scan_workspace(lib, d, code, workspace, dev):
     return workspace, workspace.nbytes
 
 
+@_streamed
 def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool = False,
-               states=None, workspace=None, stream=None) -> Tuple:
+               states=None, workspace=None) -> Tuple:
     """Gated linear recurrence over a sequence (m3_gated_scan):
     h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(f), y = h * silu(g)
     (y = h without g).
@@ -661,13 +677,14 @@ def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool 
     if states is None and want_states:
         states = x.new_empty((nb, nc, nd), dtype=torch.float32)
     workspace, ws_bytes = _scan_workspace(lib, d, code, workspace, dev)
-    _launch(dev, stream, lib.m3_gated_scan, ctypes.byref(d), code, _at(x), _at(f), _at(g),
+    _launch(dev, lib.m3_gated_scan, ctypes.byref(d), code, _at(x), _at(f), _at(g),
             _at(h0), _at(y), _at(h_last), _at(states), _at(workspace), ws_bytes)
     return y, h_last, states
 
 
+@_streamed
 def gated_scan_backward(dy, x, f, g, states, *, dh_last=None, dx=None, df=None, dg=None,
-                        workspace=None, stream=None):
+                        workspace=None):
     """Gradients of sum(y * dy) (+ sum(h_last * dh_last)) for gated_scan's
     inputs (m3_gated_scan_backward).  `states` is what gated_scan kept for the
     same inputs; g None when it had none.  dx, df, dg may be given (slices of
@@ -693,7 +710,7 @@ def gated_scan_backward(dy, x, f, g, states, *, dh_last=None, dx=None, df=None, 
     dx, df, dg = new(dx), new(df), None if g is None else new(dg)
     dh0 = states.new_empty((nb, nd))
     workspace, ws_bytes = _scan_workspace(lib, d, code, workspace, dev)
-    _launch(dev, stream, lib.m3_gated_scan_backward, ctypes.byref(d), code, _at(dy), _at(x),
+    _launch(dev, lib.m3_gated_scan_backward, ctypes.byref(d), code, _at(dy), _at(x),
             _at(f), _at(g), _at(states), _at(dh_last), _at(dx), _at(df), _at(dg),
             _at(dh0), _at(workspace), ws_bytes)
     out = {"x": dx, "f": df, "h0": dh0}
@@ -702,7 +719,8 @@ def gated_scan_backward(dy, x, f, g, states, *, dh_last=None, dx=None, df=None, 
     return out
 
 
-def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None, stream=None) -> Tuple:
+@_streamed
+def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None) -> Tuple:
     """One token of the gated linear recurrence (m3_gated_scan_step).
 
     h [B,D] float32; x, f, g [B,D] float32 or bfloat16.  h_out defaults to h
@@ -726,13 +744,14 @@ def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None, stream=None) -> Tupl
     _gpu(dev)
     if y is None:
         y = _like(x, ld == 0)
-    _launch(dev, stream, lib.m3_gated_scan_step, ctypes.byref(d), code, _at(h), _at(h_out),
+    _launch(dev, lib.m3_gated_scan_step, ctypes.byref(d), code, _at(h), _at(h_out),
             _at(x), _at(f), _at(g), _at(y))
     return y, h_out
 
 
+@_streamed
 def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None, sum_out=None,
-               want_stats: bool = True, stream=None) -> Tuple:
+               want_stats: bool = True) -> Tuple:
     """Layer norm over the last dimension with the residual sum fused
     (m3_layer_norm): s = x + residual, y = (s - mean) rstd weight + bias.
 
@@ -768,13 +787,14 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None
     mean = rstd = None
     if want_stats:
         mean, rstd = weight.new_empty(shape[:-1]), weight.new_empty(shape[:-1])
-    _launch(dev, stream, lib.m3_layer_norm, ctypes.byref(d), code, _at(x), _at(residual),
+    _launch(dev, lib.m3_layer_norm, ctypes.byref(d), code, _at(x), _at(residual),
             _at(weight), _at(bias), float(eps), _at(y), _at(sum_out), _at(mean), _at(rstd))
     return y, s, mean, rstd
 
 
+@_streamed
 def layer_norm_backward(dy, s, weight, mean, rstd, *, dsum=None, dx=None, want_bias: bool = True,
-                        workspace=None, stream=None):
+                        workspace=None):
     """Gradients of layer_norm (m3_layer_norm_backward): s, mean and rstd as
     layer_norm returned them, dsum the gradient that reaches s past the norm
     (the residual stream's).  dx may be dy or dsum (in place).  Returns a
@@ -808,7 +828,7 @@ def layer_norm_backward(dy, s, weight, mean, rstd, *, dsum=None, dx=None, want_b
     elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and on the first tensor's device")
     ws_bytes = 0 if workspace is None else workspace.nbytes
-    _launch(dev, stream, lib.m3_layer_norm_backward, ctypes.byref(d), code, _at(dy), _at(s),
+    _launch(dev, lib.m3_layer_norm_backward, ctypes.byref(d), code, _at(dy), _at(s),
             _at(weight), _at(mean), _at(rstd), _at(dsum), _at(dx), _at(dw),
             _at(db), _at(workspace), ws_bytes)
     out = {"x": dx, "weight": dw}
@@ -842,7 +862,8 @@ def _cache_same(codes, scales, slots, dev):
     return code
 
 
-def state_store(h, codes, scales, slots=None, *, stream=None) -> None:
+@_streamed
+def state_store(h, codes, scales, slots=None) -> None:
     """Quantises states h [S,H,N,P] float32 into the cache's slots
     (m3_state_store).  slots [S] int32, negative or past the pool: idle; None:
     state i into slot i."""
@@ -855,11 +876,12 @@ def state_store(h, codes, scales, slots=None, *, stream=None) -> None:
     _gpu(dev)
     n, nh, nn, npd = codes.shape
     d = M3Dims(ns, 1, nh, npd, nn, 1)
-    _launch(dev, stream, lib.m3_state_store, ctypes.byref(d), code, _at(h), _at(codes),
+    _launch(dev, lib.m3_state_store, ctypes.byref(d), code, _at(h), _at(codes),
             _at(scales), _at(slots), n)
 
 
-def state_load(codes, scales, slots=None, *, dtype=None, h=None, stream=None):
+@_streamed
+def state_load(codes, scales, slots=None, *, dtype=None, h=None):
     """The states of the cache's slots [S,H,N,P] as float32 (or bfloat16 by
     dtype) (m3_state_load); zeros for idle slots; slots None: the whole pool."""
     import torch
@@ -876,13 +898,14 @@ def state_load(codes, scales, slots=None, *, dtype=None, h=None, stream=None):
     if h is None:
         h = scales.new_empty((ns, nh, nn, npd), dtype=dtype or torch.float32)
     d = M3Dims(ns, 1, nh, npd, nn, 1)
-    _launch(dev, stream, lib.m3_state_load, ctypes.byref(d), code, _type_code(h), _at(codes),
+    _launch(dev, lib.m3_state_load, ctypes.byref(d), code, _type_code(h), _at(codes),
             _at(scales), _at(slots), n, _at(h))
     return h
 
 
+@_streamed
 def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, A, lam, theta, *,
-                       y=None, stream=None):
+                       y=None):
     """One decode step on states in an 8-bit cache, in place
     (m3_decode_step_cached).
 
@@ -919,7 +942,7 @@ def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, 
     if y is None:
         y = (torch.empty if slots is None else torch.zeros)(xs, dtype=x_t.dtype, device=dev)
     d = M3Dims(ns, 1, nh, npd, nn, nr)
-    _launch(dev, stream, lib.m3_decode_step_cached, ctypes.byref(d), tcode, code, _at(codes),
+    _launch(dev, lib.m3_decode_step_cached, ctypes.byref(d), tcode, code, _at(codes),
             _at(scales), _at(slots), n, _at(x_t), _at(x_prev), _at(B_t), _at(B_prev),
             _at(C_t), _at(dt), _at(A), _at(lam), _at(theta), _at(y))
     return y

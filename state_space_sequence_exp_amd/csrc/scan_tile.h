@@ -253,15 +253,21 @@ __device__ __forceinline__ unsigned long long peek(const unsigned long long* p) 
 // About a quarter of a second of sleeps.
 constexpr int kScanSpins = 1 << 18;
 
-// The word at p once it is there; a NaN state and error word 1 if it never is.
+// The word at p once it is there; a NaN state and error word 1 if it never is
+// (or, seen now and then, if another wait has run out already).
 __device__ __forceinline__ unsigned long long await(const unsigned long long* p, int* err) {
   unsigned long long w = peek(p);
-  for (int i = 0; w == 0 && i < kScanSpins; ++i) {
+  for (int i = 1; w == 0 && i < kScanSpins; ++i) {
     __builtin_amdgcn_s_sleep(1);
     w = peek(p);
+    if (i % 256 == 0 &&
+        __hip_atomic_load(err, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0)
+      break;
   }
   if (w == 0) {
-    __hip_atomic_store(err, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    int none = 0;  // the first error stays
+    __hip_atomic_compare_exchange_strong(err, &none, 1, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
     w = word_of(0.f, __uint_as_float(0x7fc00000u));
   }
   return w;

@@ -298,3 +298,120 @@ def test_captured_and_replayed():
         got = [o.clone() for o in out]
         for a, b in zip(got, work(None)):
             assert torch.equal(a, b)
+
+
+def busy():
+    """Work that keeps the current stream from what is enqueued behind it for
+    some milliseconds."""
+    import torch
+    a = torch.zeros(4096, 4096, device="cuda")
+    for _ in range(16):
+        a = a @ a
+    return a
+
+
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_own_allocations_are_on_the_call_s_stream(handle):
+    """With `stream` the workspace that a call makes and zero-fills by itself
+    is ordered with its kernels, not with the current stream's work."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    _, t = draw(77, 3, 1100, 136, "bf16", True)
+    args = (t["x"], t["f"], t["g"])
+    want = m3.gated_scan(*args, h0=t["h0"], want_states=True)
+    wd = m3.gated_scan_backward(t["dy"], *args, want[2], dh_last=t["dh_last"])
+    side = torch.cuda.Stream()
+    at = side.cuda_stream if handle else side
+    dirty = torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del dirty
+    keep = busy()
+    got = m3.gated_scan(*args, h0=t["h0"], want_states=True, stream=at)
+    gd = m3.gated_scan_backward(t["dy"], *args, got[2], dh_last=t["dh_last"], stream=at)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(gd[k], wd[k]) for k in wd)
+    torch.cuda.synchronize()
+    del keep
+    base = m3.gated_scan(*args, h0=t["h0"], stream=0)     # the default stream's handle
+    torch.cuda.synchronize()
+    assert torch.equal(base[0], want[0])
+
+
+@pytest.mark.parametrize("ticket", [1 << 20, 1])
+def test_dirty_workspace_is_reported(ticket):
+    """A chain counter that is not zero on entry: the workgroups past the
+    chain's end compute nothing and set error word 2, those inside it wait for
+    a place that nobody takes until they see that word, and everything ends.  A
+    zero-filled workspace serves again."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    B, T, D = 1, 200, 64
+    v, t = draw(78, B, T, D, "f32", False)
+    ws = torch.zeros(m3.gated_scan_workspace_size(B, T, D, torch.float32), dtype=torch.uint8, device="cuda")
+    ws[256:260].view(torch.int32)[0] = ticket
+    y, _, st = m3.gated_scan(t["x"], t["f"], want_states=True, workspace=ws)
+    assert m3.prefill_workspace_error(ws, clear=True) == 2
+    if ticket == 1:
+        assert y[:, 128:].isnan().all()
+    ws.zero_()
+    y, _, st = m3.gated_scan(t["x"], t["f"], want_states=True, workspace=ws)
+    assert m3.prefill_workspace_error(ws) == 0 and not ws.any()
+    assert torch.equal(y, m3.gated_scan(t["x"], t["f"])[0])
+
+
+def test_two_calls_at_once():
+    """Calls that overlap on two streams, each with its own workspace."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    shapes = [(2, 3000, 520), (1, 6000, 200)]
+    ins = [draw(90 + i, *s, "bf16", True)[1] for i, s in enumerate(shapes)]
+    want = [m3.gated_scan(t["x"], t["f"], t["g"], want_states=True) for t in ins]
+    wd = [m3.gated_scan_backward(t["dy"], t["x"], t["f"], t["g"], w[2]) for t, w in zip(ins, want)]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, (t, s) in enumerate(zip(ins, streams)):
+            o = m3.gated_scan(t["x"], t["f"], t["g"], want_states=True, stream=s)
+            d = m3.gated_scan_backward(t["dy"], t["x"], t["f"], t["g"], o[2], stream=s)
+            got[i].append((o, d))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, d in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
+            assert all(torch.equal(d[k], wd[i][k]) for k in d)
+
+
+def test_graphs_share_a_workspace():
+    """Two captured graphs and eager calls of other shapes on one workspace,
+    one after the other."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    shapes = [(2, 900, 136), (1, 2500, 72)]
+    ins = [draw(95 + i, *s, "bf16", True)[1] for i, s in enumerate(shapes)]
+    need = max(m3.gated_scan_workspace_size(*s, torch.bfloat16) for s in shapes)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def work(t):
+        y, last, st = m3.gated_scan(t["x"], t["f"], t["g"], want_states=True, workspace=ws)
+        d = m3.gated_scan_backward(t["dy"], t["x"], t["f"], t["g"], st, workspace=ws)
+        return [y, last, st, d["x"], d["f"], d["g"], d["h0"]]
+
+    want = [[o.clone() for o in work(t)] for t in ins]
+    torch.cuda.synchronize()
+    graphs = []
+    for t in ins:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = work(t)
+        graphs.append((graph, out))
+    for k in range(4):
+        for i, (graph, out) in enumerate(graphs):
+            for o in out:
+                o.zero_()
+            graph.replay()
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+            assert all(torch.equal(a, b) for a, b in zip(work(ins[1 - i]), want[1 - i]))
+        torch.cuda.synchronize()
+    assert not ws.any()

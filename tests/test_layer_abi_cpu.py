@@ -252,6 +252,10 @@ def test_binding_refuses():
         m3.gated_scan_backward(x, x, x, None, torch.zeros(2, 1, 8), dg=x)
     with pytest.raises(ValueError):
         m3.gated_scan_step(torch.zeros(2, 8), x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        m3.gated_scan(x, x, stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        m3.gated_scan(x=x, f=x, stream=0)
     w = torch.ones(8)
     with pytest.raises(ValueError, match="GPU"):
         m3.layer_norm(x, w)
