@@ -117,20 +117,27 @@ __device__ __forceinline__ int slot_of(const CacheArgs& a, int i) {
   const int s = a.slots ? a.slots[i] : i;
   return (s < 0 || s >= a.n_slots) ? -1 : s;
 }
-// Whether an entry before i names the same slot (every thread of the
-// workgroup calls it and gets the same answer).
-__device__ __forceinline__ bool named_before(const CacheArgs& a, int i, int slot) {
-  if (!a.slots) return false;
+// Whether this thread sees an entry before i that names the same slot: the NT
+// threads of a workgroup look at all of them, 8 a thread in flight.
+template <int NT>
+__device__ __forceinline__ int named_before(const CacheArgs& a, int i, int slot) {
   int same = 0;
-  for (int j = threadIdx.x; j < i; j += kThreads) same |= a.slots[j] == slot ? 1 : 0;
-  return __syncthreads_or(same) != 0;
+  if (a.slots)
+    for (int j0 = threadIdx.x; j0 < i; j0 += 8 * NT) {
+      int s[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] = j0 + q * NT < i ? a.slots[j0 + q * NT] : -1;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) same |= s[q] == slot ? 1 : 0;
+    }
+  return same;
 }
 
 template <int kCode>
 __global__ void __launch_bounds__(kThreads) store_kernel(CacheArgs a) {
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
   const int slot = slot_of(a, i);
-  if (slot < 0 || named_before(a, i, slot)) return;
+  if (slot < 0 || __syncthreads_or(named_before<kThreads>(a, i, slot))) return;
   const int lanes = a.P / 8;
   const float* h = a.h_in + ((size_t)i * a.H + head) * a.N * a.P;
   const size_t unit = (size_t)slot * a.H + head;
@@ -285,10 +292,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(CacheArgs a) {
   }
   // of entries with one slot the first takes it; also the barrier before the
   // coefficients are read
-  int same = 0;
-  if (a.slots)
-    for (int j = tid; j < i; j += NT) same |= a.slots[j] == slot ? 1 : 0;
-  if (__syncthreads_or(same)) return;
+  if (__syncthreads_or(named_before<NT>(a, i, slot))) return;
 
   for (int kp = rg; kp < npair; kp += groups) {  // the lanes of a row together
     const PairCoef<R>& q = s_pair[kp];

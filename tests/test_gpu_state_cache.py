@@ -346,3 +346,41 @@ def test_captured_and_replayed():
         at = slots.long()
         assert torch.equal(back, b2) and torch.equal(y, y2)
         assert torch.equal(codes[at], c2[at]) and torch.equal(scales[at], s2[at])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_entries_repeated_slots(fmt):
+    """The first of a slot's entries is found however far ahead it lies, and
+    with the y of a call on another stream zero-filled there."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    from oracle import layer as O
+    S, H, N, P = 4500, 1, 4, 16
+    rng = np.random.default_rng(10)
+    slots = np.arange(S, dtype=np.int32)
+    for first, later in ((0, 4499), (1, 2049), (300, 301), (511, 512), (2047, 4095), (7, 520), (2500, 2600)):
+        slots[later] = first
+    kept = np.flatnonzero(slots == np.arange(S))
+    h = rows(rng, S, H, N, P)
+    codes, scales = m3.state_cache(S, H, N, P, code_type(fmt))
+    t = torch.from_numpy(slots).cuda()
+    m3.state_store(to_gpu_f32(h), codes, scales, t)
+    c, s = O.quantise(h[kept], fmt)
+    want = np.zeros((S, H, N, P), np.uint8)
+    want[kept] = c
+    assert np.array_equal(raw(codes), want)
+    _, g = decode_inputs(rng, S, H, N, P, 1, "bf16")
+    args = (g["x"], g["x_prev"], g["B"], g["B_prev"], g["C"], g["dt"], g["A"], g["lam"], g["theta"])
+    both = []
+    for stream in (None, torch.cuda.Stream()):
+        k = (codes.clone(), scales.clone())
+        torch.cuda.synchronize()
+        both.append((m3.decode_step_cached(*k, t, *args, stream=stream),) + k)
+        torch.cuda.synchronize()
+    for a, b in zip(*both):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    idle = np.setdiff1d(np.arange(S), kept)
+    assert not both[0][0][idle].any() and both[0][0][kept].flatten(1).any(1).all()
+    plain = (codes.clone(), scales.clone())
+    y = m3.decode_step_cached(*plain, None, *args)        # every state its own slot
+    assert torch.equal(y[kept], both[0][0][kept])
