@@ -786,7 +786,8 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None
         y = _like(x, ld == 0)
     mean = rstd = None
     if want_stats:
-        mean, rstd = weight.new_empty(shape[:-1]), weight.new_empty(shape[:-1])
+        mean = weight.new_empty(shape[:-1])
+        rstd = torch.empty_like(mean)
     _launch(dev, lib.m3_layer_norm, ctypes.byref(d), code, _at(x), _at(residual),
             _at(weight), _at(bias), float(eps), _at(y), _at(sum_out), _at(mean), _at(rstd))
     return y, s, mean, rstd
@@ -820,11 +821,11 @@ def layer_norm_backward(dy, s, weight, mean, rstd, *, dsum=None, dx=None, want_b
     _gpu(dev)
     if dx is None:
         dx = _like(s, d.ld_sum == 0)
-    dw = weight.new_empty((nd,))
-    db = weight.new_empty((nd,)) if want_bias else None
+    dw = torch.empty_like(weight)
+    db = torch.empty_like(weight) if want_bias else None
     need = int(lib.m3_layer_norm_backward_workspace_size(ctypes.byref(d), code))
     if workspace is None and need > 0:
-        workspace = weight.new_empty((need,), dtype=torch.uint8)
+        workspace = weight.new_empty((need + 3) // 4)
     elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and on the first tensor's device")
     ws_bytes = 0 if workspace is None else workspace.nbytes

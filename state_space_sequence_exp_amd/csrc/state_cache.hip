@@ -101,6 +101,49 @@ __device__ __forceinline__ float top8(const float (&h)[8]) {
   const float a = max_abs(max_abs(h[0], h[1]), h[2]), b = max_abs(max_abs(h[3], h[4]), h[5]);
   return max_abs(max_abs(a, b), max_abs(h[6], h[7]));
 }
+__device__ __forceinline__ float top16(const float (&h)[16]) {
+  float t = max_abs(h[0], h[1]);
+#pragma unroll
+  for (int e = 2; e < 16; e += 2) t = max_abs(max_abs(t, h[e]), h[e + 1]);
+  return t;
+}
+// a = (a of lanes 0-31, b of lanes 0-31), b = (a of 32-63, b of 32-63).
+__device__ __forceinline__ void swap_halves(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+// The same in quarters: a keeps its lanes 0-15 and 32-47 and gets b's of them
+// in 16-31 and 48-63; b gets a's of 16-31 and 48-63 in 0-15 and 32-47.
+__device__ __forceinline__ void swap_rows(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+template <int kCode>
+__device__ __forceinline__ void unpack16(const uint4& w, float scale, float (&v)[16]) {
+  Code<kCode>::unpack4(w.x, v);
+  Code<kCode>::unpack4(w.y, v + 4);
+  Code<kCode>::unpack4(w.z, v + 8);
+  Code<kCode>::unpack4(w.w, v + 12);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] *= scale;
+}
+// Codes of 16 values of a row.
+template <int kCode>
+__device__ __forceinline__ uint4 quantise16(const float (&h)[16], float amax, float inv) {
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = h[e] * inv;
+  const bool bad = !(amax < __builtin_inff());
+  if (__builtin_expect(__any(bad), 0)) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = bad ? 0.f : v[e];
+  }
+  return make_uint4(Code<kCode>::pack4(v), Code<kCode>::pack4(v + 4), Code<kCode>::pack4(v + 8),
+                    Code<kCode>::pack4(v + 12));
+}
+
 // Maximum over the `lanes` (2, 4, 8 or 16) consecutive lanes of a row, by lane
 // moves inside the 16 lanes of a DPP row: lane xor 1, xor 2, then (all four of
 // a quad being equal) the mirrored half row and row.
@@ -205,9 +248,33 @@ __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
 // and C of row 0 (R each) and of row 1.
 template <int R>
 struct PairCoef {
-  float cs, sn, pad[2];
+  float cs, sn, pad[R == 2 ? 6 : 2];
   float bp[2][R], b[2][R], c[2][R];
 };
+
+template <typename T, int R, bool kTrap, bool kRot, int NT>
+__device__ __forceinline__ void pair_coefficients(const CacheArgs& a, size_t in, int npair, float d,
+                                                  PairCoef<R>* s_pair) {
+  for (int kp = threadIdx.x; kp < npair; kp += NT) {
+    PairCoef<R>& q = s_pair[kp];
+    if constexpr (kRot) {
+      const float psi = d * a.theta[in * npair + kp];
+      sincosf(psi, &q.sn, &q.cs);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const size_t at = (in * R + r) * (2 * npair) + 2 * kp;
+      const float2 b = load_pair(static_cast<const T*>(a.B_t) + at);
+      const float2 c = load_pair(static_cast<const T*>(a.C_t) + at);
+      q.b[0][r] = b.x; q.b[1][r] = b.y;
+      q.c[0][r] = c.x; q.c[1][r] = c.y;
+      if constexpr (kTrap) {
+        const float2 p = load_pair(static_cast<const T*>(a.B_prev) + at);
+        q.bp[0][r] = p.x; q.bp[1][r] = p.y;
+      }
+    }
+  }
+}
 
 // sum_r b[r] x[r][e] in order, each product and sum rounded (a product of two
 // bfloat16 values is exact, so there the fused form is the same).
@@ -271,25 +338,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(CacheArgs a) {
   const float d = a.dt[in], la = kTrap ? a.lam[in] : 1.f;
   const float alpha = expf(d * a.A[head]);
   const float cu = (1.f - la) * d, cv = la * d;
-  for (int kp = tid; kp < npair; kp += NT) {
-    PairCoef<R>& q = s_pair[kp];
-    if constexpr (kRot) {
-      const float psi = d * a.theta[in * npair + kp];
-      sincosf(psi, &q.sn, &q.cs);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const size_t at = (in * R + r) * N + 2 * kp;
-      const float2 b = load_pair(static_cast<const T*>(a.B_t) + at);
-      const float2 c = load_pair(static_cast<const T*>(a.C_t) + at);
-      q.b[0][r] = b.x; q.b[1][r] = b.y;
-      q.c[0][r] = c.x; q.c[1][r] = c.y;
-      if constexpr (kTrap) {
-        const float2 p = load_pair(static_cast<const T*>(a.B_prev) + at);
-        q.bp[0][r] = p.x; q.bp[1][r] = p.y;
-      }
-    }
-  }
+  pair_coefficients<T, R, kTrap, kRot, NT>(a, in, npair, d, s_pair);
   // of entries with one slot the first takes it; also the barrier before the
   // coefficients are read
   if (__syncthreads_or(named_before<NT>(a, i, slot))) return;
@@ -365,7 +414,184 @@ hipError_t launch_decode_nt(const CacheArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// One wave a unit once there is a wave for every SIMD, four before that; from
+// The same step with the sums over r on the matrix units, a wave a unit, for
+// bfloat16 inputs, states of 64 columns and whole sets of 16 row pairs.
+//
+// A 16x16x1 instruction takes one r of the outer product of 16 rows with 64
+// columns and rounds each sum once, as a fused multiply-add does, so R of them
+// in order are rank_sum (a sum of zeros is +0 here, whatever their signs: the
+// cache holds the same values).  Lane (g, c) = (lane / 16, lane % 16) gets row
+// c's columns 16 g + 4 b + j as value j of block b, so that a lane has 16
+// consecutive columns where the x given to row 4 g + j of block b is that
+// column's.  The c are 16 row pairs, one product for the pair's first rows and
+// one for the second.
+//
+// What is left to the vector units is 17 operations an element at R = 4
+// instead of 23.5, and a row's scale costs half as much (four lanes share a
+// row, not eight).  Measured in turn on 256 x 32 units, N = 128, R = 4: 55 us
+// against 58.5 (int8) and 62.5 (e4m3); 128 x 64, N = 64, R = 1: 24.5 against
+// 26; R = 2: 27.5 against 30; 2048 units, N = 128, R = 4: 17.2 against 20.2;
+// 1024: 11.7 against 15.0.  Below 1024 units four waves a unit are faster (512:
+// 9.1 against 11.4), and with four waves this form is not (9.4); with 17 pairs
+// instead of 16 it takes 21 us against 19 (8192 units, R = 1).  165 registers at R = 4
+// let three waves run on a SIMD (unbounded it takes 207, two waves and 64 us).
+template <int R>
+__device__ __forceinline__ void outer(const float (&x)[R], const float (&b)[R], float (&v)[16]) {
+  typedef float f32x16 __attribute__((ext_vector_type(16)));
+  f32x16 t = f32x16(0.f);
+#pragma unroll
+  for (int r = 0; r < R; ++r) t = __builtin_amdgcn_mfma_f32_16x16x1f32(x[r], b[r], t, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = t[e];
+}
+
+template <int R, int kCode, bool kTrap, bool kRot>
+__global__ void __launch_bounds__(kWave, R > 2 ? 3 : 4) decode_outer_kernel(CacheArgs a) {
+#pragma clang fp contract(off)
+  constexpr int P = 64, kRound = R < 2 ? R : 2, kPitch = kRound * P + 4;
+  extern __shared__ __align__(16) float dsm[];
+  const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
+  const int slot = slot_of(a, i);
+  if (slot < 0) return;
+  const int N = a.N, npair = N / 2;
+  const int lane = threadIdx.x, g = lane / 16, c = lane % 16;
+  const size_t in = (size_t)i * a.H + head;       // this token's inputs
+  const size_t unit = (size_t)slot * a.H + head;  // its state
+  PairCoef<R>* s_pair = reinterpret_cast<PairCoef<R>*>(dsm);
+
+  char* codes = static_cast<char*>(a.codes) + unit * N * P;
+  float* scales = a.scales + unit * N;
+  struct In {
+    uint4 w0, w1;
+    float s0, s1;
+  };
+  // this lane's pair of the 16 from k0 on (behind the last: of the last ones, unused)
+  const auto request = [&](int k0) {
+    const int kp = min(k0, npair - 16) + c;
+    const uint32_t at = 2 * kp * P + 16 * g;
+    return In{*reinterpret_cast<const uint4*>(codes + at),
+              *reinterpret_cast<const uint4*>(codes + at + P), scales[2 * kp], scales[2 * kp + 1]};
+  };
+  In cur = request(0);
+  float xc[R], xq[R], yp[R][16];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const size_t at = (in * R + r) * P + 16 * (c / 4) + 4 * g + c % 4;
+    xc[r] = to_f32(static_cast<const bf16*>(a.x_t)[at]);
+    if constexpr (kTrap) xq[r] = to_f32(static_cast<const bf16*>(a.x_prev)[at]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) yp[r][e] = 0.f;
+  }
+  const float d = a.dt[in], la = kTrap ? a.lam[in] : 1.f;
+  const float alpha = expf(d * a.A[head]);
+  const float cu = (1.f - la) * d, cv = la * d;
+  pair_coefficients<bf16, R, kTrap, kRot, kWave>(a, in, npair, d, s_pair);
+  if (__syncthreads_or(named_before<kWave>(a, i, slot))) return;
+
+  for (int k0 = 0; k0 < npair; k0 += 16) {
+    const int kp = k0 + c;
+    const PairCoef<R>& q = s_pair[kp];
+    // one outer product at a time, behind the vector work that does not need
+    // it, kept in this order (the compiler's own takes more registers)
+    float v0[16], v1[16], o[16];
+    if constexpr (kTrap) outer<R>(xq, q.bp[0], o);
+    unpack16<kCode>(cur.w0, cur.s0, v0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kTrap) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v0[e] = v0[e] + cu * o[e];
+      outer<R>(xq, q.bp[1], o);
+    }
+    unpack16<kCode>(cur.w1, cur.s1, v1);
+    __builtin_amdgcn_sched_barrier(0);
+    cur = request(k0 + 16);
+    if constexpr (kTrap) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v1[e] = v1[e] + cu * o[e];
+    }
+    outer<R>(xc, q.b[0], o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float h0 = v0[e], h1 = v1[e];
+      if constexpr (kRot) {
+        const float n0 = q.cs * h0 - q.sn * h1, n1 = q.sn * h0 + q.cs * h1;
+        h0 = n0;
+        h1 = n1;
+      }
+      v0[e] = alpha * h0;
+      v1[e] = alpha * h1;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v0[e] = v0[e] + cv * o[e];
+    outer<R>(xc, q.b[1], o);
+    float top = top16(v0);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) yp[r][e] = __builtin_fmaf(q.c[0][r], v0[e], yp[r][e]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v1[e] = v1[e] + cv * o[e];
+    float top1 = top16(v1);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) yp[r][e] = __builtin_fmaf(q.c[1][r], v1[e], yp[r][e]);
+    // lanes 0-31 take the first rows' scales, 32-63 the second rows': one
+    // division for both
+    swap_halves(top, top1);
+    top = max_abs(top, top1);
+    top1 = top;
+    swap_rows(top, top1);
+    top = max_abs(top, top1);
+    float scale, i0;
+    row_scale<kCode>(top, &scale, &i0);
+    float i1 = i0, t0 = top, t1 = top;
+    swap_halves(i0, i1);
+    swap_halves(t0, t1);
+    const uint32_t at = 2 * kp * P + 16 * g;
+    *reinterpret_cast<uint4*>(codes + at) = quantise16<kCode>(v0, t0, i0);
+    *reinterpret_cast<uint4*>(codes + at + P) = quantise16<kCode>(v1, t1, i1);
+    if (g % 2 == 0) scales[2 * kp + g / 2] = scale;
+  }
+  // y: each lane's sums over its row pairs, then those of the 16 lanes that
+  // share its columns, up to two r at a time
+#pragma unroll
+  for (int r0 = 0; r0 < R; r0 += kRound) {
+    __syncthreads();  // the coefficients or the sums before these are read
+#pragma unroll
+    for (int r = 0; r < kRound; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(dsm + c * kPitch + r * P + 16 * g + e) =
+            make_float4(yp[r0 + r][e], yp[r0 + r][e + 1], yp[r0 + r][e + 2], yp[r0 + r][e + 3]);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRound; ++r) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sum += dsm[k * kPitch + r * P + lane];
+      static_cast<bf16*>(a.y)[(in * R + r0 + r) * P + lane] = from_f32<bf16>(sum);
+    }
+  }
+}
+
+template <int R, int kCode, bool kTrap, bool kRot>
+hipError_t launch_outer(const CacheArgs& a, hipStream_t stream) {
+  const size_t coef = sizeof(PairCoef<R>) * (a.N / 2);
+  const size_t part = sizeof(float) * 16 * ((R < 2 ? R : 2) * 64 + 4);
+  const size_t lds = coef > part ? coef : part;
+  const hipError_t e = lds_limit(
+      reinterpret_cast<const void*>(&decode_outer_kernel<R, kCode, kTrap, kRot>), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((decode_outer_kernel<R, kCode, kTrap, kRot>), dim3(a.S * a.H), dim3(kWave), lds,
+                     stream, a);
+  return hipGetLastError();
+}
+
+// The matrix units where they serve; else one wave a unit once there is a wave
+// for every SIMD, four before that; from
 // 2048 units on where a wave takes 16 turns or more (a workgroup of four then
 // pays longer), and always where a wave holds the whole unit.  Measured, us for
 // one wave / four: N = 128, P = 64, R = 4, bfloat16: 12.4 / 6.8 with 256 units,
@@ -377,6 +603,9 @@ template <typename T, int R, int kCode, bool kTrap, bool kRot>
 hipError_t launch_decode_form(const CacheArgs& a, hipStream_t stream) {
   const int groups = kWave / (a.P / 8), turns = (a.N / 2 + groups - 1) / groups;
   const int64_t units = (int64_t)a.S * a.H;
+  if constexpr (sizeof(T) == 2)
+    if (a.P == 64 && a.N % 32 == 0 && units >= 1024)
+      return launch_outer<R, kCode, kTrap, kRot>(a, stream);
   if (turns <= 1 || units >= (turns >= 16 ? 2048 : 1024))
     return launch_decode_nt<T, R, kCode, kTrap, kRot, 64>(a, stream);
   return launch_decode_nt<T, R, kCode, kTrap, kRot, 256>(a, stream);

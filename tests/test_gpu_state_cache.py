@@ -175,6 +175,8 @@ CASES = [
     (2, 1, 256, 16, 4), (1, 2, 22, 128, 2), (4, 3, 256, 64, 2),
     # a wave a unit: a wave for every SIMD and more, whole units, ragged pairs
     (37, 28, 66, 64, 1), (33, 32, 128, 64, 4), (130, 16, 98, 128, 2), (3, 5, 64, 16, 2), (1100, 1, 34, 32, 1),
+    # bfloat16: sums over r on the matrix units
+    (33, 32, 32, 64, 1), (9, 128, 96, 64, 2), (257, 4, 256, 64, 4), (1024, 1, 64, 64, 1),
 ]
 
 
@@ -384,3 +386,51 @@ def test_many_entries_repeated_slots(fmt):
     plain = (codes.clone(), scales.clone())
     y = m3.decode_step_cached(*plain, None, *args)        # every state its own slot
     assert torch.equal(y[kept], both[0][0][kept])
+
+
+@pytest.mark.parametrize("lam,theta", [(True, True), (False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("R", [1, 2, 4])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_batch_size_does_not_change_the_cache(fmt, R, lam, theta):
+    """A batch large enough for the matrix units writes the codes and scales
+    that small batches write, to the last bit (a zero's sign aside), with idle
+    and repeated entries, zero rows and a NaN among them.  Each y is a sum of N
+    fused terms in two orders, either off by at most N 2^-24 of the terms' sum
+    (a term is at most |C| times its row's largest value, Q scale), and rounded
+    to bfloat16 twice."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    S, H, N, P, step = 300, 4, 64, 64, 60
+    Q = 127 if fmt == "int8" else 448
+    rng = np.random.default_rng(61 + R)
+    _, t = decode_inputs(rng, S, H, N, P, R, "bf16")
+    h = rows(rng, S, H, N, P)
+    h[5] = 0
+    codes, scales = cache_with(h, fmt)
+    scales[7, 1, 9] = float("nan")
+    slots = torch.randperm(S, dtype=torch.int32, generator=torch.Generator().manual_seed(3))
+    slots[[3, 50, 299]] = torch.tensor([-1, S, -7], dtype=torch.int32)
+    slots[40] = slots[20]
+    slots = slots.cuda()
+    got = []
+    for n in (S, step):
+        c, s = codes.clone(), scales.clone()
+        y = torch.full((S, H, R, P), 3.0, dtype=torch.bfloat16, device="cuda")
+        for i in range(0, S, n):
+            k = slice(i, i + n)
+            m3.decode_step_cached(c, s, slots[k], t["x"][k], t["x_prev"][k] if lam else None, t["B"][k],
+                                  t["B_prev"][k] if lam else None, t["C"][k], t["dt"][k], t["A"],
+                                  t["lam"][k] if lam else None, t["theta"][k] if theta else None, y=y[k])
+        got.append((c, s, y.double()))
+    (c0, s0, y0), (c1, s1, y1) = got
+    assert torch.equal(c0.float(), c1.float()) and torch.equal(s0.nan_to_num(-1.0), s1.nan_to_num(-1.0))
+    assert (s0.isnan().sum() == 2) if theta else (s0.isnan().sum() == 1)
+    live = [i for i in range(S) if i not in (3, 40, 50, 299)]
+    assert (y0[[3, 40, 50, 299]] == 3).all()
+    size = s0[slots[live].long()].double().nan_to_num(0.0) * Q            # [live, H, N]
+    terms = (t["C"][live].double().abs() * size[:, :, None]).sum(-1)      # [live, H, R]
+    off = 2 * N * 2.0 ** -24 * terms[..., None]
+    nan = y0[live].isnan()
+    assert torch.equal(nan, y1[live].isnan()) and nan.sum() == R * P
+    tol = off + 2 * 2.0 ** -8 * (y1[live].abs() + off)
+    assert ((y0[live] - y1[live]).abs() <= tol)[~nan].all()
