@@ -203,27 +203,49 @@ __global__ void __launch_bounds__(kThreads) store_kernel(CacheArgs a) {
   }
 }
 
+// A thread reads the codes of one 16-byte vector of the output at a time (4
+// floats, 8 bfloat16), so that a wave writes whole lines, and has four in
+// flight: 68 us for 256 x 32 states of 128 x 64 into floats (4.9 TB/s), 41 us
+// into bfloat16.  (With 8 columns a thread, two vectors side by side, 92 and 46.)
 template <int kCode, typename T>
 __global__ void __launch_bounds__(kThreads) load_kernel(CacheArgs a) {
+  constexpr int E = 16 / (int)sizeof(T), W = E / 4, K = 4;
+  struct Words {
+    uint32_t w[W];
+  };
+  typedef T Out __attribute__((ext_vector_type(E)));
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
   const int slot = slot_of(a, i);
-  const int lanes = a.P / 8;
-  T* h = static_cast<T*>(a.h_out) + ((size_t)i * a.H + head) * a.N * a.P;
-  const size_t unit = (size_t)(slot < 0 ? 0 : slot) * a.H + head;
-  const uint2* codes =
-      reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(a.codes) + unit * a.N * a.P);
-  for (int p = threadIdx.x; p < a.N * lanes; p += kThreads) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (slot >= 0) {
-      const uint2 w = codes[p];
-      const float scale = a.scales[unit * a.N + p / lanes];
-      Code<kCode>::unpack4(w.x, v);
-      Code<kCode>::unpack4(w.y, v + 4);
+  const int lanes = a.P / E, all = a.N * lanes;
+  Out* h = reinterpret_cast<Out*>(static_cast<T*>(a.h_out) + ((size_t)i * a.H + head) * a.N * a.P);
+  if (slot < 0) {
+    for (int p = threadIdx.x; p < all; p += kThreads) h[p] = Out(from_f32<T>(0.f));
+    return;
+  }
+  const size_t unit = (size_t)slot * a.H + head;
+  const Words* codes =
+      reinterpret_cast<const Words*>(static_cast<const unsigned char*>(a.codes) + unit * a.N * a.P);
+  for (int p0 = threadIdx.x; p0 < all; p0 += K * kThreads) {
+    Words w[K];
+    float scale[K];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= scale;
+    for (int k = 0; k < K; ++k) {
+      const int p = min(p0 + k * kThreads, all - 1);
+      w[k] = codes[p];
+      scale[k] = a.scales[unit * a.N + p / lanes];
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[(size_t)p * 8 + e] = from_f32<T>(v[e]);
+    for (int k = 0; k < K; ++k) {
+      Out o;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float v[4];
+        Code<kCode>::unpack4(w[k].w[j], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[4 * j + e] = from_f32<T>(v[e] * scale[k]);
+      }
+      if (p0 + k * kThreads < all) h[p0 + k * kThreads] = o;
+    }
   }
 }
 
