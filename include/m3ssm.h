@@ -424,8 +424,8 @@ typedef struct {
   int64_t batch;    /* sequences (>= 0) */
   int64_t seqlen;   /* T (>= 0; ignored by m3_gated_scan_step) */
   int64_t channels; /* D (>= 1) */
-  /* elements from one token to the next, >= channels and < 2^22 - 1024; 0
-     means channels */
+  /* elements from one token to the next, >= channels; 0 means channels.  At
+     most 2^22 - 1024, but for single tokens (seqlen 1, the step) */
   int64_t ld_x, ld_f, ld_g, ld_y;    /* ld_y also of dy */
   int64_t ld_dx, ld_df, ld_dg;       /* backward only */
 } m3_scan_dims;
@@ -580,7 +580,8 @@ m3_status m3_state_load(const m3_dims* dims, m3_code code, m3_dtype dtype, const
  * not overlap an input.
  *
  * The codes are defined by float operations, each rounded, none fused, so
- * that every evaluation writes the same cache (a last bit can decide a code):
+ * that every evaluation writes the same cache (a last bit can decide a code;
+ * the sign of a zero is left open):
  *
  *   h = code * scale
  *   h = h + ((1 - lam) * dt) * (sum_r B_prev[r] * x_prev[r])

@@ -54,7 +54,7 @@ m3_status check_scan(const m3_scan_dims* d, bool backward) {
     if ((double)d->batch * (double)d->seqlen * (double)ld_of(lds[i], d->channels) > kMaxElements)
       return M3_ERR_NOT_SUPPORTED;
     // a chunk's rows are addressed by 32-bit byte offsets
-    if (ld_of(lds[i], d->channels) > kMaxScanLd) return M3_ERR_NOT_SUPPORTED;
+    if (d->seqlen > 1 && ld_of(lds[i], d->channels) > kMaxScanLd) return M3_ERR_NOT_SUPPORTED;
   }
   // one workgroup a chunk and channel tile, of 512 threads at most
   if (d->batch > INT_MAX || d->channels > INT_MAX / 2 || d->seqlen > INT_MAX - M3_SCAN_CHUNK ||

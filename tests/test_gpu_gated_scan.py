@@ -415,3 +415,26 @@ def test_graphs_share_a_workspace():
             assert all(torch.equal(a, b) for a, b in zip(work(ins[1 - i]), want[1 - i]))
         torch.cuda.synchronize()
     assert not ws.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_single_tokens_of_long_sequences(dtype):
+    """One token of every sequence, read out of arrays whose sequences lie
+    further apart than a chunk's rows may."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    B, T, D = 3, 4200, 1001
+    assert T * D > 1 << 22
+    _, t = draw(97, B, 1, D, dtype, True)
+    wide = [torch.zeros(B, T, D, dtype=torch_type(dtype), device="cuda") for _ in range(3)]
+    for w, k in zip(wide, "xfg"):
+        w[:, 4100] = t[k][:, 0]
+    want = m3.gated_scan(t["x"], t["f"], t["g"], h0=t["h0"], want_states=True)
+    got = m3.gated_scan(*(w[:, 4100:4101] for w in wide), h0=t["h0"], want_states=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    d = m3.gated_scan_backward(t["dy"], *(w[:, 4100:4101] for w in wide), got[2])
+    e = m3.gated_scan_backward(t["dy"], t["x"], t["f"], t["g"], want[2])
+    assert all(torch.equal(d[k], e[k]) for k in d)
+    y, h = m3.gated_scan_step(t["h0"].clone(), *(w[:, 4100] for w in wide))
+    z, k = m3.gated_scan_step(t["h0"].clone(), t["x"][:, 0], t["f"][:, 0], t["g"][:, 0])
+    assert torch.equal(y, z) and torch.equal(h, k)

@@ -42,7 +42,7 @@ def test_scan_shapes(lib, bad, code):
     assert lib.m3_gated_scan(ctypes.byref(d), 0, *[OK] * 7, ws, n, None) == code
     assert lib.m3_gated_scan_backward(ctypes.byref(d), 0, *[OK] * 10, ws, n, None) == code
     assert lib.m3_gated_scan_workspace_size(ctypes.byref(d), 0) == 0
-    if "t" not in bad:
+    if "t" not in bad and bad.get("ld_y") != 1 << 22:      # single tokens may lie that far apart
         assert lib.m3_gated_scan_step(ctypes.byref(d), 0, *[OK] * 6, None) == code
 
 
