@@ -14,6 +14,10 @@
 // the thread that owns it, over all rows of its workgroup (up to 256 groups of
 // rows); the teams of a workgroup are joined in the LDS, the groups by a
 // second kernel, both in a fixed order.
+//
+// 8192 x 2048 bfloat16 with the residual and its gradient: forward 26 us (5.1
+// TB/s), backward 29 and 4 for the joining kernel (4.6 without it); rows that
+// are not 16-byte aligned run at half to two thirds of that.
 #include <algorithm>
 
 #include "layer_internal.h"
