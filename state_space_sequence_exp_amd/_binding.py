@@ -648,6 +648,8 @@ def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool 
     want_states keeps the state entering every 64 tokens, for the backward.
     A workspace (gated_scan_workspace_size bytes, zero-filled once) may be
     kept for later calls; calls that overlap need distinct ones.
+    y, h_last and states may be given; y must not overlap an input, nor
+    h_last h0.
     Returns (y, h_last [B,D] float32, states [B,ceil(T/64),D] float32 or None).
     """
     import torch
