@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(ScanForward<T>::kThreads, 4) scan_kernel(ScanA
 
   Pack<T, V> x[K], f[K], g[K];
   const bool full = nt >= K && n >= V;
-  load_rows<kVec>(f, rf, full, nt, n, kPassGate<T>);
-  load_rows<kVec>(x, rx, full, nt, n, 0u);
+  load_rows<kVec>(f, rf, full, nt, n, a.D >= V, kPassGate<T>);
+  load_rows<kVec>(x, rx, full, nt, n, a.D >= V, 0u);
   // per token the map from the state before the thread's first
   float A[K][V], B[K][V];
   bool masks = false;  // in this wave
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(ScanForward<T>::kThreads, 4) scan_kernel(ScanA
   }
   if constexpr (kGate) {
     const Rows<T> rg(a.g, row0 * a.ld_g + d0, a.ld_g, tok, cl);
-    load_rows<kVec>(g, rg, full, nt, n, 0u);
+    load_rows<kVec>(g, rg, full, nt, n, a.D >= V, 0u);
   }
   __syncthreads();
   Run total = Run{1.f, 0.f};

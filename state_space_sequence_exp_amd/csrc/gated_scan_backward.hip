@@ -45,10 +45,10 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
 
   Pack<T, V> x[K], f[K], dy[K], g[K];
   const bool full = nt >= K && n >= V;
-  load_rows<kVec>(f, rf, full, nt, n, kPassGate<T>);
-  load_rows<kVec>(x, rx, full, nt, n, 0u);
-  load_rows<kVec>(dy, rd, full, nt, n, 0u);
-  if constexpr (kGate) load_rows<kVec>(g, rg, full, nt, n, 0u);
+  load_rows<kVec>(f, rf, full, nt, n, a.D >= V, kPassGate<T>);
+  load_rows<kVec>(x, rx, full, nt, n, a.D >= V, 0u);
+  load_rows<kVec>(dy, rd, full, nt, n, a.D >= V, 0u);
+  if constexpr (kGate) load_rows<kVec>(g, rg, full, nt, n, a.D >= V, 0u);
   // per token: the gate, the map from the state before the thread's first
   // token to that before this one, dL/dh without what comes from behind, and
   // dy silu'(g)

@@ -76,6 +76,23 @@ __device__ __forceinline__ uint32_t pack_word(const float (&v)[2]) {
 }
 __device__ __forceinline__ uint32_t pack_word(const float (&v)[1]) { return __float_as_uint(v[0]); }
 
+// Channel i of a pack becomes channel i - by (0 <= by), zeros behind.
+template <typename T, int V>
+__device__ __forceinline__ void move_down(Pack<T, V>& r, int by) {
+  constexpr int W = 4 / (int)sizeof(T), kWords = Pack<T, V>::kWords;
+#pragma unroll
+  for (int step = kWords / 2; step > 0; step /= 2)  // whole words
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      r.w[i] = by & (step * W) ? (i + step < kWords ? r.w[i + step] : 0u) : r.w[i];
+  if constexpr (W == 2)
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      r.w[i] = by & 1 ? r.w[i] >> 16 | (i + 1 < kWords ? r.w[i + 1] << 16 : 0u) : r.w[i];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) r.w[i] = by < V ? r.w[i] : 0u;
+}
+
 // n of V channels from p (n <= 0: none, zeros).  kVec: p is aligned to V
 // elements and n is V or <= 0; else p has element alignment and the last lane
 // of a row may hold fewer.
@@ -152,30 +169,53 @@ struct Rows {
   char* base;
   int64_t step;
   uint32_t at;
+  int tok, cl;
   __device__ __forceinline__ Rows(const void* p, int64_t first, int64_t ld, int tok, int cl)
       : base(static_cast<char*>(const_cast<void*>(p)) + first * (int64_t)sizeof(T)),
         step(ld * (int64_t)sizeof(T)),
-        at((uint32_t)((tok * (uint32_t)ld + cl) * sizeof(T))) {}
+        at((uint32_t)((tok * (uint32_t)ld + cl) * sizeof(T))),
+        tok(tok),
+        cl(cl) {}
   __device__ __forceinline__ void* operator[](int k) const { return base + k * step + at; }
+  // row k (it may be negative: the tile's rows before the thread's), `less`
+  // channels down
+  __device__ __forceinline__ const void* below(int k, int less) const {
+    return base + (int64_t)(cl - less) * (int64_t)sizeof(T) + (uint32_t)((tok + k) * (uint32_t)step);
+  }
 };
 
 // A thread's K tokens of an array: `nt` of them inside the sequence and `n` of
 // the lane's channels inside the row (`full`: all); what lies outside is
-// filled with `fill` words.
+// filled with `fill` words, channels with zeros.
+//
+// Rows that are not vectors throughout: where a row has V channels at all
+// (`wide`), a thread at an edge loads the last token again and the row's last
+// V channels, and moves its own down once every load is under way.  (Guarded
+// loads of a cut vector's channels wait for each other: B3 T777 D1023 bfloat16
+// 17.2 us against 12.4, D1001 13.2 against 12.4.  Whole vectors, which are
+// there or not, are faster under guards: D1000 10.7 against 11.3.)
 template <bool kVec, typename T, int V, int K>
 __device__ __forceinline__ void load_rows(Pack<T, V> (&v)[K], const Rows<T>& r, bool full, int nt,
-                                          int n, uint32_t fill) {
+                                          int n, bool wide, uint32_t fill) {
   if (full) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = load_pack<T, V, kVec>(r[k], V);
+    return;
+  }
+  if (!kVec && wide) {
+    const int less = n < V ? V - n : 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = load_pack<T, V, kVec>(r.below(min(k, nt - 1), less), V);
+#pragma unroll
+    for (int k = 0; k < K; ++k) move_down<T, V>(v[k], less);
   } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      v[k] = load_pack<T, V, kVec>(r[k], k < nt ? n : 0);
-#pragma unroll
-      for (int i = 0; i < v[k].kWords; ++i) v[k].w[i] = k < nt ? v[k].w[i] : fill;
-    }
+    for (int k = 0; k < K; ++k) v[k] = load_pack<T, V, kVec>(r[k], k < nt ? n : 0);
   }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < v[k].kWords; ++i) v[k].w[i] = k < nt ? v[k].w[i] : fill;
 }
 template <bool kVec, typename T, int V, int K>
 __device__ __forceinline__ void store_rows(const Pack<T, V> (&v)[K], const Rows<T>& r, bool full,

@@ -47,6 +47,8 @@ CASES = [
     # B, T, D: one token, one chunk and its ends, ragged chunks, odd widths, several groups of chunks
     (1, 1, 8), (2, 1, 1), (3, 2, 65), (1, 7, 130), (2, 255, 64), (2, 256, 72), (1, 257, 200),
     (2, 63, 20), (1, 64, 64), (2, 65, 128), (2, 127, 64), (2, 128, 132), (1, 129, 200), (2, 513, 33), (3, 777, 129), (1, 2100, 16), (5, 300, 256), (1, 4500, 12),
+    # cut vectors at the ends of rows and of tiles, rows narrower than a vector
+    (2, 70, 2), (1, 200, 3), (2, 131, 131), (1, 140, 387), (3, 65, 67), (2, 1, 5),
 ]
 
 
