@@ -16,8 +16,7 @@
 // second kernel, both in a fixed order.
 //
 // 8192 x 2048 bfloat16 with the residual and its gradient: forward 26 us (5.1
-// TB/s), backward 29 and 4 for the joining kernel (4.6 without it); rows that
-// are not 16-byte aligned run at half to two thirds of that.
+// TB/s), backward 29 and 4 for the joining kernel (4.6 without it); at 0.6 to 0.9 of that.
 #include <algorithm>
 
 #include "layer_internal.h"
@@ -62,19 +61,35 @@ __device__ __forceinline__ Vec pack(const float (&v)[kE<T>]) {
 // n of a vector's elements at p (n <= 0: none; the rest zeros).  kVec: rows
 // are 16-byte aligned and n is a whole vector or <= 0; else elements are
 // aligned and the last vector of a row may be cut.
+//
+// A cut vector of bfloat16 (`wide`) is loaded as the row's last 8 elements, and
+// trim moves its own down when they are used, not before: guarded loads of
+// single elements are put together as they arrive and so wait for each other
+// in every row, and for the row that was requested ahead.  16384 rows with the
+// residual, forward / backward: 2047 wide 48 / 63 us against 52 / 86, 2100 wide
+// 61 / 102 against 96 / 100, 4095 wide 117 / 141 against 198 / 210.  One element
+// alone waits for nobody (4097 wide: 143 / 216 against 117 / 183), nor do
+// floats, each of which has a register (4095 wide: 228 / 252 against 224 / 209).
+template <typename T>
+__device__ __forceinline__ bool loads_whole(int D) {
+  return sizeof(T) == 2 && D >= kE<T> && D % kE<T> != 1;
+}
 template <typename T, bool kVec>
-__device__ __forceinline__ Vec load_vec(const T* p, int n) {
+__device__ __forceinline__ Vec load_vec(const T* p, int n, bool wide) {
+  constexpr int E = kE<T>;
   Vec r = {{0u, 0u, 0u, 0u}};
-  if (n >= kE<T>) {
-    if constexpr (kVec) {
+  if constexpr (kVec) {
+    if (n >= E) {
       const uint4 u = *reinterpret_cast<const uint4*>(p);
       r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
-    } else {
-      __builtin_memcpy(r.w, p, 16);
     }
-  } else if constexpr (!kVec) {
+  } else if (wide) {
+    if (n > 0) __builtin_memcpy(r.w, p - (n < E ? E - n : 0), 16);
+  } else if (n >= E) {
+    __builtin_memcpy(r.w, p, 16);
+  } else {
 #pragma unroll
-    for (int i = 0; i < kE<T>; ++i)
+    for (int i = 0; i < E; ++i)
       if (i < n) {
         if constexpr (sizeof(T) == 2)
           r.w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i & 1));
@@ -83,6 +98,22 @@ __device__ __forceinline__ Vec load_vec(const T* p, int n) {
       }
   }
   return r;
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void trim(Vec& r, int n, bool wide) {
+  constexpr int E = kE<T>, W = 4 / (int)sizeof(T);
+  if (!kVec && sizeof(T) == 2 && wide && n > 0 && n < E) {
+    const int by = E - n;
+#pragma unroll
+    for (int step = 2; step > 0; step /= 2)  // whole words
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r.w[i] = by & (step * W) ? (i + step < 4 ? r.w[i + step] : 0u) : r.w[i];
+    if constexpr (W == 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r.w[i] = by & 1 ? r.w[i] >> 16 | (i < 3 ? r.w[i + 1] << 16 : 0u) : r.w[i];
+  }
 }
 template <typename T, bool kVec>
 __device__ __forceinline__ void store_vec(T* p, int n, const Vec& r) {
@@ -132,11 +163,22 @@ __device__ __forceinline__ float team_sum(float v, float* s) {
   return v;
 }
 
+// Waves a SIMD that the forward kernel's registers allow.  The launch has as
+// many workgroups as that makes, each walking as many rows as the others: with
+// more, those that find no place start when the rest is done (1000 x 4097
+// float with the residual: 16.2 us for four a compute unit where two fit, 13.8
+// for two; 1000 x 6001: 21.1 and 18.2).
 template <typename T, int TPR, int NV, bool kVec>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs a) {
+constexpr int kNormWaves = NV == 1 ? (sizeof(T) == 2 && TPR == 512 && !kVec ? 6 : 8)
+                           : TPR == 512 && NV == 2 ? 6
+                           : sizeof(T) == 4 && NV == 2 && kVec ? 8 : 4;
+
+template <typename T, int TPR, int NV, bool kVec>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256, (kNormWaves<T, TPR, NV, kVec>)) norm_kernel(NormArgs a) {
   constexpr int E = kE<T>, NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
   __shared__ float s_sum[2][NT / kWave];
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+  const bool wide = loads_whole<T>(a.D);
   const float inv = 1.f / (float)a.D;
   float w[NV][E], b[NV][E];
 #pragma unroll
@@ -155,9 +197,9 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs a)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e0 = (j * TPR + t) * E, n = row < a.rows ? a.D - e0 : 0;
-      p[j] = load_vec<T, kVec>(static_cast<const T*>(a.x) + row * a.ld_x + e0, n);
+      p[j] = load_vec<T, kVec>(static_cast<const T*>(a.x) + row * a.ld_x + e0, n, wide);
       if (a.residual)
-        q[j] = load_vec<T, kVec>(static_cast<const T*>(a.residual) + row * a.ld_res + e0, n);
+        q[j] = load_vec<T, kVec>(static_cast<const T*>(a.residual) + row * a.ld_res + e0, n, wide);
     }
   };
   if constexpr (kAhead) request(r, next_x, next_res);
@@ -176,9 +218,12 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_kernel(NormArgs a)
     float v[NV][E], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      const int n = a.D - (j * TPR + t) * E;
+      trim<T, kVec>(x[j], n, wide);
       unpack<T>(x[j], v[j]);
       if (a.residual) {
         float q[E];
+        trim<T, kVec>(res[j], n, wide);
         unpack<T>(res[j], q);
 #pragma unroll
         for (int i = 0; i < E; ++i) v[j][i] += q[i];
@@ -228,6 +273,7 @@ struct BwRow {
 };
 template <typename T, int TPR, int NV, bool kVec>
 __device__ __forceinline__ void load_bw(const NormArgs& a, int64_t r, int t, BwRow<T, NV>& q) {
+  const bool wide = loads_whole<T>(a.D);
   if (r >= a.rows) {  // a row of zeros adds nothing
 #pragma unroll
     for (int j = 0; j < NV; ++j) q.s[j] = q.dy[j] = q.ds[j] = Vec{{0u, 0u, 0u, 0u}};
@@ -237,9 +283,9 @@ __device__ __forceinline__ void load_bw(const NormArgs& a, int64_t r, int t, BwR
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e0 = (j * TPR + t) * kE<T>, n = a.D - e0;
-    q.s[j] = load_vec<T, kVec>(static_cast<const T*>(a.sum) + r * a.ld_sum + e0, n);
-    q.dy[j] = load_vec<T, kVec>(static_cast<const T*>(a.dy) + r * a.ld_dy + e0, n);
-    q.ds[j] = a.dsum ? load_vec<T, kVec>(static_cast<const T*>(a.dsum) + r * a.ld_dsum + e0, n)
+    q.s[j] = load_vec<T, kVec>(static_cast<const T*>(a.sum) + r * a.ld_sum + e0, n, wide);
+    q.dy[j] = load_vec<T, kVec>(static_cast<const T*>(a.dy) + r * a.ld_dy + e0, n, wide);
+    q.ds[j] = a.dsum ? load_vec<T, kVec>(static_cast<const T*>(a.dsum) + r * a.ld_dsum + e0, n, wide)
                      : Vec{{0u, 0u, 0u, 0u}};
   }
   q.mean = a.mean[r];
@@ -279,6 +325,10 @@ __global__ void __launch_bounds__(kBwThreads) norm_backward_kernel(NormArgs a, i
     float q[NV][E], g[NV][E], sp = 0.f, spq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      const int n = a.D - (j * TPR + t) * E;
+      trim<T, kVec>(cur.s[j], n, loads_whole<T>(a.D));
+      trim<T, kVec>(cur.dy[j], n, loads_whole<T>(a.D));
+      trim<T, kVec>(cur.ds[j], n, loads_whole<T>(a.D));
       unpack<T>(cur.s[j], q[j]);
       unpack<T>(cur.dy[j], g[j]);
 #pragma unroll
@@ -388,17 +438,17 @@ bool vec16(const void* p, int64_t ld, size_t es) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)ld * es % 16 == 0);
 }
 
+template <typename T, int TPR, int NV, bool kVec>
+hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
+  constexpr int NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
+  const int64_t most = 256 * (kNormWaves<T, TPR, NV, kVec> * 4 * kWave / NT);
+  const dim3 grid((unsigned)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, most));
+  hipLaunchKernelGGL((norm_kernel<T, TPR, NV, kVec>), grid, dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
 template <typename T, int TPR, int NV>
 hipError_t launch_fwd(const NormArgs& a, bool vec, hipStream_t stream) {
-  constexpr int NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
-  // up to 2048 threads a compute unit, each team walking its rows
-  const int64_t most = 256 * (2048 / NT);
-  const dim3 grid((unsigned)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, most));
-  if (vec)
-    hipLaunchKernelGGL((norm_kernel<T, TPR, NV, true>), grid, dim3(NT), 0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_kernel<T, TPR, NV, false>), grid, dim3(NT), 0, stream, a);
-  return hipGetLastError();
+  return vec ? launch_fwd_v<T, TPR, NV, true>(a, stream) : launch_fwd_v<T, TPR, NV, false>(a, stream);
 }
 
 // The team for a row of `vecs` vectors: one a thread up to 1024; wide float

@@ -39,7 +39,9 @@ def run_case(M, D, dtype, residual, bias, seed, x=None, eps=1e-5):
 
 
 SHAPES = [(1, 1), (1, 2), (3, 5), (2, 64), (7, 65), (5, 127), (1, 512), (70, 520), (300, 72), (9, 1001),
-          (4, 2048), (1030, 264), (33, 4097), (6, 8192), (3, 16384), (2, 16383), (4101, 520), (5003, 1000), (1030, 4100), (7, 6001)]
+          (4, 2048), (1030, 264), (33, 4097), (6, 8192), (3, 16384), (2, 16383), (4101, 520), (5003, 1000), (1030, 4100), (7, 6001),
+          # rows whose last vector is cut after 1 to 7 elements
+          (5, 9), (41, 130), (40, 131), (300, 1100), (50, 2045), (260, 1030), (600, 2047)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
