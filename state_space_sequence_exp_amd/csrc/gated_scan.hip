@@ -6,9 +6,9 @@
 //
 // Bound by memory: x, f and g are read once and y is written once.  B1 T16384
 // D4096 bfloat16 with the gate takes 113 us (4.8 TB/s, 5.2 with the chain's
-// words; copies reach 5.2 to 6.1).  What a short call takes is
-// the latency of its steps: 10 us for B3 T777 D1024, of which about 1 us a
-// place of the chain; rows that are not vectors throughout add 2 us to that.
+// words; copies reach 5.2 to 6.1).  What a short call takes is the latency of
+// its steps: 10 us for B3 T777 D1024, of which about 1 us a place of the chain;
+// rows that are not vectors throughout add 2 us to that.
 //
 // A workgroup requests its chunk of x and f and walks each thread's tokens
 // once, keeping for every token the map from the state before the thread's

@@ -16,7 +16,8 @@
 // second kernel, both in a fixed order.
 //
 // 8192 x 2048 bfloat16 with the residual and its gradient: forward 26 us (5.1
-// TB/s), backward 29 and 4 for the joining kernel (4.6 without it); at 0.6 to 0.9 of that.
+// TB/s), backward 29 and 4 for the joining kernel (4.6 without it); rows that
+// are not 16-byte aligned run at 0.6 to 0.9 of that.
 #include <algorithm>
 
 #include "layer_internal.h"
