@@ -449,10 +449,11 @@ size_t m3_gated_scan_workspace_size(const m3_scan_dims* dims, m3_dtype dtype);
  * The whole sequence: y for every token, h_last if not NULL, states if not
  * NULL.  g, h0 (zeros) may be NULL.  Pointers need element alignment only;
  * where every array's rows start at a multiple of four elements and channels
- * is one, they are moved as such vectors.  y must not
- * overlap x, f or g (slices of one wider array lie between each other's rows),
- * nor h_last h0.  seqlen == 0 writes h_last = h0 (zeros when NULL; there it may
- * be h0 itself); batch == 0 enqueues nothing.
+ * is one, they are moved as such vectors.  The outputs and the workspace must
+ * not overlap the inputs or each other (slices of one wider array lie between
+ * each other's rows; rows at different distances whose extents meet are
+ * refused).  seqlen == 0 writes h_last = h0 (zeros when NULL; there it may be
+ * h0 itself); batch == 0 enqueues nothing.
  */
 m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x, const void* f,
                         const void* g, const float* h0, void* y, float* h_last, float* states,
@@ -468,9 +469,9 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
  *
  * dx, df, dg in the storage type, dh0 float.  Where the gate is a mask (a is
  * 0 or 1 in float) df is 0; where it passes the state, dx is 0.  dh_last and
- * dh0 may be NULL; dg is required exactly when g is given.  The outputs must
- * not overlap the inputs or each other, nor dh0 dh_last.  seqlen == 0 writes
- * dh0 = dh_last.
+ * dh0 may be NULL; dg is required exactly when g is given.  The outputs and
+ * the workspace must not overlap the inputs or each other, as above.  seqlen
+ * == 0 writes dh0 = dh_last.
  */
 m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const void* dy,
                                  const void* x, const void* f, const void* g,
@@ -481,8 +482,8 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
 /*
  * One token for `batch` sequences (dims->seqlen ignored; row b of x, f, g, y
  * at b ld): h_out = a h_in + (1 - a) x, y = h_out * silu(g).  h_in, h_out
- * [batch, D] float, dense; h_out may be h_in but must not partially overlap
- * it; y must not overlap x, f or g.  g may be NULL.
+ * [batch, D] float, dense; h_out may be h_in.  The outputs must not overlap
+ * the inputs otherwise, nor each other.  g may be NULL.
  */
 m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const float* h_in,
                              float* h_out, const void* x, const void* f, const void* g, void* y,

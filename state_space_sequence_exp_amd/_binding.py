@@ -648,8 +648,8 @@ def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool 
     want_states keeps the state entering every 64 tokens, for the backward.
     A workspace (gated_scan_workspace_size bytes, zero-filled once) may be
     kept for later calls; calls that overlap need distinct ones.
-    y, h_last and states may be given; y must not overlap an input, nor
-    h_last h0.
+    y, h_last and states may be given; they must not overlap an input or
+    each other.
     Returns (y, h_last [B,D] float32, states [B,ceil(T/64),D] float32 or None).
     """
     import torch
@@ -726,7 +726,8 @@ def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None) -> Tuple:
     """One token of the gated linear recurrence (m3_gated_scan_step).
 
     h [B,D] float32; x, f, g [B,D] float32 or bfloat16.  h_out defaults to h
-    itself (in-place update).  Returns (y [B,D], h_out)."""
+    itself (in-place update); y must not lie over either.  Returns (y [B,D],
+    h_out)."""
     import torch
     lib = _lib or load_library()
     shape, dev, dt = x.shape, x.get_device(), x.dtype

@@ -89,38 +89,64 @@ m3::ScanArgs scan_args(const m3_scan_dims* d) {
   return a;
 }
 
-// Whether two arrays share an element: `rows` rows of n elements of es bytes,
-// ld elements apart.  Slices of one wider array (the same ld) lie between each
-// other's rows; arrays of different ld whose extents meet are taken to share.
-bool rows_meet(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t n,
-               size_t es) {
-  if (!a || !b) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  const uintptr_t extent_a = ((uintptr_t)(rows - 1) * (uintptr_t)lda + (uintptr_t)n) * es;
-  const uintptr_t extent_b = ((uintptr_t)(rows - 1) * (uintptr_t)ldb + (uintptr_t)n) * es;
-  if (x >= y ? x - y >= extent_b : y - x >= extent_a) return false;
-  if (lda != ldb) return true;
-  const uintptr_t apart = x >= y ? x - y : y - x, pitch = (uintptr_t)lda * es, row = (uintptr_t)n * es;
-  const uintptr_t k = apart / pitch, at = apart % pitch;
-  return at < row || (at + row > pitch && k + 1 < (uintptr_t)rows);
+// The memory of one array of a call: `rows` rows of `row` bytes, `pitch` bytes
+// apart (a null array has none).
+struct Span {
+  uintptr_t at;
+  uintptr_t rows, row, pitch;
+};
+Span rows_of(const void* p, int64_t rows, int64_t n, int64_t ld, size_t es) {
+  if (!p || rows < 1) return Span{};
+  const uintptr_t row = (uintptr_t)n * es;
+  return Span{reinterpret_cast<uintptr_t>(p), (uintptr_t)rows, row, rows > 1 ? (uintptr_t)ld * es : row};
+}
+Span bytes_of(const void* p, size_t n) {
+  return p && n ? Span{reinterpret_cast<uintptr_t>(p), 1, n, n} : Span{};
+}
+
+// Whether two arrays share a byte.  Slices of one wider array (the same pitch)
+// lie between each other's rows, and so may a dense array; arrays of different
+// pitch whose extents meet are taken to share.
+bool meet(const Span& a, const Span& b) {
+  if (!a.row || !b.row) return false;
+  const Span &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
+  const uintptr_t off = hi.at - lo.at;
+  if (off >= (lo.rows - 1) * lo.pitch + lo.row) return false;
+  if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
+  const uintptr_t k = off / lo.pitch, at = off % lo.pitch;
+  return at < lo.row || (at + hi.row > lo.pitch && k + 1 < lo.rows);
 }
 // The same, but one array in the place of the other is fine.
-bool rows_cross(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t n,
-                size_t es) {
-  return !(a == b && lda == ldb) && rows_meet(a, lda, b, ldb, rows, n, es);
+bool cross(const Span& a, const Span& b) {
+  const bool same = a.at == b.at && a.rows == b.rows && a.row == b.row && a.pitch == b.pitch;
+  return !same && meet(a, b);
+}
+// Whether an output lies over an input or another output.
+template <size_t NO, size_t NI>
+bool outputs_meet(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+    for (size_t j = 0; j < NI; ++j)
+      if (meet(out[i], in[j])) return true;
+  }
+  return false;
 }
 
 // Whether [a, a + na) and [b, b + nb) meet.
 bool bytes_meet(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x >= y ? x - y < nb : y - x < na;
+  return meet(bytes_of(a, na), bytes_of(b, nb));
 }
 
 // Whether [a, a + n) and [b, b + n) overlap without being the same.
 bool partial_overlap(const void* a, const void* b, size_t n) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x != y && x < y + n && y < x + n;
+}
+
+// What a call may write of its workspace.
+Span workspace_of(const m3_scan_dims* d, m3_dtype dtype, void* workspace) {
+  return bytes_of(workspace, m3_gated_scan_workspace_size(d, dtype));
 }
 
 }  // namespace
@@ -164,11 +190,13 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
   a.h_last = h_last;
   a.states = states;
   a.workspace = workspace;
-  const int64_t rows = a.B * a.T;
   // (a sequence's last tile writes h_last while others may still read h0)
-  if (bytes_meet(h0, state_bytes, h_last, state_bytes) || rows_meet(y, a.ld_y, x, a.ld_x, rows, a.D, es) ||
-      rows_meet(y, a.ld_y, f, a.ld_f, rows, a.D, es) || rows_meet(y, a.ld_y, g, a.ld_g, rows, a.D, es))
-    return M3_ERR_INVALID_VALUE;
+  const int64_t rows = a.B * a.T;
+  const Span out[] = {rows_of(y, rows, a.D, a.ld_y, es), bytes_of(h_last, state_bytes),
+                      bytes_of(states, state_bytes * a.nC), workspace_of(dims, dtype, workspace)};
+  const Span in[] = {rows_of(x, rows, a.D, a.ld_x, es), rows_of(f, rows, a.D, a.ld_f, es),
+                     rows_of(g, rows, a.D, a.ld_g, es), bytes_of(h0, state_bytes)};
+  if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
   return done(m3::launch_scan(a, dtype, s));
 }
 
@@ -210,16 +238,13 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* dims, m3_dtype dtype, const
   a.dh0 = dh0;
   a.workspace = workspace;
   const int64_t rows = a.B * a.T;
-  const void* const out[] = {dx, df, dg};
-  const void* const in[] = {dy, x, f, g};
-  const int64_t ld_out[] = {a.ld_dx, a.ld_df, a.ld_dg}, ld_in[] = {a.ld_y, a.ld_x, a.ld_f, a.ld_g};
-  if (bytes_meet(dh_last, state_bytes, dh0, state_bytes)) return M3_ERR_INVALID_VALUE;
-  for (int i = 0; i < 3; ++i) {
-    for (int j = 0; j < 4; ++j)
-      if (rows_meet(out[i], ld_out[i], in[j], ld_in[j], rows, a.D, es)) return M3_ERR_INVALID_VALUE;
-    for (int j = 0; j < i; ++j)
-      if (rows_meet(out[i], ld_out[i], out[j], ld_out[j], rows, a.D, es)) return M3_ERR_INVALID_VALUE;
-  }
+  const Span out[] = {rows_of(dx, rows, a.D, a.ld_dx, es), rows_of(df, rows, a.D, a.ld_df, es),
+                      rows_of(dg, rows, a.D, a.ld_dg, es), bytes_of(dh0, state_bytes),
+                      workspace_of(dims, dtype, workspace)};
+  const Span in[] = {rows_of(dy, rows, a.D, a.ld_y, es), rows_of(x, rows, a.D, a.ld_x, es),
+                     rows_of(f, rows, a.D, a.ld_f, es), rows_of(g, rows, a.D, a.ld_g, es),
+                     bytes_of(states, state_bytes * a.nC), bytes_of(dh_last, state_bytes)};
+  if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
   return done(m3::launch_scan_backward(a, dtype, s));
 }
 
@@ -251,9 +276,12 @@ m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const flo
   a.f = f;
   a.g = g;
   a.y = y;
-  if (rows_meet(y, a.ld_y, x, a.ld_x, a.B, a.D, es) || rows_meet(y, a.ld_y, f, a.ld_f, a.B, a.D, es) ||
-      rows_meet(y, a.ld_y, g, a.ld_g, a.B, a.D, es))
-    return M3_ERR_INVALID_VALUE;
+  const size_t state_bytes = (size_t)a.B * a.D * sizeof(float);
+  const Span ys = rows_of(y, a.B, a.D, a.ld_y, es), state = bytes_of(h_out, state_bytes);
+  const Span out[] = {ys, state};
+  const Span in[] = {rows_of(x, a.B, a.D, a.ld_x, es), rows_of(f, a.B, a.D, a.ld_f, es),
+                     rows_of(g, a.B, a.D, a.ld_g, es)};
+  if (outputs_meet(out, in) || meet(ys, bytes_of(h_in, state_bytes))) return M3_ERR_INVALID_VALUE;
   return done(m3::launch_scan_step(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -310,11 +338,9 @@ m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
     return M3_ERR_INVALID_VALUE;
   m3::NormArgs a = norm_args(dims);
   // an output takes an input's place whole or not at all, and the outputs differ
-  if (rows_meet(y, a.ld_y, sum_out, a.ld_sum, a.rows, a.D, es) ||
-      rows_cross(y, a.ld_y, x, a.ld_x, a.rows, a.D, es) ||
-      rows_cross(y, a.ld_y, residual, a.ld_res, a.rows, a.D, es) ||
-      rows_cross(sum_out, a.ld_sum, x, a.ld_x, a.rows, a.D, es) ||
-      rows_cross(sum_out, a.ld_sum, residual, a.ld_res, a.rows, a.D, es))
+  const Span xs = rows_of(x, a.rows, a.D, a.ld_x, es), rs = rows_of(residual, a.rows, a.D, a.ld_res, es);
+  const Span ys = rows_of(y, a.rows, a.D, a.ld_y, es), ss = rows_of(sum_out, a.rows, a.D, a.ld_sum, es);
+  if (meet(ys, ss) || cross(ys, xs) || cross(ys, rs) || cross(ss, xs) || cross(ss, rs))
     return M3_ERR_INVALID_VALUE;
   a.eps = eps;
   a.x = x;
@@ -350,9 +376,10 @@ m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const
     if (!need(dy, es) || !need(s, es) || !need(weight, 4) || !need(mean, 4) || !need(rstd, 4) ||
         !maybe(dsum, es) || !need(dx, es))
       return M3_ERR_INVALID_VALUE;
-    if (rows_cross(dx, a.ld_dx, dy, a.ld_dy, a.rows, a.D, es) ||
-        rows_cross(dx, a.ld_dx, dsum, a.ld_dsum, a.rows, a.D, es) ||
-        rows_meet(dx, a.ld_dx, s, a.ld_sum, a.rows, a.D, es))
+    const Span dxs = rows_of(dx, a.rows, a.D, a.ld_dx, es);
+    if (cross(dxs, rows_of(dy, a.rows, a.D, a.ld_dy, es)) ||
+        cross(dxs, rows_of(dsum, a.rows, a.D, a.ld_dsum, es)) ||
+        meet(dxs, rows_of(s, a.rows, a.D, a.ld_sum, es)))
       return M3_ERR_INVALID_VALUE;
     if (!workspace || workspace_bytes < m3_layer_norm_backward_workspace_size(dims, dtype))
       return M3_ERR_WORKSPACE;
