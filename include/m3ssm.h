@@ -499,8 +499,9 @@ m3_status m3_gated_scan_step(const m3_scan_dims* dims, m3_dtype dtype, const flo
  * from the values as stored in s: the variance from the centred values, not
  * from a difference of sums.  weight, bias [channels] float; bias may be NULL.
  * sum_out receives s (NULL: not kept; it may be x itself or residual itself,
- * with the same ld); y may be x or residual too, but not sum_out.  Arrays that
- * overlap otherwise are refused.  mean and
+ * with the same ld); y may be x or residual too, but not sum_out.  Outputs
+ * (y, sum_out, mean, rstd) that overlap an input or each other otherwise are
+ * refused.  mean and
  * rstd [rows] float, or NULL, are what the backward pass needs.  channels is
  * at most 16384.  Row r of an array is at r ld; every pointer needs element
  * alignment, and 16-byte aligned rows are read in vectors.
@@ -526,8 +527,9 @@ m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
  *        gradient of x and of residual alike)
  *   dweight = sum over rows of dy q,  dbias = sum over rows of dy    (float)
  *
- * dbias may be NULL.  dx may be dy or dsum (same ld) but must not
- * overlap them otherwise, nor s.  The sums over rows are
+ * dbias may be NULL.  dx may be dy or dsum (same ld); it must not overlap
+ * them otherwise, nor another array of the call.  Nor may the workspace; dweight
+ * and dbias, written last, must not overlap dx or each other.  The sums over rows are
  * taken in a fixed order: a call repeats bit for bit.  rows == 0 writes
  * zeros to dweight and dbias.  The workspace needs 16-byte alignment.
  */

@@ -340,7 +340,12 @@ m3_status m3_layer_norm(const m3_norm_dims* dims, m3_dtype dtype, const void* x,
   // an output takes an input's place whole or not at all, and the outputs differ
   const Span xs = rows_of(x, a.rows, a.D, a.ld_x, es), rs = rows_of(residual, a.rows, a.D, a.ld_res, es);
   const Span ys = rows_of(y, a.rows, a.D, a.ld_y, es), ss = rows_of(sum_out, a.rows, a.D, a.ld_sum, es);
-  if (meet(ys, ss) || cross(ys, xs) || cross(ys, rs) || cross(ss, xs) || cross(ss, rs))
+  if (cross(ys, xs) || cross(ys, rs) || cross(ss, xs) || cross(ss, rs)) return M3_ERR_INVALID_VALUE;
+  const size_t stat = (size_t)a.rows * sizeof(float), cols = (size_t)a.D * sizeof(float);
+  const Span means = bytes_of(mean, stat), rstds = bytes_of(rstd, stat);
+  const Span out[] = {ys, ss, means, rstds};
+  const Span in[] = {bytes_of(weight, cols), bytes_of(bias, cols)};
+  if (outputs_meet(out, in) || meet(means, xs) || meet(means, rs) || meet(rstds, xs) || meet(rstds, rs))
     return M3_ERR_INVALID_VALUE;
   a.eps = eps;
   a.x = x;
@@ -372,19 +377,28 @@ m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const
   const uintptr_t es = esize_of(dtype);
   if (!need(dweight, 4) || !maybe(dbias, 4)) return M3_ERR_INVALID_VALUE;
   m3::NormArgs a = norm_args(dims);
+  const size_t cols = (size_t)a.D * sizeof(float);
   if (dims->rows > 0) {
     if (!need(dy, es) || !need(s, es) || !need(weight, 4) || !need(mean, 4) || !need(rstd, 4) ||
         !maybe(dsum, es) || !need(dx, es))
       return M3_ERR_INVALID_VALUE;
-    const Span dxs = rows_of(dx, a.rows, a.D, a.ld_dx, es);
-    if (cross(dxs, rows_of(dy, a.rows, a.D, a.ld_dy, es)) ||
-        cross(dxs, rows_of(dsum, a.rows, a.D, a.ld_dsum, es)) ||
-        meet(dxs, rows_of(s, a.rows, a.D, a.ld_sum, es)))
-      return M3_ERR_INVALID_VALUE;
     if (!workspace || workspace_bytes < m3_layer_norm_backward_workspace_size(dims, dtype))
       return M3_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return M3_ERR_INVALID_VALUE;
+    const Span dxs = rows_of(dx, a.rows, a.D, a.ld_dx, es), dys = rows_of(dy, a.rows, a.D, a.ld_dy, es);
+    const Span dss = rows_of(dsum, a.rows, a.D, a.ld_dsum, es), ss = rows_of(s, a.rows, a.D, a.ld_sum, es);
+    if (cross(dxs, dys) || cross(dxs, dss)) return M3_ERR_INVALID_VALUE;
+    const size_t stat = (size_t)a.rows * sizeof(float);
+    const Span ws = bytes_of(workspace, m3_layer_norm_backward_workspace_size(dims, dtype));
+    const Span dws = bytes_of(dweight, cols), dbs = bytes_of(dbias, cols);
+    const Span early[] = {dxs, ws};
+    const Span in[] = {ss, bytes_of(weight, cols), bytes_of(mean, stat), bytes_of(rstd, stat)};
+    // the weights' gradients are written when all else has been read
+    if (outputs_meet(early, in) || meet(ws, dys) || meet(ws, dss) || meet(dws, dxs) || meet(dws, ws) ||
+        meet(dbs, dxs) || meet(dbs, ws))
+      return M3_ERR_INVALID_VALUE;
   }
+  if (meet(bytes_of(dweight, cols), bytes_of(dbias, cols))) return M3_ERR_INVALID_VALUE;
   a.dy = dy;
   a.sum = const_cast<void*>(s);
   a.weight = weight;

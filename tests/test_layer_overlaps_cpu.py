@@ -84,3 +84,33 @@ def test_scan_backward(lib):
     for j in range(10):
         q = p[:10] + [p[j]]
         assert call([ctypes.c_void_p(a) for a in q]) == INV, j
+
+
+def test_layer_norm(lib):
+    M, D = 40, 64
+    d = bnd.M3NormDims(M, D)
+    call = lambda p: lib.m3_layer_norm(ctypes.byref(d), 0, *p[:4], 1e-5, *p[4:], None)
+    row, col, stat = 4 * M * D, 4 * D, 4 * M
+    sizes = [row, row, col, col, row, row, stat, stat]      # x residual weight bias | y sum mean rstd
+    pairs = [(i, j) for i in (4, 5) for j in (2, 3, 6, 7)]
+    pairs += [(i, j) for i in (6, 7) for j in range(8) if i != j]
+    all_refused(call, sizes, pairs)
+
+
+def test_layer_norm_backward(lib):
+    M, D = 40, 64
+    d = bnd.M3NormDims(M, D)
+    ws = lib.m3_layer_norm_backward_workspace_size(ctypes.byref(d), 0)
+    call = lambda p: lib.m3_layer_norm_backward(ctypes.byref(d), 0, *p, 1 << 40, None)
+    row, col, stat = 4 * M * D, 4 * D, 4 * M
+    # dy s weight mean rstd dsum | dx dweight dbias workspace
+    sizes = [row, row, col, stat, stat, row, row, col, col, ws]
+    all_refused(call, sizes, [(6, j) for j in (1, 2, 3, 4, 7, 8)] + [(7, 6), (7, 8), (8, 6), (8, 7)])
+    p = apart(10)
+    for j in range(9):
+        for shift in (0, -(ws - 16)):
+            q = p[:9] + [p[j] + shift]
+            assert call([ctypes.c_void_p(a) for a in q]) == INV, j
+    d.rows = 0                                               # zeros to both, one over the other
+    p[8] = p[7] + 4
+    assert call([ctypes.c_void_p(a) for a in p]) == INV
