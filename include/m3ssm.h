@@ -561,7 +561,8 @@ m3_status m3_layer_norm_backward(const m3_norm_dims* dims, m3_dtype dtype, const
  * once, store and decode take its first entry and treat the others as idle.
  *
  * codes and h need 16-byte alignment, other pointers element alignment
- * (decode: as m3_decode_step).  P is 16, 32, 64 or 128; N even, as
+ * (decode: as m3_decode_step).  What a call writes must not overlap what it
+ * reads: the whole pool counts.  P is 16, 32, 64 or 128; N even, as
  * m3_decode_step; batch * H at most 2^24 - 1.
  */
 typedef enum { M3_CODE_INT8 = 0, M3_CODE_E4M3 = 1 } m3_code;

@@ -133,11 +133,6 @@ bool outputs_meet(const Span (&out)[NO], const Span (&in)[NI]) {
   return false;
 }
 
-// Whether [a, a + na) and [b, b + nb) meet.
-bool bytes_meet(const void* a, size_t na, const void* b, size_t nb) {
-  return meet(bytes_of(a, na), bytes_of(b, nb));
-}
-
 // Whether [a, a + n) and [b, b + n) overlap without being the same.
 bool partial_overlap(const void* a, const void* b, size_t n) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -447,6 +442,21 @@ m3::CacheArgs cache_args(const m3_dims* d, void* codes, float* scales, const int
   return a;
 }
 
+// The memory of a cache's codes and scales (as much as there is of one that no
+// memory could hold).
+struct CacheSpans {
+  Span codes, scales, slots;
+};
+CacheSpans cache_spans(const m3::CacheArgs& a) {
+  const double rows = (double)a.n_slots * (double)a.H * (double)a.N;
+  const size_t most = SIZE_MAX / 4;
+  const bool fits = rows * a.P < (double)most;
+  return {bytes_of(a.codes, fits ? (size_t)a.n_slots * a.H * a.N * a.P : most),
+          bytes_of(a.scales, fits ? (size_t)a.n_slots * a.H * a.N * sizeof(float) : most),
+          bytes_of(a.slots, (size_t)a.S * sizeof(int32_t))};
+}
+size_t state_elements(const m3::CacheArgs& a) { return (size_t)a.S * a.H * a.N * a.P; }
+
 }  // namespace
 
 extern "C" {
@@ -460,6 +470,10 @@ m3_status m3_state_store(const m3_dims* dims, m3_code code, const float* h, void
   if (!need(h, 16) || !need(codes, 16) || !need(scales, 4)) return M3_ERR_INVALID_VALUE;
   m3::CacheArgs a = cache_args(dims, codes, scales, slots, n_slots);
   a.h_in = h;
+  const CacheSpans c = cache_spans(a);
+  const Span out[] = {c.codes, c.scales};
+  const Span in[] = {c.slots, bytes_of(h, state_elements(a) * sizeof(float))};
+  if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
   return done(m3::launch_state_store(a, code, static_cast<hipStream_t>(stream)));
 }
 
@@ -475,6 +489,10 @@ m3_status m3_state_load(const m3_dims* dims, m3_code code, m3_dtype dtype, const
   m3::CacheArgs a = cache_args(dims, const_cast<void*>(codes), const_cast<float*>(scales), slots,
                                n_slots);
   a.h_out = h;
+  const CacheSpans c = cache_spans(a);
+  const Span out[] = {bytes_of(h, state_elements(a) * esize_of(dtype))};
+  const Span in[] = {c.codes, c.scales, c.slots};
+  if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
   return done(m3::launch_state_load(a, code, dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -499,11 +517,6 @@ m3_status m3_decode_step_cached(const m3_dims* dims, m3_dtype dtype, m3_code cod
   if (!maybe(lam, 4) || !maybe(theta, 4) || !maybe(x_prev, 4 * es) || !maybe(B_prev, 2 * es) ||
       (lam && (!x_prev || !B_prev)))
     return M3_ERR_INVALID_VALUE;
-  const size_t units = (size_t)dims->batch * dims->nheads * R;
-  const size_t xy = units * dims->headdim_p * es, bc = units * dims->dstate_n * es;
-  if (bytes_meet(y_t, xy, x_t, xy) || bytes_meet(y_t, xy, B_t, bc) || bytes_meet(y_t, xy, C_t, bc) ||
-      (lam && (bytes_meet(y_t, xy, x_prev, xy) || bytes_meet(y_t, xy, B_prev, bc))))
-    return M3_ERR_INVALID_VALUE;
   m3::CacheArgs a = cache_args(dims, codes, scales, slots, n_slots);
   a.R = (int)R;
   a.x_t = x_t;
@@ -516,6 +529,15 @@ m3_status m3_decode_step_cached(const m3_dims* dims, m3_dtype dtype, m3_code cod
   a.lam = lam;
   a.theta = theta;
   a.y = y_t;
+  const size_t heads = (size_t)a.S * a.H;
+  const size_t xy = heads * R * a.P * es, bc = heads * R * a.N * es, each = heads * sizeof(float);
+  const CacheSpans c = cache_spans(a);
+  const Span out[] = {c.codes, c.scales, bytes_of(y_t, xy)};
+  const Span in[] = {c.slots, bytes_of(x_t, xy), bytes_of(lam ? x_prev : nullptr, xy), bytes_of(B_t, bc),
+                     bytes_of(lam ? B_prev : nullptr, bc), bytes_of(C_t, bc), bytes_of(dt, each),
+                     bytes_of(A, (size_t)a.H * sizeof(float)), bytes_of(lam, each),
+                     bytes_of(theta, each * (a.N / 2))};
+  if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
   return done(m3::launch_decode_cached(a, code, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -114,3 +114,51 @@ def test_layer_norm_backward(lib):
     d.rows = 0                                               # zeros to both, one over the other
     p[8] = p[7] + 4
     assert call([ctypes.c_void_p(a) for a in p]) == INV
+
+
+def test_state_cache(lib):
+    """The whole pool counts, its last slot as its first."""
+    S, H, N, P, slots = 2, 3, 34, 32, 5
+    d = bnd.M3Dims(S, 1, H, P, N, 1)
+    codes, scales, at, h = slots * H * N * P, 4 * slots * H * N, 4 * S, 4 * S * H * N * P
+    all_sizes = [h, codes, scales, at]
+
+    def aligned(sizes, pairs, call):
+        p = apart(len(sizes))
+        for i, j in pairs:
+            for shift in (0, (sizes[j] - 4) // 16 * 16, -((sizes[i] - 4) // 16 * 16)):
+                q = list(p)
+                q[i] = p[j] + shift
+                assert call([ctypes.c_void_p(a) for a in q]) == INV, (i, j, shift)
+
+    store = lambda p: lib.m3_state_store(ctypes.byref(d), 0, *p, slots, None)
+    aligned(all_sizes, [(1, 0), (1, 2), (1, 3), (2, 0), (2, 3)], store)
+    load = lambda p: lib.m3_state_load(ctypes.byref(d), 0, 0, p[1], p[2], p[3], slots, p[0], None)
+    aligned(all_sizes, [(0, 1), (0, 2), (0, 3)], load)
+
+
+def test_decode_cached(lib):
+    S, H, N, P, R, slots = 2, 3, 34, 32, 2, 5
+    d = bnd.M3Dims(S, 1, H, P, N, R)
+    x, b, each = 4 * S * H * R * P, 4 * S * H * R * N, 4 * S * H
+    # codes scales slots | x_t x_prev B_t B_prev C_t dt A lam theta y_t
+    sizes = [slots * H * N * P, 4 * slots * H * N, 4 * S, x, x, b, b, b, each, 4 * H, each, each * N // 2, x]
+    call = lambda p: lib.m3_decode_step_cached(ctypes.byref(d), 0, 0, *p[:3], slots, *p[3:], None)
+    p = apart(13)
+    for i in (0, 1, 12):
+        for j in range(13):
+            if i == j:
+                continue
+            for shift in (0, (sizes[j] - 4) // 16 * 16, -((sizes[i] - 4) // 16 * 16)):
+                q = list(p)
+                q[i] = p[j] + shift
+                assert call([ctypes.c_void_p(a) for a in q]) == INV, (i, j, shift)
+
+
+def test_pool_that_no_memory_holds(lib):
+    """Its size does not wrap round to one that misses the states."""
+    d = bnd.M3Dims(1, 1, 1 << 22, 128, 128, 1)
+    p = [ctypes.c_void_p(a) for a in apart(4)]
+    slots = (1 << 31) - 1
+    assert lib.m3_state_store(ctypes.byref(d), 0, *p, slots, None) == INV
+    assert lib.m3_state_load(ctypes.byref(d), 0, 0, p[1], p[2], p[3], slots, p[0], None) == INV
