@@ -29,6 +29,11 @@
 #include "layer_internal.h"
 #include "m3_device.h"
 
+// For the whole file: a fused operation is one rounding less, which is another
+// code now and then (the product h (Q / amax), say, is rounded before the sum
+// that rounds it to a whole number).
+#pragma clang fp contract(off)
+
 namespace m3 {
 namespace {
 
@@ -307,7 +312,6 @@ __device__ __forceinline__ void pair_coefficients(const CacheArgs& a, size_t in,
 // bfloat16 values is exact, so there the fused form is the same).
 template <typename T, int R>
 __device__ __forceinline__ float rank_sum(const float (&b)[R], const float (&x)[R][8], int e) {
-#pragma clang fp contract(off)
   float t = b[0] * x[0][e];
 #pragma unroll
   for (int r = 1; r < R; ++r) {
@@ -330,7 +334,6 @@ struct PairIn {
 // worked on.
 template <typename T, int R, int kCode, bool kTrap, bool kRot, int NT>
 __global__ void __launch_bounds__(NT) decode_kernel(CacheArgs a) {
-#pragma clang fp contract(off)
   extern __shared__ __align__(16) float dsm[];
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
   const int slot = slot_of(a, i);
@@ -474,7 +477,6 @@ __device__ __forceinline__ void outer(const float (&x)[R], const float (&b)[R], 
 
 template <int R, int kCode, bool kTrap, bool kRot>
 __global__ void __launch_bounds__(kWave, R > 2 ? 3 : 4) decode_outer_kernel(CacheArgs a) {
-#pragma clang fp contract(off)
   constexpr int P = 64, kRound = R < 2 ? R : 2, kPitch = kRound * P + 4;
   extern __shared__ __align__(16) float dsm[];
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
