@@ -507,16 +507,20 @@ def backward(x, dt, A, lam, theta, B, C, dy, *, dh_final=None, workspace=None, s
 _types = None
 
 
-def _type_code(t) -> int:
-    """M3_F32 or M3_BF16 of a tensor's type."""
+def _dtype_code(dtype) -> int:
+    """M3_F32 or M3_BF16 of a torch type (or of the code itself)."""
     global _types
     if _types is None:
         import torch
-        _types = {torch.float32: M3_F32, torch.bfloat16: M3_BF16}
-    code = _types.get(t.dtype)
+        _types = {torch.float32: M3_F32, torch.bfloat16: M3_BF16, M3_F32: M3_F32, M3_BF16: M3_BF16}
+    code = _types.get(dtype)
     if code is None:
-        raise TypeError("expected float32 or bfloat16, got %s" % t.dtype)
+        raise TypeError("expected float32 or bfloat16, got %s" % dtype)
     return code
+
+
+def _type_code(t) -> int:
+    return _dtype_code(t.dtype)
 
 
 def _launch(dev: int, fn, *args):
@@ -616,10 +620,8 @@ def _code_of(codes) -> int:
 
 def gated_scan_workspace_size(batch, seqlen, channels, dtype) -> int:
     """Bytes of workspace gated_scan and gated_scan_backward need (0: none)."""
-    import torch
-    code = dtype if isinstance(dtype, int) else (M3_BF16 if dtype == torch.bfloat16 else M3_F32)
     d = M3ScanDims(int(batch), int(seqlen), int(channels))
-    return int(load_library().m3_gated_scan_workspace_size(ctypes.byref(d), code))
+    return int(load_library().m3_gated_scan_workspace_size(ctypes.byref(d), _dtype_code(dtype)))
 
 
 def _scan_workspace(lib, d, code, workspace, dev):
