@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 import os
 from typing import Optional, Tuple
@@ -540,12 +541,14 @@ def _streamed(fn):
     (a torch stream or its handle, of the first tensor's device) that makes
     another one current for the call: what the call allocates and zero-fills
     is then ordered with its kernels."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None:
+        if stream is None or not (args or first in kw):
             return fn(*args, **kw)
         import torch
-        dev = (args[0] if args else next(iter(kw.values()))).get_device()
+        dev = (args[0] if args else kw[first]).get_device()
         _gpu(dev)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)

@@ -13,3 +13,18 @@ def test_scan_workspace_size_of_other_types():
             m3.gated_scan_workspace_size(2, 300, 64, dtype)
     for code, dtype in ((m3.M3_F32, torch.float32), (m3.M3_BF16, torch.bfloat16)):
         assert m3.gated_scan_workspace_size(2, 300, 64, code) == m3.gated_scan_workspace_size(2, 300, 64, dtype) > 0
+
+
+def test_stream_with_arguments_by_name():
+    """The call's device is its first tensor's, in whatever order the arguments
+    are named (CPU tensors: refused for that, not for the order)."""
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    with pytest.raises(ValueError, match="GPU"):
+        m3.layer_norm(eps=1e-5, residual=None, weight=w, x=x, stream=0)
+    c, s = m3.state_cache(4, 2, 16, 16, device="cpu")
+    with pytest.raises(ValueError, match="GPU"):
+        m3.state_load(slots=None, scales=s, codes=c, stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        m3.gated_scan(g=None, f=torch.zeros(1, 2, 8), x=torch.zeros(1, 2, 8), stream=0)
+    with pytest.raises(TypeError, match="'x'"):
+        m3.layer_norm(weight=w, stream=0)
