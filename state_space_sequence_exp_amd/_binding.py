@@ -761,8 +761,9 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None
 
     x, residual [..., D] float32 or bfloat16, D <= 16384, rows at one
     distance; weight, bias [D] float32.  sum_out may be x or residual (in
-    place).  Returns (y, s, mean, rstd): s is x itself without a residual,
-    mean and rstd [...] float32 (None without want_stats)."""
+    place).  Returns (y, s, mean, rstd): s is x itself without a residual
+    (None where y took its place), mean and rstd [...] float32 (None without
+    want_stats)."""
     import torch
     lib = _lib or load_library()
     shape, dev, dt = x.shape, x.get_device(), x.dtype
@@ -788,6 +789,8 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None
     s = x if sum_out is None else sum_out
     if y is None:
         y = _like(x, ld == 0)
+    elif s is x and y.data_ptr() == x.data_ptr():
+        s = None
     mean = rstd = None
     if want_stats:
         mean = weight.new_empty(shape[:-1])
