@@ -508,7 +508,7 @@ def backward(x, dt, A, lam, theta, B, C, dy, *, dh_final=None, workspace=None, s
 _types = None
 
 
-def _dtype_code(dtype) -> int:
+def _type_code(dtype) -> int:
     """M3_F32 or M3_BF16 of a torch type (or of the code itself)."""
     global _types
     if _types is None:
@@ -620,7 +620,7 @@ def _code_of(codes) -> int:
 def gated_scan_workspace_size(batch, seqlen, channels, dtype) -> int:
     """Bytes of workspace gated_scan and gated_scan_backward need (0: none)."""
     d = M3ScanDims(int(batch), int(seqlen), int(channels))
-    return int(load_library().m3_gated_scan_workspace_size(ctypes.byref(d), _dtype_code(dtype)))
+    return int(load_library().m3_gated_scan_workspace_size(ctypes.byref(d), _type_code(dtype)))
 
 
 def _scan_workspace(lib, d, code, workspace, dev):
@@ -659,7 +659,7 @@ def gated_scan(x, f, g=None, *, h0=None, y=None, h_last=None, want_states: bool 
     if len(shape) != 3:
         raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
     nb, nt, nd = shape
-    code = _dtype_code(dt)
+    code = _type_code(dt)
     ld = _rows(x, "x", dt, shape, dev)
     d = M3ScanDims(nb, nt, nd, ld, _rows(f, "f", dt, shape, dev),
                    0 if g is None else _rows(g, "g", dt, shape, dev))
@@ -699,7 +699,7 @@ def gated_scan_backward(dy, x, f, g, states, *, dh_last=None, dx=None, df=None, 
     if len(shape) != 3:
         raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
     nb, nt, nd = shape
-    code = _dtype_code(dt)
+    code = _type_code(dt)
     _same(states, "states", torch.float32, (nb, -(-nt // SCAN_CHUNK), nd), dev)
     if dh_last is not None:
         _same(dh_last, "dh_last", torch.float32, (nb, nd), dev)
@@ -734,7 +734,7 @@ def gated_scan_step(h, x, f, g=None, *, h_out=None, y=None) -> Tuple:
     shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) != 2:
         raise ValueError("x: expected [B, D], got %s" % (tuple(shape),))
-    code = _dtype_code(dt)
+    code = _type_code(dt)
     ld = _rows(x, "x", dt, shape, dev)
     d = M3ScanDims(shape[0], 1, shape[1], ld, _rows(f, "f", dt, shape, dev),
                    0 if g is None else _rows(g, "g", dt, shape, dev))
@@ -769,7 +769,7 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, y=None
     shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) < 1:
         raise ValueError("x: expected [..., D]")
-    code = _dtype_code(dt)
+    code = _type_code(dt)
     nd = shape[-1]
     rows = math.prod(shape[:-1])
     ld = _rows(x, "x", dt, shape, dev)
@@ -813,7 +813,7 @@ def layer_norm_backward(dy, s, weight, mean, rstd, *, dsum=None, dx=None, want_b
     shape, dev, dt = s.shape, s.get_device(), s.dtype
     if len(shape) < 1:
         raise ValueError("s: expected [..., D]")
-    code = _dtype_code(dt)
+    code = _type_code(dt)
     nd = shape[-1]
     d = M3NormDims(math.prod(shape[:-1]), nd)
     d.ld_sum = _rows(s, "s", dt, shape, dev)
@@ -906,7 +906,7 @@ def state_load(codes, scales, slots=None, *, dtype=None, h=None):
     if h is None:
         h = scales.new_empty((ns, nh, nn, npd), dtype=dtype or torch.float32)
     d = M3Dims(ns, 1, nh, npd, nn, 1)
-    _launch(dev, lib.m3_state_load, ctypes.byref(d), code, _dtype_code(h.dtype), _at(codes),
+    _launch(dev, lib.m3_state_load, ctypes.byref(d), code, _type_code(h.dtype), _at(codes),
             _at(scales), _at(slots), n, _at(h))
     return h
 
@@ -929,7 +929,7 @@ def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, 
     n, nh, nn, npd = codes.shape
     ns, nr = x_t.shape[0], x_t.shape[2]
     xs, bs = (ns, nh, nr, npd), (ns, nh, nr, nn)
-    tcode = _dtype_code(x_t.dtype)
+    tcode = _type_code(x_t.dtype)
     if slots is not None and slots.shape[0] != ns:
         raise ValueError("slots: expected shape %s, got %s" % ((ns,), tuple(slots.shape)))
     if lam is not None and (x_prev is None or B_prev is None):

@@ -28,3 +28,14 @@ def test_stream_with_arguments_by_name():
         m3.gated_scan(g=None, f=torch.zeros(1, 2, 8), x=torch.zeros(1, 2, 8), stream=0)
     with pytest.raises(TypeError, match="'x'"):
         m3.layer_norm(weight=w, stream=0)
+
+
+def test_each_name_is_defined_once():
+    """A helper of the layer operators does not replace one that the other
+    entry points use."""
+    import ast
+    import collections
+    from state_space_sequence_exp_amd import _binding
+    names = collections.Counter(n.name for n in ast.parse(open(_binding.__file__).read()).body
+                                if isinstance(n, (ast.FunctionDef, ast.ClassDef)))
+    assert [n for n, k in names.items() if k > 1] == []
