@@ -403,8 +403,10 @@ m3_status m3_block_postpass(const m3_dims* dims, m3_dtype dtype, const void* y,
  * Masks are gate values: f = +inf passes the state on and x is not looked at
  * (padding: x may hold anything, NaN included), f = -inf starts afresh from
  * x and the state before is not looked at (the first token of a document
- * packed behind another).  A finite f beyond float's range of the sigmoid
- * acts as the infinity it rounds to.
+ * packed behind another).  A finite f whose a or 1 - a underflows in float (|f|
+ * from about 87 on) acts as that infinity.  Nothing else hides a state: a NaN
+ * one stays NaN, however small the gates' product, until f = -inf drops it, and
+ * an infinite one does not become finite (it may become NaN).
  *
  * Layouts: x, f, g, y and their gradients [batch, T, D], token t of sequence
  * b at (b T + t) ld with D contiguous channels; each array has its own ld in

@@ -52,16 +52,25 @@ __device__ __forceinline__ float gate_step(float z, float h, float x) {
   return __builtin_fmaf(gate_w(z), x, gate_keep<kMask>(z, h));
 }
 
-constexpr float kLeastA = 1.17549435e-38f;
+constexpr float kLeastA = 1.40129846e-45f;  // 2^-149
 
 // A run of steps as a map of the state before it: h -> A h + B.  A is 0 only
 // where a gate of the run dropped the state (then h is not looked at): a
-// product that underflows stays at the smallest normal float.
+// product that underflows stays at the smallest float, so that a NaN state
+// that is merely forgotten is NaN after the run as well.
 struct Run {
   float A, B;
 };
 __device__ __forceinline__ float run_apply(Run r, float h) {
   return __builtin_fmaf(r.A, r.A == 0.f ? 0.f : h, r.B);
+}
+// The factor A of a run with one more gate.  `least`: the smallest that it may
+// be, kLeastA to begin with, 0 from a gate on that drops the state (also behind
+// a NaN gate, which makes no number of A).
+template <bool kMask>
+__device__ __forceinline__ float run_factor(float z, float A, float& least) {
+  if constexpr (kMask) least = gate_drops(z) ? 0.f : least;
+  return fmaxf(gate_keep<false>(z, A), least);
 }
 // `first`, then `then`.
 __device__ __forceinline__ Run run_join(Run first, Run then) {

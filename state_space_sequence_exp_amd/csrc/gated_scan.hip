@@ -51,9 +51,11 @@ __global__ void __launch_bounds__(ScanForward<T>::kThreads, 4) scan_kernel(ScanA
   const bool full = nt >= K && n >= V;
   load_rows<kVec>(f, rf, full, nt, n, a.D >= V, kPassGate<T>);
   load_rows<kVec>(x, rx, full, nt, n, a.D >= V, 0u);
-  // per token the map from the state before the thread's first
+  // per token the map from the state before the thread's first; where a gate
+  // dropped that state A is NaN, which stays so under the output gate (A is NaN
+  // nowhere else: a NaN gate makes B NaN, and so does a NaN output gate)
+  const float kDropped = __uint_as_float(0x7fc00000u);
   float A[K][V], B[K][V];
-  bool masks = false;  // in this wave
 #pragma unroll
   for (int i = 0; i < Cfg::kWords; ++i) {
     float z[K][W], least = 1.f;
@@ -67,31 +69,31 @@ __global__ void __launch_bounds__(ScanForward<T>::kThreads, 4) scan_kernel(ScanA
         least = fminf(least, __builtin_fabsf(z[k][e]));
       }
     }
+    Run whole[W];  // of the thread's tokens
     const auto walk = [&](auto mask) {
       constexpr bool kMask = decltype(mask)::value;
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         Run r = Run{1.f, 0.f};
+        float least = kLeastA;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           float xv[W];
           unpack_word(x[k].w[i], xv);
-          r.A = gate_keep<false>(z[k][e], r.A);
+          r.A = run_factor<kMask>(z[k][e], r.A, least);
           r.B = gate_step<kMask>(z[k][e], r.B, xv[e]);
-          A[k][i * W + e] = r.A;
+          A[k][i * W + e] = kMask && r.A == 0.f ? kDropped : r.A;
           B[k][i * W + e] = r.B;
         }
+        whole[e] = r;
       }
     };
-    const bool some = __any(gate_masks(least));
-    masks |= some;
-    if (some) walk(std::true_type{});
+    if (__any(gate_masks(least))) walk(std::true_type{});
     else walk(std::false_type{});
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const int v = i * W + e;
-      Run r = Run{A[K - 1][v], B[K - 1][v]}, before;
-      if (!some) r.A = fmaxf(r.A, kLeastA);
+      Run r = whole[e], before;
       wave_join<Cfg, false>(r, before);
       s_run[v][tid] = before;
       if (lane / Cfg::kAcross == Cfg::kShare - 1) s_wave[wave][cl + v] = r;
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(ScanForward<T>::kThreads, 4) scan_kernel(ScanA
       float y[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        const float p = A[k][i * W + e];
-        y[e] = __builtin_fmaf(p, masks && p == 0.f ? 0.f : h[e], B[k][i * W + e]);
+        const float p = A[k][i * W + e], q = B[k][i * W + e];
+        y[e] = p == p ? __builtin_fmaf(p, h[e], q) : q;
       }
       x[k].w[i] = pack_word(y);
       renew(x[k].w[i]);

@@ -11,6 +11,8 @@
 // the first.  The state that enters a chunk was kept by the forward pass, so
 // only u has to come from another workgroup.  A thread's tokens make a map of
 // the state before them and one of the u behind them; both have the same A.
+// Behind the first gate that drops the state (and only there: a factor that
+// underflows is no such gate) the state before the thread is not looked at.
 #include "scan_tile.h"
 
 namespace m3 {
@@ -54,11 +56,15 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
   // dy silu'(g)
   float z[K][V], A[K][V], B[K][V], dh[K][V], dsilu[kGate ? K : 1][V];
   Run whole[V];  // of the thread's tokens
+  int drop[V];   // the first token whose gate drops the state (K: none)
 #pragma unroll
   for (int i = 0; i < Cfg::kWords; ++i) {
     Run r[W], u[W];
 #pragma unroll
-    for (int e = 0; e < W; ++e) r[e] = u[e] = Run{1.f, 0.f};
+    for (int e = 0; e < W; ++e) {
+      r[e] = u[e] = Run{1.f, 0.f};
+      drop[i * W + e] = K;
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float xv[W], fv[W];
@@ -90,12 +96,15 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
           dsilu[k][v] = dv[e] * (sg * __builtin_fmaf(gv[e], 1.f - sg, 1.f));
         }
         u[e].B = gate_keep<true>(z[k][v], dh[k][v] + u[e].B);
+        drop[v] = gate_drops(z[k][v]) ? k : drop[v];
       }
     }
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const int v = i * W + e;
       Run o;
+      // (A may be NaN where a gate before the one that dropped the state was)
+      r[e].A = drop[v] < K ? 0.f : fmaxf(r[e].A, kLeastA);
       whole[v] = r[e];
       u[e].A = r[e].A;
       wave_join<Cfg, false>(r[e], o);
@@ -170,7 +179,8 @@ __global__ void __launch_bounds__(ScanBackward<T>::kThreads, 4)
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         const int v = i * W + e;
-        const float q = z[k][v], before = run_apply(Run{A[k][v], B[k][v]}, h[e]);
+        const float q = z[k][v], kept = __builtin_fmaf(A[k][v], h[e], B[k][v]);
+        const float before = k > drop[v] ? B[k][v] : kept;
         if constexpr (kGate) dg[e] = dsilu[k][v] * after[e];
         const float G = dh[k][v] + u[e], s = __builtin_fabsf(q), slope = s * (1.f - s);
         dx[e] = gate_passes(q) ? 0.f : G * gate_w(q);

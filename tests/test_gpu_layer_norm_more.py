@@ -29,8 +29,8 @@ def test_no_sum_where_y_takes_the_place_of_x():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_near_the_root_of_the_largest_float(dtype):
-    """Values whose squares are 2^-14 to 2^-11 of the largest float, so that the
-    sums of 384 of them stay below it (in float: 384 x 2^115 < 2^124)."""
+    """Values up to 2^57: the sums of 384 of their squares stay below 2^123, so
+    in float."""
     rng = np.random.default_rng(15)
     x = rng.standard_normal((4, 384))
     x = np.clip(x, -4, 4) * np.array([[2.0 ** 55], [2.0 ** 55], [2.0 ** 55], [2.0 ** -55]])
