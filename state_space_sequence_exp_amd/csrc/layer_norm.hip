@@ -71,8 +71,13 @@ __device__ __forceinline__ Vec pack(const float (&v)[kE<T>]) {
 // 61 / 102 against 96 / 100, 4095 wide 117 / 141 against 198 / 210.  One element
 // alone waits for nobody (4097 wide: 143 / 216 against 117 / 183), nor do
 // floats, each of which has a register (4095 wide: 228 / 252 against 224 / 209).
+// Rows of such widths have kernels of their own (kCut), without the registers
+// of the other form: in one kernel with it, 4097 wide took 132 us forward and
+// 12281 wide (4096 rows) 161 backward, against 118 and 138.  (The other way round it
+// does not pay: a kernel that knows `wide` spills at 1024 threads, 8191 wide
+// 257 us forward against 242.)
 template <typename T>
-__device__ __forceinline__ bool loads_whole(int D) {
+__host__ __device__ __forceinline__ bool loads_whole(int D) {
   return sizeof(T) == 2 && D >= kE<T> && D % kE<T> != 1;
 }
 template <typename T, bool kVec>
@@ -174,12 +179,12 @@ constexpr int kNormWaves = NV == 1 ? (sizeof(T) == 2 && TPR == 512 && !kVec ? 6 
                            : TPR == 512 && NV == 2 ? 6
                            : sizeof(T) == 4 && NV == 2 && kVec ? 8 : 4;
 
-template <typename T, int TPR, int NV, bool kVec>
+template <typename T, int TPR, int NV, bool kVec, bool kCut>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, (kNormWaves<T, TPR, NV, kVec>)) norm_kernel(NormArgs a) {
   constexpr int E = kE<T>, NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
   __shared__ float s_sum[2][NT / kWave];
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
-  const bool wide = loads_whole<T>(a.D);
+  const bool wide = !kCut && loads_whole<T>(a.D);
   const float inv = 1.f / (float)a.D;
   float w[NV][E], b[NV][E];
 #pragma unroll
@@ -272,9 +277,9 @@ struct BwRow {
   Vec s[NV], dy[NV], ds[NV];
   float mean, rstd;
 };
-template <typename T, int TPR, int NV, bool kVec>
+template <typename T, int TPR, int NV, bool kVec, bool kCut>
 __device__ __forceinline__ void load_bw(const NormArgs& a, int64_t r, int t, BwRow<T, NV>& q) {
-  const bool wide = loads_whole<T>(a.D);
+  const bool wide = !kCut && loads_whole<T>(a.D);
   if (r >= a.rows) {  // a row of zeros adds nothing
 #pragma unroll
     for (int j = 0; j < NV; ++j) q.s[j] = q.dy[j] = q.ds[j] = Vec{{0u, 0u, 0u, 0u}};
@@ -293,7 +298,7 @@ __device__ __forceinline__ void load_bw(const NormArgs& a, int64_t r, int t, BwR
   q.rstd = a.rstd[r];
 }
 
-template <typename T, int TPR, int NV, bool kVec>
+template <typename T, int TPR, int NV, bool kVec, bool kCut>
 __global__ void __launch_bounds__(kBwThreads) norm_backward_kernel(NormArgs a, int rounds) {
   constexpr int E = kE<T>, kTeams = kBwThreads / TPR, C = TPR * NV * E;  // columns of a team
   __shared__ float s_p[2][kBwThreads / kWave], s_pq[2][kBwThreads / kWave];
@@ -315,21 +320,21 @@ __global__ void __launch_bounds__(kBwThreads) norm_backward_kernel(NormArgs a, i
   // registers hold both
   constexpr bool kAhead = NV == 1;
   BwRow<T, NV> cur, next;
-  if constexpr (kAhead) load_bw<T, TPR, NV, kVec>(a, r, t, next);
+  if constexpr (kAhead) load_bw<T, TPR, NV, kVec, kCut>(a, r, t, next);
   for (int k = 0; k < rounds; ++k, r += step) {
     if constexpr (kAhead) {
       cur = next;
-      load_bw<T, TPR, NV, kVec>(a, k + 1 < rounds ? r + step : a.rows, t, next);
+      load_bw<T, TPR, NV, kVec, kCut>(a, k + 1 < rounds ? r + step : a.rows, t, next);
     } else {
-      load_bw<T, TPR, NV, kVec>(a, r, t, cur);
+      load_bw<T, TPR, NV, kVec, kCut>(a, r, t, cur);
     }
     float q[NV][E], g[NV][E], sp = 0.f, spq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int n = a.D - (j * TPR + t) * E;
-      trim<T, kVec>(cur.s[j], n, loads_whole<T>(a.D));
-      trim<T, kVec>(cur.dy[j], n, loads_whole<T>(a.D));
-      trim<T, kVec>(cur.ds[j], n, loads_whole<T>(a.D));
+      trim<T, kVec>(cur.s[j], n, !kCut && loads_whole<T>(a.D));
+      trim<T, kVec>(cur.dy[j], n, !kCut && loads_whole<T>(a.D));
+      trim<T, kVec>(cur.ds[j], n, !kCut && loads_whole<T>(a.D));
       unpack<T>(cur.s[j], q[j]);
       unpack<T>(cur.dy[j], g[j]);
 #pragma unroll
@@ -439,17 +444,20 @@ bool vec16(const void* p, int64_t ld, size_t es) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)ld * es % 16 == 0);
 }
 
-template <typename T, int TPR, int NV, bool kVec>
+template <typename T, int TPR, int NV, bool kVec, bool kCut>
 hipError_t launch_fwd_v(const NormArgs& a, hipStream_t stream) {
   constexpr int NT = TPR > 256 ? TPR : 256, kTeams = NT / TPR;
   const int64_t most = 256 * (kNormWaves<T, TPR, NV, kVec> * 4 * kWave / NT);
   const dim3 grid((unsigned)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, most));
-  hipLaunchKernelGGL((norm_kernel<T, TPR, NV, kVec>), grid, dim3(NT), 0, stream, a);
+  hipLaunchKernelGGL((norm_kernel<T, TPR, NV, kVec, kCut>), grid, dim3(NT), 0, stream, a);
   return hipGetLastError();
 }
 template <typename T, int TPR, int NV>
 hipError_t launch_fwd(const NormArgs& a, bool vec, hipStream_t stream) {
-  return vec ? launch_fwd_v<T, TPR, NV, true>(a, stream) : launch_fwd_v<T, TPR, NV, false>(a, stream);
+  if (vec) return launch_fwd_v<T, TPR, NV, true, false>(a, stream);
+  if constexpr (sizeof(T) == 2)
+    if (!loads_whole<T>(a.D)) return launch_fwd_v<T, TPR, NV, false, true>(a, stream);
+  return launch_fwd_v<T, TPR, NV, false, false>(a, stream);
 }
 
 // The team for a row of `vecs` vectors: one a thread up to 1024; wide float
@@ -479,22 +487,24 @@ hipError_t launch_fwd_t(const NormArgs& a, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-template <typename T, int TPR, int NV, bool kVec>
+template <typename T, int TPR, int NV, bool kVec, bool kCut>
 hipError_t launch_bw_v(const NormArgs& a, int groups, hipStream_t stream) {
   constexpr int kTeams = kBwThreads / TPR;
   const size_t lds = kTeams > 1 ? sizeof(float) * (size_t)kTeams * 2 * TPR * NV * kE<T> : 0;
-  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&norm_backward_kernel<T, TPR, NV, kVec>), lds);
+  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&norm_backward_kernel<T, TPR, NV, kVec, kCut>), lds);
   if (e != hipSuccess) return e;
   const int64_t step = (int64_t)groups * kTeams;
   const int rounds = (int)((a.rows + step - 1) / step);
-  hipLaunchKernelGGL((norm_backward_kernel<T, TPR, NV, kVec>), dim3(groups), dim3(kBwThreads), lds,
+  hipLaunchKernelGGL((norm_backward_kernel<T, TPR, NV, kVec, kCut>), dim3(groups), dim3(kBwThreads), lds,
                      stream, a, rounds);
   return hipGetLastError();
 }
 template <typename T, int TPR, int NV>
 hipError_t launch_bw(const NormArgs& a, bool vec, int groups, hipStream_t stream) {
-  return vec ? launch_bw_v<T, TPR, NV, true>(a, groups, stream)
-             : launch_bw_v<T, TPR, NV, false>(a, groups, stream);
+  if (vec) return launch_bw_v<T, TPR, NV, true, false>(a, groups, stream);
+  if constexpr (sizeof(T) == 2)
+    if (!loads_whole<T>(a.D)) return launch_bw_v<T, TPR, NV, false, true>(a, groups, stream);
+  return launch_bw_v<T, TPR, NV, false, false>(a, groups, stream);
 }
 
 template <typename T>

@@ -35,3 +35,11 @@ def test_rows_near_the_root_of_the_largest_float(dtype):
     x = rng.standard_normal((4, 384))
     x = np.clip(x, -4, 4) * np.array([[2.0 ** 55], [2.0 ** 55], [2.0 ** 55], [2.0 ** -55]])
     run_case(4, 384, dtype, False, True, 16, x=x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(5, 8193), (3, 12281), (300, 513), (70, 1025), (40, 2049), (2, 16377)],
+                         ids=lambda s: "%dx%d" % s)
+def test_one_element_behind_the_last_vector(shape, dtype):
+    """Rows whose last vector holds one element, in every size of team."""
+    run_case(*shape, dtype, shape[0] % 2 == 0, True, seed=sum(shape))
