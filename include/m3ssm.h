@@ -434,7 +434,8 @@ typedef struct {
 
 /*
  * Bytes of device workspace m3_gated_scan and m3_gated_scan_backward need (0:
- * none, as with up to 64 tokens, or an unsupported shape).  Host only.
+ * none, as with up to 64 tokens, or an unsupported shape).  Host only.  (The
+ * backward pass needs all of it, the forward pass about half.)
  *
  * The workspace (256-byte aligned) holds the counters and words by which the
  * chunks of a sequence hand on their states.  They are zero on entry and left
@@ -469,8 +470,9 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, m3_dtype dtype, const void* x,
  *   dx_t = G_t (1 - a_t)        df_t = G_t (h_{t-1} - x_t) a_t (1 - a_t)
  *   dg_t = dy_t h_t silu'(g_t)  dh0  = a_0 G_0
  *
- * dx, df, dg in the storage type, dh0 float.  Where the gate is a mask (a is
- * 0 or 1 in float) df is 0; where it passes the state, dx is 0.  dh_last and
+ * dx, df, dg in the storage type, dh0 float.  Where the gate is a mask (f
+ * infinite, or a or 1 - a underflows: |f| from about 87 on) df is 0; where it
+ * passes the state, dx is 0.  dh_last and
  * dh0 may be NULL; dg is required exactly when g is given.  The outputs and
  * the workspace must not overlap the inputs or each other, as above.  seqlen
  * == 0 writes dh0 = dh_last.

@@ -7,8 +7,10 @@
 // Bound by memory: x, f and g are read once and y is written once.  B1 T16384
 // D4096 bfloat16 with the gate takes 113 us (4.8 TB/s, 5.2 with the chain's
 // words; copies reach 5.2 to 6.1).  What a short call takes is the latency of
-// its steps: 10 us for B3 T777 D1024, of which about 1 us a place of the chain;
-// rows that are not vectors throughout add 2 us to that.
+// its steps: B1 D1024 bfloat16 6.9 us for one place of the chain (up to 128
+// tokens), 8.1 for two, about 0.3 more for each further one (9.8 for 8, 12.1 for
+// 16, 16.5 for 32); B3 T777 D1024 10.5.  Rows that are not vectors throughout add
+// 2 us to that: a wave at an edge has its loads of f back before it requests x.
 //
 // A workgroup requests its chunk of x and f and walks each thread's tokens
 // once, keeping for every token the map from the state before the thread's
@@ -16,7 +18,7 @@
 // published, g is requested, and once the state that enters the chunk is known
 // every state is A h + B.  (Walking the tokens a second time instead keeps
 // one float a token less and takes 63 vector operations an element with the
-// output gate, against 37: 139 us for B1 T16384 D4096 bf16 and bound by them.)
+// output gate, against 38: 139 us for B1 T16384 D4096 bf16 and bound by them.)
 #include <type_traits>
 
 #include "scan_tile.h"

@@ -8,7 +8,10 @@
 // team of 64 to 1024 threads that keeps it in registers, NV 16-byte
 // vectors a thread, between the sum, the centred squares and the output; the
 // threads keep their columns of the weights while their team walks rows.  The
-// sums go by lane moves in a wave and by the LDS between waves.
+// sums go by lane moves in a wave and by the LDS between waves.  (Rows above
+// 8192 channels ask for more than the 128 registers that 1024 threads leave a
+// thread in the backward pass: it spills 3 to 13 of them for bfloat16, 11 or 27
+// for float.)
 //
 // The backward pass keeps each column's dweight and dbias in the registers of
 // the thread that owns it, over all rows of its workgroup (up to 256 groups of
@@ -16,8 +19,13 @@
 // second kernel, both in a fixed order.
 //
 // 8192 x 2048 bfloat16 with the residual and its gradient: forward 26 us (5.1
-// TB/s), backward 29 and 4 for the joining kernel (4.6 without it); rows that
-// are not 16-byte aligned run at 0.6 to 0.9 of that.
+// TB/s), backward 29 and 4 for the joining kernel (4.6 without it).  Rows that
+// are not 16-byte aligned run at 0.6 to 0.9 of that.  A row that leaves its team
+// idle costs more in the backward pass, which has one workgroup a compute unit:
+// 16384 x 2100 bfloat16 (263 vectors in a team of 512) 102 us, x 2047 63.  Above
+// 8192 channels, 2048 rows with the residual's gradient, bfloat16 / float: 12288
+// wide 65 / 102 us (its bytes take 37 / 75), 16384 wide 89 / 136 (50 / 100), 16383
+// wide 118 / 174; 8192 wide, which does not spill, 52 / 62 (25 / 50).
 #include <algorithm>
 
 #include "layer_internal.h"
@@ -169,7 +177,8 @@ __device__ __forceinline__ float team_sum(float v, float* s) {
   return v;
 }
 
-// Waves a SIMD that the forward kernel's registers allow.  The launch has as
+// Waves a SIMD that the forward kernel's registers allow (bfloat16 rows off the
+// vectors' alignment in teams of 1024 spill one).  The launch has as
 // many workgroups as that makes, each walking as many rows as the others: with
 // more, those that find no place start when the rest is done (1000 x 4097
 // float with the residual: 16.2 us for four a compute unit where two fit, 13.8

@@ -13,9 +13,11 @@
 // the registers let run.  Measured on B1 T16384 and B4 T2048, D4096, bfloat16
 // with the output gate: tiles of 128 bytes of channels reach 4.1 TB/s where
 // these reach 4.7; the forward pass with V = 2 and 64 tokens runs three
-// workgroups a unit instead of two and is no faster (142 against 123 us), as a
+// workgroups a unit instead of two and is no faster (142 against 123 us when
+// this was measured, now 113), as a
 // long sequence then has twice the tiles to chain; the backward pass with V =
-// 4 and 128 tokens fills its registers and runs two (126 against 116 us).
+// 4 and 128 tokens fills its registers and runs two (126 against 116 us then,
+// now 109).
 #pragma once
 
 #include <hip/hip_runtime.h>
