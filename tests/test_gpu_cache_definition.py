@@ -6,8 +6,7 @@ cosine are first read out of the kernel itself, as the y of states of ones."""
 import numpy as np
 import pytest
 
-from layer_util import put, stored, torch_type
-from gpu_util import from_gpu
+from layer_util import put, stored
 from test_gpu_state_cache import cache_with, raw, rows
 
 pytestmark = pytest.mark.gpu

@@ -82,7 +82,6 @@ def test_a_nan_gate_before_a_document(at, dtype):
     """A gate that is NaN spoils its document from there on, forward, and all
     before it in the gradients, but neither the next document nor the next one's
     gradients."""
-    import state_space_sequence_exp_amd as m3
     from oracle import layer as O
     T, D = 300, 40
     v = draw(5, T, D, dtype, True)
@@ -116,3 +115,31 @@ def test_a_large_state_is_forgotten(T, dtype):
     o = O.gated_scan(v["x"], v["f"], None, v["h0"])
     close(got["y"], o["y"], o["e_y"], dtype, "y")
     close(got["last"], o["h_last"], o["e_last"], "f32", "h_last")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_arrays_between_each_other_s_rows(dtype):
+    """A step whose y, x and f are slices of one wide array, and whose state lies
+    dense between two of its rows: nothing overlaps, nothing is refused, and the
+    results are those of arrays apart."""
+    import torch
+    import state_space_sequence_exp_amd as m3
+    B, D = 2, 24
+    ty = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    wide = torch.randn(B, 12 * D, device="cuda", generator=gen).to(ty)
+    y, x, f = (wide[:, i * D:(i + 1) * D] for i in range(3))
+    h = wide.view(-1)[4 * D:4 * D + B * D * 4 // wide.element_size()].view(torch.float32).view(B, D)
+    h.copy_(torch.randn(B, D, device="cuda", generator=gen))
+    keep = wide.clone()
+    want_y, want_h = m3.gated_scan_step(h.clone(), x.clone(), f.clone())
+    got_y, got_h = m3.gated_scan_step(h, x, f, y=y)
+    assert got_y is y and got_h is h and torch.equal(y, want_y) and torch.equal(h, want_h)
+    at = slice(4 * D, 4 * D + B * D * 4 // wide.element_size())
+    keep[:, :D] = y
+    keep.view(-1)[at] = wide.view(-1)[at]
+    bits = lambda a: a.view(torch.uint8)              # (halves of a state may read as NaN in the storage type)
+    assert torch.equal(bits(wide), bits(keep))
+    for bad in (x, f, h if dtype == "f32" else x):
+        with pytest.raises(m3.M3Error):
+            m3.gated_scan_step(h, x, f, y=bad)
