@@ -28,6 +28,7 @@
 // magnitude comes from the lanes that share the row.
 #include "layer_internal.h"
 #include "m3_device.h"
+#include "slots.h"
 
 // For the whole file: a fused operation is one rounding less, which is another
 // code now and then (the product h (Q / amax), say, is rounded before the sum
@@ -165,32 +166,11 @@ __device__ __forceinline__ float row_top(float top, int lanes) {
   return top;
 }
 
-// The slot of entry i, or -1 when it is idle.
-__device__ __forceinline__ int slot_of(const CacheArgs& a, int i) {
-  const int s = a.slots ? a.slots[i] : i;
-  return (s < 0 || s >= a.n_slots) ? -1 : s;
-}
-// Whether this thread sees an entry before i that names the same slot: the NT
-// threads of a workgroup look at all of them, 8 a thread in flight.
-template <int NT>
-__device__ __forceinline__ int named_before(const CacheArgs& a, int i, int slot) {
-  int same = 0;
-  if (a.slots)
-    for (int j0 = threadIdx.x; j0 < i; j0 += 8 * NT) {
-      int s[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s[q] = j0 + q * NT < i ? a.slots[j0 + q * NT] : -1;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) same |= s[q] == slot ? 1 : 0;
-    }
-  return same;
-}
-
 template <int kCode>
 __global__ void __launch_bounds__(kThreads) store_kernel(CacheArgs a) {
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
-  const int slot = slot_of(a, i);
-  if (slot < 0 || __syncthreads_or(named_before<kThreads>(a, i, slot))) return;
+  const int slot = slot_of(a.slots, a.n_slots, i);
+  if (slot < 0 || __syncthreads_or(named_before<kThreads>(a.slots, i, slot))) return;
   const int lanes = a.P / 8;
   const float* h = a.h_in + ((size_t)i * a.H + head) * a.N * a.P;
   const size_t unit = (size_t)slot * a.H + head;
@@ -225,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(CacheArgs a) {
   };
   typedef T Out __attribute__((ext_vector_type(E)));
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
-  const int slot = slot_of(a, i);
+  const int slot = slot_of(a.slots, a.n_slots, i);
   const int lanes = a.P / E, all = a.N * lanes;
   Out* h = reinterpret_cast<Out*>(static_cast<T*>(a.h_out) + ((size_t)i * a.H + head) * a.N * a.P);
   if (slot < 0) {
@@ -336,7 +316,7 @@ template <typename T, int R, int kCode, bool kTrap, bool kRot, int NT>
 __global__ void __launch_bounds__(NT) decode_kernel(CacheArgs a) {
   extern __shared__ __align__(16) float dsm[];
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
-  const int slot = slot_of(a, i);
+  const int slot = slot_of(a.slots, a.n_slots, i);
   if (slot < 0) return;
   const int N = a.N, P = a.P, npair = N / 2, lanes = P / 8;
   const int tid = threadIdx.x, c8 = tid % lanes, rg = tid / lanes, groups = NT / lanes;
@@ -371,7 +351,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(CacheArgs a) {
   pair_coefficients<T, R, kTrap, kRot, NT>(a, in, npair, d, s_pair);
   // of entries with one slot the first takes it; also the barrier before the
   // coefficients are read
-  if (__syncthreads_or(named_before<NT>(a, i, slot))) return;
+  if (__syncthreads_or(named_before<NT>(a.slots, i, slot))) return;
 
   for (int kp = rg; kp < npair; kp += groups) {  // the lanes of a row together
     const PairCoef<R>& q = s_pair[kp];
@@ -480,7 +460,7 @@ __global__ void __launch_bounds__(kWave, R > 2 ? 3 : 4) decode_outer_kernel(Cach
   constexpr int P = 64, kRound = R < 2 ? R : 2, kPitch = kRound * P + 4;
   extern __shared__ __align__(16) float dsm[];
   const int i = blockIdx.x / a.H, head = blockIdx.x % a.H;
-  const int slot = slot_of(a, i);
+  const int slot = slot_of(a.slots, a.n_slots, i);
   if (slot < 0) return;
   const int N = a.N, npair = N / 2;
   const int lane = threadIdx.x, g = lane / 16, c = lane % 16;
@@ -515,7 +495,7 @@ __global__ void __launch_bounds__(kWave, R > 2 ? 3 : 4) decode_outer_kernel(Cach
   const float alpha = expf(d * a.A[head]);
   const float cu = (1.f - la) * d, cv = la * d;
   pair_coefficients<bf16, R, kTrap, kRot, kWave>(a, in, npair, d, s_pair);
-  if (__syncthreads_or(named_before<kWave>(a, i, slot))) return;
+  if (__syncthreads_or(named_before<kWave>(a.slots, i, slot))) return;
 
   for (int k0 = 0; k0 < npair; k0 += 16) {
     const int kp = k0 + c;
