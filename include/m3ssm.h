@@ -605,6 +605,166 @@ m3_status m3_decode_step_cached(const m3_dims* dims, m3_dtype dtype, m3_code cod
                                 const float* A, const float* lam, const float* theta, void* y_t,
                                 void* stream);
 
+/*
+ * Short causal convolution over the tokens, one filter a channel, as it stands
+ * before a selective scan.  Per sequence b and channel d:
+ *
+ *   y_t = act(bias[d] + sum_{k=0..W-1} weight[d][k] x_{t-(W-1)+k})
+ *
+ * act(v) = v * sigmoid(v) with `silu` nonzero, v otherwise.  Inputs before the
+ * first token come from state_in [batch, W-1, D] (the W-1 inputs before it, the
+ * oldest first, in the storage type; NULL: zeros), and state_out (NULL: not
+ * kept), of the same form, receives the last W-1 inputs of each sequence, so
+ * that a prompt can be taken in pieces.
+ *
+ * lengths [batch] int32 (device; NULL: all seqlen) holds the tokens of each
+ * sequence, taken as 0 where negative and as seqlen where larger.  The tokens
+ * from there on are padding: their x is not looked at, their y is 0.
+ *
+ * Layouts: x, y [batch, T, D], token t of sequence b at (b T + t) ld, D
+ * contiguous; weight [D, W], bias [D] float.  W is 2, 3 or 4.  Pointers need
+ * element alignment; any ld and width is moved in vectors of 16 bytes but for
+ * the rest of a row.  Sums are float, rounded once.  Outputs must not overlap an
+ * input or each other.
+ */
+typedef struct {
+  int64_t batch;    /* sequences (>= 0) */
+  int64_t seqlen;   /* T (>= 0; ignored by m3_causal_conv_step) */
+  int64_t channels; /* D (>= 1) */
+  int64_t width;    /* W, taps: 2, 3 or 4 */
+  /* elements from one token to the next, >= channels; 0 means channels */
+  int64_t ld_x, ld_y;
+} m3_conv_dims;
+
+/* seqlen == 0 copies the states; batch == 0 enqueues nothing.  At most 2^24 - 1
+ * workgroups of 256 vectors by 8 tokens. */
+m3_status m3_causal_conv(const m3_conv_dims* dims, m3_dtype dtype, const void* x,
+                         const float* weight, const float* bias, int silu, const void* state_in,
+                         const int32_t* lengths, void* y, void* state_out, void* stream);
+
+/*
+ * One token for `batch` sequences (row b of x and y at b ld) whose states lie in
+ * a pool state [n_slots, W-1, D], updated in place.  slots [batch] int32
+ * (device) as for the 8-bit state cache: NULL means row b in slot b; a row whose
+ * entry is negative or >= n_slots is idle, as is every later row that names a
+ * slot again, and its y and state are left as they are.
+ */
+m3_status m3_causal_conv_step(const m3_conv_dims* dims, m3_dtype dtype, void* state,
+                              const int32_t* slots, int64_t n_slots, const void* x,
+                              const float* weight, const float* bias, int silu, void* y,
+                              void* stream);
+
+/*
+ * Selective state space scan: a state of N numbers a channel, each with a decay
+ * of its own, the step size chosen by the input.  Per sequence b and channel d:
+ *
+ *   s_t      = softplus(dt_t + dt_bias[d])       (dt_t + dt_bias[d] without softplus)
+ *   h_t[n]   = exp(s_t A[d][n]) h_{t-1}[n] + s_t x_t B_t[n]        h_{-1} = h0
+ *   y_t      = (sum_n C_t[n] h_t[n] + skip[d] x_t) * silu(z_t)
+ *
+ * dt_bias (0), skip (0), z (no gate) and h0 (0) may be NULL.
+ *
+ * Layouts: x, dt, z, y [batch, T, D] and B, C [batch, T, N], token t of sequence
+ * b at (b T + t) ld, the last axis contiguous, each array with its own ld: the
+ * slices of wider projections are read in place.  They are of the storage type;
+ * A [D, N], skip, dt_bias [D] and the states h0, h_last [batch, D, N] are float,
+ * dense.  N is 1 to 64.  Pointers need element alignment.  Steps, decays, states
+ * and sums are float whatever the storage type, y is rounded once.
+ *
+ * lengths as for m3_causal_conv: nothing of the padding is looked at, its y is
+ * 0, h_last is the state after a sequence's own last token.
+ *
+ * A <= 0 and finite inputs are preconditions, not checked.  Outputs and the
+ * workspace must not overlap an input or each other.
+ */
+#define M3_SELECT_MAX_STATES 64
+
+typedef struct {
+  int64_t batch;    /* sequences (>= 0) */
+  int64_t seqlen;   /* T (>= 0; ignored by m3_selective_scan_step) */
+  int64_t channels; /* D (>= 1) */
+  int64_t dstate_n; /* N: 1..64 */
+  /* elements from one token to the next, >= the row; 0 means the row */
+  int64_t ld_x, ld_dt, ld_z, ld_y, ld_b, ld_c;
+} m3_select_dims;
+
+/*
+ * Bytes of device workspace m3_selective_scan needs for these dims; 0: none.  A
+ * batch of many channels needs none; one of few channels and many tokens is cut
+ * into segments, whose states lie there between two launches.  It need not be
+ * cleared and keeps nothing between calls; calls that overlap need distinct
+ * ones.  256-byte aligned.  Host only.
+ */
+size_t m3_selective_scan_workspace_size(const m3_select_dims* dims, m3_dtype dtype);
+
+/* seqlen == 0 writes h_last = h0 (zeros when NULL); batch == 0 enqueues nothing. */
+m3_status m3_selective_scan(const m3_select_dims* dims, m3_dtype dtype, const void* x,
+                            const void* dt, const float* A, const void* B, const void* C,
+                            const float* skip, const void* z, const float* dt_bias, int softplus,
+                            const float* h0, const int32_t* lengths, void* y, float* h_last,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for `batch` sequences (row b of x, dt, z, y, B, C at b ld) whose
+ * states lie in a pool h [n_slots, D, N] float, updated in place.  slots as for
+ * m3_causal_conv_step.
+ */
+m3_status m3_selective_scan_step(const m3_select_dims* dims, m3_dtype dtype, float* h,
+                                 const int32_t* slots, int64_t n_slots, const void* x,
+                                 const void* dt, const float* A, const void* B, const void* C,
+                                 const float* skip, const void* z, const float* dt_bias,
+                                 int softplus, void* y, void* stream);
+
+/*
+ * Gated feed-forward projections: both products, the activation and the gate in
+ * one kernel.  Per row of x [rows, K]:
+ *
+ *   g = x w_gate^T,  u = x w_up^T,  h = silu(g) * u        [rows, F]
+ *
+ * w_gate, w_up [F, K] (a row an output).  x, the weights and h are of the storage
+ * type; products are summed in float (bfloat16: on the bfloat16 matrix units,
+ * float: on the float ones) and h is rounded once.  gate and up [rows, F] float
+ * (both or neither NULL) receive g and u for the backward pass.
+ *
+ * Row r of an array is at r ld.  Pointers need element alignment; the products
+ * run fastest where every row of x and of the weights starts at a multiple of 16
+ * bytes and K is a multiple of 16 bytes.  Outputs must not overlap an input or
+ * each other.  rows, K and F at most 2^31 - 1, ld at most 2^24 - 1.
+ */
+typedef struct {
+  int64_t rows;     /* (>= 0) */
+  int64_t channels; /* K (>= 1) */
+  int64_t hidden;   /* F (>= 1) */
+  /* elements from one row to the next, >= the row; 0 means the row */
+  int64_t ld_x, ld_wgate, ld_wup, ld_h, ld_gate, ld_up;
+  int64_t ld_dh, ld_dx, ld_dwgate, ld_dwup; /* backward only */
+} m3_ffn_dims;
+
+m3_status m3_gated_ffn(const m3_ffn_dims* dims, m3_dtype dtype, const void* x,
+                       const void* w_gate, const void* w_up, void* h, float* gate, float* up,
+                       void* stream);
+
+/*
+ * Gradients of sum <h, dh> from the same inputs and the gate and up that
+ * m3_gated_ffn kept:
+ *
+ *   du = dh silu(g),  dg = dh u silu'(g)      (rounded to the storage type)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ *
+ * in the storage type, summed in float in a fixed order: a call repeats bit for
+ * bit.  dx may be NULL (inputs that learn nothing), and so may dw_gate and dw_up
+ * together (weights that do not).  rows == 0 writes zeros to dw_gate and dw_up.
+ * The workspace (256-byte aligned) holds dg and du; it need not be cleared.
+ * Outputs and the workspace must not overlap an input or each other.
+ */
+size_t m3_gated_ffn_backward_workspace_size(const m3_ffn_dims* dims, m3_dtype dtype);
+
+m3_status m3_gated_ffn_backward(const m3_ffn_dims* dims, m3_dtype dtype, const void* dh,
+                                const void* x, const void* w_gate, const void* w_up,
+                                const float* gate, const float* up, void* dx, void* dw_gate,
+                                void* dw_up, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

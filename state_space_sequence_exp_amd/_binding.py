@@ -36,7 +36,9 @@ ABI_SYMBOLS = ("m3_version", "m3_status_string", "m3_prefill_workspace_size", "m
                "m3_gated_scan_workspace_size", "m3_gated_scan", "m3_gated_scan_backward",
                "m3_gated_scan_step", "m3_layer_norm", "m3_layer_norm_backward_workspace_size",
                "m3_layer_norm_backward", "m3_state_store", "m3_state_load",
-               "m3_decode_step_cached")
+               "m3_decode_step_cached", "m3_causal_conv", "m3_causal_conv_step",
+               "m3_selective_scan_workspace_size", "m3_selective_scan", "m3_selective_scan_step",
+               "m3_gated_ffn", "m3_gated_ffn_backward_workspace_size", "m3_gated_ffn_backward")
 
 
 class M3Error(RuntimeError):
@@ -59,6 +61,21 @@ class M3ScanDims(ctypes.Structure):
 class M3NormDims(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int64) for k in ("rows", "channels", "ld_x", "ld_residual", "ld_sum",
                                               "ld_y", "ld_dy", "ld_dsum", "ld_dx")]
+
+
+class M3ConvDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("batch", "seqlen", "channels", "width", "ld_x", "ld_y")]
+
+
+class M3SelectDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("batch", "seqlen", "channels", "dstate_n", "ld_x", "ld_dt",
+                                              "ld_z", "ld_y", "ld_b", "ld_c")]
+
+
+class M3FfnDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "channels", "hidden", "ld_x", "ld_wgate", "ld_wup",
+                                              "ld_h", "ld_gate", "ld_up", "ld_dh", "ld_dx", "ld_dwgate",
+                                              "ld_dwup")]
 
 
 _lib = None
@@ -135,6 +152,23 @@ def load_library(path: Optional[str] = None):
     lib.m3_state_load.argtypes = [dp, i, i, vp, vp, vp, i64, vp, vp]
     lib.m3_decode_step_cached.restype = i
     lib.m3_decode_step_cached.argtypes = [dp, i, i, vp, vp, vp, i64] + [vp] * 11
+    cp, ep, fp = (ctypes.POINTER(t) for t in (M3ConvDims, M3SelectDims, M3FfnDims))
+    lib.m3_causal_conv.restype = i
+    lib.m3_causal_conv.argtypes = [cp, i, vp, vp, vp, i] + [vp] * 5
+    lib.m3_causal_conv_step.restype = i
+    lib.m3_causal_conv_step.argtypes = [cp, i, vp, vp, i64, vp, vp, vp, i, vp, vp]
+    lib.m3_selective_scan_workspace_size.restype = sz
+    lib.m3_selective_scan_workspace_size.argtypes = [ep, i]
+    lib.m3_selective_scan.restype = i
+    lib.m3_selective_scan.argtypes = [ep, i] + [vp] * 8 + [i] + [vp] * 5 + [sz, vp]
+    lib.m3_selective_scan_step.restype = i
+    lib.m3_selective_scan_step.argtypes = [ep, i, vp, vp, i64] + [vp] * 8 + [i, vp, vp]
+    lib.m3_gated_ffn.restype = i
+    lib.m3_gated_ffn.argtypes = [fp, i] + [vp] * 7
+    lib.m3_gated_ffn_backward_workspace_size.restype = sz
+    lib.m3_gated_ffn_backward_workspace_size.argtypes = [fp, i]
+    lib.m3_gated_ffn_backward.restype = i
+    lib.m3_gated_ffn_backward.argtypes = [fp, i] + [vp] * 10 + [sz, vp]
     if path is None:
         _lib = lib
     return lib
@@ -955,3 +989,308 @@ def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, 
             _at(scales), _at(slots), n, _at(x_t), _at(x_prev), _at(B_t), _at(B_prev),
             _at(C_t), _at(dt), _at(A), _at(lam), _at(theta), _at(y))
     return y
+
+
+def _lengths(lengths, nb, dev):
+    import torch
+    if lengths is not None:
+        _same(lengths, "lengths", torch.int32, (nb,), dev)
+
+
+def _pool_slots(slots, nb, n_slots, dev):
+    import torch
+    if slots is not None:
+        _same(slots, "slots", torch.int32, (nb,), dev)
+    elif nb > n_slots:
+        raise ValueError("%d rows without slots for a pool of %d" % (nb, n_slots))
+
+
+@_streamed
+def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths=None, y=None,
+                state_out=None, want_state: bool = True) -> Tuple:
+    """Short causal convolution over the tokens, one filter of W = 2, 3 or 4 taps
+    a channel (m3_causal_conv): y_t = act(bias + sum_k weight[:, k] x_{t-(W-1)+k}),
+    act the silu with silu=True, the identity without.
+
+    x [B,T,D] float32 or bfloat16, tokens at one distance (a slice of a wider
+    projection is read in place); weight [D,W], bias [D] float32.  state
+    [B,W-1,D] in x's type: the inputs before the first token, the oldest first
+    (None: zeros).  lengths [B] int32: the tokens of each sequence; those behind
+    are padding, not looked at, their y is 0.  y and state_out may be given;
+    they must not overlap an input or each other.
+    Returns (y, state [B,W-1,D]: the last W-1 inputs, for the next piece or
+    causal_conv_step; None without want_state).
+    """
+    import torch
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
+    if len(shape) != 3:
+        raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
+    nb, nt, nd = shape
+    code = _type_code(dt)
+    if weight.dim() != 2:
+        raise ValueError("weight: expected [D, W], got %s" % (tuple(weight.shape),))
+    nw = weight.shape[1]
+    ld = _rows(x, "x", dt, shape, dev)
+    d = M3ConvDims(nb, nt, nd, nw, ld)
+    _same(weight, "weight", torch.float32, (nd, nw), dev)
+    if bias is not None:
+        _same(bias, "bias", torch.float32, (nd,), dev)
+    kept = (nb, nw - 1, nd)
+    if state is not None:
+        _same(state, "state", dt, kept, dev)
+    if state_out is not None:
+        _same(state_out, "state_out", dt, kept, dev)
+    _lengths(lengths, nb, dev)
+    if y is not None:
+        d.ld_y = _rows(y, "y", dt, shape, dev)
+    _gpu(dev)
+    if y is None:
+        y = _like(x, ld == 0)
+    if state_out is None and want_state:
+        state_out = x.new_empty(kept)
+    _launch(dev, lib.m3_causal_conv, ctypes.byref(d), code, _at(x), _at(weight), _at(bias),
+            int(bool(silu)), _at(state), _at(lengths), _at(y), _at(state_out))
+    return y, state_out
+
+
+@_streamed
+def causal_conv_step(state, x, weight, bias=None, *, silu: bool = False, slots=None, y=None):
+    """One token of the short causal convolution, its states updated in place
+    (m3_causal_conv_step).
+
+    state [slots,W-1,D] in x's type; x [B,D] float32 or bfloat16; slots [B] int32
+    names each row's state (negative, past the pool, or named by a row before:
+    idle; None: row b in slot b).  Returns y [B,D], whose idle rows are left as
+    they were (zeros when y is not given)."""
+    import torch
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
+    if len(shape) != 2:
+        raise ValueError("x: expected [B, D], got %s" % (tuple(shape),))
+    nb, nd = shape
+    code = _type_code(dt)
+    if weight.dim() != 2 or state.dim() != 3:
+        raise ValueError("expected weight [D, W] and state [slots, W-1, D], got %s and %s"
+                         % (tuple(weight.shape), tuple(state.shape)))
+    nw, ns = weight.shape[1], state.shape[0]
+    ld = _rows(x, "x", dt, shape, dev)
+    d = M3ConvDims(nb, 1, nd, nw, ld)
+    _same(weight, "weight", torch.float32, (nd, nw), dev)
+    if bias is not None:
+        _same(bias, "bias", torch.float32, (nd,), dev)
+    _same(state, "state", dt, (ns, nw - 1, nd), dev)
+    _pool_slots(slots, nb, ns, dev)
+    if y is not None:
+        d.ld_y = _rows(y, "y", dt, shape, dev)
+    _gpu(dev)
+    if y is None:
+        y = _like(x, ld == 0) if slots is None else x.new_zeros(shape)
+    _launch(dev, lib.m3_causal_conv_step, ctypes.byref(d), code, _at(state), _at(slots), ns,
+            _at(x), _at(weight), _at(bias), int(bool(silu)), _at(y))
+    return y
+
+
+def selective_scan_workspace_size(batch, seqlen, channels, N, dtype) -> int:
+    """Bytes of workspace selective_scan needs (0: none)."""
+    d = M3SelectDims(int(batch), int(seqlen), int(channels), int(N))
+    return int(load_library().m3_selective_scan_workspace_size(ctypes.byref(d), _type_code(dtype)))
+
+
+@_streamed
+def selective_scan(x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, softplus: bool = True,
+                   h0=None, lengths=None, y=None, h_last=None, workspace=None) -> Tuple:
+    """Selective state space scan over a sequence (m3_selective_scan): per channel
+    N states, s = softplus(dt + dt_bias) (dt + dt_bias with softplus=False),
+    h[n] = exp(s A[n]) h[n] + s x B[n], y = (sum_n C[n] h[n] + skip x) silu(z).
+
+    x, dt, z [B,T,D] and B, C [B,T,N], N <= 64, float32 or bfloat16 (one type),
+    tokens at one distance in each (slices of wider projections are read in
+    place); A [D,N], skip, dt_bias [D] float32; h0 [B,D,N] float32 or None
+    (zeros).  lengths [B] int32: the tokens of each sequence; those behind are
+    padding, not looked at, their y is 0.  y and h_last may be given; they must
+    not overlap an input or each other.  A workspace
+    (selective_scan_workspace_size bytes, of any content) may be kept for later
+    calls; calls that overlap need distinct ones.
+    Returns (y [B,T,D], h_last [B,D,N] float32: each sequence's state after its
+    own last token)."""
+    import torch
+    lib = _lib or load_library()
+    shape, dev, dtype = x.shape, x.get_device(), x.dtype
+    if len(shape) != 3 or A.dim() != 2:
+        raise ValueError("expected x [B, T, D] and A [D, N], got %s and %s"
+                         % (tuple(shape), tuple(A.shape)))
+    nb, nt, nd = shape
+    nn = A.shape[1]
+    code = _type_code(dtype)
+    thin = (nb, nt, nn)
+    ld = _rows(x, "x", dtype, shape, dev)
+    d = M3SelectDims(nb, nt, nd, nn, ld, _rows(dt, "dt", dtype, shape, dev),
+                     0 if z is None else _rows(z, "z", dtype, shape, dev), 0,
+                     _rows(B, "B", dtype, thin, dev), _rows(C, "C", dtype, thin, dev))
+    _same(A, "A", torch.float32, (nd, nn), dev)
+    if skip is not None:
+        _same(skip, "skip", torch.float32, (nd,), dev)
+    if dt_bias is not None:
+        _same(dt_bias, "dt_bias", torch.float32, (nd,), dev)
+    if h0 is not None:
+        _same(h0, "h0", torch.float32, (nb, nd, nn), dev)
+    if h_last is not None:
+        _same(h_last, "h_last", torch.float32, (nb, nd, nn), dev)
+    _lengths(lengths, nb, dev)
+    if y is not None:
+        d.ld_y = _rows(y, "y", dtype, shape, dev)
+    _gpu(dev)
+    if y is None:
+        y = _like(x, ld == 0)
+    if h_last is None:
+        h_last = A.new_empty((nb, nd, nn))
+    need = int(lib.m3_selective_scan_workspace_size(ctypes.byref(d), code))
+    ws_bytes = 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the first tensor's device")
+        ws_bytes = workspace.nbytes
+    _launch(dev, lib.m3_selective_scan, ctypes.byref(d), code, _at(x), _at(dt), _at(A), _at(B), _at(C),
+            _at(skip), _at(z), _at(dt_bias), int(bool(softplus)), _at(h0), _at(lengths), _at(y),
+            _at(h_last), _at(workspace) if need else None, ws_bytes)
+    return y, h_last
+
+
+@_streamed
+def selective_scan_step(h, x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, softplus: bool = True,
+                        slots=None, y=None):
+    """One token of the selective scan, its states updated in place
+    (m3_selective_scan_step).
+
+    h [slots,D,N] float32; x, dt, z [B,D] and B, C [B,N] float32 or bfloat16;
+    slots [B] int32 as for causal_conv_step; the rest as for selective_scan.
+    Returns y [B,D], whose idle rows are left as they were (zeros when y is not
+    given)."""
+    import torch
+    lib = _lib or load_library()
+    shape, dev, dtype = x.shape, x.get_device(), x.dtype
+    if len(shape) != 2 or A.dim() != 2 or h.dim() != 3:
+        raise ValueError("expected h [slots, D, N], x [B, D] and A [D, N], got %s, %s and %s"
+                         % (tuple(h.shape), tuple(shape), tuple(A.shape)))
+    nb, nd = shape
+    nn, ns = A.shape[1], h.shape[0]
+    code = _type_code(dtype)
+    ld = _rows(x, "x", dtype, shape, dev)
+    d = M3SelectDims(nb, 1, nd, nn, ld, _rows(dt, "dt", dtype, shape, dev),
+                     0 if z is None else _rows(z, "z", dtype, shape, dev), 0,
+                     _rows(B, "B", dtype, (nb, nn), dev), _rows(C, "C", dtype, (nb, nn), dev))
+    _same(A, "A", torch.float32, (nd, nn), dev)
+    _same(h, "h", torch.float32, (ns, nd, nn), dev)
+    if skip is not None:
+        _same(skip, "skip", torch.float32, (nd,), dev)
+    if dt_bias is not None:
+        _same(dt_bias, "dt_bias", torch.float32, (nd,), dev)
+    _pool_slots(slots, nb, ns, dev)
+    if y is not None:
+        d.ld_y = _rows(y, "y", dtype, shape, dev)
+    _gpu(dev)
+    if y is None:
+        y = _like(x, ld == 0) if slots is None else x.new_zeros(shape)
+    _launch(dev, lib.m3_selective_scan_step, ctypes.byref(d), code, _at(h), _at(slots), ns, _at(x),
+            _at(dt), _at(A), _at(B), _at(C), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+            _at(y))
+    return y
+
+
+@_streamed
+def gated_ffn(x, w_gate, w_up, *, want_pre: bool = False, h=None, gate=None, up=None) -> Tuple:
+    """Gated feed-forward projections (m3_gated_ffn): h = silu(x w_gate^T) * (x
+    w_up^T), both products, the activation and the gate in one kernel.
+
+    x [...,K], w_gate, w_up [F,K] float32 or bfloat16 (one type), rows at one
+    distance.  want_pre keeps the two products, in float32, for the backward pass.
+    h, gate and up may be given (gate and up together); they must not overlap an
+    input or each other.
+    Returns (h [...,F], gate, up [...,F] float32 or None)."""
+    import torch
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
+    if len(shape) < 1 or w_gate.dim() != 2:
+        raise ValueError("expected x [..., K] and w_gate [F, K], got %s and %s"
+                         % (tuple(shape), tuple(w_gate.shape)))
+    code = _type_code(dt)
+    nk, nf = shape[-1], w_gate.shape[0]
+    out = shape[:-1] + (nf,)
+    d = M3FfnDims(math.prod(shape[:-1]), nk, nf, _rows(x, "x", dt, shape, dev),
+                  _rows(w_gate, "w_gate", dt, (nf, nk), dev), _rows(w_up, "w_up", dt, (nf, nk), dev))
+    if h is not None:
+        d.ld_h = _rows(h, "h", dt, out, dev)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up go together")
+    if gate is not None:
+        d.ld_gate = _rows(gate, "gate", torch.float32, out, dev)
+        d.ld_up = _rows(up, "up", torch.float32, out, dev)
+    _gpu(dev)
+    if h is None:
+        h = x.new_empty(out)
+    if gate is None and want_pre:
+        gate, up = (x.new_empty(out, dtype=torch.float32) for _ in range(2))
+    _launch(dev, lib.m3_gated_ffn, ctypes.byref(d), code, _at(x), _at(w_gate), _at(w_up), _at(h),
+            _at(gate), _at(up))
+    return h, gate, up
+
+
+def gated_ffn_backward_workspace_size(rows, channels, hidden, dtype) -> int:
+    """Bytes of workspace gated_ffn_backward needs (0 for no rows)."""
+    d = M3FfnDims(int(rows), int(channels), int(hidden))
+    return int(load_library().m3_gated_ffn_backward_workspace_size(ctypes.byref(d), _type_code(dtype)))
+
+
+@_streamed
+def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, dx=None, dw_gate=None, dw_up=None,
+                       want_x: bool = True, want_weights: bool = True, workspace=None):
+    """Gradients of sum(h * dh) for gated_ffn's inputs (m3_gated_ffn_backward);
+    gate and up as gated_ffn kept them.  dx, dw_gate and dw_up may be given (the
+    last two together).  A workspace (gated_ffn_backward_workspace_size bytes, of
+    any content) may be kept for later calls; calls that overlap need distinct
+    ones.  Returns a dict: x (absent without want_x), w_gate and w_up (absent
+    without want_weights) in the inputs' type."""
+    import torch
+    lib = _lib or load_library()
+    shape, dev, dt = x.shape, x.get_device(), x.dtype
+    if len(shape) < 1 or w_gate.dim() != 2:
+        raise ValueError("expected x [..., K] and w_gate [F, K], got %s and %s"
+                         % (tuple(shape), tuple(w_gate.shape)))
+    code = _type_code(dt)
+    nk, nf = shape[-1], w_gate.shape[0]
+    rows, out = math.prod(shape[:-1]), shape[:-1] + (nf,)
+    if (dw_gate is None) != (dw_up is None):
+        raise ValueError("dw_gate and dw_up go together")
+    if (dx is not None and not want_x) or (dw_gate is not None and not want_weights):
+        raise ValueError("a gradient that is given is wanted")
+    d = M3FfnDims(rows, nk, nf, _rows(x, "x", dt, shape, dev),
+                  _rows(w_gate, "w_gate", dt, (nf, nk), dev), _rows(w_up, "w_up", dt, (nf, nk), dev),
+                  0, _rows(gate, "gate", torch.float32, out, dev), _rows(up, "up", torch.float32, out, dev),
+                  _rows(dh, "dh", dt, out, dev))
+    if dx is not None:
+        d.ld_dx = _rows(dx, "dx", dt, shape, dev)
+    if dw_gate is not None:
+        d.ld_dwgate = _rows(dw_gate, "dw_gate", dt, (nf, nk), dev)
+        d.ld_dwup = _rows(dw_up, "dw_up", dt, (nf, nk), dev)
+    _gpu(dev)
+    if dx is None and want_x:
+        dx = x.new_empty(shape)
+    if dw_gate is None and want_weights:
+        dw_gate, dw_up = x.new_empty((nf, nk)), x.new_empty((nf, nk))
+    need = int(lib.m3_gated_ffn_backward_workspace_size(ctypes.byref(d), code))
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the first tensor's device")
+    _launch(dev, lib.m3_gated_ffn_backward, ctypes.byref(d), code, _at(dh), _at(x), _at(w_gate),
+            _at(w_up), _at(gate), _at(up), _at(dx), _at(dw_gate), _at(dw_up), _at(workspace),
+            0 if workspace is None else workspace.nbytes)
+    res = {}
+    if dx is not None:
+        res["x"] = dx
+    if dw_gate is not None:
+        res["w_gate"], res["w_up"] = dw_gate, dw_up
+    return res

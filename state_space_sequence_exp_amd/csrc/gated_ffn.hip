@@ -1,0 +1,478 @@
+// gated_ffn.hip -- gated feed-forward projections, h = silu(x Wg^T) * (x Wu^T),
+// and their gradients
+//
+//   du = dh silu(g), dg = dh u silu'(g),  dx = dg Wg + du Wu,
+//   dWg = dg^T x, dWu = du^T x
+//
+// Three of the products run on one kernel: C[m][n] = sum_k A[m][k] B[n][k], both
+// operands with k contiguous.  Forward, the B rows of a wave are its hidden units'
+// rows of Wg, then of Wu, so that a lane ends with g and u of the same elements
+// and the activation costs no memory.  Backward, one pass over dh, g and u writes
+// [dg | du] and its transpose, and x and the weights are transposed beside them:
+// the gradients' operands then have k contiguous, aligned and padded with zeros.
+// (dg and du are rounded to the storage type, as the matrix units take it; g and u
+// are kept in float, or each gradient would carry their rounding as well: 0.0031
+// relative in bfloat16 instead of 0.0024, where rounding the result alone is 0.0017.)
+#include <type_traits>
+
+#include "gate.h"
+#include "layer_internal.h"
+#include "vec_io.h"
+
+namespace m3 {
+namespace {
+
+constexpr int kRowBytes = 128, kChunks = kRowBytes / 16;  // of k in a tile's row
+
+// ---- matrix products ---------------------------------------------------------
+
+template <typename T>
+struct GemmArgs {
+  int M, N, K;                 // N: hidden units (dual), columns of C otherwise
+  const T *A, *B, *B2;         // B2: the second weight matrix (dual)
+  int64_t lda, ldb, ldb2;
+  T* C;
+  float *gate, *up;            // dual: g and u, unless null
+  int64_t ldc, ld_gate, ld_up;
+  T* C2;                       // split: where A's rows from `split` on go; each half has `rows` rows
+  int64_t ldc2;
+  int split, rows;
+  int gridM, gridN;
+};
+enum Mode { kDual, kPlain, kSplit };
+
+// acc[n 4g..4g+3][m l%16] += sum over the chunks' k: a lane's 16 bytes of a row are
+// 8 bfloat16 or 4 float k, any order of k being the same for both operands.
+__device__ __forceinline__ f32x4 mma_chunk(u32x4 n, u32x4 m, f32x4 c, bf16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, n), __builtin_bit_cast(bf16x8, m), c,
+                                                 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma_chunk(u32x4 n, u32x4 m, f32x4 c, float) {
+  const f32x4 a = __builtin_bit_cast(f32x4, n), b = __builtin_bit_cast(f32x4, m);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 load_chunk(const T* p, int n) {
+  return __builtin_bit_cast(u32x4, load_run<T, 16 / (int)sizeof(T)>(p, n));
+}
+
+// A tile's row is 128 bytes of k, its 16-byte chunks permuted by the row so that
+// the rows read together lie on different banks.
+__device__ __forceinline__ int chunk_at(int row, int chunk) { return row * kChunks + (chunk ^ (row & 7)); }
+
+template <typename T, int WM, int WN, int FM, int FN, Mode kMode>
+__global__ void __launch_bounds__(WM * WN * kWave) gemm_kernel(GemmArgs<T> g) {
+  constexpr int NT = WM * WN * kWave, BM = WM * FM * 16, BN = WN * FN * 16, E = 16 / (int)sizeof(T);
+  constexpr int BK = kRowBytes / (int)sizeof(T), kPass = NT / kChunks;  // rows a pass loads
+  constexpr int NA = BM / kPass, NB = BN / kPass;
+  __shared__ u32x4 s_tile[2][(BM + BN) * kChunks];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, l4 = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN;
+
+  // Neighbouring tiles on one XCD; eight rows of tiles side by side, so that a
+  // chip's worth of tiles shares few rows of both operands.
+  const int groups = g.gridM * g.gridN, x = blockIdx.x & 7, q = groups >> 3, rest = groups & 7;
+  const int at = x * q + min(x, rest) + (int)(blockIdx.x >> 3);
+  const int band = at / (8 * g.gridN), inBand = at - band * 8 * g.gridN, high = min(8, g.gridM - band * 8);
+  const int m0 = (band * 8 + inBand % high) * BM;
+  const int n0 = inBand / high * (kMode == kDual ? BN / 2 : BN);
+
+  const int row = tid / kChunks, chunk = tid % kChunks;
+  const T* pa[NA];
+  const T* pb[NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+    pa[i] = g.A + (int64_t)min(m0 + i * kPass + row, g.M - 1) * g.lda + chunk * E;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int r = i * kPass + row;
+    if constexpr (kMode == kDual) {
+      const int w = r / (FN * 16), in = r % (FN * 16), col = n0 + w * FN * 8 + in % (FN * 8);
+      const bool second = in >= FN * 8;
+      pb[i] = (second ? g.B2 : g.B) + (int64_t)min(col, g.N - 1) * (second ? g.ldb2 : g.ldb) + chunk * E;
+    } else {
+      pb[i] = g.B + (int64_t)min(n0 + r, g.N - 1) * g.ldb + chunk * E;
+    }
+  }
+  u32x4 ra[NA], rb[NB];
+  const auto request = [&](int k0) {
+    if (k0 + BK <= g.K) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) __builtin_memcpy(&ra[i], pa[i] + k0, 16);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) __builtin_memcpy(&rb[i], pb[i] + k0, 16);
+    } else {
+      const int n = g.K - k0 - chunk * E;
+#pragma unroll
+      for (int i = 0; i < NA; ++i) ra[i] = load_chunk<T>(pa[i] + k0, n);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) rb[i] = load_chunk<T>(pb[i] + k0, n);
+    }
+  };
+  const auto put = [&](u32x4* s) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) s[chunk_at(i * kPass + row, chunk)] = ra[i];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) s[chunk_at(BM + i * kPass + row, chunk)] = rb[i];
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  request(0);
+  put(s_tile[0]);
+  __syncthreads();
+  int buf = 0;
+  for (int k0 = 0; k0 < g.K; k0 += BK, buf ^= 1) {
+    const bool more = k0 + BK < g.K;
+    if (more) request(k0 + BK);
+    const u32x4* s = s_tile[buf];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4 fa[FM], fb[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = s[chunk_at(BM + (wn * FN + j) * 16 + l16, kk * 4 + l4)];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[i] = s[chunk_at((wm * FM + i) * 16 + l16, kk * 4 + l4)];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mma_chunk(fb[j], fa[i], acc[i][j], T());
+    }
+    if (more) put(s_tile[buf ^ 1]);
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int m = m0 + (wm * FM + i) * 16 + l16;
+    if (m >= g.M) continue;
+    if constexpr (kMode == kDual) {
+#pragma unroll
+      for (int j = 0; j < FN / 2; ++j) {
+        const int n = n0 + (wn * (FN / 2) + j) * 16 + 4 * l4, left = g.N - n;
+        if (left <= 0) continue;
+        float gv[4], uv[4], hv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gv[e] = acc[i][j][e];
+          uv[e] = acc[i][j + FN / 2][e];
+          hv[e] = gv[e] * sigmoid_of(gv[e]) * uv[e];
+        }
+        store_run<T, 4>(g.C + (int64_t)m * g.ldc + n, left, to_run<T, 4>(hv));
+        if (g.gate) {
+          store_run<float, 4>(g.gate + (int64_t)m * g.ld_gate + n, left, to_run<float, 4>(gv));
+          store_run<float, 4>(g.up + (int64_t)m * g.ld_up + n, left, to_run<float, 4>(uv));
+        }
+      }
+    } else {
+      T* c = g.C + (int64_t)m * g.ldc;
+      if constexpr (kMode == kSplit) {
+        const bool second = m >= g.split;
+        const int r = second ? m - g.split : m;
+        if (r >= g.rows) continue;
+        if (second) c = g.C2 + (int64_t)r * g.ldc2;
+      }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int n = n0 + (wn * FN + j) * 16 + 4 * l4, left = g.N - n;
+        if (left <= 0) continue;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
+        store_run<T, 4>(c + n, left, to_run<T, 4>(v));
+      }
+    }
+  }
+}
+
+// The tile: the largest that still leaves about a tile a CU.
+template <typename T, int WM, int WN, int FM, int FN, Mode kMode>
+void launch_gemm_tile(GemmArgs<T> g, hipStream_t stream) {
+  constexpr int BM = WM * FM * 16, BN = WN * FN * 16 / (kMode == kDual ? 2 : 1);
+  g.gridM = (g.M + BM - 1) / BM;
+  g.gridN = (g.N + BN - 1) / BN;
+  hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode>), dim3((unsigned)g.gridM * g.gridN),
+                     dim3(WM * WN * kWave), 0, stream, g);
+}
+template <typename T, Mode kMode>
+void launch_gemm(const GemmArgs<T>& g, hipStream_t stream) {
+  const double cols = kMode == kDual ? 2.0 * g.N : g.N, area = (double)g.M * cols;
+  if (area >= 192.0 * 256 * 256) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, stream);
+  else if (area >= 192.0 * 128 * 128) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, stream);
+  else launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, stream);
+}
+
+// ---- few rows ------------------------------------------------------------------
+// Up to 16 FM rows (a decode batch): the weights are read once, straight into the
+// matrix units' layout.  A workgroup owns 16 hidden units; its eight waves share
+// out k and add their parts in the LDS, in order.
+constexpr int kFewWaves = 8;
+
+template <typename T, int FM>
+__global__ void __launch_bounds__(kFewWaves * kWave) few_kernel(GemmArgs<T> g) {
+  constexpr int E = 16 / (int)sizeof(T), KS = 4 * E;  // k of a step
+  __shared__ f32x4 s_part[kFewWaves][2 * FM][kWave];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, l4 = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const T* pg = g.B + (int64_t)min(n0 + l16, g.N - 1) * g.ldb;
+  const T* pu = g.B2 + (int64_t)min(n0 + l16, g.N - 1) * g.ldb2;
+  const T* px[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) px[i] = g.A + (int64_t)min(i * 16 + l16, g.M - 1) * g.lda;
+  const int steps = (g.K + KS - 1) / KS, each = (steps + kFewWaves - 1) / kFewWaves;
+  const int s0 = wave * each, s1 = min(s0 + each, steps);
+  f32x4 acc[FM][2];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const auto some = [&](auto count, int s) {
+    constexpr int U = decltype(count)::value;
+    u32x4 wg[U], wu[U], xv[U][FM];
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const int k = (s + v) * KS + l4 * E, n = g.K - k;
+      wg[v] = load_chunk<T>(pg + k, n);
+      wu[v] = load_chunk<T>(pu + k, n);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) xv[v][i] = load_chunk<T>(px[i] + k, n);
+    }
+#pragma unroll
+    for (int v = 0; v < U; ++v)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        acc[i][0] = mma_chunk(wg[v], xv[v][i], acc[i][0], T());
+        acc[i][1] = mma_chunk(wu[v], xv[v][i], acc[i][1], T());
+      }
+  };
+  int s = s0;
+  for (; s + 4 <= s1; s += 4) some(std::integral_constant<int, 4>{}, s);
+  for (; s < s1; ++s) some(std::integral_constant<int, 1>{}, s);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    s_part[wave][2 * i][lane] = acc[i][0];
+    s_part[wave][2 * i + 1][lane] = acc[i][1];
+  }
+  __syncthreads();
+  if (wave >= FM) return;
+  f32x4 gv = s_part[0][2 * wave][lane], uv = s_part[0][2 * wave + 1][lane];
+#pragma unroll
+  for (int w = 1; w < kFewWaves; ++w) {
+    gv += s_part[w][2 * wave][lane];
+    uv += s_part[w][2 * wave + 1][lane];
+  }
+  const int m = wave * 16 + l16, n = n0 + 4 * l4, left = g.N - n;
+  if (m >= g.M || left <= 0) return;
+  float gs[4], us[4], hs[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    gs[e] = gv[e];
+    us[e] = uv[e];
+    hs[e] = gs[e] * sigmoid_of(gs[e]) * us[e];
+  }
+  store_run<T, 4>(g.C + (int64_t)m * g.ldc + n, left, to_run<T, 4>(hs));
+  if (g.gate) {
+    store_run<float, 4>(g.gate + (int64_t)m * g.ld_gate + n, left, to_run<float, 4>(gs));
+    store_run<float, 4>(g.up + (int64_t)m * g.ld_up + n, left, to_run<float, 4>(us));
+  }
+}
+
+// ---- the backward pass's operands ------------------------------------------------
+
+constexpr int kSide = 64;  // of a transposed tile
+
+// Rows r0 .. of a tile that lies in the LDS transposed, [column][row], to dst
+// [columns, pitch]: 16 bytes a thread.
+template <typename T, int P>
+__device__ __forceinline__ void put_columns(const T (&s)[kSide][P], T* dst, int64_t pitch, int c0, int r0, int cols) {
+  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
+  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
+    const int c = i / kAcross, r = i % kAcross * E;
+    if (c0 + c >= cols) continue;
+    u32x4 v;
+    T tmp[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) tmp[e] = s[c][r + e];
+    __builtin_memcpy(&v, tmp, 16);
+    *reinterpret_cast<u32x4*>(dst + (int64_t)(c0 + c) * pitch + r0 + r) = v;
+  }
+}
+
+// [dg | du] (Fp columns each, zeros from F on) and its transpose (Mp columns, zeros
+// from M on); either may be null.
+template <typename T>
+__global__ void __launch_bounds__(256) slopes_kernel(FfnArgs a, T* both, T* turned, int Fp, int Mp) {
+  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E, P = kSide + 4 / (int)sizeof(T);
+  __shared__ T s_g[kSide][P], s_u[kSide][P];
+  const int across = Fp / kSide, f0 = blockIdx.x % across * kSide, m0 = blockIdx.x / across * kSide;
+  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
+    const int r = i / kAcross, c = i % kAcross * E, m = m0 + r, n = m < a.M ? a.F - f0 - c : 0;
+    const Raw<T, E> dh = load_run<T, E>(static_cast<const T*>(a.dh) + (int64_t)m * a.ld_dh + f0 + c, n);
+    const Raw<float, E> g = load_run<float, E>(a.gate + (int64_t)m * a.ld_gate + f0 + c, n);
+    const Raw<float, E> u = load_run<float, E>(a.up + (int64_t)m * a.ld_up + f0 + c, n);
+    float dg[E], du[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float gv = run_at(g, e), d = run_at(dh, e), sg = sigmoid_of(gv);
+      du[e] = d * (gv * sg);
+      dg[e] = d * run_at(u, e) * (sg * __builtin_fmaf(gv, 1.f - sg, 1.f));
+    }
+    const Raw<T, E> rg = to_run<T, E>(dg), ru = to_run<T, E>(du);
+    if (both && m < a.M) {
+      T* p = both + (int64_t)m * 2 * Fp + f0 + c;
+      __builtin_memcpy(p, rg.w, 16);
+      __builtin_memcpy(p + Fp, ru.w, 16);
+    }
+    if (turned) {
+      T tg[E], tu[E];
+      __builtin_memcpy(tg, rg.w, 16);
+      __builtin_memcpy(tu, ru.w, 16);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        s_g[c + e][r] = tg[e];
+        s_u[c + e][r] = tu[e];
+      }
+    }
+  }
+  if (!turned) return;
+  __syncthreads();
+  put_columns<T, P>(s_g, turned, Mp, f0, m0, Fp);
+  put_columns<T, P>(s_u, turned + (int64_t)Fp * Mp, Mp, f0, m0, Fp);
+}
+
+// dst [C, pitch] = src [R, C] transposed, zeros from R to the next multiple of 64.
+template <typename T>
+__global__ void __launch_bounds__(256) turn_kernel(const T* src, int64_t ld, int R, int C, T* dst, int64_t pitch) {
+  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E, P = kSide + 4 / (int)sizeof(T);
+  __shared__ T s[kSide][P];
+  const int across = (C + kSide - 1) / kSide, c0 = blockIdx.x % across * kSide, r0 = blockIdx.x / across * kSide;
+  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
+    const int r = i / kAcross, c = i % kAcross * E;
+    const Raw<T, E> v = load_run<T, E>(src + (int64_t)(r0 + r) * ld + c0 + c, r0 + r < R ? C - c0 - c : 0);
+    T t[E];
+    __builtin_memcpy(t, v.w, 16);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[c + e][r] = t[e];
+  }
+  __syncthreads();
+  put_columns<T, P>(s, dst, pitch, c0, r0, C);
+}
+
+int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
+size_t area_bytes(int64_t n, int es) { return ((size_t)n * es + 255) / 256 * 256; }
+
+template <typename T>
+void launch_turn(const void* src, int64_t ld, int R, int C, T* dst, int64_t pitch, hipStream_t stream) {
+  hipLaunchKernelGGL((turn_kernel<T>), dim3((unsigned)(padded(C) / kSide * (padded(R) / kSide))), dim3(256), 0,
+                     stream, static_cast<const T*>(src), ld, R, C, dst, pitch);
+}
+
+template <typename T>
+hipError_t launch_ffn_t(const FfnArgs& a, hipStream_t stream) {
+  GemmArgs<T> g = {};
+  g.M = a.M;
+  g.N = a.F;
+  g.K = a.K;
+  g.A = static_cast<const T*>(a.x);
+  g.B = static_cast<const T*>(a.wg);
+  g.B2 = static_cast<const T*>(a.wu);
+  g.lda = a.ld_x;
+  g.ldb = a.ld_wg;
+  g.ldb2 = a.ld_wu;
+  g.C = static_cast<T*>(a.h);
+  g.gate = a.gate;
+  g.up = a.up;
+  g.ldc = a.ld_h;
+  g.ld_gate = a.ld_gate;
+  g.ld_up = a.ld_up;
+  const dim3 few((unsigned)((a.F + 15) / 16));
+  if (a.M <= 16) hipLaunchKernelGGL((few_kernel<T, 1>), few, dim3(kFewWaves * kWave), 0, stream, g);
+  else if (a.M <= 32) hipLaunchKernelGGL((few_kernel<T, 2>), few, dim3(kFewWaves * kWave), 0, stream, g);
+  else launch_gemm<T, kDual>(g, stream);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
+  const int Fp = (int)padded(a.F), Mp = (int)padded(a.M), es = (int)sizeof(T);
+  char* ws = static_cast<char*>(a.workspace);
+  T* both = reinterpret_cast<T*>(ws);                 // [M, 2 Fp]
+  ws += area_bytes((int64_t)a.M * 2 * Fp, es);
+  T* turned = reinterpret_cast<T*>(ws);               // [2 Fp, Mp]
+  ws += area_bytes((int64_t)Mp * 2 * Fp, es);
+  T* xT = reinterpret_cast<T*>(ws);                   // [K, Mp]
+  ws += area_bytes((int64_t)a.K * Mp, es);
+  T* wT = reinterpret_cast<T*>(ws);                   // [K, 2 Fp]
+  hipLaunchKernelGGL((slopes_kernel<T>), dim3((unsigned)(Fp / kSide * (Mp / kSide))), dim3(256), 0, stream, a,
+                     a.dx ? both : nullptr, a.dwg ? turned : nullptr, Fp, Mp);
+  if (a.dx) {
+    launch_turn<T>(a.wg, a.ld_wg, a.F, a.K, wT, 2 * Fp, stream);
+    launch_turn<T>(a.wu, a.ld_wu, a.F, a.K, wT + Fp, 2 * Fp, stream);
+    GemmArgs<T> g = {};
+    g.M = a.M;
+    g.N = a.K;
+    g.K = 2 * Fp;
+    g.A = both;
+    g.B = wT;
+    g.lda = g.ldb = 2 * Fp;
+    g.C = static_cast<T*>(a.dx);
+    g.ldc = a.ld_dx;
+    launch_gemm<T, kPlain>(g, stream);
+  }
+  if (a.dwg) {
+    launch_turn<T>(a.x, a.ld_x, a.M, a.K, xT, Mp, stream);
+    GemmArgs<T> g = {};
+    g.M = 2 * Fp;
+    g.N = a.K;
+    g.K = Mp;
+    g.A = turned;
+    g.B = xT;
+    g.lda = g.ldb = Mp;
+    g.C = static_cast<T*>(a.dwg);
+    g.ldc = a.ld_dwg;
+    g.C2 = static_cast<T*>(a.dwu);
+    g.ldc2 = a.ld_dwu;
+    g.split = Fp;
+    g.rows = a.F;
+    launch_gemm<T, kSplit>(g, stream);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) zero_rows_kernel(T* p, int64_t ld, int R, int C) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < (int64_t)R * C) p[i / C * ld + i % C] = from_f32<T>(0.f);
+}
+template <typename T>
+hipError_t launch_ffn_no_rows_t(const FfnArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)a.F * a.K + 255) / 256));
+  hipLaunchKernelGGL((zero_rows_kernel<T>), grid, dim3(256), 0, stream, static_cast<T*>(a.dwg), a.ld_dwg, a.F, a.K);
+  hipLaunchKernelGGL((zero_rows_kernel<T>), grid, dim3(256), 0, stream, static_cast<T*>(a.dwu), a.ld_dwu, a.F, a.K);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize) {
+  if (M == 0) return 0;
+  const int64_t Fp = padded(F), Mp = padded(M);
+  return area_bytes(M * 2 * Fp, esize) + area_bytes(Mp * 2 * Fp, esize) + area_bytes(K * Mp, esize) +
+         area_bytes(K * 2 * Fp, esize);
+}
+
+hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {
+  return dtype == M3_BF16 ? launch_ffn_t<bf16>(a, stream) : launch_ffn_t<float>(a, stream);
+}
+hipError_t launch_ffn_backward(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {
+  if (a.M == 0)
+    return dtype == M3_BF16 ? launch_ffn_no_rows_t<bf16>(a, stream) : launch_ffn_no_rows_t<float>(a, stream);
+  return dtype == M3_BF16 ? launch_ffn_backward_t<bf16>(a, stream) : launch_ffn_backward_t<float>(a, stream);
+}
+
+}  // namespace m3

@@ -1,6 +1,7 @@
 // layer_internal.h -- host-side interface between the C ABI of the layer
-// operators (layer_api.hip: gated recurrence, layer norm, 8-bit state cache)
-// and their kernel launchers.  Not installed; not part of the ABI.
+// operators (layer_api.hip: gated recurrence, layer norm, 8-bit state cache;
+// selective_api.hip: short convolution, selective scan, gated feed-forward) and
+// their kernel launchers.  Not installed; not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -89,5 +90,62 @@ hipError_t launch_state_store(const CacheArgs& a, m3_code code, hipStream_t stre
 hipError_t launch_state_load(const CacheArgs& a, m3_code code, m3_dtype dtype, hipStream_t stream);
 hipError_t launch_decode_cached(const CacheArgs& a, m3_code code, m3_dtype dtype,
                                 hipStream_t stream);
+
+// One convolution call (ld in elements, never 0).
+struct ConvArgs {
+  int64_t B, T, D, ld_x, ld_y;
+  int W;
+  bool silu;
+  const void* x;
+  const float *weight, *bias;  // bias may be null
+  const void* state_in;        // may be null (zeros)
+  const int32_t* lengths;      // may be null (all T)
+  void* y;
+  void* state_out;             // may be null; the step: the pool
+  const int32_t* slots;        // the step: may be null (identity)
+  int n_slots;
+};
+// Workgroups of a call.
+double conv_groups(int64_t B, int64_t T, int64_t D, int esize);
+double conv_step_groups(int64_t B, int64_t D, int esize);
+hipError_t launch_conv(const ConvArgs& a, m3_dtype dtype, hipStream_t stream);
+hipError_t launch_conv_step(const ConvArgs& a, m3_dtype dtype, hipStream_t stream);
+
+struct SelectArgs {
+  int64_t B, T, D;
+  int N;
+  int64_t ld_x, ld_dt, ld_z, ld_y, ld_b, ld_c;
+  bool softplus;
+  const void *x, *dt, *z, *Bt, *Ct;        // z may be null
+  const float *A, *skip, *dt_bias, *h0;    // all but A may be null
+  const int32_t* lengths;                  // may be null (all T)
+  void* y;
+  float* h_last;                           // may be null; the step: the pool
+  const int32_t* slots;                    // the step: may be null (identity)
+  int n_slots;
+  void* workspace;
+};
+// Segments that a scan's tokens are cut into (1: not cut), the workspace that
+// takes, and the workgroups of a launch.
+int select_segments(int64_t B, int64_t T, int64_t D, int N);
+size_t select_workspace(int64_t B, int64_t T, int64_t D, int N);
+double select_groups(int64_t B, int64_t T, int64_t D, int N);
+double select_step_groups(int64_t B, int64_t D, int N);
+hipError_t launch_select(const SelectArgs& a, m3_dtype dtype, hipStream_t stream);
+hipError_t launch_select_step(const SelectArgs& a, m3_dtype dtype, hipStream_t stream);
+
+struct FfnArgs {
+  int M, K, F;
+  int64_t ld_x, ld_wg, ld_wu, ld_h, ld_gate, ld_up, ld_dh, ld_dx, ld_dwg, ld_dwu;
+  const void *x, *wg, *wu;
+  void* h;
+  float *gate, *up;            // forward out (may be null), backward in
+  const void* dh;
+  void *dx, *dwg, *dwu;        // may be null
+  void* workspace;
+};
+size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize);
+hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream);
+hipError_t launch_ffn_backward(const FfnArgs& a, m3_dtype dtype, hipStream_t stream);
 
 }  // namespace m3

@@ -1,0 +1,388 @@
+// selective_scan.hip -- the selective state space scan: N states a channel, each
+// with a decay of its own,
+//
+//   s = softplus(dt + dt_bias),  h[n] = exp(s A[n]) h[n] + (s x) B[n]
+//   y = (sum_n C[n] h[n] + skip x) * silu(z)
+//
+// over whole sequences and for one token.
+//
+// A prompt is bound by vector operations: a state and token takes a product, an
+// exponential, a product and two fused sums.  A lane owns the states n, n + 16,
+// ... of one channel, so that the 16 lanes of a DPP row own a channel and a wave
+// four of them: with a state a lane a layer of 4096 channels and 16 states is
+// 1024 waves, one a SIMD, without cutting the sequence.  Steps s and s x lie one
+// token a lane and reach the row as DPP operands, which cost nothing; the sums
+// over n of 16 tokens are taken together, halving the tokens a lane keeps at each
+// of four exchanges, so that lane i ends with token i's.
+//
+// A workgroup of four waves takes 16 channels through tiles of 64 tokens.  Its
+// threads load the tile as it lies in memory, four channels of a token each,
+// compute the steps once and turn them in the LDS; the next tile's loads are in
+// flight meanwhile.  Neighbouring workgroups, which share cache lines, run on one
+// XCD.
+//
+// With few channels (see select_segments) the tokens are cut into segments: a
+// first launch takes each from a zero state to its end state and sum of steps
+// (the decay of a whole segment is exp(A sum s)), the second joins those before
+// its segment and scans on from there.
+#include <type_traits>
+
+#include "gate.h"
+#include "layer_internal.h"
+#include "slots.h"
+#include "vec_io.h"
+
+namespace m3 {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int kTile = 64;               // tokens
+constexpr int kRow = 16;                // lanes of a DPP row: a channel's
+constexpr int kChan = kWaves * kWave / kRow;  // channels of a workgroup
+constexpr int kPitch = kTile + 4;       // of the LDS's token rows
+
+// log(1 + exp(v)): with e = exp(-|v|), max(v, 0) + log1p(e), and log1p(e) = log(w)
+// + (e - (w - 1)) / w for w the rounded 1 + e, which keeps a small e's digits.
+__device__ __forceinline__ float softplus_of(float v) {
+  const float e = exp_neg(__builtin_fabsf(v)), w = 1.f + e;
+  const float low = (e - (w - 1.f)) * __builtin_amdgcn_rcpf(w);
+  return fmaxf(v, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(w), 0.693147180559945309f, low);
+}
+
+// Lane i of every row of 16 lanes, in all of its lanes.
+template <int i>
+__device__ __forceinline__ float row_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + i, 0xf, 0xf, true));
+}
+template <int kCtrl>
+__device__ __forceinline__ float swap_lanes(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+}
+// Halves the tokens: `up` lanes keep the upper half and take the other lanes' part of it.
+template <int kCtrl, int n>
+__device__ __forceinline__ void halve(float (&p)[kRow], bool up) {
+#pragma unroll
+  for (int q = 0; q < n; ++q) {
+    const float keep = up ? p[q + n] : p[q], give = up ? p[q] : p[q + n];
+    p[q] = keep + swap_lanes<kCtrl>(give);
+  }
+}
+// Lane i of a row: the sum of p[i] over its 16 lanes.
+__device__ __forceinline__ float row_sums(float (&p)[kRow], int i) {
+  halve<0x128, 8>(p, i & 8);  // row_ror:8
+  halve<0x141, 4>(p, i & 4);  // row_half_mirror: lane i xor 7
+  halve<0x4e, 2>(p, i & 2);   // quad_perm: lane i xor 2
+  halve<0xb1, 1>(p, i & 1);   // lane i xor 1
+  return p[0];
+}
+
+// The w-th workgroup's place when each of the 8 XCDs takes a run of neighbours.
+__device__ __forceinline__ int xcd_place(int w, int groups) {
+  const int x = w & 7, q = groups >> 3, rest = groups & 7;
+  return x * q + min(x, rest) + (w >> 3);
+}
+
+// What one thread brings of a tile: four channels of one token, and its share of
+// that token's B and C.
+template <typename T, int NL, bool kLocal>
+struct Piece {
+  Raw<T, 4> x, dt, z, b[NL], c[NL];
+};
+
+template <typename T, int NL, bool kLocal>
+__global__ void __launch_bounds__(kThreads)
+select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, float* sums) {
+  constexpr int kN = kRow * NL;  // states held, the last of them zeros where N is less
+  __shared__ float s_dt[kChan][kPitch], s_dx[kChan][kPitch];
+  __shared__ float s_b[kN][kPitch], s_c[kLocal ? 1 : kN][kPitch];
+  __shared__ float s_y[kLocal ? 1 : kTile][kChan + 4];
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & (kRow - 1);
+  const int groups = (int)gridDim.x, place = xcd_place((int)blockIdx.x, groups);
+  const int launched = kLocal ? segs - 1 : segs;     // nothing follows the last segment's end
+  const int tile0 = place % tiles, seg = place / tiles % launched;
+  const int64_t bq = place / tiles / launched;
+  const int64_t d0 = (int64_t)tile0 * kChan;
+  const int N = a.N;
+  const int64_t len = a.lengths ? min(max((int64_t)a.lengths[bq], (int64_t)0), a.T) : a.T;
+  const int64_t t0 = seg * segLen, t1 = min(t0 + segLen, a.T);
+
+  // the states of this lane
+  const int ch = (tid >> 6) * (kWave / kRow) + (lane >> 4);
+  const int64_t d = d0 + ch;
+  float A2[NL], h[NL];
+#pragma unroll
+  for (int k = 0; k < NL; ++k) {
+    const int n = i + kRow * k;
+    const bool in = d < a.D && n < N;
+    A2[k] = in ? a.A[d * N + n] * kLog2e : 0.f;
+    h[k] = 0.f;
+    if constexpr (!kLocal) {
+      if (in) {
+        if (a.h0) h[k] = a.h0[(bq * a.D + d) * N + n];
+        for (int s = 0; s < seg; ++s) {
+          const int64_t at = (bq * (segs - 1) + s) * a.D + d;
+          h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[k] * sums[at]), h[k], ends[at * N + n]);
+        }
+      }
+    }
+  }
+  float total = 0.f;  // of the steps of this lane's tokens
+
+  // what this thread brings
+  const int tk = tid >> 2, part = tid & 3, c0 = part * 4;
+  const int nc = (int)max((int64_t)0, min((int64_t)4, a.D - d0 - c0));
+  float bias[4], skip[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    bias[e] = a.dt_bias && e < nc ? a.dt_bias[d0 + c0 + e] : 0.f;
+    skip[e] = a.skip && e < nc ? a.skip[d0 + c0 + e] : 0.f;
+  }
+  const auto request = [&](int64_t t) {
+    Piece<T, NL, kLocal> p = {};
+    if (t + tk < min(t1, len)) {
+      const int64_t row = bq * a.T + t + tk;
+      p.x = load_run<T, 4>(static_cast<const T*>(a.x) + row * a.ld_x + d0 + c0, nc);
+      p.dt = load_run<T, 4>(static_cast<const T*>(a.dt) + row * a.ld_dt + d0 + c0, nc);
+      if constexpr (!kLocal)
+        if (a.z) p.z = load_run<T, 4>(static_cast<const T*>(a.z) + row * a.ld_z + d0 + c0, nc);
+#pragma unroll
+      for (int q = 0; q < NL; ++q) {
+        const int n = (part * NL + q) * 4;
+        p.b[q] = load_run<T, 4>(static_cast<const T*>(a.Bt) + row * a.ld_b + n, N - n);
+        if constexpr (!kLocal)
+          p.c[q] = load_run<T, 4>(static_cast<const T*>(a.Ct) + row * a.ld_c + n, N - n);
+      }
+    }
+    return p;
+  };
+
+  Piece<T, NL, kLocal> next = request(t0);
+  for (int64_t t = t0; t < t1; t += kTile) {
+    const bool live = t + tk < min(t1, len);
+    const Raw<T, 4> x = next.x, z = next.z;
+    if (t >= len) {  // padding from here on
+      if constexpr (kLocal) break;
+      if (t + tk < t1)
+        store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t + tk) * a.ld_y + d0 + c0, nc, no_run<T, 4>());
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = run_at(next.dt, e) + bias[e];
+      const float step = live ? (a.softplus ? softplus_of(v) : v) : 0.f;
+      s_dt[c0 + e][tk] = step;
+      s_dx[c0 + e][tk] = step * run_at(x, e);
+    }
+#pragma unroll
+    for (int q = 0; q < NL; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s_b[(part * NL + q) * 4 + e][tk] = run_at(next.b[q], e);
+        if constexpr (!kLocal) s_c[(part * NL + q) * 4 + e][tk] = run_at(next.c[q], e);
+      }
+    __syncthreads();
+    next = request(t + kTile);
+    for (int j = 0; j < kTile; j += kRow) {
+      const float vdt = s_dt[ch][j + i], vdx = s_dx[ch][j + i];
+      float p[kRow];
+      if constexpr (kLocal) total += vdt;
+      const auto four = [&](auto first) {  // tokens first .. first + 3 of the 16
+        constexpr int f = decltype(first)::value;
+        float4 b4[NL], c4[NL];
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+          b4[k] = *reinterpret_cast<const float4*>(&s_b[i + kRow * k][j + f]);
+          if constexpr (!kLocal) c4[k] = *reinterpret_cast<const float4*>(&s_c[i + kRow * k][j + f]);
+        }
+        const auto one = [&](auto tok) {
+          constexpr int q = decltype(tok)::value;
+#pragma unroll
+          for (int k = 0; k < NL; ++k) {
+            const float decay = __builtin_amdgcn_exp2f(row_lane<f + q>(vdt) * A2[k]);
+            h[k] = __builtin_fmaf(decay, h[k], row_lane<f + q>(vdx) * (&b4[k].x)[q]);
+            if constexpr (!kLocal)
+              p[f + q] = k ? __builtin_fmaf((&c4[k].x)[q], h[k], p[f + q]) : (&c4[k].x)[q] * h[k];
+          }
+        };
+        one(std::integral_constant<int, 0>{});
+        one(std::integral_constant<int, 1>{});
+        one(std::integral_constant<int, 2>{});
+        one(std::integral_constant<int, 3>{});
+      };
+      four(std::integral_constant<int, 0>{});
+      four(std::integral_constant<int, 4>{});
+      four(std::integral_constant<int, 8>{});
+      four(std::integral_constant<int, 12>{});
+      if constexpr (!kLocal) s_y[j + i][ch] = row_sums(p, i);
+    }
+    __syncthreads();
+    if constexpr (!kLocal) {
+      if (t + tk < t1) {
+        const float4 sum = *reinterpret_cast<const float4*>(&s_y[tk][c0]);
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = __builtin_fmaf(skip[e], run_at(x, e), (&sum.x)[e]);
+          if (a.z) {
+            const float g = run_at(z, e);
+            y[e] = y[e] * (g * sigmoid_of(g));
+          }
+          y[e] = live ? y[e] : 0.f;
+        }
+        store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t + tk) * a.ld_y + d0 + c0, nc, to_run<T, 4>(y));
+      }
+    }
+  }
+
+  if constexpr (kLocal) {
+    total += swap_lanes<0xb1>(total);
+    total += swap_lanes<0x4e>(total);
+    total += swap_lanes<0x141>(total);
+    total += swap_lanes<0x140>(total);
+    const int64_t at = (bq * (segs - 1) + seg) * a.D + d;
+    if (d < a.D && i == 0) sums[at] = total;
+#pragma unroll
+    for (int k = 0; k < NL; ++k)
+      if (d < a.D && i + kRow * k < N) ends[at * N + i + kRow * k] = h[k];
+  } else if (a.h_last && seg == segs - 1) {
+#pragma unroll
+    for (int k = 0; k < NL; ++k)
+      if (d < a.D && i + kRow * k < N) a.h_last[(bq * a.D + d) * N + i + kRow * k] = h[k];
+  }
+}
+
+// One token: a lane owns four neighbouring states, LQ lanes a channel; bound by
+// the state's 8 bytes.  A thread takes kSteps channels, all requested before the
+// rows before its own are searched for its slot.
+constexpr int kSteps = 4;
+
+template <typename T, int LQ>
+__global__ void __launch_bounds__(kThreads) select_step_kernel(SelectArgs a, int tiles) {
+  constexpr int kAcross = kThreads / LQ;  // channels side by side
+  const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+  const int slot = slot_of(a.slots, a.n_slots, b);
+  if (slot < 0) return;
+  const int q = threadIdx.x % LQ, n0 = 4 * q, N = a.N;
+  const int64_t first = (int64_t)tile * kAcross * kSteps + threadIdx.x / LQ;
+  const Raw<T, 4> Bv = load_run<T, 4>(static_cast<const T*>(a.Bt) + b * a.ld_b + n0, N - n0);
+  const Raw<T, 4> Cv = load_run<T, 4>(static_cast<const T*>(a.Ct) + b * a.ld_c + n0, N - n0);
+  Raw<float, 4> hv[kSteps], Av[kSteps];
+  float x[kSteps], dt[kSteps], z[kSteps], skip[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t d = first + s * kAcross;
+    const bool in = d < a.D;
+    hv[s] = load_run<float, 4>(a.h_last + ((int64_t)slot * a.D + d) * N + n0, in ? N - n0 : 0);
+    Av[s] = load_run<float, 4>(a.A + d * N + n0, in ? N - n0 : 0);
+    x[s] = in ? to_f32(static_cast<const T*>(a.x)[b * a.ld_x + d]) : 0.f;
+    dt[s] = in ? to_f32(static_cast<const T*>(a.dt)[b * a.ld_dt + d]) : 0.f;
+    if (a.dt_bias && in) dt[s] += a.dt_bias[d];
+    z[s] = in && a.z ? to_f32(static_cast<const T*>(a.z)[b * a.ld_z + d]) : 0.f;
+    skip[s] = in && a.skip ? a.skip[d] : 0.f;
+  }
+  if (__syncthreads_or(named_before<kThreads>(a.slots, b, slot))) return;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t d = first + s * kAcross;
+    const float step = a.softplus ? softplus_of(dt[s]) : dt[s], dx = step * x[s];
+    float h[4], y = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float decay = __builtin_amdgcn_exp2f(step * (run_at(Av[s], e) * kLog2e));
+      h[e] = __builtin_fmaf(decay, run_at(hv[s], e), dx * run_at(Bv, e));
+      y = __builtin_fmaf(run_at(Cv, e), h[e], y);
+    }
+    if constexpr (LQ > 1) y += swap_lanes<0xb1>(y);
+    if constexpr (LQ > 2) y += swap_lanes<0x4e>(y);
+    if constexpr (LQ > 4) y += swap_lanes<0x141>(y);
+    if constexpr (LQ > 8) y += swap_lanes<0x140>(y);
+    if (d >= a.D) continue;
+    store_run<float, 4>(a.h_last + ((int64_t)slot * a.D + d) * N + n0, N - n0, to_run<float, 4>(h));
+    y = __builtin_fmaf(skip[s], x[s], y);
+    if (a.z) y = y * (z[s] * sigmoid_of(z[s]));
+    if (q == 0) static_cast<T*>(a.y)[b * a.ld_y + d] = from_f32<T>(y);
+  }
+}
+
+int64_t channel_tiles(int64_t D) { return (D + kChan - 1) / kChan; }
+int64_t segment_tokens(int64_t T, int segs) {
+  const int64_t n = (T + segs - 1) / segs;
+  return (n + kTile - 1) / kTile * kTile;
+}
+int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+template <typename T, int NL>
+void launch_select_n(const SelectArgs& a, hipStream_t stream) {
+  const int tiles = (int)channel_tiles(a.D), segs = select_segments(a.B, a.T, a.D, a.N);
+  const int64_t len = segment_tokens(a.T, segs);
+  float* ends = static_cast<float*>(a.workspace);
+  float* sums = ends + a.B * (segs - 1) * a.D * a.N;
+  const unsigned units = (unsigned)(a.B * tiles);
+  if (segs > 1)
+    hipLaunchKernelGGL((select_kernel<T, NL, true>), dim3(units * (segs - 1)), dim3(kThreads), 0, stream, a,
+                       tiles, segs, len, ends, sums);
+  hipLaunchKernelGGL((select_kernel<T, NL, false>), dim3(units * segs), dim3(kThreads), 0, stream, a, tiles,
+                     segs, len, ends, sums);
+}
+template <typename T>
+hipError_t launch_select_t(const SelectArgs& a, hipStream_t stream) {
+  if (a.N <= kRow) launch_select_n<T, 1>(a, stream);
+  else if (a.N <= 2 * kRow) launch_select_n<T, 2>(a, stream);
+  else launch_select_n<T, 4>(a, stream);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_select_step_t(const SelectArgs& a, hipStream_t stream) {
+  const int lq = lanes_of(a.N), each = kThreads / lq * kSteps;
+  const int tiles = (int)((a.D + each - 1) / each);
+  const dim3 grid((unsigned)select_step_groups(a.B, a.D, a.N));
+#define M3_STEP_LAUNCH(LQ) \
+  hipLaunchKernelGGL((select_step_kernel<T, LQ>), grid, dim3(kThreads), 0, stream, a, tiles)
+  switch (lq) {
+    case 1: M3_STEP_LAUNCH(1); break;
+    case 2: M3_STEP_LAUNCH(2); break;
+    case 4: M3_STEP_LAUNCH(4); break;
+    case 8: M3_STEP_LAUNCH(8); break;
+    default: M3_STEP_LAUNCH(16);
+  }
+#undef M3_STEP_LAUNCH
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// A wave holds four channels; with fewer than 512 of them on the 1024 SIMDs the
+// tokens are cut so that there are about 2048, into segments of four tiles at
+// least.  Cutting does two thirds of the work twice.
+int select_segments(int64_t B, int64_t T, int64_t D, int N) {
+  const int64_t waves = B * channel_tiles(D) * kWaves;
+  if (waves < 1 || waves >= 512) return 1;
+  int64_t segs = 2048 / waves;
+  if (segs > T / (4 * kTile)) segs = T / (4 * kTile);
+  if (segs < 3) return 1;
+  const int64_t len = segment_tokens(T, (int)segs);
+  return (int)((T + len - 1) / len);
+}
+
+size_t select_workspace(int64_t B, int64_t T, int64_t D, int N) {
+  const int segs = select_segments(B, T, D, N);
+  return (size_t)B * (segs - 1) * D * (N + 1) * sizeof(float);
+}
+
+double select_groups(int64_t B, int64_t T, int64_t D, int N) {
+  return (double)B * (double)channel_tiles(D) * select_segments(B, T, D, N);
+}
+double select_step_groups(int64_t B, int64_t D, int N) {
+  const int each = kThreads / lanes_of(N) * kSteps;
+  return (double)B * (double)((D + each - 1) / each);
+}
+
+hipError_t launch_select(const SelectArgs& a, m3_dtype dtype, hipStream_t stream) {
+  return dtype == M3_BF16 ? launch_select_t<bf16>(a, stream) : launch_select_t<float>(a, stream);
+}
+hipError_t launch_select_step(const SelectArgs& a, m3_dtype dtype, hipStream_t stream) {
+  return dtype == M3_BF16 ? launch_select_step_t<bf16>(a, stream) : launch_select_step_t<float>(a, stream);
+}
+
+}  // namespace m3

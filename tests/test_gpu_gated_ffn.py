@@ -1,0 +1,179 @@
+"""GPU tests of the gated feed-forward projections and their gradients against
+the fp64 oracle's bounds: one row to several tiles, odd widths, strided rows,
+each gradient alone, streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import from_gpu
+from layer_util import HALF_STEP, close, stored
+from oracle import selective as O
+from test_gpu_selective import sliced
+
+pytestmark = pytest.mark.gpu
+TYPES = ["f32", "bf16"]
+
+
+def inputs(seed, M, K, F, dtype):
+    rng = np.random.default_rng(seed)
+    v = dict(x=stored(rng, (M, K), dtype), wg=stored(rng, (F, K), dtype, 0.0, K ** -0.5),
+             wu=stored(rng, (F, K), dtype, 0.0, K ** -0.5), dh=stored(rng, (M, F), dtype))
+    return {k: a[0] for k, a in v.items()}, {k: a[1] for k, a in v.items()}
+
+
+def check(r, t, dtype, back=True):
+    import state_space_sequence_exp_amd as m3
+    h, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True)
+    o = O.gated_ffn(r["x"], r["wg"], r["wu"])
+    close(h, o["h"], o["e_h"], dtype, "h")
+    close(g, o["g"], o["e_g"], "f32", "gate")
+    close(u, o["u"], o["e_u"], "f32", "up")
+    alone, none, _ = m3.gated_ffn(t["x"], t["wg"], t["wu"])
+    assert none is None and torch.equal(alone, h)
+    if not back:
+        return
+    d = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u)
+    w = O.gated_ffn_backward(r["dh"], r["x"], r["wg"], r["wu"], HALF_STEP[dtype] if dtype == "bf16" else 0.0)
+    for k, q in (("x", "dx"), ("w_gate", "dw_gate"), ("w_up", "dw_up")):
+        close(d[k], w[q], w["e_" + q], dtype, q)
+    return h, g, u, d
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F", [(1, 1, 1), (1, 64, 16), (2, 7, 33), (16, 100, 50), (17, 512, 40), (32, 31, 300),
+                                   (33, 64, 64), (65, 130, 257), (128, 96, 128), (300, 520, 200), (7, 2050, 70)])
+def test_ffn(dtype, M, K, F):
+    r, t = inputs([M, K, F], M, K, F, dtype)
+    check(r, t, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F", [(1000, 264, 1100), (2050, 192, 1800), (2305, 129, 2817)])
+def test_ffn_larger_tiles(dtype, M, K, F):
+    """Sizes that take the larger tiles, with rests in every direction."""
+    r, t = inputs([M, K, F], M, K, F, dtype)
+    check(r, t, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [5, 90])
+def test_ffn_strided(dtype, M):
+    """Slices of wider rows, at odd elements, give the same bits; what lies beside
+    the outputs' rows is left as it was."""
+    import state_space_sequence_exp_amd as m3
+    r, t = inputs([3, M], M, 72, 136, dtype)
+    h, g, u, d = check(r, t, dtype)
+    s = {k: sliced(v) for k, v in t.items()}
+    outs = [sliced(torch.zeros_like(v)) for v in (h, g, u, d["x"], d["w_gate"], d["w_up"])]
+    m3.gated_ffn(s["x"], s["wg"], s["wu"], h=outs[0], gate=outs[1], up=outs[2])
+    m3.gated_ffn_backward(s["dh"], s["x"], s["wg"], s["wu"], outs[1], outs[2], dx=outs[3], dw_gate=outs[4],
+                          dw_up=outs[5])
+    for o, want in zip(outs, (h, g, u, d["x"], d["w_gate"], d["w_up"])):
+        assert torch.equal(o, want)
+        assert torch.isnan(o._base[..., :3]).all() and torch.isnan(o._base[..., -2:]).all()
+
+
+def test_ffn_leading_axes_and_parts():
+    import state_space_sequence_exp_amd as m3
+    _, t = inputs(4, 30, 40, 48, "bf16")
+    h, g, u = m3.gated_ffn(t["x"].view(2, 3, 5, 40), t["wg"], t["wu"], want_pre=True)
+    assert h.shape == g.shape == (2, 3, 5, 48) and g.dtype == torch.float32
+    args = (t["dh"].view(2, 3, 5, 48), t["x"].view(2, 3, 5, 40), t["wg"], t["wu"], g, u)
+    d = m3.gated_ffn_backward(*args)
+    only_x, only_w = m3.gated_ffn_backward(*args, want_weights=False), m3.gated_ffn_backward(*args, want_x=False)
+    assert set(only_x) == {"x"} and torch.equal(only_x["x"], d["x"]) and d["x"].shape == (2, 3, 5, 40)
+    assert set(only_w) == {"w_gate", "w_up"} and all(torch.equal(only_w[k], d[k]) for k in only_w)
+    assert m3.gated_ffn_backward(*args, want_x=False, want_weights=False) == {}
+    need = m3.gated_ffn_backward_workspace_size(30, 40, 48, torch.bfloat16)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")      # NaN
+    again = m3.gated_ffn_backward(*args, workspace=ws)
+    assert all(torch.equal(again[k], d[k]) for k in d) and (ws[need:] == 255).all()
+
+
+def test_ffn_no_rows():
+    import state_space_sequence_exp_amd as m3
+    _, t = inputs(5, 4, 24, 32, "f32")
+    x, dh = t["x"][:0], t["dh"][:0]
+    h, g, u = m3.gated_ffn(x, t["wg"], t["wu"], want_pre=True)
+    assert h.shape == (0, 32)
+    d = m3.gated_ffn_backward(dh, x, t["wg"], t["wu"], g, u)
+    assert d["x"].shape == (0, 24) and not d["w_gate"].any() and not d["w_up"].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [3, 100])
+def test_ffn_extremes(dtype, M):
+    """A NaN or an infinity stays in the rows and units that it belongs to; gates far
+    below zero give zeros, far above the product."""
+    import state_space_sequence_exp_amd as m3
+    _, t = inputs([6, M], M, 70, 90, dtype)
+    h, _, _ = m3.gated_ffn(t["x"], t["wg"], t["wu"])
+    t["x"][1, 69], t["wu"][80, 3] = float("nan"), float("inf")
+    h2, _, _ = m3.gated_ffn(t["x"], t["wg"], t["wu"])
+    assert h2[1].isnan().all() and not h2[[0, 2], 80].isfinite().any()
+    keep = [i for i in range(M) if i != 1]
+    cols = [i for i in range(90) if i != 80]
+    assert torch.equal(h2[keep][:, cols], h[keep][:, cols])
+    one = torch.ones(M, 8, dtype=t["x"].dtype, device="cuda")
+    w = torch.full((4, 8), 1.0, dtype=one.dtype, device="cuda")
+    w[1], w[2], w[3] = -200.0, 200.0, 0.0
+    h3, g, u = m3.gated_ffn(one, w, torch.ones_like(w), want_pre=True)
+    assert (h3[:, 1] == 0).all() and (h3[:, 2] == 12800).all() and (h3[:, 3] == 0).all()
+    d = m3.gated_ffn_backward(torch.ones_like(h3), one, w, torch.ones_like(w), g, u)
+    assert all(v.isfinite().all() for v in d.values())
+    assert (d["w_gate"][1] == 0).all() and (d["w_gate"][2] == 8 * M).all() and (d["w_gate"][3] == 4 * M).all()
+
+
+def test_ffn_gradients_by_differences():
+    """The gradients against central differences of the forward pass itself, float32:
+    steps of 1/64 make the difference's own error of third order, below 1e-3."""
+    import state_space_sequence_exp_amd as m3
+    _, t = inputs(7, 12, 24, 20, "f32")
+    h, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True)
+    d = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u)
+    loss = lambda **k: float((m3.gated_ffn(*({**t, **k}[q] for q in ("x", "wg", "wu")))[0].double()
+                              * t["dh"].double()).sum())
+    rng = np.random.default_rng(1)
+    for k, key in (("x", "x"), ("wg", "w_gate"), ("wu", "w_up")):
+        for _ in range(5):
+            at = tuple(int(rng.integers(0, n)) for n in t[k].shape)
+            hi, lo = t[k].clone(), t[k].clone()
+            hi[at] += 1 / 64
+            lo[at] -= 1 / 64
+            assert abs((loss(**{k: hi}) - loss(**{k: lo})) * 32 - float(d[key][at])) < 5e-3
+
+
+def test_ffn_streams_and_graphs():
+    import state_space_sequence_exp_amd as m3
+    _, t = inputs(8, 70, 64, 96, "bf16")
+
+    def both(t):
+        h, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True)
+        return (h,) + tuple(m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u).values())
+
+    want = both(t)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    h, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True, stream=st)
+    d = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u, stream=st)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((h,) + tuple(d.values()), want))
+    graphs = []
+    for _ in range(2):
+        held = {k: v.clone() for k, v in t.items()}
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both(held)
+        graphs.append((g, held, out))
+    for _ in range(3):
+        ins = [{k: torch.randn_like(v) for k, v in t.items()} for _ in graphs]
+        for (g, held, _), v in zip(graphs, ins):
+            for k, a in v.items():
+                held[k].copy_(a)
+        for g, _, _ in graphs:
+            g.replay()
+        wants = [both(v) for v in ins]
+        torch.cuda.synchronize()
+        for (_, _, out), w in zip(graphs, wants):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
