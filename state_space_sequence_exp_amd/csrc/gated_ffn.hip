@@ -59,18 +59,48 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int n) {
   return __builtin_bit_cast(u32x4, load_run<T, 16 / (int)sizeof(T)>(p, n));
 }
 
-// A tile's row is 128 bytes of k, its 16-byte chunks permuted by the row so that
-// the rows read together lie on different banks.
+// A tile's row is 128 bytes of k (a cache line: rows of 64 bytes take twice the
+// requests), its 16-byte chunks permuted by the row so that eight rows read together
+// lie on different banks.
 __device__ __forceinline__ int chunk_at(int row, int chunk) { return row * kChunks + (chunk ^ (row & 7)); }
 
-template <typename T, int WM, int WN, int FM, int FN, Mode kMode>
-__global__ void __launch_bounds__(WM * WN * kWave) gemm_kernel(GemmArgs<T> g) {
+// All of the workgroup's LDS accesses before this are done before any after it
+// (outstanding global loads are not waited for, as __syncthreads would).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// 16 bytes a lane from base + off (elements of T) straight into the LDS, lane
+// after lane from byte address `lds` on.  The compiler does not know of the write:
+// wait_loads, then a barrier, come before any read of it.  (Its own load to the LDS
+// it waits for whole before the next read of any LDS array.)
+template <typename T>
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const T* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off * (uint32_t)sizeof(T)), "s"(base)
+               : "memory", "m0");
+}
+// Until at most n of this wave's loads are outstanding.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
+}
+
+// kDirect: rows of both operands start at multiples of 16 bytes; their tiles go
+// straight into the LDS, three ahead of the one that is multiplied.  Otherwise they
+// pass through registers, one ahead.
+template <typename T, int WM, int WN, int FM, int FN, Mode kMode, bool kDirect>
+__global__ void __launch_bounds__(WM* WN* kWave) __attribute__((amdgpu_waves_per_eu(FM * FN > 32 ? 1 : 2, FM * FN > 32 ? 1 : 2)))
+gemm_kernel(GemmArgs<T> g) {
   constexpr int NT = WM * WN * kWave, BM = WM * FM * 16, BN = WN * FN * 16, E = 16 / (int)sizeof(T);
   constexpr int BK = kRowBytes / (int)sizeof(T), kPass = NT / kChunks;  // rows a pass loads
   constexpr int NA = BM / kPass, NB = BN / kPass;
   __shared__ u32x4 s_tile[2][(BM + BN) * kChunks];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, l4 = lane >> 4;
-  const int wm = wave / WN, wn = wave % WN;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, l4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
 
   // Neighbouring tiles on one XCD; eight rows of tiles side by side, so that a
   // chip's worth of tiles shares few rows of both operands.
@@ -80,73 +110,138 @@ __global__ void __launch_bounds__(WM * WN * kWave) gemm_kernel(GemmArgs<T> g) {
   const int m0 = (band * 8 + inBand % high) * BM;
   const int n0 = inBand / high * (kMode == kDual ? BN / 2 : BN);
 
-  const int row = tid / kChunks, chunk = tid % kChunks;
-  const T* pa[NA];
-  const T* pb[NB];
+  // What this thread brings: one chunk of every kPass-th row, rows past the end
+  // standing for the last.  Straight loads put lane after lane, so that it is the
+  // lane's chunk of memory that is permuted.
+  const int row = tid / kChunks;
+  const int chunk = kDirect ? (tid % kChunks) ^ (row & 7) : tid % kChunks;
+  const T* const baseA = g.A + (int64_t)m0 * g.lda;
+  uint32_t offA[NA], offB[NB];
 #pragma unroll
   for (int i = 0; i < NA; ++i)
-    pa[i] = g.A + (int64_t)min(m0 + i * kPass + row, g.M - 1) * g.lda + chunk * E;
+    offA[i] = (uint32_t)min(i * kPass + row, g.M - 1 - m0) * (uint32_t)g.lda + chunk * E;
+  // (whether a wave's rows of pass i are the second matrix's)
+  const auto second = [&](int i) { return (i * kPass + wave * (kWave / kChunks)) % (FN * 16) >= FN * 8; };
+  const T* const base1 = g.B + (int64_t)n0 * g.ldb;
+  const T* const base2 = kMode == kDual ? g.B2 + (int64_t)n0 * g.ldb2 : base1;
+  const auto baseB = [&](int i) { return kMode == kDual && second(i) ? base2 : base1; };
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
     const int r = i * kPass + row;
-    if constexpr (kMode == kDual) {
-      const int w = r / (FN * 16), in = r % (FN * 16), col = n0 + w * FN * 8 + in % (FN * 8);
-      const bool second = in >= FN * 8;
-      pb[i] = (second ? g.B2 : g.B) + (int64_t)min(col, g.N - 1) * (second ? g.ldb2 : g.ldb) + chunk * E;
-    } else {
-      pb[i] = g.B + (int64_t)min(n0 + r, g.N - 1) * g.ldb + chunk * E;
-    }
+    const int col = kMode == kDual ? r / (FN * 16) * FN * 8 + r % (FN * 8) : r;
+    const int64_t ld = kMode == kDual && second(i) ? g.ldb2 : g.ldb;
+    offB[i] = (uint32_t)min(col, g.N - 1 - n0) * (uint32_t)ld + chunk * E;
   }
-  u32x4 ra[NA], rb[NB];
-  const auto request = [&](int k0) {
-    if (k0 + BK <= g.K) {
-#pragma unroll
-      for (int i = 0; i < NA; ++i) __builtin_memcpy(&ra[i], pa[i] + k0, 16);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) __builtin_memcpy(&rb[i], pb[i] + k0, 16);
-    } else {
-      const int n = g.K - k0 - chunk * E;
-#pragma unroll
-      for (int i = 0; i < NA; ++i) ra[i] = load_chunk<T>(pa[i] + k0, n);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) rb[i] = load_chunk<T>(pb[i] + k0, n);
-    }
-  };
-  const auto put = [&](u32x4* s) {
-#pragma unroll
-    for (int i = 0; i < NA; ++i) s[chunk_at(i * kPass + row, chunk)] = ra[i];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) s[chunk_at(BM + i * kPass + row, chunk)] = rb[i];
-  };
 
   f32x4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Frags {
+    u32x4 a[FM], b[FN];
+  };
+  const int get_at[2] = {chunk_at(l16, l4), chunk_at(l16, 4 + l4)};
+  const auto get = [&](Frags& f, int stage, int half) {  // of a row's 128 bytes
+    const u32x4* s = s_tile[stage] + get_at[half];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) f.b[j] = s[(BM + (wn * FN + j) * 16) * kChunks];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f.a[i] = s[(wm * FM + i) * 16 * kChunks];
+  };
+  const auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = mma_chunk(f.b[j], f.a[i], acc[i][j], T());
+  };
+  u32x4 ra[NA], rb[NB];
+  const auto request = [&](int k0) {
+    const int n = g.K - k0 - chunk * E;  // elements from this thread's chunk to the row's end
+#pragma unroll
+    for (int i = 0; i < NA; ++i) ra[i] = load_chunk<T>(baseA + k0 + offA[i], n);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) rb[i] = load_chunk<T>(baseB(i) + k0 + offB[i], n);
+  };
+  const int put_at = chunk_at(row, chunk);  // (kPass is a multiple of 8)
+  const auto put = [&](int stage) {
+    u32x4* s = s_tile[stage] + put_at;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) s[i * kPass * kChunks] = ra[i];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) s[(BM + i * kPass) * kChunks] = rb[i];
+  };
 
-  request(0);
-  put(s_tile[0]);
-  __syncthreads();
-  int buf = 0;
-  for (int k0 = 0; k0 < g.K; k0 += BK, buf ^= 1) {
-    const bool more = k0 + BK < g.K;
-    if (more) request(k0 + BK);
-    const u32x4* s = s_tile[buf];
+  int done = 0;  // tiles multiplied
+  if constexpr (kDirect) {
+    const int whole = g.K / BK;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)&s_tile[0][0];
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds0 + wave * (kWave * 16));
+    const auto bring = [&](int t) {
+      const uint32_t to = lds + (t & 1) * (uint32_t)sizeof s_tile[0];
+      const int k0 = min(t, whole - 1) * BK;  // (past the end: a tile again, into a stage that no one reads)
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 fa[FM], fb[FN];
+      for (int i = 0; i < NA; ++i) load_to_lds(to + i * kPass * kRowBytes, baseA + k0, offA[i]);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = s[chunk_at(BM + (wn * FN + j) * 16 + l16, kk * 4 + l4)];
+      for (int i = 0; i < NB; ++i) load_to_lds(to + (BM + i * kPass) * kRowBytes, baseB(i) + k0, offB[i]);
+    };
+    // the fragments' reads one by one between the products
+    const auto order = [] {
+      constexpr int kReads = FM + FN, kEach = FM * FN * (sizeof(T) == 2 ? 1 : 4) / kReads;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = s[chunk_at((wm * FM + i) * 16 + l16, kk * 4 + l4)];
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mma_chunk(fb[j], fa[i], acc[i][j], T());
+      for (int i = 0; i < kReads; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (whole > 0) {
+      bring(0);
+      bring(1);
+      wait_loads<NA + NB>();
+      lds_barrier();
+      Frags f0, f1;
+      get(f0, 0, 0);
+      for (; done < whole; ++done) {
+        __builtin_amdgcn_sched_barrier(0);
+        get(f1, done & 1, 1);
+        multiply(f0);
+        order();
+        wait_loads<0>();  // the next tile has come, and every wave has read this one
+        lds_barrier();
+        bring(done + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        get(f0, (done & 1) ^ 1, 0);
+        multiply(f1);
+        order();
+      }
+      wait_loads<0>();
+      lds_barrier();
     }
-    if (more) put(s_tile[buf ^ 1]);
-    __syncthreads();
+    if (done * BK < g.K) {
+      request(done * BK);
+      put(0);
+      lds_barrier();
+      Frags rest;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        get(rest, 0, half);
+        multiply(rest);
+      }
+    }
+  } else {
+    request(0);
+    for (int k0 = 0; k0 < g.K; k0 += BK, done ^= 1) {
+      put(done);
+      lds_barrier();
+      if (k0 + BK < g.K) request(k0 + BK);
+      Frags f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        get(f, done, half);
+        multiply(f);
+      }
+    }
   }
 
 #pragma unroll
@@ -192,21 +287,28 @@ __global__ void __launch_bounds__(WM * WN * kWave) gemm_kernel(GemmArgs<T> g) {
   }
 }
 
-// The tile: the largest that still leaves about a tile a CU.
 template <typename T, int WM, int WN, int FM, int FN, Mode kMode>
-void launch_gemm_tile(GemmArgs<T> g, hipStream_t stream) {
+void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
   constexpr int BM = WM * FM * 16, BN = WN * FN * 16 / (kMode == kDual ? 2 : 1);
   g.gridM = (g.M + BM - 1) / BM;
   g.gridN = (g.N + BN - 1) / BN;
-  hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode>), dim3((unsigned)g.gridM * g.gridN),
-                     dim3(WM * WN * kWave), 0, stream, g);
+  const dim3 grid((unsigned)g.gridM * g.gridN), block(WM * WN * kWave);
+  if (direct)
+    hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, true>), grid, block, 0, stream, g);
+  else
+    hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, false>), grid, block, 0, stream, g);
 }
+// The tile: the largest that still leaves about a tile a CU.
 template <typename T, Mode kMode>
 void launch_gemm(const GemmArgs<T>& g, hipStream_t stream) {
+  const auto rows16 = [](const T* p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+  };
+  const bool direct = rows16(g.A, g.lda) && rows16(g.B, g.ldb) && (kMode != kDual || rows16(g.B2, g.ldb2));
   const double cols = kMode == kDual ? 2.0 * g.N : g.N, area = (double)g.M * cols;
-  if (area >= 192.0 * 256 * 256) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, stream);
-  else if (area >= 192.0 * 128 * 128) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, stream);
-  else launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, stream);
+  if (area >= 192.0 * 256 * 256) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
+  else if (area >= 192.0 * 128 * 128) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
+  else launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
 }
 
 // ---- few rows ------------------------------------------------------------------
