@@ -64,14 +64,6 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int n) {
 // lie on different banks.
 __device__ __forceinline__ int chunk_at(int row, int chunk) { return row * kChunks + (chunk ^ (row & 7)); }
 
-// All of the workgroup's LDS accesses before this are done before any after it
-// (outstanding global loads are not waited for, as __syncthreads would).
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // 16 bytes a lane from base + off (elements of T) straight into the LDS, lane
 // after lane from byte address `lds` on.  The compiler does not know of the write:
 // wait_loads, then a barrier, come before any read of it.  (Its own load to the LDS

@@ -70,6 +70,14 @@ __device__ __forceinline__ float dpp_move(float v) {
       __builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRowMask, 0xf, false));
 }
 
+// All of the workgroup's LDS accesses before this are done before any after it
+// (outstanding global loads are not waited for, as __syncthreads would).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Inclusive prefix sum across the 64 lanes of a wave, in DPP steps: shifts by
 // 1, 2, 4 and 8 within each row of 16 lanes, then the last lane of row 0 (and
 // of row 2) added to row 1 (row 3), then the last lane of row 1 added to rows

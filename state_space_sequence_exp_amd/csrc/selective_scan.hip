@@ -15,10 +15,12 @@
 // over n of 16 tokens are taken together, halving the tokens a lane keeps at each
 // of four exchanges, so that lane i ends with token i's.
 //
-// A workgroup of four waves takes 16 channels through tiles of 64 tokens.  Its
-// threads load the tile as it lies in memory, four channels of a token each,
-// compute the steps once and turn them in the LDS; the next tile's loads are in
-// flight meanwhile.  Neighbouring workgroups, which share cache lines, run on one
+// A workgroup takes 16 channels through tiles of 64 tokens.  Four of its waves scan
+// a tile while the other four make ready: they load the tile after it as it lies in
+// memory, four channels of a token each, compute its steps once, turn them in the
+// LDS, and finish and store the outputs of the tile before.  (With every wave doing
+// both in turn, the one wave a SIMD of B1 T16384 D4096 waits for its own loads and
+// barriers: 589 us.)  Neighbouring workgroups, which share cache lines, run on one
 // XCD.
 //
 // With few channels (see select_segments) the tokens are cut into segments: a
@@ -35,7 +37,7 @@
 namespace m3 {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int kThreads = 256, kWaves = kThreads / kWave;  // of either half of a scan's workgroup
 constexpr int kTile = 64;               // tokens
 constexpr int kRow = 16;                // lanes of a DPP row: a channel's
 constexpr int kChan = kWaves * kWave / kRow;  // channels of a workgroup
@@ -89,15 +91,21 @@ struct Piece {
   Raw<T, 4> x, dt, z, b[NL], c[NL];
 };
 
+template <int NL, bool kLocal>
+struct Stage {
+  static constexpr int kN = kRow * NL;  // states held, the last of them zeros where N is less
+  float dt[kChan][kPitch], dx[kChan][kPitch];
+  float b[kN][kPitch], c[kLocal ? 1 : kN][kPitch];
+  float y[kLocal ? 1 : kTile][kChan + 4];
+};
+
 template <typename T, int NL, bool kLocal>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(2 * kThreads)
 select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, float* sums) {
-  constexpr int kN = kRow * NL;  // states held, the last of them zeros where N is less
-  __shared__ float s_dt[kChan][kPitch], s_dx[kChan][kPitch];
-  __shared__ float s_b[kN][kPitch], s_c[kLocal ? 1 : kN][kPitch];
-  __shared__ float s_y[kLocal ? 1 : kTile][kChan + 4];
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & (kRow - 1);
-  const int groups = (int)gridDim.x, place = xcd_place((int)blockIdx.x, groups);
+  __shared__ Stage<NL, kLocal> s_stage[2];
+  const int tid = threadIdx.x & (kThreads - 1), lane = tid & 63, i = lane & (kRow - 1);
+  const bool scans = __builtin_amdgcn_readfirstlane(threadIdx.x) < kThreads;
+  const int place = xcd_place((int)blockIdx.x, (int)gridDim.x);
   const int launched = kLocal ? segs - 1 : segs;     // nothing follows the last segment's end
   const int tile0 = place % tiles, seg = place / tiles % launched;
   const int64_t bq = place / tiles / launched;
@@ -105,30 +113,87 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
   const int N = a.N;
   const int64_t len = a.lengths ? min(max((int64_t)a.lengths[bq], (int64_t)0), a.T) : a.T;
   const int64_t t0 = seg * segLen, t1 = min(t0 + segLen, a.T);
+  const int64_t tEnd = min(t1, len);                 // padding from there on
+  const int nTiles = tEnd > t0 ? (int)((tEnd - t0 + kTile - 1) / kTile) : 0;
 
-  // the states of this lane
-  const int ch = (tid >> 6) * (kWave / kRow) + (lane >> 4);
-  const int64_t d = d0 + ch;
-  float A2[NL], h[NL];
+  if (scans) {
+    const int ch = (tid >> 6) * (kWave / kRow) + (lane >> 4);
+    const int64_t d = d0 + ch;
+    float A2[NL], h[NL];
 #pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    const int n = i + kRow * k;
-    const bool in = d < a.D && n < N;
-    A2[k] = in ? a.A[d * N + n] * kLog2e : 0.f;
-    h[k] = 0.f;
-    if constexpr (!kLocal) {
-      if (in) {
-        if (a.h0) h[k] = a.h0[(bq * a.D + d) * N + n];
-        for (int s = 0; s < seg; ++s) {
-          const int64_t at = (bq * (segs - 1) + s) * a.D + d;
-          h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[k] * sums[at]), h[k], ends[at * N + n]);
+    for (int k = 0; k < NL; ++k) {
+      const int n = i + kRow * k;
+      const bool in = d < a.D && n < N;
+      A2[k] = in ? a.A[d * N + n] * kLog2e : 0.f;
+      h[k] = 0.f;
+      if constexpr (!kLocal) {
+        if (in) {
+          if (a.h0) h[k] = a.h0[(bq * a.D + d) * N + n];
+          for (int s = 0; s < seg; ++s) {
+            const int64_t at = (bq * (segs - 1) + s) * a.D + d;
+            h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[k] * sums[at]), h[k], ends[at * N + n]);
+          }
         }
       }
     }
+    float total = 0.f;  // of the steps of this lane's tokens
+    lds_barrier();
+    for (int q = 0; q < nTiles; ++q) {
+      Stage<NL, kLocal>& st = s_stage[q & 1];
+      for (int j = 0; j < kTile; j += kRow) {
+        const float vdt = st.dt[ch][j + i], vdx = st.dx[ch][j + i];
+        float p[kRow];
+        if constexpr (kLocal) total += vdt;
+        const auto four = [&](auto first) {  // tokens first .. first + 3 of the 16
+          constexpr int f = decltype(first)::value;
+          float4 b4[NL], c4[NL];
+#pragma unroll
+          for (int k = 0; k < NL; ++k) {
+            b4[k] = *reinterpret_cast<const float4*>(&st.b[i + kRow * k][j + f]);
+            if constexpr (!kLocal) c4[k] = *reinterpret_cast<const float4*>(&st.c[i + kRow * k][j + f]);
+          }
+          const auto one = [&](auto tok) {
+            constexpr int e = decltype(tok)::value;
+#pragma unroll
+            for (int k = 0; k < NL; ++k) {
+              const float decay = __builtin_amdgcn_exp2f(row_lane<f + e>(vdt) * A2[k]);
+              h[k] = __builtin_fmaf(decay, h[k], row_lane<f + e>(vdx) * (&b4[k].x)[e]);
+              if constexpr (!kLocal)
+                p[f + e] = k ? __builtin_fmaf((&c4[k].x)[e], h[k], p[f + e]) : (&c4[k].x)[e] * h[k];
+            }
+          };
+          one(std::integral_constant<int, 0>{});
+          one(std::integral_constant<int, 1>{});
+          one(std::integral_constant<int, 2>{});
+          one(std::integral_constant<int, 3>{});
+        };
+        four(std::integral_constant<int, 0>{});
+        four(std::integral_constant<int, 4>{});
+        four(std::integral_constant<int, 8>{});
+        four(std::integral_constant<int, 12>{});
+        if constexpr (!kLocal) st.y[j + i][ch] = row_sums(p, i);
+      }
+      lds_barrier();
+    }
+    if constexpr (kLocal) {
+      total += swap_lanes<0xb1>(total);
+      total += swap_lanes<0x4e>(total);
+      total += swap_lanes<0x141>(total);
+      total += swap_lanes<0x140>(total);
+      const int64_t at = (bq * (segs - 1) + seg) * a.D + d;
+      if (d < a.D && i == 0) sums[at] = total;
+#pragma unroll
+      for (int k = 0; k < NL; ++k)
+        if (d < a.D && i + kRow * k < N) ends[at * N + i + kRow * k] = h[k];
+    } else if (a.h_last && seg == segs - 1) {
+#pragma unroll
+      for (int k = 0; k < NL; ++k)
+        if (d < a.D && i + kRow * k < N) a.h_last[(bq * a.D + d) * N + i + kRow * k] = h[k];
+    }
+    return;
   }
-  float total = 0.f;  // of the steps of this lane's tokens
 
-  // what this thread brings
+  // what a thread of the other half brings and finishes
   const int tk = tid >> 2, part = tid & 3, c0 = part * 4;
   const int nc = (int)max((int64_t)0, min((int64_t)4, a.D - d0 - c0));
   float bias[4], skip[4];
@@ -137,117 +202,80 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
     bias[e] = a.dt_bias && e < nc ? a.dt_bias[d0 + c0 + e] : 0.f;
     skip[e] = a.skip && e < nc ? a.skip[d0 + c0 + e] : 0.f;
   }
-  const auto request = [&](int64_t t) {
+  const auto request = [&](int q) {
     Piece<T, NL, kLocal> p = {};
-    if (t + tk < min(t1, len)) {
-      const int64_t row = bq * a.T + t + tk;
+    const int64_t t = t0 + (int64_t)q * kTile + tk;
+    if (t < tEnd) {
+      const int64_t row = bq * a.T + t;
       p.x = load_run<T, 4>(static_cast<const T*>(a.x) + row * a.ld_x + d0 + c0, nc);
       p.dt = load_run<T, 4>(static_cast<const T*>(a.dt) + row * a.ld_dt + d0 + c0, nc);
       if constexpr (!kLocal)
         if (a.z) p.z = load_run<T, 4>(static_cast<const T*>(a.z) + row * a.ld_z + d0 + c0, nc);
 #pragma unroll
-      for (int q = 0; q < NL; ++q) {
-        const int n = (part * NL + q) * 4;
-        p.b[q] = load_run<T, 4>(static_cast<const T*>(a.Bt) + row * a.ld_b + n, N - n);
-        if constexpr (!kLocal)
-          p.c[q] = load_run<T, 4>(static_cast<const T*>(a.Ct) + row * a.ld_c + n, N - n);
+      for (int v = 0; v < NL; ++v) {
+        const int n = (part * NL + v) * 4;
+        p.b[v] = load_run<T, 4>(static_cast<const T*>(a.Bt) + row * a.ld_b + n, N - n);
+        if constexpr (!kLocal) p.c[v] = load_run<T, 4>(static_cast<const T*>(a.Ct) + row * a.ld_c + n, N - n);
       }
     }
     return p;
   };
-
-  Piece<T, NL, kLocal> next = request(t0);
-  for (int64_t t = t0; t < t1; t += kTile) {
-    const bool live = t + tk < min(t1, len);
-    const Raw<T, 4> x = next.x, z = next.z;
-    if (t >= len) {  // padding from here on
-      if constexpr (kLocal) break;
-      if (t + tk < t1)
-        store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t + tk) * a.ld_y + d0 + c0, nc, no_run<T, 4>());
-      continue;
-    }
+  const auto put = [&](int q, const Piece<T, NL, kLocal>& p) {
+    Stage<NL, kLocal>& st = s_stage[q & 1];
+    const bool live = t0 + (int64_t)q * kTile + tk < tEnd;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float v = run_at(next.dt, e) + bias[e];
+      const float v = run_at(p.dt, e) + bias[e];
       const float step = live ? (a.softplus ? softplus_of(v) : v) : 0.f;
-      s_dt[c0 + e][tk] = step;
-      s_dx[c0 + e][tk] = step * run_at(x, e);
+      st.dt[c0 + e][tk] = step;
+      st.dx[c0 + e][tk] = step * run_at(p.x, e);
     }
 #pragma unroll
-    for (int q = 0; q < NL; ++q)
+    for (int v = 0; v < NL; ++v)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s_b[(part * NL + q) * 4 + e][tk] = run_at(next.b[q], e);
-        if constexpr (!kLocal) s_c[(part * NL + q) * 4 + e][tk] = run_at(next.c[q], e);
+        st.b[(part * NL + v) * 4 + e][tk] = run_at(p.b[v], e);
+        if constexpr (!kLocal) st.c[(part * NL + v) * 4 + e][tk] = run_at(p.c[v], e);
       }
-    __syncthreads();
-    next = request(t + kTile);
-    for (int j = 0; j < kTile; j += kRow) {
-      const float vdt = s_dt[ch][j + i], vdx = s_dx[ch][j + i];
-      float p[kRow];
-      if constexpr (kLocal) total += vdt;
-      const auto four = [&](auto first) {  // tokens first .. first + 3 of the 16
-        constexpr int f = decltype(first)::value;
-        float4 b4[NL], c4[NL];
+  };
+  struct Held {
+    Raw<T, 4> x, z;
+  };
+  const auto finish = [&](int q, const Held& v) {
+    const int64_t t = t0 + (int64_t)q * kTile + tk;
+    if (t >= tEnd) return;
+    const float4 sum = *reinterpret_cast<const float4*>(&s_stage[q & 1].y[kLocal ? 0 : tk][c0]);
+    float y[4];
 #pragma unroll
-        for (int k = 0; k < NL; ++k) {
-          b4[k] = *reinterpret_cast<const float4*>(&s_b[i + kRow * k][j + f]);
-          if constexpr (!kLocal) c4[k] = *reinterpret_cast<const float4*>(&s_c[i + kRow * k][j + f]);
-        }
-        const auto one = [&](auto tok) {
-          constexpr int q = decltype(tok)::value;
-#pragma unroll
-          for (int k = 0; k < NL; ++k) {
-            const float decay = __builtin_amdgcn_exp2f(row_lane<f + q>(vdt) * A2[k]);
-            h[k] = __builtin_fmaf(decay, h[k], row_lane<f + q>(vdx) * (&b4[k].x)[q]);
-            if constexpr (!kLocal)
-              p[f + q] = k ? __builtin_fmaf((&c4[k].x)[q], h[k], p[f + q]) : (&c4[k].x)[q] * h[k];
-          }
-        };
-        one(std::integral_constant<int, 0>{});
-        one(std::integral_constant<int, 1>{});
-        one(std::integral_constant<int, 2>{});
-        one(std::integral_constant<int, 3>{});
-      };
-      four(std::integral_constant<int, 0>{});
-      four(std::integral_constant<int, 4>{});
-      four(std::integral_constant<int, 8>{});
-      four(std::integral_constant<int, 12>{});
-      if constexpr (!kLocal) s_y[j + i][ch] = row_sums(p, i);
-    }
-    __syncthreads();
-    if constexpr (!kLocal) {
-      if (t + tk < t1) {
-        const float4 sum = *reinterpret_cast<const float4*>(&s_y[tk][c0]);
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = __builtin_fmaf(skip[e], run_at(x, e), (&sum.x)[e]);
-          if (a.z) {
-            const float g = run_at(z, e);
-            y[e] = y[e] * (g * sigmoid_of(g));
-          }
-          y[e] = live ? y[e] : 0.f;
-        }
-        store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t + tk) * a.ld_y + d0 + c0, nc, to_run<T, 4>(y));
+    for (int e = 0; e < 4; ++e) {
+      y[e] = __builtin_fmaf(skip[e], run_at(v.x, e), (&sum.x)[e]);
+      if (a.z) {
+        const float g = run_at(v.z, e);
+        y[e] = y[e] * (g * sigmoid_of(g));
       }
     }
-  }
+    store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t) * a.ld_y + d0 + c0, nc, to_run<T, 4>(y));
+  };
 
-  if constexpr (kLocal) {
-    total += swap_lanes<0xb1>(total);
-    total += swap_lanes<0x4e>(total);
-    total += swap_lanes<0x141>(total);
-    total += swap_lanes<0x140>(total);
-    const int64_t at = (bq * (segs - 1) + seg) * a.D + d;
-    if (d < a.D && i == 0) sums[at] = total;
-#pragma unroll
-    for (int k = 0; k < NL; ++k)
-      if (d < a.D && i + kRow * k < N) ends[at * N + i + kRow * k] = h[k];
-  } else if (a.h_last && seg == segs - 1) {
-#pragma unroll
-    for (int k = 0; k < NL; ++k)
-      if (d < a.D && i + kRow * k < N) a.h_last[(bq * a.D + d) * N + i + kRow * k] = h[k];
+  Held before = {}, now = {};
+  Piece<T, NL, kLocal> next = request(0);
+  if (nTiles > 0) put(0, next);
+  now = Held{next.x, next.z};
+  next = request(1);
+  lds_barrier();
+  for (int q = 0; q < nTiles; ++q) {
+    if constexpr (!kLocal)
+      if (q > 0) finish(q - 1, before);
+    before = now;
+    now = Held{next.x, next.z};
+    if (q + 1 < nTiles) put(q + 1, next);
+    next = request(q + 2);
+    lds_barrier();
+  }
+  if constexpr (!kLocal) {
+    if (nTiles > 0) finish(nTiles - 1, before);
+    for (int64_t t = max(tEnd, t0) + tk; t < t1; t += kTile)
+      store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t) * a.ld_y + d0 + c0, nc, no_run<T, 4>());
   }
 }
 
@@ -319,9 +347,9 @@ void launch_select_n(const SelectArgs& a, hipStream_t stream) {
   float* sums = ends + a.B * (segs - 1) * a.D * a.N;
   const unsigned units = (unsigned)(a.B * tiles);
   if (segs > 1)
-    hipLaunchKernelGGL((select_kernel<T, NL, true>), dim3(units * (segs - 1)), dim3(kThreads), 0, stream, a,
+    hipLaunchKernelGGL((select_kernel<T, NL, true>), dim3(units * (segs - 1)), dim3(2 * kThreads), 0, stream, a,
                        tiles, segs, len, ends, sums);
-  hipLaunchKernelGGL((select_kernel<T, NL, false>), dim3(units * segs), dim3(kThreads), 0, stream, a, tiles,
+  hipLaunchKernelGGL((select_kernel<T, NL, false>), dim3(units * segs), dim3(2 * kThreads), 0, stream, a, tiles,
                      segs, len, ends, sums);
 }
 template <typename T>
