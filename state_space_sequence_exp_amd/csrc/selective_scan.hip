@@ -60,21 +60,54 @@ template <int kCtrl>
 __device__ __forceinline__ float swap_lanes(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
 }
-// Halves the tokens: `up` lanes keep the upper half and take the other lanes' part of it.
-template <int kCtrl, int n>
-__device__ __forceinline__ void halve(float (&p)[kRow], bool up) {
-#pragma unroll
-  for (int q = 0; q < n; ++q) {
-    const float keep = up ? p[q + n] : p[q], give = up ? p[q] : p[q + n];
-    p[q] = keep + swap_lanes<kCtrl>(give);
-  }
-}
-// Lane i of a row: the sum of p[i] over its 16 lanes.
-__device__ __forceinline__ float row_sums(float (&p)[kRow], int i) {
-  halve<0x128, 8>(p, i & 8);  // row_ror:8
-  halve<0x141, 4>(p, i & 4);  // row_half_mirror: lane i xor 7
-  halve<0x4e, 2>(p, i & 2);   // quad_perm: lane i xor 2
-  halve<0xb1, 1>(p, i & 1);   // lane i xor 1
+// Lane i of a row: the sum of p[i] over its 16 lanes.  Four exchanges, each of which
+// halves the tokens a lane keeps: with the lane 8 away, lane xor 7, xor 2 and xor 1.
+// In the first two the lanes that keep the upper half of the tokens are whole banks
+// of four, so that each sum is written for its own lanes alone, by the DPP's bank
+// mask (33 operations for 16 tokens; with selects before the sums, 45).  A DPP
+// operand is read two operations after it was written, at the earliest: what is
+// written here is, and the two waits see to the rest.
+__device__ __forceinline__ float row_sums(float (&p)[kRow]) {
+  const unsigned long long odd2 = 0xccccccccccccccccull, odd1 = 0xaaaaaaaaaaaaaaaaull;  // lanes with bit 1, 0
+  asm(
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %0, %8, %8 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %1, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %2, %10, %10 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %3, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %3, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %4, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %4, %12, %12 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %5, %5, %5 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %6, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %6, %14, %14 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %7, %7, %7 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %7, %15, %15 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %0, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %2, %6, %6 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %3, %3, %3 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %3, %7, %7 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %0, %0, %0 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %2, %2 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %1, %1, %1 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %3, %3, %3 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_e64 %0, %0, %2, %16\n\t"
+      "v_cndmask_b32_e64 %1, %1, %3, %16\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %1, %1, %1 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_e64 %0, %0, %1, %17"
+      : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]), "+v"(p[4]), "+v"(p[5]), "+v"(p[6]), "+v"(p[7]),
+        "+v"(p[8]), "+v"(p[9]), "+v"(p[10]), "+v"(p[11]), "+v"(p[12]), "+v"(p[13]), "+v"(p[14]), "+v"(p[15])
+      : "s"(odd2), "s"(odd1));
   return p[0];
 }
 
@@ -125,16 +158,29 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
       const int n = i + kRow * k;
       const bool in = d < a.D && n < N;
       A2[k] = in ? a.A[d * N + n] * kLog2e : 0.f;
-      h[k] = 0.f;
-      if constexpr (!kLocal) {
-        if (in) {
-          if (a.h0) h[k] = a.h0[(bq * a.D + d) * N + n];
-          for (int s = 0; s < seg; ++s) {
-            const int64_t at = (bq * (segs - 1) + s) * a.D + d;
-            h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[k] * sums[at]), h[k], ends[at * N + n]);
-          }
+      h[k] = !kLocal && in && a.h0 ? a.h0[(bq * a.D + d) * N + n] : 0.f;
+    }
+    if constexpr (!kLocal) {
+      // the segments before, eight at a time in flight (past the last: none, its decay 1)
+      for (int s0 = 0; s0 < seg; s0 += 8) {
+        float sum[8], end[8][NL];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const int64_t at = (bq * (segs - 1) + min(s0 + v, seg - 1)) * a.D + min(d, a.D - 1);
+          const bool in = s0 + v < seg;
+          sum[v] = in ? sums[at] : 0.f;
+#pragma unroll
+          for (int k = 0; k < NL; ++k) end[v][k] = in ? ends[at * N + min(i + kRow * k, N - 1)] : 0.f;
         }
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+#pragma unroll
+          for (int k = 0; k < NL; ++k)
+            h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[k] * sum[v]), h[k], end[v][k]);
       }
+#pragma unroll
+      for (int k = 0; k < NL; ++k)  // lanes without a state hold none
+        if (d >= a.D || i + kRow * k >= N) h[k] = 0.f;
     }
     float total = 0.f;  // of the steps of this lane's tokens
     lds_barrier();
@@ -171,7 +217,7 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
         four(std::integral_constant<int, 4>{});
         four(std::integral_constant<int, 8>{});
         four(std::integral_constant<int, 12>{});
-        if constexpr (!kLocal) st.y[j + i][ch] = row_sums(p, i);
+        if constexpr (!kLocal) st.y[j + i][ch] = row_sums(p);
       }
       lds_barrier();
     }
@@ -257,19 +303,24 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
     store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t) * a.ld_y + d0 + c0, nc, to_run<T, 4>(y));
   };
 
+  // (two tiles' loads are in flight; the outputs are stored last, so that no wait
+  // for loads is one for the stores too)
   Held before = {}, now = {};
-  Piece<T, NL, kLocal> next = request(0);
+  Piece<T, NL, kLocal> next = request(0), later = request(1);
   if (nTiles > 0) put(0, next);
   now = Held{next.x, next.z};
-  next = request(1);
+  next = later;
+  later = request(2);
   lds_barrier();
   for (int q = 0; q < nTiles; ++q) {
-    if constexpr (!kLocal)
-      if (q > 0) finish(q - 1, before);
+    const Held last = before;
     before = now;
     now = Held{next.x, next.z};
     if (q + 1 < nTiles) put(q + 1, next);
-    next = request(q + 2);
+    next = later;
+    later = request(q + 3);
+    if constexpr (!kLocal)
+      if (q > 0) finish(q - 1, last);
     lds_barrier();
   }
   if constexpr (!kLocal) {
