@@ -991,18 +991,44 @@ def decode_step_cached(codes, scales, slots, x_t, x_prev, B_t, B_prev, C_t, dt, 
     return y
 
 
-def _lengths(lengths, nb, dev):
-    import torch
-    if lengths is not None:
-        _same(lengths, "lengths", torch.int32, (nb,), dev)
+_tensors = None
 
 
-def _pool_slots(slots, nb, n_slots, dev):
-    import torch
-    if slots is not None:
-        _same(slots, "slots", torch.int32, (nb,), dev)
-    elif nb > n_slots:
-        raise ValueError("%d rows without slots for a pool of %d" % (nb, n_slots))
+def _look():
+    """The module that looks at a call's tensors (see csrc/tensors.cpp); _dense and
+    _spaced say what it found wrong."""
+    global _tensors
+    if _tensors is None:
+        load_library()
+        try:
+            from . import _tensors as found
+        except ImportError as e:
+            raise RuntimeError("_tensors.so not found beside libm3ssm.so; build it with "
+                               "`python -m state_space_sequence_exp_amd.build`") from e
+        _tensors = found
+    return _tensors
+
+
+def _dense(names, dtype, shape, dev: int, *ts):
+    """Addresses of dense arrays of this type and shape on device `dev` (None: 0)."""
+    got = _tensors.dense(dtype, shape, dev, *ts)
+    if got is None:
+        for name, t in zip(names, ts):
+            if t is not None:
+                _same(t, name, dtype, shape, dev)
+        raise ValueError("%s: expected dense arrays" % (names,))
+    return got
+
+
+def _spaced(names, dtype, shape, dev: int, *ts):
+    """Address and row distance of each of these arrays of rows (None: 0, 0)."""
+    got = _tensors.rows(dtype, shape, dev, *ts)
+    if got is None:
+        for name, t in zip(names, ts):
+            if t is not None:
+                _rows(t, name, dtype, shape, dev)
+        raise ValueError("%s: expected arrays of rows" % (names,))
+    return got
 
 
 @_streamed
@@ -1022,7 +1048,7 @@ def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths
     causal_conv_step; None without want_state).
     """
     import torch
-    lib = _lib or load_library()
+    _tensors or _look()
     shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) != 3:
         raise ValueError("x: expected [B, T, D], got %s" % (tuple(shape),))
@@ -1031,26 +1057,20 @@ def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths
     if weight.dim() != 2:
         raise ValueError("weight: expected [D, W], got %s" % (tuple(weight.shape),))
     nw = weight.shape[1]
-    ld = _rows(x, "x", dt, shape, dev)
-    d = M3ConvDims(nb, nt, nd, nw, ld)
-    _same(weight, "weight", torch.float32, (nd, nw), dev)
-    if bias is not None:
-        _same(bias, "bias", torch.float32, (nd,), dev)
-    kept = (nb, nw - 1, nd)
-    if state is not None:
-        _same(state, "state", dt, kept, dev)
-    if state_out is not None:
-        _same(state_out, "state_out", dt, kept, dev)
-    _lengths(lengths, nb, dev)
-    if y is not None:
-        d.ld_y = _rows(y, "y", dt, shape, dev)
+    px, ldx, py, ldy = _spaced(("x", "y"), dt, shape, dev, x, y)
+    pw, = _dense(("weight",), torch.float32, (nd, nw), dev, weight)
+    pb, = _dense(("bias",), torch.float32, (nd,), dev, bias)
+    ps, pk = _dense(("state", "state_out"), dt, (nb, nw - 1, nd), dev, state, state_out)
+    pl, = _dense(("lengths",), torch.int32, (nb,), dev, lengths)
     _gpu(dev)
     if y is None:
-        y = _like(x, ld == 0)
+        y = _like(x, ldx == 0)
+        py = y.data_ptr()
     if state_out is None and want_state:
-        state_out = x.new_empty(kept)
-    _launch(dev, lib.m3_causal_conv, ctypes.byref(d), code, _at(x), _at(weight), _at(bias),
-            int(bool(silu)), _at(state), _at(lengths), _at(y), _at(state_out))
+        state_out = torch.empty((nb, nw - 1, nd), dtype=dt, device=x.device)
+        pk = state_out.data_ptr()
+    d = M3ConvDims(nb, nt, nd, nw, ldx, ldy)
+    _launch(dev, _lib.m3_causal_conv, ctypes.byref(d), code, px, pw, pb, 1 if silu else 0, ps, pl, py, pk)
     return y, state_out
 
 
@@ -1064,7 +1084,7 @@ def causal_conv_step(state, x, weight, bias=None, *, silu: bool = False, slots=N
     idle; None: row b in slot b).  Returns y [B,D], whose idle rows are left as
     they were (zeros when y is not given)."""
     import torch
-    lib = _lib or load_library()
+    _tensors or _look()
     shape, dev, dt = x.shape, x.get_device(), x.dtype
     if len(shape) != 2:
         raise ValueError("x: expected [B, D], got %s" % (tuple(shape),))
@@ -1074,21 +1094,36 @@ def causal_conv_step(state, x, weight, bias=None, *, silu: bool = False, slots=N
         raise ValueError("expected weight [D, W] and state [slots, W-1, D], got %s and %s"
                          % (tuple(weight.shape), tuple(state.shape)))
     nw, ns = weight.shape[1], state.shape[0]
-    ld = _rows(x, "x", dt, shape, dev)
-    d = M3ConvDims(nb, 1, nd, nw, ld)
-    _same(weight, "weight", torch.float32, (nd, nw), dev)
-    if bias is not None:
-        _same(bias, "bias", torch.float32, (nd,), dev)
-    _same(state, "state", dt, (ns, nw - 1, nd), dev)
-    _pool_slots(slots, nb, ns, dev)
-    if y is not None:
-        d.ld_y = _rows(y, "y", dt, shape, dev)
+    px, ldx, py, ldy = _spaced(("x", "y"), dt, shape, dev, x, y)
+    pw, = _dense(("weight",), torch.float32, (nd, nw), dev, weight)
+    pb, = _dense(("bias",), torch.float32, (nd,), dev, bias)
+    ps, = _dense(("state",), dt, (ns, nw - 1, nd), dev, state)
+    pi = _pool_slots(slots, nb, ns, dev)
     _gpu(dev)
     if y is None:
-        y = _like(x, ld == 0) if slots is None else x.new_zeros(shape)
-    _launch(dev, lib.m3_causal_conv_step, ctypes.byref(d), code, _at(state), _at(slots), ns,
-            _at(x), _at(weight), _at(bias), int(bool(silu)), _at(y))
+        y = _step_output(x, ldx, slots)
+        py = y.data_ptr()
+    d = M3ConvDims(nb, 1, nd, nw, ldx, ldy)
+    _launch(dev, _lib.m3_causal_conv_step, ctypes.byref(d), code, ps, pi, ns, px, pw, pb,
+            1 if silu else 0, py)
     return y
+
+
+def _pool_slots(slots, nb, n_slots, dev):
+    import torch
+    if slots is None:
+        if nb > n_slots:
+            raise ValueError("%d rows without slots for a pool of %d" % (nb, n_slots))
+        return 0
+    return _dense(("slots",), torch.int32, (nb,), dev, slots)[0]
+
+
+def _step_output(x, ld, slots):
+    """A single-token call's new y: zeros where rows may be idle."""
+    import torch
+    if slots is None:
+        return _like(x, ld == 0)
+    return torch.zeros(x.shape, dtype=x.dtype, device=x.device)
 
 
 def selective_scan_workspace_size(batch, seqlen, channels, N, dtype) -> int:
@@ -1115,7 +1150,7 @@ def selective_scan(x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, softplus:
     Returns (y [B,T,D], h_last [B,D,N] float32: each sequence's state after its
     own last token)."""
     import torch
-    lib = _lib or load_library()
+    _tensors or _look()
     shape, dev, dtype = x.shape, x.get_device(), x.dtype
     if len(shape) != 3 or A.dim() != 2:
         raise ValueError("expected x [B, T, D] and A [D, N], got %s and %s"
@@ -1123,39 +1158,30 @@ def selective_scan(x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, softplus:
     nb, nt, nd = shape
     nn = A.shape[1]
     code = _type_code(dtype)
-    thin = (nb, nt, nn)
-    ld = _rows(x, "x", dtype, shape, dev)
-    d = M3SelectDims(nb, nt, nd, nn, ld, _rows(dt, "dt", dtype, shape, dev),
-                     0 if z is None else _rows(z, "z", dtype, shape, dev), 0,
-                     _rows(B, "B", dtype, thin, dev), _rows(C, "C", dtype, thin, dev))
-    _same(A, "A", torch.float32, (nd, nn), dev)
-    if skip is not None:
-        _same(skip, "skip", torch.float32, (nd,), dev)
-    if dt_bias is not None:
-        _same(dt_bias, "dt_bias", torch.float32, (nd,), dev)
-    if h0 is not None:
-        _same(h0, "h0", torch.float32, (nb, nd, nn), dev)
-    if h_last is not None:
-        _same(h_last, "h_last", torch.float32, (nb, nd, nn), dev)
-    _lengths(lengths, nb, dev)
-    if y is not None:
-        d.ld_y = _rows(y, "y", dtype, shape, dev)
+    px, ldx, pt, ldt, pz, ldz, py, ldy = _spaced(("x", "dt", "z", "y"), dtype, shape, dev, x, dt, z, y)
+    pB, ldb, pC, ldc = _spaced(("B", "C"), dtype, (nb, nt, nn), dev, B, C)
+    pA, = _dense(("A",), torch.float32, (nd, nn), dev, A)
+    pk, pd = _dense(("skip", "dt_bias"), torch.float32, (nd,), dev, skip, dt_bias)
+    p0, ph = _dense(("h0", "h_last"), torch.float32, (nb, nd, nn), dev, h0, h_last)
+    pl, = _dense(("lengths",), torch.int32, (nb,), dev, lengths)
     _gpu(dev)
     if y is None:
-        y = _like(x, ld == 0)
+        y = _like(x, ldx == 0)
+        py = y.data_ptr()
     if h_last is None:
-        h_last = A.new_empty((nb, nd, nn))
-    need = int(lib.m3_selective_scan_workspace_size(ctypes.byref(d), code))
-    ws_bytes = 0
+        h_last = torch.empty((nb, nd, nn), dtype=torch.float32, device=x.device)
+        ph = h_last.data_ptr()
+    d = M3SelectDims(nb, nt, nd, nn, ldx, ldt, ldz, ldy, ldb, ldc)
+    need = _lib.m3_selective_scan_workspace_size(ctypes.byref(d), code)
+    pw = ws_bytes = 0
     if need:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous and on the first tensor's device")
-        ws_bytes = workspace.nbytes
-    _launch(dev, lib.m3_selective_scan, ctypes.byref(d), code, _at(x), _at(dt), _at(A), _at(B), _at(C),
-            _at(skip), _at(z), _at(dt_bias), int(bool(softplus)), _at(h0), _at(lengths), _at(y),
-            _at(h_last), _at(workspace) if need else None, ws_bytes)
+        pw, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _launch(dev, _lib.m3_selective_scan, ctypes.byref(d), code, px, pt, pA, pB, pC, pk, pz, pd,
+            1 if softplus else 0, p0, pl, py, ph, pw, ws_bytes)
     return y, h_last
 
 
@@ -1170,7 +1196,7 @@ def selective_scan_step(h, x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, s
     Returns y [B,D], whose idle rows are left as they were (zeros when y is not
     given)."""
     import torch
-    lib = _lib or load_library()
+    _tensors or _look()
     shape, dev, dtype = x.shape, x.get_device(), x.dtype
     if len(shape) != 2 or A.dim() != 2 or h.dim() != 3:
         raise ValueError("expected h [slots, D, N], x [B, D] and A [D, N], got %s, %s and %s"
@@ -1178,26 +1204,30 @@ def selective_scan_step(h, x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, s
     nb, nd = shape
     nn, ns = A.shape[1], h.shape[0]
     code = _type_code(dtype)
-    ld = _rows(x, "x", dtype, shape, dev)
-    d = M3SelectDims(nb, 1, nd, nn, ld, _rows(dt, "dt", dtype, shape, dev),
-                     0 if z is None else _rows(z, "z", dtype, shape, dev), 0,
-                     _rows(B, "B", dtype, (nb, nn), dev), _rows(C, "C", dtype, (nb, nn), dev))
-    _same(A, "A", torch.float32, (nd, nn), dev)
-    _same(h, "h", torch.float32, (ns, nd, nn), dev)
-    if skip is not None:
-        _same(skip, "skip", torch.float32, (nd,), dev)
-    if dt_bias is not None:
-        _same(dt_bias, "dt_bias", torch.float32, (nd,), dev)
-    _pool_slots(slots, nb, ns, dev)
-    if y is not None:
-        d.ld_y = _rows(y, "y", dtype, shape, dev)
+    px, ldx, pt, ldt, pz, ldz, py, ldy = _spaced(("x", "dt", "z", "y"), dtype, shape, dev, x, dt, z, y)
+    pB, ldb, pC, ldc = _spaced(("B", "C"), dtype, (nb, nn), dev, B, C)
+    pA, = _dense(("A",), torch.float32, (nd, nn), dev, A)
+    ph, = _dense(("h",), torch.float32, (ns, nd, nn), dev, h)
+    pk, pd = _dense(("skip", "dt_bias"), torch.float32, (nd,), dev, skip, dt_bias)
+    pi = _pool_slots(slots, nb, ns, dev)
     _gpu(dev)
     if y is None:
-        y = _like(x, ld == 0) if slots is None else x.new_zeros(shape)
-    _launch(dev, lib.m3_selective_scan_step, ctypes.byref(d), code, _at(h), _at(slots), ns, _at(x),
-            _at(dt), _at(A), _at(B), _at(C), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
-            _at(y))
+        y = _step_output(x, ldx, slots)
+        py = y.data_ptr()
+    d = M3SelectDims(nb, 1, nd, nn, ldx, ldt, ldz, ldy, ldb, ldc)
+    _launch(dev, _lib.m3_selective_scan_step, ctypes.byref(d), code, ph, pi, ns, px, pt, pA, pB, pC,
+            pk, pz, pd, 1 if softplus else 0, py)
     return y
+
+
+def _ffn_shapes(x, w_gate):
+    """Rows, K, F and the shape of h."""
+    shape = x.shape
+    if len(shape) < 1 or w_gate.dim() != 2:
+        raise ValueError("expected x [..., K] and w_gate [F, K], got %s and %s"
+                         % (tuple(shape), tuple(w_gate.shape)))
+    nf, lead = w_gate.shape[0], shape[:-1]
+    return math.prod(lead), shape[-1], nf, (*lead, nf)
 
 
 @_streamed
@@ -1211,30 +1241,25 @@ def gated_ffn(x, w_gate, w_up, *, want_pre: bool = False, h=None, gate=None, up=
     input or each other.
     Returns (h [...,F], gate, up [...,F] float32 or None)."""
     import torch
-    lib = _lib or load_library()
-    shape, dev, dt = x.shape, x.get_device(), x.dtype
-    if len(shape) < 1 or w_gate.dim() != 2:
-        raise ValueError("expected x [..., K] and w_gate [F, K], got %s and %s"
-                         % (tuple(shape), tuple(w_gate.shape)))
+    _tensors or _look()
+    dev, dt = x.get_device(), x.dtype
+    rows, nk, nf, out = _ffn_shapes(x, w_gate)
     code = _type_code(dt)
-    nk, nf = shape[-1], w_gate.shape[0]
-    out = shape[:-1] + (nf,)
-    d = M3FfnDims(math.prod(shape[:-1]), nk, nf, _rows(x, "x", dt, shape, dev),
-                  _rows(w_gate, "w_gate", dt, (nf, nk), dev), _rows(w_up, "w_up", dt, (nf, nk), dev))
-    if h is not None:
-        d.ld_h = _rows(h, "h", dt, out, dev)
+    px, ldx = _spaced(("x",), dt, x.shape, dev, x)
+    pg, ldg, pu, ldu = _spaced(("w_gate", "w_up"), dt, (nf, nk), dev, w_gate, w_up)
+    ph, ldh = _spaced(("h",), dt, out, dev, h)
     if (gate is None) != (up is None):
         raise ValueError("gate and up go together")
-    if gate is not None:
-        d.ld_gate = _rows(gate, "gate", torch.float32, out, dev)
-        d.ld_up = _rows(up, "up", torch.float32, out, dev)
+    qg, lqg, qu, lqu = _spaced(("gate", "up"), torch.float32, out, dev, gate, up)
     _gpu(dev)
     if h is None:
-        h = x.new_empty(out)
+        h = torch.empty(out, dtype=dt, device=x.device)
+        ph = h.data_ptr()
     if gate is None and want_pre:
-        gate, up = (x.new_empty(out, dtype=torch.float32) for _ in range(2))
-    _launch(dev, lib.m3_gated_ffn, ctypes.byref(d), code, _at(x), _at(w_gate), _at(w_up), _at(h),
-            _at(gate), _at(up))
+        gate, up = (torch.empty(out, dtype=torch.float32, device=x.device) for _ in range(2))
+        qg, qu = gate.data_ptr(), up.data_ptr()
+    d = M3FfnDims(rows, nk, nf, ldx, ldg, ldu, ldh, lqg, lqu)
+    _launch(dev, _lib.m3_gated_ffn, ctypes.byref(d), code, px, pg, pu, ph, qg, qu)
     return h, gate, up
 
 
@@ -1254,40 +1279,35 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, dx=None, dw_gate=None, 
     ones.  Returns a dict: x (absent without want_x), w_gate and w_up (absent
     without want_weights) in the inputs' type."""
     import torch
-    lib = _lib or load_library()
+    _tensors or _look()
     shape, dev, dt = x.shape, x.get_device(), x.dtype
-    if len(shape) < 1 or w_gate.dim() != 2:
-        raise ValueError("expected x [..., K] and w_gate [F, K], got %s and %s"
-                         % (tuple(shape), tuple(w_gate.shape)))
+    rows, nk, nf, out = _ffn_shapes(x, w_gate)
     code = _type_code(dt)
-    nk, nf = shape[-1], w_gate.shape[0]
-    rows, out = math.prod(shape[:-1]), shape[:-1] + (nf,)
     if (dw_gate is None) != (dw_up is None):
         raise ValueError("dw_gate and dw_up go together")
     if (dx is not None and not want_x) or (dw_gate is not None and not want_weights):
         raise ValueError("a gradient that is given is wanted")
-    d = M3FfnDims(rows, nk, nf, _rows(x, "x", dt, shape, dev),
-                  _rows(w_gate, "w_gate", dt, (nf, nk), dev), _rows(w_up, "w_up", dt, (nf, nk), dev),
-                  0, _rows(gate, "gate", torch.float32, out, dev), _rows(up, "up", torch.float32, out, dev),
-                  _rows(dh, "dh", dt, out, dev))
-    if dx is not None:
-        d.ld_dx = _rows(dx, "dx", dt, shape, dev)
-    if dw_gate is not None:
-        d.ld_dwgate = _rows(dw_gate, "dw_gate", dt, (nf, nk), dev)
-        d.ld_dwup = _rows(dw_up, "dw_up", dt, (nf, nk), dev)
+    px, ldx, pdx, lddx = _spaced(("x", "dx"), dt, shape, dev, x, dx)
+    pg, ldg, pu, ldu, pdg, lddg, pdu, lddu = _spaced(("w_gate", "w_up", "dw_gate", "dw_up"), dt, (nf, nk), dev,
+                                                     w_gate, w_up, dw_gate, dw_up)
+    qg, lqg, qu, lqu = _spaced(("gate", "up"), torch.float32, out, dev, gate, up)
+    pdh, lddh = _spaced(("dh",), dt, out, dev, dh)
     _gpu(dev)
     if dx is None and want_x:
-        dx = x.new_empty(shape)
+        dx = torch.empty(shape, dtype=dt, device=x.device)
+        pdx = dx.data_ptr()
     if dw_gate is None and want_weights:
-        dw_gate, dw_up = x.new_empty((nf, nk)), x.new_empty((nf, nk))
-    need = int(lib.m3_gated_ffn_backward_workspace_size(ctypes.byref(d), code))
+        dw_gate, dw_up = (torch.empty((nf, nk), dtype=dt, device=x.device) for _ in range(2))
+        pdg, pdu = dw_gate.data_ptr(), dw_up.data_ptr()
+    d = M3FfnDims(rows, nk, nf, ldx, ldg, ldu, 0, lqg, lqu, lddh, lddx, lddg, lddu)
+    need = _lib.m3_gated_ffn_backward_workspace_size(ctypes.byref(d), code)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and on the first tensor's device")
-    _launch(dev, lib.m3_gated_ffn_backward, ctypes.byref(d), code, _at(dh), _at(x), _at(w_gate),
-            _at(w_up), _at(gate), _at(up), _at(dx), _at(dw_gate), _at(dw_up), _at(workspace),
-            0 if workspace is None else workspace.nbytes)
+    pw, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _launch(dev, _lib.m3_gated_ffn_backward, ctypes.byref(d), code, pdh, px, pg, pu, qg, qu, pdx, pdg, pdu,
+            pw, ws_bytes)
     res = {}
     if dx is not None:
         res["x"] = dx

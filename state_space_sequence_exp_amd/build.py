@@ -3,7 +3,8 @@
     python -m state_space_sequence_exp_amd.build
 
 compiles every ``csrc/*.hip`` with hipcc for gfx950 (in parallel) and links
-``state_space_sequence_exp_amd/libm3ssm.so``.  Packed-fp32 VALU instructions
+``state_space_sequence_exp_amd/libm3ssm.so``, and builds ``_tensors.so`` beside
+it, through which the binding looks at a call's tensors.  Packed-fp32 VALU instructions
 are disabled for all device code; a few prefill sources take a measured
 instruction-scheduling strategy (SCHED).
 """
@@ -96,7 +97,34 @@ def build(verbose: bool = False, jobs: int = 8, extra_flags=(), out: str = LIB_P
         os.replace(out_tmp, out)
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
+    if out == LIB_PATH:
+        build_tensors()
     return out
+
+
+TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
+TENSORS_PATH = os.path.join(PKG, "_tensors.so")
+
+
+def build_tensors() -> str:
+    """The binding's look at a call's tensors (_tensors.so: host code only,
+    against the headers and libraries of the torch that is installed)."""
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    out_tmp = TENSORS_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], TENSORS_SRC, "-o", out_tmp,
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (TENSORS_SRC, r.stdout, r.stderr))
+    os.replace(out_tmp, TENSORS_PATH)
+    return TENSORS_PATH
 
 
 PROBE_SRC = os.path.join(CSRC, "probe", "copy_probe.hip")

@@ -6,9 +6,10 @@
 // y written once, a token moves its W - 1 kept inputs both ways.
 //
 // A thread owns one vector of 16 bytes of channels over a run of tokens, kept in
-// registers as a window that slides: only the W - 1 inputs before its run are
-// read twice, from the caches.  Runs are 8 tokens times as many as leave the chip
-// full of threads.
+// registers as a window that slides by four tokens (by eight it takes more registers
+// and leaves fewer waves: 35 us instead of 32 for B4 T2048 D4096 bfloat16, 4.1 TB/s):
+// only the W - 1 inputs before its run are read twice, from the caches.  Runs are
+// four such windows, fewer where that leaves the chip short of threads.
 #include "gate.h"
 #include "layer_internal.h"
 #include "slots.h"
@@ -17,7 +18,7 @@
 namespace m3 {
 namespace {
 
-constexpr int kThreads = 256, kRun = 8;
+constexpr int kThreads = 256, kRun = 4;
 
 template <int V, int W>
 struct Taps {
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a, int til
 
 int vectors(int64_t D, int esize) { return (int)((D * esize + 15) / 16); }
 
-// Tokens a thread takes: four runs of 8, fewer where that would leave less than
-// 2^17 threads (two waves a SIMD).
+// Tokens a thread takes: four windows, fewer where that would leave less than 2^17
+// threads (two waves a SIMD).
 int run_tokens(int64_t B, int64_t T, int64_t D, int esize) {
   int run = 4 * kRun;
   while (run > kRun && (double)B * (double)((T + run - 1) / run) * vectors(D, esize) < 131072.0) run /= 2;

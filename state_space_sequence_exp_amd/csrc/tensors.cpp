@@ -1,0 +1,135 @@
+// tensors.cpp -- what a call of the short operators asks of its tensors, asked in
+// one go: a Python module of two functions.  A tensor's type, shape, device, strides
+// and address cost about a microsecond from Python; a single-token call has a dozen
+// tensors and runs for five.
+//
+//   dense(dtype, shape, device index, t, ...) -> (address, ...)
+//   rows(dtype, shape, device index, t, ...)  -> (address, distance, ...)
+//
+// Every t is a tensor of this type, shape and device, contiguous (dense), or with a
+// contiguous last axis and its rows at one distance (rows: 0 for a contiguous one,
+// else elements from one row to the next), or None (address 0).  None is returned
+// where one is not: the caller then finds out which, and says so.
+#include <Python.h>
+
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+
+namespace {
+
+constexpr int kMaxDims = 8;
+
+struct Wanted {
+  at::ScalarType type;
+  int64_t sizes[kMaxDims];
+  Py_ssize_t dims;
+  long device;
+};
+
+// The first three arguments.
+bool wanted(PyObject* const* args, Py_ssize_t n, Wanted& w) {
+  if (n < 3 || !THPDtype_Check(args[0]) || !PyTuple_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "expected (dtype, shape, device index, tensors...)");
+    return false;
+  }
+  w.type = reinterpret_cast<THPDtype*>(args[0])->scalar_type;
+  w.dims = PyTuple_GET_SIZE(args[1]);
+  if (w.dims > kMaxDims) return true;  // (no tensor is found to have it)
+  for (Py_ssize_t i = 0; i < w.dims; ++i) {
+    w.sizes[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], i));
+    if (w.sizes[i] == -1 && PyErr_Occurred()) return false;
+  }
+  w.device = PyLong_AsLong(args[2]);
+  return !(w.device == -1 && PyErr_Occurred());
+}
+
+bool matches(const at::Tensor& t, const Wanted& w) {
+  if (t.scalar_type() != w.type || t.dim() != w.dims || w.dims > kMaxDims || t.layout() != at::kStrided) return false;
+  const at::IntArrayRef sizes = t.sizes();
+  for (Py_ssize_t i = 0; i < w.dims; ++i)
+    if (sizes[i] != w.sizes[i]) return false;
+  return (t.is_cuda() ? (long)t.get_device() : -1) == w.device;
+}
+
+// Elements from one row to the next (0: contiguous), or -1.
+int64_t distance(const at::Tensor& t) {
+  if (t.is_contiguous()) return 0;
+  const at::IntArrayRef sizes = t.sizes(), strides = t.strides();
+  const int64_t last = t.dim() - 1, row = last < 0 ? 1 : sizes[last];
+  if (row > 1 && strides[last] != 1) return -1;
+  int64_t ld = 0, step = 0;
+  for (int64_t i = last - 1; i >= 0; --i) {
+    if (sizes[i] == 1) continue;
+    if (ld == 0) ld = step = strides[i];
+    if (strides[i] != step || strides[i] < row) return -1;
+    step *= sizes[i];
+  }
+  return ld;
+}
+
+template <bool kRows>
+PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Wanted w;
+  if (!wanted(args, n, w)) return nullptr;
+  constexpr int kEach = kRows ? 2 : 1;
+  PyObject* out = PyTuple_New((n - 3) * kEach);
+  if (!out) return nullptr;
+  for (Py_ssize_t i = 3; i < n; ++i) {
+    int64_t ld = 0;
+    uintptr_t at = 0;
+    if (args[i] != Py_None) {
+      bool good = THPVariable_Check(args[i]);
+      if (good) {
+        const at::Tensor& t = THPVariable_Unpack(args[i]);
+        good = matches(t, w);
+        if (good && kRows) good = (ld = distance(t)) >= 0;
+        if (good && !kRows) good = t.is_contiguous();
+        if (good) at = reinterpret_cast<uintptr_t>(t.data_ptr());
+      }
+      if (!good) {
+        Py_DECREF(out);
+        Py_RETURN_NONE;
+      }
+    }
+    PyObject* address = PyLong_FromUnsignedLongLong(at);
+    if (!address) {
+      Py_DECREF(out);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(out, (i - 3) * kEach, address);
+    if (kRows) {
+      PyObject* between = PyLong_FromLongLong(ld);
+      if (!between) {
+        Py_DECREF(out);
+        return nullptr;
+      }
+      PyTuple_SET_ITEM(out, (i - 3) * kEach + 1, between);
+    }
+  }
+  return out;
+}
+
+// (no C++ exception reaches Python's frames: torch's own become its errors)
+template <bool kRows>
+PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  try {
+    return check<kRows>(self, args, n);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+PyMethodDef methods[] = {
+    {"dense", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<false>)), METH_FASTCALL,
+     "Addresses of contiguous tensors of one type, shape and device; None where one is not."},
+    {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<true>)), METH_FASTCALL,
+     "Addresses and row distances of tensors of one type, shape and device; None where one is not."},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensors() { return PyModule_Create(&module); }
