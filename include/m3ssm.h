@@ -727,9 +727,10 @@ m3_status m3_selective_scan_step(const m3_select_dims* dims, m3_dtype dtype, flo
  * (both or neither NULL) receive g and u for the backward pass.
  *
  * Row r of an array is at r ld.  Pointers need element alignment; the products
- * run fastest where every row of x and of the weights starts at a multiple of 16
- * bytes and K is a multiple of 16 bytes.  Outputs must not overlap an input or
- * each other.  rows, K and F at most 2^31 - 1, ld at most 2^24 - 1.
+ * run fastest where every row of x and of the weights starts at a multiple of 4
+ * bytes (float rows always do).  Outputs must not overlap an input or each other.
+ * K, F and every ld are at most 2^22 - 1 (backward: F at most 2^21 - 64, rows at
+ * most 2^22 - 64).
  */
 typedef struct {
   int64_t rows;     /* (>= 0) */

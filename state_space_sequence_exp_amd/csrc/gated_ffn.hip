@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(WM* WN* kWave) __attribute__((amdgpu_waves_per
 gemm_kernel(GemmArgs<T> g) {
   constexpr int NT = WM * WN * kWave, BM = WM * FM * 16, BN = WN * FN * 16, E = 16 / (int)sizeof(T);
   constexpr int BK = kRowBytes / (int)sizeof(T), kPass = NT / kChunks;  // rows a pass loads
-  constexpr int NA = BM / kPass, NB = BN / kPass;
-  __shared__ u32x4 s_tile[2][(BM + BN) * kChunks];
+  constexpr int NA = BM / kPass, NB = BN / kPass, kStages = kDirect && BM + BN <= 128 ? 4 : 2;
+  __shared__ u32x4 s_tile[kStages][(BM + BN) * kChunks];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, l4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
 
@@ -147,21 +147,23 @@ gemm_kernel(GemmArgs<T> g) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = mma_chunk(f.b[j], f.a[i], acc[i][j], T());
   };
-  u32x4 ra[NA], rb[NB];
-  const auto request = [&](int k0) {
+  struct Moved {  // through registers
+    u32x4 a[NA], b[NB];
+  };
+  const auto request = [&](Moved& r, int k0) {
     const int n = g.K - k0 - chunk * E;  // elements from this thread's chunk to the row's end
 #pragma unroll
-    for (int i = 0; i < NA; ++i) ra[i] = load_chunk<T>(baseA + k0 + offA[i], n);
+    for (int i = 0; i < NA; ++i) r.a[i] = load_chunk<T>(baseA + k0 + offA[i], n);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) rb[i] = load_chunk<T>(baseB(i) + k0 + offB[i], n);
+    for (int i = 0; i < NB; ++i) r.b[i] = load_chunk<T>(baseB(i) + k0 + offB[i], n);
   };
   const int put_at = chunk_at(row, chunk);  // (kPass is a multiple of 8)
-  const auto put = [&](int stage) {
+  const auto put = [&](const Moved& r, int stage) {
     u32x4* s = s_tile[stage] + put_at;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) s[i * kPass * kChunks] = ra[i];
+    for (int i = 0; i < NA; ++i) s[i * kPass * kChunks] = r.a[i];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) s[(BM + i * kPass) * kChunks] = rb[i];
+    for (int i = 0; i < NB; ++i) s[(BM + i * kPass) * kChunks] = r.b[i];
   };
 
   int done = 0;  // tiles multiplied
@@ -170,7 +172,7 @@ gemm_kernel(GemmArgs<T> g) {
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)&s_tile[0][0];
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds0 + wave * (kWave * 16));
     const auto bring = [&](int t) {
-      const uint32_t to = lds + (t & 1) * (uint32_t)sizeof s_tile[0];
+      const uint32_t to = lds + (t & (kStages - 1)) * (uint32_t)sizeof s_tile[0];
       const int k0 = min(t, whole - 1) * BK;  // (past the end: a tile again, into a stage that no one reads)
 #pragma unroll
       for (int i = 0; i < NA; ++i) load_to_lds(to + i * kPass * kRowBytes, baseA + k0, offA[i]);
@@ -179,7 +181,8 @@ gemm_kernel(GemmArgs<T> g) {
     };
     // the fragments' reads one by one between the products
     const auto order = [] {
-      constexpr int kReads = FM + FN, kEach = FM * FN * (sizeof(T) == 2 ? 1 : 4) / kReads;
+      constexpr int kReads = FM + FN, kProducts = FM * FN * (sizeof(T) == 2 ? 1 : 4);
+      constexpr int kEach = kProducts < kReads ? 1 : kProducts / kReads;
 #pragma unroll
       for (int i = 0; i < kReads; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -188,31 +191,32 @@ gemm_kernel(GemmArgs<T> g) {
       __builtin_amdgcn_sched_barrier(0);
     };
     if (whole > 0) {
-      bring(0);
-      bring(1);
-      wait_loads<NA + NB>();
+#pragma unroll
+      for (int t = 0; t < kStages; ++t) bring(t);
+      wait_loads<(kStages - 1) * (NA + NB)>();
       lds_barrier();
       Frags f0, f1;
       get(f0, 0, 0);
       for (; done < whole; ++done) {
         __builtin_amdgcn_sched_barrier(0);
-        get(f1, done & 1, 1);
+        get(f1, done & (kStages - 1), 1);
         multiply(f0);
         order();
-        wait_loads<0>();  // the next tile has come, and every wave has read this one
+        wait_loads<(kStages - 2) * (NA + NB)>();  // the next tile has come, and every wave has read this one
         lds_barrier();
-        bring(done + 2);
+        bring(done + kStages);
         __builtin_amdgcn_sched_barrier(0);
-        get(f0, (done & 1) ^ 1, 0);
+        get(f0, (done + 1) & (kStages - 1), 0);
         multiply(f1);
         order();
       }
       wait_loads<0>();
       lds_barrier();
     }
-    if (done * BK < g.K) {
-      request(done * BK);
-      put(0);
+    if (kMode == kDual && done * BK < g.K) {  // (the workspace's rows are whole tiles)
+      Moved r;
+      request(r, done * BK);
+      put(r, 0);
       lds_barrier();
       Frags rest;
 #pragma unroll
@@ -222,11 +226,14 @@ gemm_kernel(GemmArgs<T> g) {
       }
     }
   } else {
-    request(0);
+    Moved next, later;
+    request(next, 0);
+    request(later, BK);
     for (int k0 = 0; k0 < g.K; k0 += BK, done ^= 1) {
-      put(done);
+      put(next, done);
       lds_barrier();
-      if (k0 + BK < g.K) request(k0 + BK);
+      next = later;
+      request(later, k0 + 2 * BK);
       Frags f;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -285,22 +292,40 @@ void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
   g.gridM = (g.M + BM - 1) / BM;
   g.gridN = (g.N + BN - 1) / BN;
   const dim3 grid((unsigned)g.gridM * g.gridN), block(WM * WN * kWave);
-  if (direct)
-    hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, true>), grid, block, 0, stream, g);
-  else
-    hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, false>), grid, block, 0, stream, g);
+  if constexpr (kMode == kDual && sizeof(T) == 2)  // (float rows, and the workspace's, are aligned)
+    if (!direct) {
+      hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, false>), grid, block, 0, stream, g);
+      return;
+    }
+  hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, true>), grid, block, 0, stream, g);
 }
-// The tile: the largest that still leaves about a tile a CU.
+// The tile: of those below, the one whose rounds over the 256 CUs take the least,
+// by its area and the share of the largest tile's rate that it reaches by itself.
 template <typename T, Mode kMode>
 void launch_gemm(const GemmArgs<T>& g, hipStream_t stream) {
-  const auto rows16 = [](const T* p, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+  const auto rows4 = [](const T* p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * (int64_t)sizeof(T) % 4 == 0;
   };
-  const bool direct = rows16(g.A, g.lda) && rows16(g.B, g.ldb) && (kMode != kDual || rows16(g.B2, g.ldb2));
-  const double cols = kMode == kDual ? 2.0 * g.N : g.N, area = (double)g.M * cols;
-  if (area >= 192.0 * 256 * 256) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
-  else if (area >= 192.0 * 128 * 128) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
-  else launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
+  const bool direct = rows4(g.A, g.lda) && rows4(g.B, g.ldb) && (kMode != kDual || rows4(g.B2, g.ldb2));
+  const struct {
+    int m, n;
+    double rate;
+  } tiles[] = {{256, 256, 1.0}, {128, 128, 0.8}, {64, 64, 0.5}, {32, 64, 0.4}};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rows = (g.M + tiles[i].m - 1) / tiles[i].m;
+    const int64_t cols = ((kMode == kDual ? 2 : 1) * (int64_t)g.N + tiles[i].n - 1) / tiles[i].n;
+    const double cost = (double)((rows * cols + 255) / 256) * tiles[i].m * tiles[i].n / tiles[i].rate;
+    if (i == 0 || cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  if (best == 0) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
+  else if (best == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
+  else if (best == 2) launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
+  else launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
 }
 
 // ---- few rows ------------------------------------------------------------------
@@ -382,7 +407,7 @@ constexpr int kSide = 64;  // of a transposed tile
 
 // Rows r0 .. of a tile that lies in the LDS transposed, [column][row], to dst
 // [columns, pitch]: 16 bytes a thread.
-template <typename T, int P>
+template <typename T, int P = kSide + 4 / (int)sizeof(T)>
 __device__ __forceinline__ void put_columns(const T (&s)[kSide][P], T* dst, int64_t pitch, int c0, int r0, int cols) {
   constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
   for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
@@ -397,13 +422,60 @@ __device__ __forceinline__ void put_columns(const T (&s)[kSide][P], T* dst, int6
   }
 }
 
-// [dg | du] (Fp columns each, zeros from F on) and its transpose (Mp columns, zeros
-// from M on); either may be null.
+// The transposed tiles are 64 x 64 of T in the LDS.
 template <typename T>
-__global__ void __launch_bounds__(256) slopes_kernel(FfnArgs a, T* both, T* turned, int Fp, int Mp) {
-  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E, P = kSide + 4 / (int)sizeof(T);
-  __shared__ T s_g[kSide][P], s_u[kSide][P];
-  const int across = Fp / kSide, f0 = blockIdx.x % across * kSide, m0 = blockIdx.x / across * kSide;
+struct Turned {
+  static constexpr int P = kSide + 4 / (int)sizeof(T);
+  T s[kSide][P];
+};
+
+// dst [C, pitch] = src [R, C] transposed, zeros from R to the next multiple of 64: one tile.
+template <typename T>
+__device__ __forceinline__ void turn_tile(Turned<T>& s, int tile, const T* src, int64_t ld, int R, int C, T* dst,
+                                          int64_t pitch) {
+  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
+  const int across = (C + kSide - 1) / kSide, c0 = tile % across * kSide, r0 = tile / across * kSide;
+  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
+    const int r = i / kAcross, c = i % kAcross * E;
+    const Raw<T, E> v = load_run<T, E>(src + (int64_t)(r0 + r) * ld + c0 + c, r0 + r < R ? C - c0 - c : 0);
+    T t[E];
+    __builtin_memcpy(t, v.w, 16);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s.s[c + e][r] = t[e];
+  }
+  __syncthreads();
+  put_columns<T>(s.s, dst, pitch, c0, r0, C);
+}
+
+// What the gradients' products read, in the workspace (null: not wanted).
+template <typename T>
+struct Operands {
+  T *both, *turned, *xT, *wT;   // [M, 2 Fp], [2 Fp, Mp], [K, Mp], [K, 2 Fp]
+  int Fp, Mp;
+  int slopes, weights, inputs;  // tiles of each part
+};
+
+// One launch for all of them: [dg | du] (Fp columns each, zeros from F on) and its
+// transpose (Mp columns, zeros from M on), then the transposes of the weights side by
+// side, then that of x.
+template <typename T>
+__global__ void __launch_bounds__(256) operands_kernel(FfnArgs a, Operands<T> o) {
+  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
+  __shared__ Turned<T> s_g, s_u;
+  const int Fp = o.Fp;
+  int tile = blockIdx.x;
+  if (tile >= o.slopes) {
+    tile -= o.slopes;
+    if (tile < o.weights) {
+      turn_tile<T>(s_g, tile, static_cast<const T*>(a.wg), a.ld_wg, a.F, a.K, o.wT, 2 * (int64_t)Fp);
+    } else if (tile < 2 * o.weights) {
+      turn_tile<T>(s_g, tile - o.weights, static_cast<const T*>(a.wu), a.ld_wu, a.F, a.K, o.wT + Fp, 2 * (int64_t)Fp);
+    } else {
+      turn_tile<T>(s_g, tile - 2 * o.weights, static_cast<const T*>(a.x), a.ld_x, a.M, a.K, o.xT, o.Mp);
+    }
+    return;
+  }
+  const int across = Fp / kSide, f0 = tile % across * kSide, m0 = tile / across * kSide;
   for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
     const int r = i / kAcross, c = i % kAcross * E, m = m0 + r, n = m < a.M ? a.F - f0 - c : 0;
     const Raw<T, E> dh = load_run<T, E>(static_cast<const T*>(a.dh) + (int64_t)m * a.ld_dh + f0 + c, n);
@@ -417,54 +489,30 @@ __global__ void __launch_bounds__(256) slopes_kernel(FfnArgs a, T* both, T* turn
       dg[e] = d * run_at(u, e) * (sg * __builtin_fmaf(gv, 1.f - sg, 1.f));
     }
     const Raw<T, E> rg = to_run<T, E>(dg), ru = to_run<T, E>(du);
-    if (both && m < a.M) {
-      T* p = both + (int64_t)m * 2 * Fp + f0 + c;
+    if (o.both && m < a.M) {
+      T* p = o.both + (int64_t)m * 2 * Fp + f0 + c;
       __builtin_memcpy(p, rg.w, 16);
       __builtin_memcpy(p + Fp, ru.w, 16);
     }
-    if (turned) {
+    if (o.turned) {
       T tg[E], tu[E];
       __builtin_memcpy(tg, rg.w, 16);
       __builtin_memcpy(tu, ru.w, 16);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        s_g[c + e][r] = tg[e];
-        s_u[c + e][r] = tu[e];
+        s_g.s[c + e][r] = tg[e];
+        s_u.s[c + e][r] = tu[e];
       }
     }
   }
-  if (!turned) return;
+  if (!o.turned) return;
   __syncthreads();
-  put_columns<T, P>(s_g, turned, Mp, f0, m0, Fp);
-  put_columns<T, P>(s_u, turned + (int64_t)Fp * Mp, Mp, f0, m0, Fp);
-}
-
-// dst [C, pitch] = src [R, C] transposed, zeros from R to the next multiple of 64.
-template <typename T>
-__global__ void __launch_bounds__(256) turn_kernel(const T* src, int64_t ld, int R, int C, T* dst, int64_t pitch) {
-  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E, P = kSide + 4 / (int)sizeof(T);
-  __shared__ T s[kSide][P];
-  const int across = (C + kSide - 1) / kSide, c0 = blockIdx.x % across * kSide, r0 = blockIdx.x / across * kSide;
-  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
-    const int r = i / kAcross, c = i % kAcross * E;
-    const Raw<T, E> v = load_run<T, E>(src + (int64_t)(r0 + r) * ld + c0 + c, r0 + r < R ? C - c0 - c : 0);
-    T t[E];
-    __builtin_memcpy(t, v.w, 16);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s[c + e][r] = t[e];
-  }
-  __syncthreads();
-  put_columns<T, P>(s, dst, pitch, c0, r0, C);
+  put_columns<T>(s_g.s, o.turned, o.Mp, f0, m0, Fp);
+  put_columns<T>(s_u.s, o.turned + (int64_t)Fp * o.Mp, o.Mp, f0, m0, Fp);
 }
 
 int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
 size_t area_bytes(int64_t n, int es) { return ((size_t)n * es + 255) / 256 * 256; }
-
-template <typename T>
-void launch_turn(const void* src, int64_t ld, int R, int C, T* dst, int64_t pitch, hipStream_t stream) {
-  hipLaunchKernelGGL((turn_kernel<T>), dim3((unsigned)(padded(C) / kSide * (padded(R) / kSide))), dim3(256), 0,
-                     stream, static_cast<const T*>(src), ld, R, C, dst, pitch);
-}
 
 template <typename T>
 hipError_t launch_ffn_t(const FfnArgs& a, hipStream_t stream) {
@@ -495,18 +543,33 @@ template <typename T>
 hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
   const int Fp = (int)padded(a.F), Mp = (int)padded(a.M), es = (int)sizeof(T);
   char* ws = static_cast<char*>(a.workspace);
-  T* both = reinterpret_cast<T*>(ws);                 // [M, 2 Fp]
-  ws += area_bytes((int64_t)a.M * 2 * Fp, es);
-  T* turned = reinterpret_cast<T*>(ws);               // [2 Fp, Mp]
-  ws += area_bytes((int64_t)Mp * 2 * Fp, es);
-  T* xT = reinterpret_cast<T*>(ws);                   // [K, Mp]
-  ws += area_bytes((int64_t)a.K * Mp, es);
-  T* wT = reinterpret_cast<T*>(ws);                   // [K, 2 Fp]
-  hipLaunchKernelGGL((slopes_kernel<T>), dim3((unsigned)(Fp / kSide * (Mp / kSide))), dim3(256), 0, stream, a,
-                     a.dx ? both : nullptr, a.dwg ? turned : nullptr, Fp, Mp);
+  const auto area = [&](int64_t n) {
+    T* p = reinterpret_cast<T*>(ws);
+    ws += area_bytes(n, es);
+    return p;
+  };
+  T* const both = area((int64_t)a.M * 2 * Fp);
+  T* const turned = area((int64_t)Mp * 2 * Fp);
+  T* const xT = area((int64_t)a.K * Mp);
+  T* const wT = area((int64_t)a.K * 2 * Fp);
+  const int kTiles = (int)(padded(a.K) / kSide);
+  Operands<T> o = {};
+  o.Fp = Fp;
+  o.Mp = Mp;
+  o.slopes = Fp / kSide * (Mp / kSide);
   if (a.dx) {
-    launch_turn<T>(a.wg, a.ld_wg, a.F, a.K, wT, 2 * Fp, stream);
-    launch_turn<T>(a.wu, a.ld_wu, a.F, a.K, wT + Fp, 2 * Fp, stream);
+    o.both = both;
+    o.wT = wT;
+    o.weights = kTiles * (Fp / kSide);
+  }
+  if (a.dwg) {
+    o.turned = turned;
+    o.xT = xT;
+    o.inputs = kTiles * (Mp / kSide);
+  }
+  hipLaunchKernelGGL((operands_kernel<T>), dim3((unsigned)(o.slopes + 2 * o.weights + o.inputs)), dim3(256), 0,
+                     stream, a, o);
+  if (a.dx) {
     GemmArgs<T> g = {};
     g.M = a.M;
     g.N = a.K;
@@ -519,7 +582,6 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
     launch_gemm<T, kPlain>(g, stream);
   }
   if (a.dwg) {
-    launch_turn<T>(a.x, a.ld_x, a.M, a.K, xT, Mp, stream);
     GemmArgs<T> g = {};
     g.M = 2 * Fp;
     g.N = a.K;
