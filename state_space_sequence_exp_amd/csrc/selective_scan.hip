@@ -248,22 +248,36 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
     bias[e] = a.dt_bias && e < nc ? a.dt_bias[d0 + c0 + e] : 0.f;
     skip[e] = a.skip && e < nc ? a.skip[d0 + c0 + e] : 0.f;
   }
-  const auto request = [&](int q) {
+  // (addresses are walked, a tile at a time: a 64-bit product takes a wave as long as
+  // sixteen of its other operations)
+  const int64_t row0 = bq * a.T + t0 + tk;
+  const T* px = static_cast<const T*>(a.x) + row0 * a.ld_x + d0 + c0;
+  const T* pdt = static_cast<const T*>(a.dt) + row0 * a.ld_dt + d0 + c0;
+  const T* pz = a.z ? static_cast<const T*>(a.z) + row0 * a.ld_z + d0 + c0 : px;
+  const T* pb = static_cast<const T*>(a.Bt) + row0 * a.ld_b + part * NL * 4;
+  const T* pc = static_cast<const T*>(a.Ct) + row0 * a.ld_c + part * NL * 4;
+  T* py = static_cast<T*>(a.y) + row0 * a.ld_y + d0 + c0;
+  int64_t toGo = tEnd - t0 - tk;  // tokens from this thread's next on
+  const auto request = [&] {
     Piece<T, NL, kLocal> p = {};
-    const int64_t t = t0 + (int64_t)q * kTile + tk;
-    if (t < tEnd) {
-      const int64_t row = bq * a.T + t;
-      p.x = load_run<T, 4>(static_cast<const T*>(a.x) + row * a.ld_x + d0 + c0, nc);
-      p.dt = load_run<T, 4>(static_cast<const T*>(a.dt) + row * a.ld_dt + d0 + c0, nc);
+    if (toGo > 0) {
+      p.x = load_run<T, 4>(px, nc);
+      p.dt = load_run<T, 4>(pdt, nc);
       if constexpr (!kLocal)
-        if (a.z) p.z = load_run<T, 4>(static_cast<const T*>(a.z) + row * a.ld_z + d0 + c0, nc);
+        if (a.z) p.z = load_run<T, 4>(pz, nc);
 #pragma unroll
       for (int v = 0; v < NL; ++v) {
         const int n = (part * NL + v) * 4;
-        p.b[v] = load_run<T, 4>(static_cast<const T*>(a.Bt) + row * a.ld_b + n, N - n);
-        if constexpr (!kLocal) p.c[v] = load_run<T, 4>(static_cast<const T*>(a.Ct) + row * a.ld_c + n, N - n);
+        p.b[v] = load_run<T, 4>(pb + 4 * v, N - n);
+        if constexpr (!kLocal) p.c[v] = load_run<T, 4>(pc + 4 * v, N - n);
       }
     }
+    px += kTile * a.ld_x;
+    pdt += kTile * a.ld_dt;
+    pz += kTile * a.ld_z;
+    pb += kTile * a.ld_b;
+    pc += kTile * a.ld_c;
+    toGo -= kTile;
     return p;
   };
   const auto put = [&](int q, const Piece<T, NL, kLocal>& p) {
@@ -288,8 +302,9 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
     Raw<T, 4> x, z;
   };
   const auto finish = [&](int q, const Held& v) {
-    const int64_t t = t0 + (int64_t)q * kTile + tk;
-    if (t >= tEnd) return;
+    T* const to = py;
+    py += kTile * a.ld_y;
+    if (t0 + (int64_t)q * kTile + tk >= tEnd) return;
     const float4 sum = *reinterpret_cast<const float4*>(&s_stage[q & 1].y[kLocal ? 0 : tk][c0]);
     float y[4];
 #pragma unroll
@@ -300,17 +315,17 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
         y[e] = y[e] * (g * sigmoid_of(g));
       }
     }
-    store_run<T, 4>(static_cast<T*>(a.y) + (bq * a.T + t) * a.ld_y + d0 + c0, nc, to_run<T, 4>(y));
+    store_run<T, 4>(to, nc, to_run<T, 4>(y));
   };
 
   // (two tiles' loads are in flight; the outputs are stored last, so that no wait
   // for loads is one for the stores too)
   Held before = {}, now = {};
-  Piece<T, NL, kLocal> next = request(0), later = request(1);
+  Piece<T, NL, kLocal> next = request(), later = request();
   if (nTiles > 0) put(0, next);
   now = Held{next.x, next.z};
   next = later;
-  later = request(2);
+  later = request();
   lds_barrier();
   for (int q = 0; q < nTiles; ++q) {
     const Held last = before;
@@ -318,7 +333,7 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
     now = Held{next.x, next.z};
     if (q + 1 < nTiles) put(q + 1, next);
     next = later;
-    later = request(q + 3);
+    later = request();
     if constexpr (!kLocal)
       if (q > 0) finish(q - 1, last);
     lds_barrier();
