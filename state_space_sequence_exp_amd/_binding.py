@@ -995,8 +995,8 @@ _tensors = None
 
 
 def _look():
-    """The module that looks at a call's tensors (see csrc/tensors.cpp); _dense and
-    _spaced say what it found wrong."""
+    """The module that looks at a call's tensors and makes the new ones (see
+    csrc/tensors.cpp); _dense and _spaced say what it found wrong."""
     global _tensors
     if _tensors is None:
         load_library()
@@ -1064,10 +1064,10 @@ def causal_conv(x, weight, bias=None, *, silu: bool = False, state=None, lengths
     pl, = _dense(("lengths",), torch.int32, (nb,), dev, lengths)
     _gpu(dev)
     if y is None:
-        y = _like(x, ldx == 0)
+        y = _tensors.empty(dt, shape, x)
         py = y.data_ptr()
     if state_out is None and want_state:
-        state_out = torch.empty((nb, nw - 1, nd), dtype=dt, device=x.device)
+        state_out = _tensors.empty(dt, (nb, nw - 1, nd), x)
         pk = state_out.data_ptr()
     d = M3ConvDims(nb, nt, nd, nw, ldx, ldy)
     _launch(dev, _lib.m3_causal_conv, ctypes.byref(d), code, px, pw, pb, 1 if silu else 0, ps, pl, py, pk)
@@ -1101,7 +1101,7 @@ def causal_conv_step(state, x, weight, bias=None, *, silu: bool = False, slots=N
     pi = _pool_slots(slots, nb, ns, dev)
     _gpu(dev)
     if y is None:
-        y = _step_output(x, ldx, slots)
+        y = _step_output(x, slots)
         py = y.data_ptr()
     d = M3ConvDims(nb, 1, nd, nw, ldx, ldy)
     _launch(dev, _lib.m3_causal_conv_step, ctypes.byref(d), code, ps, pi, ns, px, pw, pb,
@@ -1118,11 +1118,11 @@ def _pool_slots(slots, nb, n_slots, dev):
     return _dense(("slots",), torch.int32, (nb,), dev, slots)[0]
 
 
-def _step_output(x, ld, slots):
+def _step_output(x, slots):
     """A single-token call's new y: zeros where rows may be idle."""
     import torch
     if slots is None:
-        return _like(x, ld == 0)
+        return _tensors.empty(x.dtype, x.shape, x)
     return torch.zeros(x.shape, dtype=x.dtype, device=x.device)
 
 
@@ -1166,17 +1166,17 @@ def selective_scan(x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, softplus:
     pl, = _dense(("lengths",), torch.int32, (nb,), dev, lengths)
     _gpu(dev)
     if y is None:
-        y = _like(x, ldx == 0)
+        y = _tensors.empty(dtype, shape, x)
         py = y.data_ptr()
     if h_last is None:
-        h_last = torch.empty((nb, nd, nn), dtype=torch.float32, device=x.device)
+        h_last = _tensors.empty(torch.float32, (nb, nd, nn), x)
         ph = h_last.data_ptr()
     d = M3SelectDims(nb, nt, nd, nn, ldx, ldt, ldz, ldy, ldb, ldc)
     need = _lib.m3_selective_scan_workspace_size(ctypes.byref(d), code)
     pw = ws_bytes = 0
     if need:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _tensors.empty(torch.uint8, (need,), x)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous and on the first tensor's device")
         pw, ws_bytes = workspace.data_ptr(), workspace.nbytes
@@ -1212,7 +1212,7 @@ def selective_scan_step(h, x, dt, A, B, C, skip=None, z=None, *, dt_bias=None, s
     pi = _pool_slots(slots, nb, ns, dev)
     _gpu(dev)
     if y is None:
-        y = _step_output(x, ldx, slots)
+        y = _step_output(x, slots)
         py = y.data_ptr()
     d = M3SelectDims(nb, 1, nd, nn, ldx, ldt, ldz, ldy, ldb, ldc)
     _launch(dev, _lib.m3_selective_scan_step, ctypes.byref(d), code, ph, pi, ns, px, pt, pA, pB, pC,
@@ -1253,10 +1253,10 @@ def gated_ffn(x, w_gate, w_up, *, want_pre: bool = False, h=None, gate=None, up=
     qg, lqg, qu, lqu = _spaced(("gate", "up"), torch.float32, out, dev, gate, up)
     _gpu(dev)
     if h is None:
-        h = torch.empty(out, dtype=dt, device=x.device)
+        h = _tensors.empty(dt, out, x)
         ph = h.data_ptr()
     if gate is None and want_pre:
-        gate, up = (torch.empty(out, dtype=torch.float32, device=x.device) for _ in range(2))
+        gate, up = _tensors.empty(torch.float32, out, x), _tensors.empty(torch.float32, out, x)
         qg, qu = gate.data_ptr(), up.data_ptr()
     d = M3FfnDims(rows, nk, nf, ldx, ldg, ldu, ldh, lqg, lqu)
     _launch(dev, _lib.m3_gated_ffn, ctypes.byref(d), code, px, pg, pu, ph, qg, qu)
@@ -1294,15 +1294,15 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, dx=None, dw_gate=None, 
     pdh, lddh = _spaced(("dh",), dt, out, dev, dh)
     _gpu(dev)
     if dx is None and want_x:
-        dx = torch.empty(shape, dtype=dt, device=x.device)
+        dx = _tensors.empty(dt, shape, x)
         pdx = dx.data_ptr()
     if dw_gate is None and want_weights:
-        dw_gate, dw_up = (torch.empty((nf, nk), dtype=dt, device=x.device) for _ in range(2))
+        dw_gate, dw_up = _tensors.empty(dt, (nf, nk), x), _tensors.empty(dt, (nf, nk), x)
         pdg, pdu = dw_gate.data_ptr(), dw_up.data_ptr()
     d = M3FfnDims(rows, nk, nf, ldx, ldg, ldu, 0, lqg, lqu, lddh, lddx, lddg, lddu)
     need = _lib.m3_gated_ffn_backward_workspace_size(ctypes.byref(d), code)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _tensors.empty(torch.uint8, (need,), x)
     elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and on the first tensor's device")
     pw, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)

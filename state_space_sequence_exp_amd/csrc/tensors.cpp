@@ -1,5 +1,5 @@
 // tensors.cpp -- what a call of the short operators asks of its tensors, asked in
-// one go: a Python module of two functions.  A tensor's type, shape, device, strides
+// one go, and the new ones it returns: a Python module of three functions.  A tensor's type, shape, device, strides
 // and address cost about a microsecond from Python; a single-token call has a dozen
 // tensors and runs for five.
 //
@@ -10,8 +10,11 @@
 // contiguous last axis and its rows at one distance (rows: 0 for a contiguous one,
 // else elements from one row to the next), or None (address 0).  None is returned
 // where one is not: the caller then finds out which, and says so.
+//
+//   empty(dtype, shape, t) -> a new tensor on t's device
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -111,6 +114,28 @@ PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out;
 }
 
+PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    if (n != 3 || !THPDtype_Check(args[0]) || !PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) > kMaxDims ||
+        !THPVariable_Check(args[2])) {
+      PyErr_SetString(PyExc_TypeError, "expected (dtype, shape of up to 8 dimensions, tensor)");
+      return nullptr;
+    }
+    int64_t sizes[kMaxDims];
+    const Py_ssize_t dims = PyTuple_GET_SIZE(args[1]);
+    for (Py_ssize_t i = 0; i < dims; ++i) {
+      sizes[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], i));
+      if (sizes[i] == -1 && PyErr_Occurred()) return nullptr;
+    }
+    const auto like = THPVariable_Unpack(args[2]).options();
+    return THPVariable_Wrap(at::empty(at::IntArrayRef(sizes, dims),
+                                      like.dtype(reinterpret_cast<THPDtype*>(args[0])->scalar_type).requires_grad(false)));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 // (no C++ exception reaches Python's frames: torch's own become its errors)
 template <bool kRows>
 PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -127,6 +152,8 @@ PyMethodDef methods[] = {
      "Addresses of contiguous tensors of one type, shape and device; None where one is not."},
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<true>)), METH_FASTCALL,
      "Addresses and row distances of tensors of one type, shape and device; None where one is not."},
+    {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&empty)), METH_FASTCALL,
+     "A new tensor of this type and shape on a tensor's device."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
