@@ -261,8 +261,8 @@ gemm_kernel(GemmArgs<T> g) {
         }
         store_run<T, 4>(g.C + (int64_t)m * g.ldc + n, left, to_run<T, 4>(hv));
         if (g.gate) {
-          store_run<float, 4>(g.gate + (int64_t)m * g.ld_gate + n, left, to_run<float, 4>(gv));
-          store_run<float, 4>(g.up + (int64_t)m * g.ld_up + n, left, to_run<float, 4>(uv));
+          store_for_later(g.gate + (int64_t)m * g.ld_gate + n, left, gv);
+          store_for_later(g.up + (int64_t)m * g.ld_up + n, left, uv);
         }
       }
     } else {
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(kFewWaves * kWave) few_kernel(GemmArgs<T> g) {
   }
   store_run<T, 4>(g.C + (int64_t)m * g.ldc + n, left, to_run<T, 4>(hs));
   if (g.gate) {
-    store_run<float, 4>(g.gate + (int64_t)m * g.ld_gate + n, left, to_run<float, 4>(gs));
-    store_run<float, 4>(g.up + (int64_t)m * g.ld_up + n, left, to_run<float, 4>(us));
+    store_for_later(g.gate + (int64_t)m * g.ld_gate + n, left, gs);
+    store_for_later(g.up + (int64_t)m * g.ld_up + n, left, us);
   }
 }
 

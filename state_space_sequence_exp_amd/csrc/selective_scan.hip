@@ -351,15 +351,6 @@ select_kernel(SelectArgs a, int tiles, int segs, int64_t segLen, float* ends, fl
 // its own are searched for its slot.
 constexpr int kSteps = 2;
 
-// (a state is next read a whole pass of the model later: it need not stay cached)
-__device__ __forceinline__ void store_state(float* p, int n, const float (&h)[4]) {
-  typedef f32x4 unaligned __attribute__((aligned(4)));
-  if (n >= 4)
-    __builtin_nontemporal_store(f32x4{h[0], h[1], h[2], h[3]}, reinterpret_cast<unaligned*>(p));
-  else
-    store_run<float, 4>(p, n, to_run<float, 4>(h));
-}
-
 template <typename T, int LQ>
 __global__ void __launch_bounds__(kThreads) select_step_kernel(SelectArgs a, int tiles) {
   constexpr int kAcross = kThreads / LQ;  // channels side by side
@@ -401,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) select_step_kernel(SelectArgs a, int
     if constexpr (LQ > 4) y += swap_lanes<0x141>(y);
     if constexpr (LQ > 8) y += swap_lanes<0x140>(y);
     if (d >= a.D) continue;
-    store_state(a.h_last + ((int64_t)slot * a.D + d) * N + n0, N - n0, h);
+    store_for_later(a.h_last + ((int64_t)slot * a.D + d) * N + n0, N - n0, h);
     y = __builtin_fmaf(skip[s], x[s], y);
     if (a.z) y = y * (z[s] * sigmoid_of(z[s]));
     if (q == 0) static_cast<T*>(a.y)[b * a.ld_y + d] = from_f32<T>(y);

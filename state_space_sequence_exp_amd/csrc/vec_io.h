@@ -84,4 +84,14 @@ __device__ __forceinline__ Raw<T, V> to_run(const float (&v)[V]) {
   return r;
 }
 
+// The first n of four floats that are next read much later: they need not stay in the
+// caches.
+__device__ __forceinline__ void store_for_later(float* p, int n, const float (&v)[4]) {
+  typedef f32x4 unaligned __attribute__((aligned(4)));
+  if (n >= 4)
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<unaligned*>(p));
+  else
+    store_run<float, 4>(p, n, to_run<float, 4>(v));
+}
+
 }  // namespace m3

@@ -56,6 +56,31 @@ def test_ffn_larger_tiles(dtype, M, K, F):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F", [(4090, 72, 4090), (4090, 71, 4090), (4090, 4090, 70), (70, 4090, 2040)])
+def test_ffn_largest_tiles(dtype, M, K, F):
+    """Sizes at which each of the three products fills the chip with its largest tiles,
+    by rows and units picked from all over the outputs: a row of dx needs every unit,
+    a unit's weights every row."""
+    import state_space_sequence_exp_amd as m3
+    r, t = inputs([9, M, K, F], M, K, F, dtype)
+    h, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True)
+    d = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u)
+    rng = np.random.default_rng(2)
+    pick = lambda n: np.unique(np.concatenate([rng.integers(0, n, 20), [0, n - 1]]))
+    rows, units = pick(M), pick(F)
+    half = HALF_STEP[dtype] if dtype == "bf16" else 0.0
+    o = O.gated_ffn(r["x"][rows], r["wg"][units], r["wu"][units])
+    at = np.ix_(rows, units)
+    for got, k, kind in ((h, "h", dtype), (g, "g", "f32"), (u, "u", "f32")):
+        close(torch.from_numpy(from_gpu(got)[at]), o[k], o["e_" + k], kind, k)
+    w = O.gated_ffn_backward(r["dh"][rows], r["x"][rows], r["wg"], r["wu"], half)
+    close(d["x"][rows], w["dx"], w["e_dx"], dtype, "dx")
+    w = O.gated_ffn_backward(r["dh"][:, units], r["x"], r["wg"][units], r["wu"][units], half)
+    for k in ("w_gate", "w_up"):
+        close(d[k][units], w["d" + k], w["e_d" + k], dtype, "d" + k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M", [5, 90])
 def test_ffn_strided(dtype, M):
     """Slices of wider rows, at odd elements, give the same bits; what lies beside
