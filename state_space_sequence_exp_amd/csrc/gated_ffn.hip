@@ -37,6 +37,8 @@ struct GemmArgs {
   T* C2;                       // split: where A's rows from `split` on go; each half has `rows` rows
   int64_t ldc2;
   int split, rows;
+  int parts, each;             // plain: k is cut into `parts` of `each`, and where they are more than
+  float* part;                 // one their sums go to part [parts, M, N]
   int gridM, gridN;
 };
 enum Mode { kDual, kPlain, kSplit };
@@ -96,8 +98,16 @@ gemm_kernel(GemmArgs<T> g) {
 
   // Neighbouring tiles on one XCD; eight rows of tiles side by side, so that a
   // chip's worth of tiles shares few rows of both operands.
-  const int groups = g.gridM * g.gridN, x = blockIdx.x & 7, q = groups >> 3, rest = groups & 7;
-  const int at = x * q + min(x, rest) + (int)(blockIdx.x >> 3);
+  const int groups = (int)gridDim.x, x = blockIdx.x & 7, q = groups >> 3, rest = groups & 7;
+  int at = x * q + min(x, rest) + (int)(blockIdx.x >> 3);
+  if constexpr (kMode == kPlain) {
+    const int part = at / (g.gridM * g.gridN);
+    at -= part * g.gridM * g.gridN;
+    g.A += (int64_t)part * g.each;
+    g.B += (int64_t)part * g.each;
+    g.K = min(g.each, g.K - part * g.each);
+    g.part += (int64_t)part * g.M * g.N;
+  }
   const int band = at / (8 * g.gridN), inBand = at - band * 8 * g.gridN, high = min(8, g.gridM - band * 8);
   const int m0 = (band * 8 + inBand % high) * BM;
   const int n0 = inBand / high * (kMode == kDual ? BN / 2 : BN);
@@ -280,10 +290,71 @@ gemm_kernel(GemmArgs<T> g) {
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
-        store_run<T, 4>(c + n, left, to_run<T, 4>(v));
+        if (kMode == kPlain && g.parts > 1)
+          store_run<float, 4>(g.part + (int64_t)m * g.N + n, left, to_run<float, 4>(v));
+        else
+          store_run<T, 4>(c + n, left, to_run<T, 4>(v));
       }
     }
   }
+}
+
+// C = the sum of the parts, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(GemmArgs<T> g) {
+  const int64_t all = (int64_t)g.M * g.N;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += (int64_t)gridDim.x * 1024) {
+    const int n = (int)min((int64_t)4, all - i);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < g.parts; ++p) {
+      const Raw<float, 4> r = load_run<float, 4>(g.part + p * all + i, n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += run_at(r, e);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) g.C[(i + e) / g.N * g.ldc + (i + e) % g.N] = from_f32<T>(v[e]);
+  }
+}
+
+// The tile, and the parts that k is cut into: of the tiles below the one whose rounds
+// over the 256 CUs take the least, by its area and the share of the largest tile's
+// rate that it reaches by itself (8192 x 2048 x 4096, both products, in one tile size
+// each: bfloat16 243, 285, 412 and 547 us; float, whose products take longer than what
+// feeds them, 1.88, 1.86, 1.94 and 2.06 ms).  With 512 rows of those the largest tile
+// would take 42 us where the second takes 22, with 100 rows 41 where the smallest
+// takes 10.  Where a product has few tiles and a long k, its parts fill the CUs
+// instead, of eight tiles of k at least (the backward pass of 100 x 2048 x 4096: float
+// 151 to 114 us, bfloat16 52 to 44);
+// joining them takes some 6 us and the parts' way through memory, in the unit of the
+// rest: a chip of largest tiles takes 128 bytes of k in 1.6 us, float in 7.4.
+struct Plan {
+  int tile, parts, each;
+};
+Plan plan_gemm(int64_t M, int64_t cols, int64_t K, int esize, bool cut) {
+  const struct {
+    int m, n;
+    double bf16, f32;
+  } tiles[] = {{256, 256, 1.0, 1.0}, {128, 128, 0.85, 1.0}, {64, 64, 0.6, 0.96}, {32, 64, 0.45, 0.9}};
+  const int64_t step = kRowBytes / esize, steps = (K + step - 1) / step;
+  Plan best = {};
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t count = (M + tiles[i].m - 1) / tiles[i].m * ((cols + tiles[i].n - 1) / tiles[i].n);
+    int64_t parts = cut ? 256 / count : 1;
+    if (parts > steps / 8) parts = steps / 8;
+    if (parts < 1) parts = 1;
+    const int64_t each = (steps + parts - 1) / parts;
+    parts = (steps + each - 1) / each;
+    const double rate = esize == 2 ? tiles[i].bf16 : tiles[i].f32;
+    double cost = (double)((count * parts + 255) / 256) * tiles[i].m * tiles[i].n / rate * (double)each;
+    if (parts > 1) cost += (6.0 + (double)parts * (double)M * (double)cols * 8.0 / 5.0e6) * (esize == 2 ? 41500.0 : 8900.0);
+    if (i == 0 || cost < least) {
+      least = cost;
+      best = Plan{i, (int)parts, (int)(each * step)};
+    }
+  }
+  return best;
 }
 
 template <typename T, int WM, int WN, int FM, int FN, Mode kMode>
@@ -291,7 +362,7 @@ void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
   constexpr int BM = WM * FM * 16, BN = WN * FN * 16 / (kMode == kDual ? 2 : 1);
   g.gridM = (g.M + BM - 1) / BM;
   g.gridN = (g.N + BN - 1) / BN;
-  const dim3 grid((unsigned)g.gridM * g.gridN), block(WM * WN * kWave);
+  const dim3 grid((unsigned)g.gridM * g.gridN * (kMode == kPlain ? g.parts : 1)), block(WM * WN * kWave);
   if constexpr (kMode == kDual && sizeof(T) == 2)  // (float rows, and the workspace's, are aligned)
     if (!direct) {
       hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, false>), grid, block, 0, stream, g);
@@ -299,38 +370,24 @@ void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
     }
   hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, true>), grid, block, 0, stream, g);
 }
-// The tile: of those below, the one whose rounds over the 256 CUs take the least,
-// by its area and the share of the largest tile's rate that it reaches by itself
-// (8192 x 2048 x 4096, both products, in one tile size each: bfloat16 243, 285, 412 and 547 us; float,
-// whose products take longer than what feeds them, 1.88, 1.86, 1.94 and 2.06 ms).
-// With 512 rows of those the largest tile would take 42 us where the second takes 22,
-// with 100 rows 41 where the smallest takes 10.
 template <typename T, Mode kMode>
-void launch_gemm(const GemmArgs<T>& g, hipStream_t stream) {
+void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
   const auto rows4 = [](const T* p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * (int64_t)sizeof(T) % 4 == 0;
   };
   const bool direct = rows4(g.A, g.lda) && rows4(g.B, g.ldb) && (kMode != kDual || rows4(g.B2, g.ldb2));
-  const struct {
-    int m, n;
-    double bf16, f32;
-  } tiles[] = {{256, 256, 1.0, 1.0}, {128, 128, 0.85, 1.0}, {64, 64, 0.6, 0.96}, {32, 64, 0.45, 0.9}};
-  int best = 0;
-  double least = 0;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t rows = (g.M + tiles[i].m - 1) / tiles[i].m;
-    const int64_t cols = ((kMode == kDual ? 2 : 1) * (int64_t)g.N + tiles[i].n - 1) / tiles[i].n;
-    const double rate = sizeof(T) == 2 ? tiles[i].bf16 : tiles[i].f32;
-    const double cost = (double)((rows * cols + 255) / 256) * tiles[i].m * tiles[i].n / rate;
-    if (i == 0 || cost < least) {
-      least = cost;
-      best = i;
-    }
-  }
-  if (best == 0) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
-  else if (best == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
-  else if (best == 2) launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
+  const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode == kPlain);
+  g.parts = plan.parts;
+  g.each = plan.each;
+  if (plan.tile == 0) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
+  else if (plan.tile == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
+  else if (plan.tile == 2) launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
   else launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
+  if constexpr (kMode == kPlain)
+    if (g.parts > 1) {
+      const int64_t quads = ((int64_t)g.M * g.N + 3) / 4, groups = (quads + 255) / 256;
+      hipLaunchKernelGGL((join_kernel<T>), dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream, g);
+    }
 }
 
 // ---- few rows ------------------------------------------------------------------
@@ -557,6 +614,7 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
   T* const turned = area((int64_t)Mp * 2 * Fp);
   T* const xT = area((int64_t)a.K * Mp);
   T* const wT = area((int64_t)a.K * 2 * Fp);
+  float* const part = reinterpret_cast<float*>(ws);   // [parts, M, K]
   const int kTiles = (int)(padded(a.K) / kSide);
   Operands<T> o = {};
   o.Fp = Fp;
@@ -584,6 +642,7 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
     g.lda = g.ldb = 2 * Fp;
     g.C = static_cast<T*>(a.dx);
     g.ldc = a.ld_dx;
+    g.part = part;
     launch_gemm<T, kPlain>(g, stream);
   }
   if (a.dwg) {
@@ -623,8 +682,9 @@ hipError_t launch_ffn_no_rows_t(const FfnArgs& a, hipStream_t stream) {
 size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize) {
   if (M == 0) return 0;
   const int64_t Fp = padded(F), Mp = padded(M);
+  const int parts = plan_gemm(M, K, 2 * Fp, esize, true).parts;  // of dx
   return area_bytes(M * 2 * Fp, esize) + area_bytes(Mp * 2 * Fp, esize) + area_bytes(K * Mp, esize) +
-         area_bytes(K * 2 * Fp, esize);
+         area_bytes(K * 2 * Fp, esize) + (parts > 1 ? (size_t)parts * M * K * sizeof(float) : 0);
 }
 
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {

@@ -115,6 +115,26 @@ def test_ffn_leading_axes_and_parts():
     assert all(torch.equal(again[k], d[k]) for k in d) and (ws[need:] == 255).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F", [(20, 48, 3000), (3, 131, 5000)])
+def test_ffn_long_sums(dtype, M, K, F):
+    """Few rows and inputs over many units: dx is summed in parts, kept in a workspace of
+    any content, in a fixed order."""
+    import state_space_sequence_exp_amd as m3
+    r, t = inputs([10, M, K, F], M, K, F, dtype)
+    h, g, u, d = check(r, t, dtype)
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float32
+    need = m3.gated_ffn_backward_workspace_size(M, K, F, kind)
+    Fp, Mp = -(-F // 64) * 64, 64
+    assert need > (M * 2 * Fp + Mp * 2 * Fp + K * Mp + K * 2 * Fp) * t["x"].element_size() + 4 * 256
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")      # NaN
+    again = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u, workspace=ws)
+    assert all(torch.equal(again[k], d[k]) for k in d) and (ws[need:] == 255).all()
+    wide = sliced(torch.zeros_like(d["x"]))
+    m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u, dx=wide)
+    assert torch.equal(wide, d["x"]) and torch.isnan(wide._base[..., :3]).all()
+
+
 def test_ffn_no_rows():
     import state_space_sequence_exp_amd as m3
     _, t = inputs(5, 4, 24, 32, "f32")
