@@ -4,12 +4,14 @@
 //   du = dh silu(g), dg = dh u silu'(g),  dx = dg Wg + du Wu,
 //   dWg = dg^T x, dWu = du^T x
 //
-// Three of the products run on one kernel: C[m][n] = sum_k A[m][k] B[n][k], both
-// operands with k contiguous.  Forward, the B rows of a wave are its hidden units'
-// rows of Wg, then of Wu, so that a lane ends with g and u of the same elements
-// and the activation costs no memory.  Backward, one pass over dh, g and u writes
-// [dg | du] and its transpose, and x and the weights are transposed beside them:
-// the gradients' operands then have k contiguous, aligned and padded with zeros.
+// The products run on one kernel: C[m][n] = sum_k A(m, k) B(n, k), tile by tile
+// through the LDS.  Forward, k is contiguous in both operands, and the B rows of a wave
+// are its hidden units' rows of Wg, then of Wu, so that a lane ends with g and u of the
+// same elements and the activation costs no memory.  Backward, one pass over dh, g and
+// u writes [dg | du]; for dx the weights are read as they lie, k by k, for their own
+// gradients [dg | du] and x are: such a tile lies in the LDS as it does in memory and
+// is turned as its fragments are read (transposed copies instead took 50 us of 795 for
+// 8192 x 2048 x 3824, half of the time with few rows).
 // (dg and du are rounded to the storage type, as the matrix units take it; g and u
 // are kept in float, or each gradient would carry their rounding as well: 0.0031
 // relative in bfloat16 instead of 0.0024, where rounding the result alone is 0.0017.)
@@ -29,19 +31,22 @@ constexpr int kRowBytes = 128, kChunks = kRowBytes / 16;  // of k in a tile's ro
 template <typename T>
 struct GemmArgs {
   int M, N, K;                 // N: hidden units (dual), columns of C otherwise
-  const T *A, *B, *B2;         // B2: the second weight matrix (dual)
+  const T *A, *B, *B2;         // B2: the second weight matrix (dual, inputs)
   int64_t lda, ldb, ldb2;
   T* C;
   float *gate, *up;            // dual: g and u, unless null
   int64_t ldc, ld_gate, ld_up;
-  T* C2;                       // split: where A's rows from `split` on go; each half has `rows` rows
+  T* C2;                       // weights: where A's columns from `split` on go
   int64_t ldc2;
-  int split, rows;
-  int parts, each;             // plain: k is cut into `parts` of `each`, and where they are more than
+  int split, rows;             // inputs, weights: each half of [dg | du] is `split` wide, `rows` of it used
+  int parts, each;             // inputs: k is cut into `parts` of `each`, and where they are more than
   float* part;                 // one their sums go to part [parts, M, N]
+  const T* zeros;              // 16 bytes of them (inputs, weights)
   int gridM, gridN;
 };
-enum Mode { kDual, kPlain, kSplit };
+// dual: x by both weights.  inputs: [dg | du] by the weights one above the other.
+// weights: [dg | du] by x, k over the rows of both.
+enum Mode { kDual, kInputs, kWeights };
 
 // acc[n 4g..4g+3][m l%16] += sum over the chunks' k: a lane's 16 bytes of a row are
 // 8 bfloat16 or 4 float k, any order of k being the same for both operands.
@@ -77,15 +82,83 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const T* base, uint32_
                : "s"(lds), "v"(off * (uint32_t)sizeof(T)), "s"(base)
                : "memory", "m0");
 }
+// The same from an address of each lane's own.
+template <typename T>
+__device__ __forceinline__ void load_to_lds_from(uint32_t lds, const T* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "memory", "m0");
+}
 // Until at most n of this wave's loads are outstanding.
 template <int n>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
 }
 
-// kDirect: rows of both operands start at multiples of 16 bytes; their tiles go
-// straight into the LDS, three ahead of the one that is multiplied.  Otherwise they
-// pass through registers, one ahead.
+// A tile of an operand whose rows are k and whose columns are the product's R rows or
+// columns from col0 on: BK rows of R elements, as they lie in memory but for units of
+// 32 bytes (float: 64) permuted by the row, so that what a fragment reads from several
+// rows at once lies on different banks.
+template <typename T, int R, int NT>
+struct TurnedTile {
+  static constexpr int E = 16 / (int)sizeof(T), BK = kRowBytes / (int)sizeof(T);
+  static constexpr int kRow = R * (int)sizeof(T), kAcross = kRow / 16;    // a row's bytes, its chunks
+  static constexpr int kPass = NT * 16 / kRow, kPasses = BK / kPass;      // rows at once
+  static_assert(kPasses * kPass == BK && kPass % 8 == 0, "passes are whole, and alike to the permutation");
+  // The permutation of a row's units, for a chunk of it.
+  __device__ __forceinline__ static int permuted(int k, int chunk) {
+    if constexpr (sizeof(T) == 4) return (((chunk >> 2) ^ ((k >> 2) & 1)) << 2) | (chunk & 3);
+    return (((chunk >> 1) ^ (kAcross >= 8 ? k & 3 : (k >> 1) & 1)) << 1) | (chunk & 1);
+  }
+  int k, col;  // of this thread's first chunk
+
+  __device__ __forceinline__ TurnedTile(int tid, int col0) {
+    k = tid / kAcross;
+    col = col0 + permuted(k, tid % kAcross) * E;
+  }
+  // The rows of the matrix at p, `left` of them, straight into the LDS at byte `lds` (this
+  // wave's); the rows behind them are zeros, from 16 bytes of them in memory (so that
+  // every tile is as many loads); columns past the end, whole chunks, stand for the last.
+  __device__ __forceinline__ void bring(uint32_t lds, const T* p, uint32_t ld, int cols, int left,
+                                        const T* zeros) const {
+    const uint32_t c = min(col, cols - E);
+    if (left >= BK) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) load_to_lds(lds + i * kPass * kRow, p, (i * kPass + k) * ld + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        load_to_lds_from(lds + i * kPass * kRow,
+                         i * kPass + k < left ? p + ((uint32_t)(i * kPass + k) * ld + c) : zeros);
+    }
+  }
+  // Fragment f (columns 16 f on) of half a tile's rows.  bfloat16: a lane names 8 bytes,
+  // four columns of row l16 / 4 of its group's eight, and gets its own column's four
+  // rows; twice.  float: four rows' elements.
+  __device__ __forceinline__ static u32x4 get(const u32x4* tile, int f, int half, int l16, int l4) {
+    const char* s = reinterpret_cast<const char*>(tile);
+    if constexpr (sizeof(T) == 2) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4* Lds;
+      const int r = l16 >> 2, k0 = half * 32 + 8 * l4 + r;
+      const char* at = s + k0 * kRow + (f ^ (kAcross >= 8 ? r & 3 : (r >> 1) & 1)) * 32 + (l16 & 3) * 8;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(at + 4 * kRow));
+      const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+      return u32x4{a.x, a.y, b.x, b.y};
+    } else {
+      const char* at = s + (half * 16 + 4 * l4) * kRow + (f ^ (l4 & 1)) * 64 + l16 * 4;
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint32_t*>(at + e * kRow);
+      return v;
+    }
+  }
+  static constexpr int kReads = sizeof(T) == 2 ? 2 : 4;  // LDS reads a fragment
+};
+
+// kDirect: rows of both operands start at multiples of 4 bytes; their tiles go straight
+// into the LDS, as many ahead as its stages hold (two of the largest tile, four of the
+// small ones, whose products take less than a load does).  Otherwise (dual) they pass
+// through registers, two ahead.
 template <typename T, int WM, int WN, int FM, int FN, Mode kMode, bool kDirect>
 __global__ void __launch_bounds__(WM* WN* kWave) __attribute__((amdgpu_waves_per_eu(FM * FN > 32 ? 1 : 2, FM * FN > 32 ? 1 : 2)))
 gemm_kernel(GemmArgs<T> g) {
@@ -100,11 +173,11 @@ gemm_kernel(GemmArgs<T> g) {
   // chip's worth of tiles shares few rows of both operands.
   const int groups = (int)gridDim.x, x = blockIdx.x & 7, q = groups >> 3, rest = groups & 7;
   int at = x * q + min(x, rest) + (int)(blockIdx.x >> 3);
-  if constexpr (kMode == kPlain) {
-    const int part = at / (g.gridM * g.gridN);
+  int part = 0;
+  if constexpr (kMode == kInputs) {
+    part = at / (g.gridM * g.gridN);
     at -= part * g.gridM * g.gridN;
     g.A += (int64_t)part * g.each;
-    g.B += (int64_t)part * g.each;
     g.K = min(g.each, g.K - part * g.each);
     g.part += (int64_t)part * g.M * g.N;
   }
@@ -112,28 +185,54 @@ gemm_kernel(GemmArgs<T> g) {
   const int m0 = (band * 8 + inBand % high) * BM;
   const int n0 = inBand / high * (kMode == kDual ? BN / 2 : BN);
 
-  // What this thread brings: one chunk of every kPass-th row, rows past the end
-  // standing for the last.  Straight loads put lane after lane, so that it is the
-  // lane's chunk of memory that is permuted.
+  constexpr bool kTurnA = kMode == kWeights, kTurnB = kMode != kDual;
+  // What this thread brings of an operand with k contiguous: one chunk of every kPass-th
+  // row, rows past the end standing for the last.  Straight loads put lane after lane,
+  // so that it is the lane's chunk of memory that is permuted.
   const int row = tid / kChunks;
   const int chunk = kDirect ? (tid % kChunks) ^ (row & 7) : tid % kChunks;
-  const T* const baseA = g.A + (int64_t)m0 * g.lda;
+  const T* const baseA = g.A + (kTurnA ? 0 : (int64_t)m0 * g.lda);
   uint32_t offA[NA], offB[NB];
+  if constexpr (!kTurnA) {
 #pragma unroll
-  for (int i = 0; i < NA; ++i)
-    offA[i] = (uint32_t)min(i * kPass + row, g.M - 1 - m0) * (uint32_t)g.lda + chunk * E;
+    for (int i = 0; i < NA; ++i)
+      offA[i] = (uint32_t)min(i * kPass + row, g.M - 1 - m0) * (uint32_t)g.lda + chunk * E;
+  }
   // (whether a wave's rows of pass i are the second matrix's)
   const auto second = [&](int i) { return (i * kPass + wave * (kWave / kChunks)) % (FN * 16) >= FN * 8; };
-  const T* const base1 = g.B + (int64_t)n0 * g.ldb;
-  const T* const base2 = kMode == kDual ? g.B2 + (int64_t)n0 * g.ldb2 : base1;
-  const auto baseB = [&](int i) { return kMode == kDual && second(i) ? base2 : base1; };
+  const T* const base1 = g.B + (kTurnB ? 0 : (int64_t)n0 * g.ldb);
+  const T* const base2 = kMode == kDual ? g.B2 + (int64_t)n0 * g.ldb2 : g.B2;
+  const auto baseB = [&](int i) { return second(i) ? base2 : base1; };
+  if constexpr (!kTurnB) {
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int r = i * kPass + row;
-    const int col = kMode == kDual ? r / (FN * 16) * FN * 8 + r % (FN * 8) : r;
-    const int64_t ld = kMode == kDual && second(i) ? g.ldb2 : g.ldb;
-    offB[i] = (uint32_t)min(col, g.N - 1 - n0) * (uint32_t)ld + chunk * E;
+    for (int i = 0; i < NB; ++i) {
+      const int r = i * kPass + row, col = r / (FN * 16) * FN * 8 + r % (FN * 8);
+      offB[i] = (uint32_t)min(col, g.N - 1 - n0) * (uint32_t)(second(i) ? g.ldb2 : g.ldb) + chunk * E;
+    }
   }
+  // ... and of operands read k by k: tile t's rows, and how many there are of them
+  const TurnedTile<T, BM, NT> turnA(tid, m0);
+  const TurnedTile<T, BN, NT> turnB(tid, n0);
+  struct Rows {
+    const T* p;
+    int64_t ld;
+    int left;
+  };
+  const auto rowsA = [&](int t) {
+    return Rows{baseA + (int64_t)t * BK * g.lda, g.lda, g.K - t * BK};
+  };
+  const auto rowsB = [&](int t) {
+    if constexpr (kMode == kInputs) {  // (a half of [dg | du] is whole tiles wide)
+      int k0 = part * g.each + t * BK;
+      const bool up = k0 >= g.split;
+      if (up) k0 -= g.split;
+      const int64_t ld = up ? g.ldb2 : g.ldb;
+      return Rows{(up ? base2 : base1) + k0 * ld, ld, g.rows - k0};
+    } else {
+      return Rows{base1 + (int64_t)t * BK * g.ldb, g.ldb, g.K - t * BK};
+    }
+  };
+  const int colsA = 2 * g.split, colsB = (g.N + E - 1) / E * E;
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -144,12 +243,18 @@ gemm_kernel(GemmArgs<T> g) {
     u32x4 a[FM], b[FN];
   };
   const int get_at[2] = {chunk_at(l16, l4), chunk_at(l16, 4 + l4)};
-  const auto get = [&](Frags& f, int stage, int half) {  // of a row's 128 bytes
-    const u32x4* s = s_tile[stage] + get_at[half];
+  const auto get = [&](Frags& f, int stage, int half) {  // of a tile's 128 bytes of k
+    const u32x4* s = s_tile[stage];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) f.b[j] = s[(BM + (wn * FN + j) * 16) * kChunks];
+    for (int j = 0; j < FN; ++j) {
+      if constexpr (kTurnB) f.b[j] = turnB.get(s + BM * kChunks, wn * FN + j, half, l16, l4);
+      else f.b[j] = s[get_at[half] + (BM + (wn * FN + j) * 16) * kChunks];
+    }
 #pragma unroll
-    for (int i = 0; i < FM; ++i) f.a[i] = s[(wm * FM + i) * 16 * kChunks];
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (kTurnA) f.a[i] = turnA.get(s, wm * FM + i, half, l16, l4);
+      else f.a[i] = s[get_at[half] + (wm * FM + i) * 16 * kChunks];
+    }
   };
   const auto multiply = [&](const Frags& f) {
 #pragma unroll
@@ -169,29 +274,43 @@ gemm_kernel(GemmArgs<T> g) {
   };
   const int put_at = chunk_at(row, chunk);  // (kPass is a multiple of 8)
   const auto put = [&](const Moved& r, int stage) {
-    u32x4* s = s_tile[stage] + put_at;
+    u32x4* const s = s_tile[stage];
 #pragma unroll
-    for (int i = 0; i < NA; ++i) s[i * kPass * kChunks] = r.a[i];
+    for (int i = 0; i < NA; ++i) s[put_at + i * kPass * kChunks] = r.a[i];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) s[(BM + i * kPass) * kChunks] = r.b[i];
+    for (int i = 0; i < NB; ++i) s[put_at + (BM + i * kPass) * kChunks] = r.b[i];
   };
 
   int done = 0;  // tiles multiplied
   if constexpr (kDirect) {
-    const int whole = g.K / BK;
+    // (read k by k, a last tile of fewer rows is filled with zeros)
+    const int whole = kTurnB ? (g.K + BK - 1) / BK : g.K / BK;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)&s_tile[0][0];
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds0 + wave * (kWave * 16));
     const auto bring = [&](int t) {
+      const int last = min(t, whole - 1);
       const uint32_t to = lds + (t & (kStages - 1)) * (uint32_t)sizeof s_tile[0];
-      const int k0 = min(t, whole - 1) * BK;  // (past the end: a tile again, into a stage that no one reads)
+      const int k0 = last * BK;  // (past the end: a tile again, into a stage that no one reads)
+      if constexpr (kTurnA) {
+        const Rows w = rowsA(last);
+        turnA.bring(to, w.p, (uint32_t)w.ld, colsA, w.left, g.zeros);
+      } else {
 #pragma unroll
-      for (int i = 0; i < NA; ++i) load_to_lds(to + i * kPass * kRowBytes, baseA + k0, offA[i]);
+        for (int i = 0; i < NA; ++i) load_to_lds(to + i * kPass * kRowBytes, baseA + k0, offA[i]);
+      }
+      if constexpr (kTurnB) {
+        const Rows w = rowsB(last);
+        turnB.bring(to + BM * kRowBytes, w.p, (uint32_t)w.ld, colsB, w.left, g.zeros);
+      } else {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) load_to_lds(to + (BM + i * kPass) * kRowBytes, baseB(i) + k0, offB[i]);
+        for (int i = 0; i < NB; ++i) load_to_lds(to + (BM + i * kPass) * kRowBytes, baseB(i) + k0, offB[i]);
+      }
     };
     // the fragments' reads one by one between the products
     const auto order = [] {
-      constexpr int kReads = FM + FN, kProducts = FM * FN * (sizeof(T) == 2 ? 1 : 4);
+      constexpr int kReads = FM * (kTurnA ? TurnedTile<T, BM, NT>::kReads : 1) +
+                             FN * (kTurnB ? TurnedTile<T, BN, NT>::kReads : 1);
+      constexpr int kProducts = FM * FN * (sizeof(T) == 2 ? 1 : 4);
       constexpr int kEach = kProducts < kReads ? 1 : kProducts / kReads;
 #pragma unroll
       for (int i = 0; i < kReads; ++i) {
@@ -223,7 +342,7 @@ gemm_kernel(GemmArgs<T> g) {
       wait_loads<0>();
       lds_barrier();
     }
-    if (kMode == kDual && done * BK < g.K) {  // (the workspace's rows are whole tiles)
+    if constexpr (kMode == kDual) if (done * BK < g.K) {
       Moved r;
       request(r, done * BK);
       put(r, 0);
@@ -277,7 +396,7 @@ gemm_kernel(GemmArgs<T> g) {
       }
     } else {
       T* c = g.C + (int64_t)m * g.ldc;
-      if constexpr (kMode == kSplit) {
+      if constexpr (kMode == kWeights) {
         const bool second = m >= g.split;
         const int r = second ? m - g.split : m;
         if (r >= g.rows) continue;
@@ -290,7 +409,7 @@ gemm_kernel(GemmArgs<T> g) {
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
-        if (kMode == kPlain && g.parts > 1)
+        if (kMode == kInputs && g.parts > 1)
           store_run<float, 4>(g.part + (int64_t)m * g.N + n, left, to_run<float, 4>(v));
         else
           store_run<T, 4>(c + n, left, to_run<T, 4>(v));
@@ -362,28 +481,29 @@ void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
   constexpr int BM = WM * FM * 16, BN = WN * FN * 16 / (kMode == kDual ? 2 : 1);
   g.gridM = (g.M + BM - 1) / BM;
   g.gridN = (g.N + BN - 1) / BN;
-  const dim3 grid((unsigned)g.gridM * g.gridN * (kMode == kPlain ? g.parts : 1)), block(WM * WN * kWave);
-  if constexpr (kMode == kDual && sizeof(T) == 2)  // (float rows, and the workspace's, are aligned)
+  const dim3 grid((unsigned)g.gridM * g.gridN * (kMode == kInputs ? g.parts : 1)), block(WM * WN * kWave);
+  if constexpr (kMode == kDual && sizeof(T) == 2)  // (float rows are aligned, the others' are made so)
     if (!direct) {
       hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, false>), grid, block, 0, stream, g);
       return;
     }
   hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, true>), grid, block, 0, stream, g);
 }
+template <typename T>
+bool rows4(const void* p, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * (int64_t)sizeof(T) % 4 == 0;
+}
 template <typename T, Mode kMode>
 void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
-  const auto rows4 = [](const T* p, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * (int64_t)sizeof(T) % 4 == 0;
-  };
-  const bool direct = rows4(g.A, g.lda) && rows4(g.B, g.ldb) && (kMode != kDual || rows4(g.B2, g.ldb2));
-  const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode == kPlain);
+  const bool direct = kMode != kDual || (rows4<T>(g.A, g.lda) && rows4<T>(g.B, g.ldb) && rows4<T>(g.B2, g.ldb2));
+  const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode == kInputs);
   g.parts = plan.parts;
   g.each = plan.each;
   if (plan.tile == 0) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
   else if (plan.tile == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
   else if (plan.tile == 2) launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
   else launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
-  if constexpr (kMode == kPlain)
+  if constexpr (kMode == kInputs)
     if (g.parts > 1) {
       const int64_t quads = ((int64_t)g.M * g.N + 3) / 4, groups = (quads + 255) / 256;
       hipLaunchKernelGGL((join_kernel<T>), dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream, g);
@@ -463,118 +583,68 @@ __global__ void __launch_bounds__(kFewWaves * kWave) few_kernel(GemmArgs<T> g) {
   }
 }
 
-// ---- the backward pass's operands ------------------------------------------------
+// ---- the backward pass ------------------------------------------------------------
 
-constexpr int kSide = 64;  // of a transposed tile
+constexpr int kSide = 64;  // the halves of [dg | du] are a multiple of this wide
 
-// Rows r0 .. of a tile that lies in the LDS transposed, [column][row], to dst
-// [columns, pitch]: 16 bytes a thread.
-template <typename T, int P = kSide + 4 / (int)sizeof(T)>
-__device__ __forceinline__ void put_columns(const T (&s)[kSide][P], T* dst, int64_t pitch, int c0, int r0, int cols) {
-  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
-  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
-    const int c = i / kAcross, r = i % kAcross * E;
-    if (c0 + c >= cols) continue;
-    u32x4 v;
-    T tmp[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) tmp[e] = s[c][r + e];
-    __builtin_memcpy(&v, tmp, 16);
-    *reinterpret_cast<u32x4*>(dst + (int64_t)(c0 + c) * pitch + r0 + r) = v;
-  }
-}
-
-// The transposed tiles are 64 x 64 of T in the LDS.
+// What the gradients' products read of the inputs: themselves, or copies whose rows are
+// whole 16-byte chunks (`pitch` elements), in as many workgroups each.
 template <typename T>
-struct Turned {
-  static constexpr int P = kSide + 4 / (int)sizeof(T);
-  T s[kSide][P];
+struct Copies {
+  T *wg, *wu, *x;
+  int pitch;
+  unsigned slopes, weights, inputs;
 };
 
-// dst [C, pitch] = src [R, C] transposed, zeros from R to the next multiple of 64: one tile.
 template <typename T>
-__device__ __forceinline__ void turn_tile(Turned<T>& s, int tile, const T* src, int64_t ld, int R, int C, T* dst,
-                                          int64_t pitch) {
-  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
-  const int across = (C + kSide - 1) / kSide, c0 = tile % across * kSide, r0 = tile / across * kSide;
-  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
-    const int r = i / kAcross, c = i % kAcross * E;
-    const Raw<T, E> v = load_run<T, E>(src + (int64_t)(r0 + r) * ld + c0 + c, r0 + r < R ? C - c0 - c : 0);
-    T t[E];
-    __builtin_memcpy(t, v.w, 16);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s.s[c + e][r] = t[e];
-  }
-  __syncthreads();
-  put_columns<T>(s.s, dst, pitch, c0, r0, C);
+__device__ __forceinline__ void copy_chunk(unsigned group, const void* from, int64_t ld, int rows, int cols, T* to,
+                                           int pitch) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int64_t across = pitch / E, at = (int64_t)group * 256 + threadIdx.x, r = at / across;
+  const int c = (int)(at - r * across) * E;
+  if (r >= rows) return;
+  const Raw<T, E> v = load_run<T, E>(static_cast<const T*>(from) + r * ld + c, cols - c);
+  __builtin_memcpy(to + r * pitch + c, v.w, 16);
 }
 
-// What the gradients' products read, in the workspace (null: not wanted).
+// [dg | du], Fp columns each, zeros from F on, a chunk of each a thread; then the copies.
 template <typename T>
-struct Operands {
-  T *both, *turned, *xT, *wT;   // [M, 2 Fp], [2 Fp, Mp], [K, Mp], [K, 2 Fp]
-  int Fp, Mp;
-  int slopes, weights, inputs;  // tiles of each part
-};
-
-// One launch for all of them: [dg | du] (Fp columns each, zeros from F on) and its
-// transpose (Mp columns, zeros from M on), then the transposes of the weights side by
-// side, then that of x.
-template <typename T>
-__global__ void __launch_bounds__(256) operands_kernel(FfnArgs a, Operands<T> o) {
-  constexpr int E = 16 / (int)sizeof(T), kAcross = kSide / E;
-  __shared__ Turned<T> s_g, s_u;
-  const int Fp = o.Fp;
-  int tile = blockIdx.x;
-  if (tile >= o.slopes) {
-    tile -= o.slopes;
-    if (tile < o.weights) {
-      turn_tile<T>(s_g, tile, static_cast<const T*>(a.wg), a.ld_wg, a.F, a.K, o.wT, 2 * (int64_t)Fp);
-    } else if (tile < 2 * o.weights) {
-      turn_tile<T>(s_g, tile - o.weights, static_cast<const T*>(a.wu), a.ld_wu, a.F, a.K, o.wT + Fp, 2 * (int64_t)Fp);
-    } else {
-      turn_tile<T>(s_g, tile - 2 * o.weights, static_cast<const T*>(a.x), a.ld_x, a.M, a.K, o.xT, o.Mp);
-    }
+__global__ void __launch_bounds__(256) operands_kernel(FfnArgs a, u32x4* zeros, T* both, int Fp, Copies<T> o) {
+  constexpr int E = 16 / (int)sizeof(T);
+  unsigned group = blockIdx.x;
+  if (group >= o.slopes) {
+    group -= o.slopes;
+    if (group < o.weights) copy_chunk<T>(group, a.wg, a.ld_wg, a.F, a.K, o.wg, o.pitch);
+    else if (group < 2 * o.weights) copy_chunk<T>(group - o.weights, a.wu, a.ld_wu, a.F, a.K, o.wu, o.pitch);
+    else copy_chunk<T>(group - 2 * o.weights, a.x, a.ld_x, a.M, a.K, o.x, o.pitch);
     return;
   }
-  const int across = Fp / kSide, f0 = tile % across * kSide, m0 = tile / across * kSide;
-  for (int i = threadIdx.x; i < kSide * kAcross; i += 256) {
-    const int r = i / kAcross, c = i % kAcross * E, m = m0 + r, n = m < a.M ? a.F - f0 - c : 0;
-    const Raw<T, E> dh = load_run<T, E>(static_cast<const T*>(a.dh) + (int64_t)m * a.ld_dh + f0 + c, n);
-    const Raw<float, E> g = load_run<float, E>(a.gate + (int64_t)m * a.ld_gate + f0 + c, n);
-    const Raw<float, E> u = load_run<float, E>(a.up + (int64_t)m * a.ld_up + f0 + c, n);
-    float dg[E], du[E];
+  const int64_t across = Fp / E, at = (int64_t)group * 256 + threadIdx.x;
+  if (at == 0) *zeros = u32x4{0u, 0u, 0u, 0u};
+  const int64_t m = at / across;
+  const int f = (int)(at - m * across) * E, n = a.F - f;
+  if (m >= a.M) return;
+  const Raw<T, E> dh = load_run<T, E>(static_cast<const T*>(a.dh) + m * a.ld_dh + f, n);
+  const Raw<float, E> g = load_run<float, E>(a.gate + m * a.ld_gate + f, n);
+  const Raw<float, E> u = load_run<float, E>(a.up + m * a.ld_up + f, n);
+  float dg[E], du[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float gv = run_at(g, e), d = run_at(dh, e), sg = sigmoid_of(gv);
-      du[e] = d * (gv * sg);
-      dg[e] = d * run_at(u, e) * (sg * __builtin_fmaf(gv, 1.f - sg, 1.f));
-    }
-    const Raw<T, E> rg = to_run<T, E>(dg), ru = to_run<T, E>(du);
-    if (o.both && m < a.M) {
-      T* p = o.both + (int64_t)m * 2 * Fp + f0 + c;
-      __builtin_memcpy(p, rg.w, 16);
-      __builtin_memcpy(p + Fp, ru.w, 16);
-    }
-    if (o.turned) {
-      T tg[E], tu[E];
-      __builtin_memcpy(tg, rg.w, 16);
-      __builtin_memcpy(tu, ru.w, 16);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        s_g.s[c + e][r] = tg[e];
-        s_u.s[c + e][r] = tu[e];
-      }
-    }
+  for (int e = 0; e < E; ++e) {
+    const float gv = run_at(g, e), d = run_at(dh, e), sg = sigmoid_of(gv);
+    du[e] = d * (gv * sg);
+    dg[e] = d * run_at(u, e) * (sg * __builtin_fmaf(gv, 1.f - sg, 1.f));
   }
-  if (!o.turned) return;
-  __syncthreads();
-  put_columns<T>(s_g.s, o.turned, o.Mp, f0, m0, Fp);
-  put_columns<T>(s_u.s, o.turned + (int64_t)Fp * o.Mp, o.Mp, f0, m0, Fp);
+  T* p = both + m * 2 * Fp + f;
+  const Raw<T, E> rg = to_run<T, E>(dg), ru = to_run<T, E>(du);
+  __builtin_memcpy(p, rg.w, 16);
+  __builtin_memcpy(p + Fp, ru.w, 16);
 }
 
 int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
 size_t area_bytes(int64_t n, int es) { return ((size_t)n * es + 255) / 256 * 256; }
+// Whether the workspace has room for copies of x and the weights: where their rows may
+// not be whole 16-byte chunks at multiples of 4 bytes.
+bool copies_kept(int64_t K, int es) { return es == 2 || K % 4 != 0; }
 
 template <typename T>
 hipError_t launch_ffn_t(const FfnArgs& a, hipStream_t stream) {
@@ -603,63 +673,71 @@ hipError_t launch_ffn_t(const FfnArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
-  const int Fp = (int)padded(a.F), Mp = (int)padded(a.M), es = (int)sizeof(T);
+  const int Fp = (int)padded(a.F), es = (int)sizeof(T);
+  constexpr int E = 16 / (int)sizeof(T);
   char* ws = static_cast<char*>(a.workspace);
+  u32x4* const zeros = reinterpret_cast<u32x4*>(ws);                // 256 bytes, the first 16 zeros
+  ws += 256;
   const auto area = [&](int64_t n) {
     T* p = reinterpret_cast<T*>(ws);
     ws += area_bytes(n, es);
     return p;
   };
-  T* const both = area((int64_t)a.M * 2 * Fp);
-  T* const turned = area((int64_t)Mp * 2 * Fp);
-  T* const xT = area((int64_t)a.K * Mp);
-  T* const wT = area((int64_t)a.K * 2 * Fp);
-  float* const part = reinterpret_cast<float*>(ws);   // [parts, M, K]
-  const int kTiles = (int)(padded(a.K) / kSide);
-  Operands<T> o = {};
-  o.Fp = Fp;
-  o.Mp = Mp;
-  o.slopes = Fp / kSide * (Mp / kSide);
-  if (a.dx) {
-    o.both = both;
-    o.wT = wT;
-    o.weights = kTiles * (Fp / kSide);
+  T* const both = area((int64_t)a.M * 2 * Fp);                      // [M, 2 Fp]
+  Copies<T> o = {};
+  o.pitch = (a.K + E - 1) / E * E;
+  const auto groups = [](int64_t rows, int64_t cols) { return (unsigned)((rows * (cols / E) + 255) / 256); };
+  o.slopes = groups(a.M, Fp);
+  FfnArgs in = a;
+  if (copies_kept(a.K, es)) {
+    o.wg = area((int64_t)a.F * o.pitch);
+    o.wu = area((int64_t)a.F * o.pitch);
+    o.x = area((int64_t)a.M * o.pitch);
+    const bool chunks = a.K % E == 0;
+    if (a.dx && !(chunks && rows4<T>(a.wg, a.ld_wg) && rows4<T>(a.wu, a.ld_wu))) {
+      o.weights = groups(a.F, o.pitch);
+      in.wg = o.wg;
+      in.wu = o.wu;
+      in.ld_wg = in.ld_wu = o.pitch;
+    }
+    if (a.dwg && !(chunks && rows4<T>(a.x, a.ld_x))) {
+      o.inputs = groups(a.M, o.pitch);
+      in.x = o.x;
+      in.ld_x = o.pitch;
+    }
   }
-  if (a.dwg) {
-    o.turned = turned;
-    o.xT = xT;
-    o.inputs = kTiles * (Mp / kSide);
-  }
-  hipLaunchKernelGGL((operands_kernel<T>), dim3((unsigned)(o.slopes + 2 * o.weights + o.inputs)), dim3(256), 0,
-                     stream, a, o);
+  float* const part = reinterpret_cast<float*>(ws);                 // [parts, M, K]
+  hipLaunchKernelGGL((operands_kernel<T>), dim3(o.slopes + 2 * o.weights + o.inputs), dim3(256), 0, stream, a, zeros,
+                     both, Fp, o);
+  GemmArgs<T> g = {};
+  g.zeros = reinterpret_cast<const T*>(zeros);
+  g.A = both;
+  g.lda = 2 * Fp;
+  g.N = a.K;
+  g.split = Fp;
+  g.rows = a.F;
   if (a.dx) {
-    GemmArgs<T> g = {};
     g.M = a.M;
-    g.N = a.K;
     g.K = 2 * Fp;
-    g.A = both;
-    g.B = wT;
-    g.lda = g.ldb = 2 * Fp;
+    g.B = static_cast<const T*>(in.wg);
+    g.B2 = static_cast<const T*>(in.wu);
+    g.ldb = in.ld_wg;
+    g.ldb2 = in.ld_wu;
     g.C = static_cast<T*>(a.dx);
     g.ldc = a.ld_dx;
     g.part = part;
-    launch_gemm<T, kPlain>(g, stream);
+    launch_gemm<T, kInputs>(g, stream);
   }
   if (a.dwg) {
-    GemmArgs<T> g = {};
     g.M = 2 * Fp;
-    g.N = a.K;
-    g.K = Mp;
-    g.A = turned;
-    g.B = xT;
-    g.lda = g.ldb = Mp;
+    g.K = a.M;
+    g.B = static_cast<const T*>(in.x);
+    g.ldb = in.ld_x;
     g.C = static_cast<T*>(a.dwg);
     g.ldc = a.ld_dwg;
     g.C2 = static_cast<T*>(a.dwu);
     g.ldc2 = a.ld_dwu;
-    g.split = Fp;
-    g.rows = a.F;
-    launch_gemm<T, kSplit>(g, stream);
+    launch_gemm<T, kWeights>(g, stream);
   }
   return hipGetLastError();
 }
@@ -681,10 +759,11 @@ hipError_t launch_ffn_no_rows_t(const FfnArgs& a, hipStream_t stream) {
 
 size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize) {
   if (M == 0) return 0;
-  const int64_t Fp = padded(F), Mp = padded(M);
+  const int64_t Fp = padded(F);
   const int parts = plan_gemm(M, K, 2 * Fp, esize, true).parts;  // of dx
-  return area_bytes(M * 2 * Fp, esize) + area_bytes(Mp * 2 * Fp, esize) + area_bytes(K * Mp, esize) +
-         area_bytes(K * 2 * Fp, esize) + (parts > 1 ? (size_t)parts * M * K * sizeof(float) : 0);
+  const int64_t pitch = (K * esize + 15) / 16 * 16 / esize;
+  const size_t copies = copies_kept(K, esize) ? 2 * area_bytes(F * pitch, esize) + area_bytes(M * pitch, esize) : 0;
+  return 256 + area_bytes(M * 2 * Fp, esize) + copies + (parts > 1 ? (size_t)parts * M * K * sizeof(float) : 0);
 }
 
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {

@@ -125,8 +125,7 @@ def test_ffn_long_sums(dtype, M, K, F):
     h, g, u, d = check(r, t, dtype)
     kind = torch.bfloat16 if dtype == "bf16" else torch.float32
     need = m3.gated_ffn_backward_workspace_size(M, K, F, kind)
-    Fp, Mp = -(-F // 64) * 64, 64
-    assert need > (M * 2 * Fp + Mp * 2 * Fp + K * Mp + K * 2 * Fp) * t["x"].element_size() + 4 * 256
+    assert need > M * 2 * -(-F // 64) * 64 * t["x"].element_size() + 512      # more than dg and du
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")      # NaN
     again = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u, workspace=ws)
     assert all(torch.equal(again[k], d[k]) for k in d) and (ws[need:] == 255).all()
