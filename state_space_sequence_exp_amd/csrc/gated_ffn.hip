@@ -114,20 +114,24 @@ struct TurnedTile {
     k = tid / kAcross;
     col = col0 + permuted(k, tid % kAcross) * E;
   }
+  // Where this thread's chunks lie, from the tile's first row on, rows being ld elements
+  // apart; columns past the end, whole chunks, stand for the last.
+  __device__ __forceinline__ void offsets(uint32_t (&off)[kPasses], uint32_t ld, int cols) const {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) off[i] = (i * kPass + k) * ld + min(col, cols - E);
+  }
   // The rows of the matrix at p, `left` of them, straight into the LDS at byte `lds` (this
   // wave's); the rows behind them are zeros, from 16 bytes of them in memory (so that
-  // every tile is as many loads); columns past the end, whole chunks, stand for the last.
-  __device__ __forceinline__ void bring(uint32_t lds, const T* p, uint32_t ld, int cols, int left,
+  // every tile is as many loads).
+  __device__ __forceinline__ void bring(uint32_t lds, const T* p, const uint32_t (&off)[kPasses], int left,
                                         const T* zeros) const {
-    const uint32_t c = min(col, cols - E);
     if (left >= BK) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) load_to_lds(lds + i * kPass * kRow, p, (i * kPass + k) * ld + c);
+      for (int i = 0; i < kPasses; ++i) load_to_lds(lds + i * kPass * kRow, p, off[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
-        load_to_lds_from(lds + i * kPass * kRow,
-                         i * kPass + k < left ? p + ((uint32_t)(i * kPass + k) * ld + c) : zeros);
+        load_to_lds_from(lds + i * kPass * kRow, i * kPass + k < left ? p + off[i] : zeros);
     }
   }
   // Fragment f (columns 16 f on) of half a tile's rows.  bfloat16: a lane names 8 bytes,
@@ -210,29 +214,14 @@ gemm_kernel(GemmArgs<T> g) {
       offB[i] = (uint32_t)min(col, g.N - 1 - n0) * (uint32_t)(second(i) ? g.ldb2 : g.ldb) + chunk * E;
     }
   }
-  // ... and of operands read k by k: tile t's rows, and how many there are of them
+  // ... and of operands read k by k.
   const TurnedTile<T, BM, NT> turnA(tid, m0);
   const TurnedTile<T, BN, NT> turnB(tid, n0);
-  struct Rows {
-    const T* p;
-    int64_t ld;
-    int left;
-  };
-  const auto rowsA = [&](int t) {
-    return Rows{baseA + (int64_t)t * BK * g.lda, g.lda, g.K - t * BK};
-  };
-  const auto rowsB = [&](int t) {
-    if constexpr (kMode == kInputs) {  // (a half of [dg | du] is whole tiles wide)
-      int k0 = part * g.each + t * BK;
-      const bool up = k0 >= g.split;
-      if (up) k0 -= g.split;
-      const int64_t ld = up ? g.ldb2 : g.ldb;
-      return Rows{(up ? base2 : base1) + k0 * ld, ld, g.rows - k0};
-    } else {
-      return Rows{base1 + (int64_t)t * BK * g.ldb, g.ldb, g.K - t * BK};
-    }
-  };
-  const int colsA = 2 * g.split, colsB = (g.N + E - 1) / E * E;
+  uint32_t turnedA[NA], turnedB[NB], turnedB2[NB];
+  const int colsB = (g.N + E - 1) / E * E;
+  if constexpr (kTurnA) turnA.offsets(turnedA, (uint32_t)g.lda, 2 * g.split);
+  if constexpr (kTurnB) turnB.offsets(turnedB, (uint32_t)g.ldb, colsB);
+  if constexpr (kMode == kInputs) turnB.offsets(turnedB2, (uint32_t)g.ldb2, colsB);
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -292,18 +281,21 @@ gemm_kernel(GemmArgs<T> g) {
       const uint32_t to = lds + (t & (kStages - 1)) * (uint32_t)sizeof s_tile[0];
       const int k0 = last * BK;  // (past the end: a tile again, into a stage that no one reads)
       if constexpr (kTurnA) {
-        const Rows w = rowsA(last);
-        turnA.bring(to, w.p, (uint32_t)w.ld, colsA, w.left, g.zeros);
+        turnA.bring(to, baseA + k0 * g.lda, turnedA, g.K - k0, g.zeros);
       } else {
 #pragma unroll
         for (int i = 0; i < NA; ++i) load_to_lds(to + i * kPass * kRowBytes, baseA + k0, offA[i]);
       }
-      if constexpr (kTurnB) {
-        const Rows w = rowsB(last);
-        turnB.bring(to + BM * kRowBytes, w.p, (uint32_t)w.ld, colsB, w.left, g.zeros);
+      const uint32_t toB = to + BM * kRowBytes;
+      if constexpr (kMode == kInputs) {  // (a half of [dg | du] is whole tiles wide)
+        const int k = part * g.each + k0;
+        if (k < g.split) turnB.bring(toB, base1 + k * g.ldb, turnedB, g.rows - k, g.zeros);
+        else turnB.bring(toB, base2 + (k - g.split) * g.ldb2, turnedB2, g.rows - (k - g.split), g.zeros);
+      } else if constexpr (kMode == kWeights) {
+        turnB.bring(toB, base1 + k0 * g.ldb, turnedB, g.K - k0, g.zeros);
       } else {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) load_to_lds(to + (BM + i * kPass) * kRowBytes, baseB(i) + k0, offB[i]);
+        for (int i = 0; i < NB; ++i) load_to_lds(toB + i * kPass * kRowBytes, baseB(i) + k0, offB[i]);
       }
     };
     // the fragments' reads one by one between the products
@@ -458,7 +450,8 @@ Plan plan_gemm(int64_t M, int64_t cols, int64_t K, int esize, bool cut) {
   const int64_t step = kRowBytes / esize, steps = (K + step - 1) / step;
   Plan best = {};
   double least = 0;
-  for (int i = 0; i < 4; ++i) {
+  const int first = esize == 2 ? 0 : 1;  // (the largest gains nothing in float)
+  for (int i = first; i < 4; ++i) {
     const int64_t count = (M + tiles[i].m - 1) / tiles[i].m * ((cols + tiles[i].n - 1) / tiles[i].n);
     int64_t parts = cut ? 256 / count : 1;
     if (parts > steps / 8) parts = steps / 8;
@@ -468,7 +461,7 @@ Plan plan_gemm(int64_t M, int64_t cols, int64_t K, int esize, bool cut) {
     const double rate = esize == 2 ? tiles[i].bf16 : tiles[i].f32;
     double cost = (double)((count * parts + 255) / 256) * tiles[i].m * tiles[i].n / rate * (double)each;
     if (parts > 1) cost += (6.0 + (double)parts * (double)M * (double)cols * 8.0 / 5.0e6) * (esize == 2 ? 41500.0 : 8900.0);
-    if (i == 0 || cost < least) {
+    if (i == first || cost < least) {
       least = cost;
       best = Plan{i, (int)parts, (int)(each * step)};
     }
@@ -499,8 +492,9 @@ void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
   const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode == kInputs);
   g.parts = plan.parts;
   g.each = plan.each;
-  if (plan.tile == 0) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
-  else if (plan.tile == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
+  if (plan.tile == 0) {
+    if constexpr (sizeof(T) == 2) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
+  } else if (plan.tile == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
   else if (plan.tile == 2) launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
   else launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
   if constexpr (kMode == kInputs)
