@@ -10,8 +10,16 @@
 // same elements and the activation costs no memory.  Backward, one pass over dh, g and
 // u writes [dg | du]; for dx the weights are read as they lie, k by k, for their own
 // gradients [dg | du] and x are: such a tile lies in the LDS as it does in memory and
-// is turned as its fragments are read (transposed copies instead took 50 us of 795 for
-// 8192 x 2048 x 3824, half of the time with few rows).
+// is turned as its fragments are read.  (Transposed copies instead take 80 us more of
+// 8192 x 2048 x 3824 in bfloat16, forward and gradients, which take 719; in float, 777 x
+// 514 x 1001, 8 us less of 86.)
+//
+// Bound by the matrix units at the rate that the chip's power leaves them: 16384 x 2048
+// x 4096 bfloat16 407 us, 1350 TFLOP/s (a product of that size alone, by the library,
+// 1370), the largest tile's waves reading their fragments of the next half tile from
+// the LDS between the matrix instructions of this one; float 145 of 155 TFLOP/s.  A few
+// rows are bound by the weights' bytes (few_kernel).
+//
 // (dg and du are rounded to the storage type, as the matrix units take it; g and u
 // are kept in float, or each gradient would carry their rounding as well: 0.0031
 // relative in bfloat16 instead of 0.0024, where rounding the result alone is 0.0017.)
@@ -164,7 +172,7 @@ struct TurnedTile {
 // small ones, whose products take less than a load does).  Otherwise (dual) they pass
 // through registers, two ahead.
 template <typename T, int WM, int WN, int FM, int FN, Mode kMode, bool kDirect>
-__global__ void __launch_bounds__(WM* WN* kWave) __attribute__((amdgpu_waves_per_eu(FM * FN > 32 ? 1 : 2, FM * FN > 32 ? 1 : 2)))
+__global__ void __launch_bounds__(WM* WN* kWave) __attribute__((amdgpu_waves_per_eu(2, 2)))
 gemm_kernel(GemmArgs<T> g) {
   constexpr int NT = WM * WN * kWave, BM = WM * FM * 16, BN = WN * FN * 16, E = 16 / (int)sizeof(T);
   constexpr int BK = kRowBytes / (int)sizeof(T), kPass = NT / kChunks;  // rows a pass loads
@@ -334,7 +342,7 @@ gemm_kernel(GemmArgs<T> g) {
       wait_loads<0>();
       lds_barrier();
     }
-    if constexpr (kMode == kDual) if (done * BK < g.K) {
+    if (kMode == kDual && done * BK < g.K) {
       Moved r;
       request(r, done * BK);
       put(r, 0);
@@ -494,9 +502,13 @@ void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
   g.each = plan.each;
   if (plan.tile == 0) {
     if constexpr (sizeof(T) == 2) launch_gemm_tile<T, 2, 4, 8, 4, kMode>(g, direct, stream);
-  } else if (plan.tile == 1) launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
-  else if (plan.tile == 2) launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
-  else launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
+  } else if (plan.tile == 1) {
+    launch_gemm_tile<T, 2, 2, 4, 4, kMode>(g, direct, stream);
+  } else if (plan.tile == 2) {
+    launch_gemm_tile<T, 2, 2, 2, 2, kMode>(g, direct, stream);
+  } else {
+    launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
+  }
   if constexpr (kMode == kInputs)
     if (g.parts > 1) {
       const int64_t quads = ((int64_t)g.M * g.N + 3) / 4, groups = (quads + 255) / 256;
@@ -506,7 +518,8 @@ void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
 
 // ---- few rows ------------------------------------------------------------------
 // Up to 16 FM rows (a decode batch): the weights are read once, straight into the
-// matrix units' layout.  A workgroup owns 16 hidden units; its eight waves share
+// matrix units' layout (4 x 2048 x 4096 bfloat16: 6.9 us, 4.9 TB/s; from 33 rows on the
+// tiles take as long, 10 us).  A workgroup owns 16 hidden units; its eight waves share
 // out k and add their parts in the LDS, in order.
 constexpr int kFewWaves = 8;
 

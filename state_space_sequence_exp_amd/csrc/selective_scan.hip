@@ -16,12 +16,17 @@
 // of four exchanges, so that lane i ends with token i's.
 //
 // A workgroup takes 16 channels through tiles of 64 tokens.  Four of its waves scan
-// a tile while the other four make ready: they load the tile after it as it lies in
-// memory, four channels of a token each, compute its steps once, turn them in the
-// LDS, and finish and store the outputs of the tile before.  (With every wave doing
-// both in turn, the one wave a SIMD of B1 T16384 D4096 waits for its own loads and
-// barriers: 589 us.)  Neighbouring workgroups, which share cache lines, run on one
-// XCD.
+// a tile while the other four make ready: they load the tiles after it as they lie in
+// memory, four channels of a token each, compute their steps once, turn them in the
+// LDS, and finish and store the outputs of the tile before.  Neighbouring workgroups,
+// which share cache lines, run on one XCD.
+//
+// B1 T16384 D4096 N16 bfloat16 with the gate takes 384 us: its scanning waves alone 320,
+// at one a SIMD, which issues an operation in about five cycles, not four; the vector
+// units are busy for 80% of the time.  (With every wave doing both halves' work in turn,
+// 589 us; the sums by matrix instructions, 586 and more: they wait for their operands
+// and hold up the wave; the sums left to the other half's waves, 703.)  With more
+// waves a state and token takes 0.31 to 0.34 ps (B4 T2048 D4096) instead of 0.36.
 //
 // With few channels (see select_segments) the tokens are cut into segments: a
 // first launch takes each from a zero state to its end state and sum of steps
