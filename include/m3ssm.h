@@ -757,7 +757,7 @@ m3_status m3_gated_ffn(const m3_ffn_dims* dims, m3_dtype dtype, const void* x,
  * together (weights that do not).  rows == 0 writes zeros to dw_gate and dw_up.
  * The workspace (256-byte aligned) holds dg and du, copies of x and the weights for
  * where their rows are not whole 16-byte chunks at multiples of 4 bytes, and the parts
- * of a dx that is summed in parts; it need not be cleared.
+ * of gradients that are summed in parts; it need not be cleared.
  * Outputs and the workspace must not overlap an input or each other.
  */
 size_t m3_gated_ffn_backward_workspace_size(const m3_ffn_dims* dims, m3_dtype dtype);

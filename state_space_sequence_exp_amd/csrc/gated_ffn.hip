@@ -47,8 +47,8 @@ struct GemmArgs {
   T* C2;                       // weights: where A's columns from `split` on go
   int64_t ldc2;
   int split, rows;             // inputs, weights: each half of [dg | du] is `split` wide, `rows` of it used
-  int parts, each;             // inputs: k is cut into `parts` of `each`, and where they are more than
-  float* part;                 // one their sums go to part [parts, M, N]
+  int parts, each;             // inputs, weights: k is cut into `parts` of `each`, and where they are more
+  float* part;                 // than one their sums go to part [parts, M, N]
   const T* zeros;              // 16 bytes of them (inputs, weights)
   int gridM, gridN;
 };
@@ -186,10 +186,11 @@ gemm_kernel(GemmArgs<T> g) {
   const int groups = (int)gridDim.x, x = blockIdx.x & 7, q = groups >> 3, rest = groups & 7;
   int at = x * q + min(x, rest) + (int)(blockIdx.x >> 3);
   int part = 0;
-  if constexpr (kMode == kInputs) {
+  if constexpr (kMode != kDual) {
     part = at / (g.gridM * g.gridN);
     at -= part * g.gridM * g.gridN;
-    g.A += (int64_t)part * g.each;
+    g.A += (int64_t)part * g.each * (kMode == kWeights ? g.lda : 1);
+    if constexpr (kMode == kWeights) g.B += (int64_t)part * g.each * g.ldb;
     g.K = min(g.each, g.K - part * g.each);
     g.part += (int64_t)part * g.M * g.N;
   }
@@ -409,7 +410,7 @@ gemm_kernel(GemmArgs<T> g) {
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
-        if (kMode == kInputs && g.parts > 1)
+        if (g.parts > 1)
           store_run<float, 4>(g.part + (int64_t)m * g.N + n, left, to_run<float, 4>(v));
         else
           store_run<T, 4>(c + n, left, to_run<T, 4>(v));
@@ -419,7 +420,7 @@ gemm_kernel(GemmArgs<T> g) {
 }
 
 // C = the sum of the parts, in order.
-template <typename T>
+template <typename T, Mode kMode>
 __global__ void __launch_bounds__(256) join_kernel(GemmArgs<T> g) {
   const int64_t all = (int64_t)g.M * g.N;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += (int64_t)gridDim.x * 1024) {
@@ -431,8 +432,21 @@ __global__ void __launch_bounds__(256) join_kernel(GemmArgs<T> g) {
       for (int e = 0; e < 4; ++e) v[e] += run_at(r, e);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) g.C[(i + e) / g.N * g.ldc + (i + e) % g.N] = from_f32<T>(v[e]);
+    for (int e = 0; e < 4; ++e) {
+      int64_t row = (i + e) / g.N;
+      const int64_t col = (i + e) - row * g.N;
+      T* c = g.C;
+      int64_t ld = g.ldc;
+      if constexpr (kMode == kWeights) {
+        if (row >= g.split) {
+          row -= g.split;
+          c = g.C2;
+          ld = g.ldc2;
+        }
+        if (row >= g.rows) continue;
+      }
+      if (e < n) c[row * ld + col] = from_f32<T>(v[e]);
+    }
   }
 }
 
@@ -443,10 +457,11 @@ __global__ void __launch_bounds__(256) join_kernel(GemmArgs<T> g) {
 // feeds them, 1.88, 1.86, 1.94 and 2.06 ms).  With 512 rows of those the largest tile
 // would take 42 us where the second takes 22, with 100 rows 41 where the smallest
 // takes 10.  Where a product has few tiles and a long k, its parts fill the CUs
-// instead, of eight tiles of k at least (the backward pass of 100 x 2048 x 4096: float
-// 151 to 114 us, bfloat16 52 to 44);
+// instead, of eight tiles of k at least (the backward pass of 256 x 2048 x 4096,
+// bfloat16: 61 to 48 us, of 20000 x 64 x 300 120 to 44, float 291 to 75);
 // joining them takes some 6 us and the parts' way through memory, in the unit of the
-// rest: a chip of largest tiles takes 128 bytes of k in 1.6 us, float in 7.4.
+// rest: a chip of largest tiles takes 128 bytes of k in 1.6 us, float in 7.4.  No tile
+// takes them in less than 0.3 us, which its loads and barriers need.
 struct Plan {
   int tile, parts, each;
 };
@@ -467,7 +482,9 @@ Plan plan_gemm(int64_t M, int64_t cols, int64_t K, int esize, bool cut) {
     const int64_t each = (steps + parts - 1) / parts;
     parts = (steps + each - 1) / each;
     const double rate = esize == 2 ? tiles[i].bf16 : tiles[i].f32;
-    double cost = (double)((count * parts + 255) / 256) * tiles[i].m * tiles[i].n / rate * (double)each;
+    double cost = (double)((count * parts + 255) / 256) * tiles[i].m * tiles[i].n / rate;
+    const double alone = esize == 2 ? 12000.0 : 2700.0;
+    cost = (cost < alone ? alone : cost) * (double)each;
     if (parts > 1) cost += (6.0 + (double)parts * (double)M * (double)cols * 8.0 / 5.0e6) * (esize == 2 ? 41500.0 : 8900.0);
     if (i == first || cost < least) {
       least = cost;
@@ -482,7 +499,7 @@ void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
   constexpr int BM = WM * FM * 16, BN = WN * FN * 16 / (kMode == kDual ? 2 : 1);
   g.gridM = (g.M + BM - 1) / BM;
   g.gridN = (g.N + BN - 1) / BN;
-  const dim3 grid((unsigned)g.gridM * g.gridN * (kMode == kInputs ? g.parts : 1)), block(WM * WN * kWave);
+  const dim3 grid((unsigned)g.gridM * g.gridN * g.parts), block(WM * WN * kWave);
   if constexpr (kMode == kDual && sizeof(T) == 2)  // (float rows are aligned, the others' are made so)
     if (!direct) {
       hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, false>), grid, block, 0, stream, g);
@@ -497,7 +514,7 @@ bool rows4(const void* p, int64_t ld) {
 template <typename T, Mode kMode>
 void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
   const bool direct = kMode != kDual || (rows4<T>(g.A, g.lda) && rows4<T>(g.B, g.ldb) && rows4<T>(g.B2, g.ldb2));
-  const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode == kInputs);
+  const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode != kDual);
   g.parts = plan.parts;
   g.each = plan.each;
   if (plan.tile == 0) {
@@ -509,10 +526,10 @@ void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
   } else {
     launch_gemm_tile<T, 2, 2, 1, 2, kMode>(g, direct, stream);
   }
-  if constexpr (kMode == kInputs)
+  if constexpr (kMode != kDual)
     if (g.parts > 1) {
       const int64_t quads = ((int64_t)g.M * g.N + 3) / 4, groups = (quads + 255) / 256;
-      hipLaunchKernelGGL((join_kernel<T>), dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream, g);
+      hipLaunchKernelGGL((join_kernel<T, kMode>), dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream, g);
     }
 }
 
@@ -713,7 +730,7 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
       in.ld_x = o.pitch;
     }
   }
-  float* const part = reinterpret_cast<float*>(ws);                 // [parts, M, K]
+  float* const part = reinterpret_cast<float*>(ws);                 // dx's parts, then the weights' gradients'
   hipLaunchKernelGGL((operands_kernel<T>), dim3(o.slopes + 2 * o.weights + o.inputs), dim3(256), 0, stream, a, zeros,
                      both, Fp, o);
   GemmArgs<T> g = {};
@@ -723,6 +740,7 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
   g.N = a.K;
   g.split = Fp;
   g.rows = a.F;
+  g.part = part;
   if (a.dx) {
     g.M = a.M;
     g.K = 2 * Fp;
@@ -732,7 +750,6 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
     g.ldb2 = in.ld_wu;
     g.C = static_cast<T*>(a.dx);
     g.ldc = a.ld_dx;
-    g.part = part;
     launch_gemm<T, kInputs>(g, stream);
   }
   if (a.dwg) {
@@ -767,10 +784,11 @@ hipError_t launch_ffn_no_rows_t(const FfnArgs& a, hipStream_t stream) {
 size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize) {
   if (M == 0) return 0;
   const int64_t Fp = padded(F);
-  const int parts = plan_gemm(M, K, 2 * Fp, esize, true).parts;  // of dx
+  const int64_t inputs = plan_gemm(M, K, 2 * Fp, esize, true).parts, weights = plan_gemm(2 * Fp, K, M, esize, true).parts;
+  const size_t x = inputs > 1 ? (size_t)inputs * M * K : 0, w = weights > 1 ? (size_t)weights * 2 * Fp * K : 0;
   const int64_t pitch = (K * esize + 15) / 16 * 16 / esize;
   const size_t copies = copies_kept(K, esize) ? 2 * area_bytes(F * pitch, esize) + area_bytes(M * pitch, esize) : 0;
-  return 256 + area_bytes(M * 2 * Fp, esize) + copies + (parts > 1 ? (size_t)parts * M * K * sizeof(float) : 0);
+  return 256 + area_bytes(M * 2 * Fp, esize) + copies + (x > w ? x : w) * sizeof(float);
 }
 
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {

@@ -134,6 +134,26 @@ def test_ffn_long_sums(dtype, M, K, F):
     assert torch.equal(wide, d["x"]) and torch.isnan(wide._base[..., :3]).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F", [(5001, 48, 40), (3000, 131, 70)])
+def test_ffn_many_rows(dtype, M, K, F):
+    """Many rows over few inputs and units: the weights' gradients are summed in parts, in a
+    workspace of any content, in a fixed order, and written alone where they are asked alone."""
+    import state_space_sequence_exp_amd as m3
+    r, t = inputs([11, M, K, F], M, K, F, dtype)
+    h, g, u, d = check(r, t, dtype)
+    args = (t["dh"], t["x"], t["wg"], t["wu"], g, u)
+    need = m3.gated_ffn_backward_workspace_size(M, K, F, torch.bfloat16 if dtype == "bf16" else torch.float32)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")      # NaN
+    again = m3.gated_ffn_backward(*args, workspace=ws)
+    assert all(torch.equal(again[k], d[k]) for k in d) and (ws[need:] == 255).all()
+    only = m3.gated_ffn_backward(*args, want_x=False)
+    assert all(torch.equal(only[k], d[k]) for k in ("w_gate", "w_up"))
+    wide = {k: sliced(torch.zeros_like(d[k])) for k in ("w_gate", "w_up")}
+    m3.gated_ffn_backward(*args, dw_gate=wide["w_gate"], dw_up=wide["w_up"])
+    assert all(torch.equal(wide[k], d[k]) and torch.isnan(wide[k]._base[..., :3]).all() for k in wide)
+
+
 def test_ffn_no_rows():
     import state_space_sequence_exp_amd as m3
     _, t = inputs(5, 4, 24, 32, "f32")
