@@ -768,12 +768,13 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
 
 template <typename T>
 __global__ void __launch_bounds__(256) zero_rows_kernel(T* p, int64_t ld, int R, int C) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < (int64_t)R * C) p[i / C * ld + i % C] = from_f32<T>(0.f);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)R * C; i += (int64_t)gridDim.x * 256)
+    p[i / C * ld + i % C] = from_f32<T>(0.f);
 }
 template <typename T>
 hipError_t launch_ffn_no_rows_t(const FfnArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)a.F * a.K + 255) / 256));
+  const int64_t groups = ((int64_t)a.F * a.K + 255) / 256;
+  const dim3 grid((unsigned)(groups < 4096 ? groups : 4096));
   hipLaunchKernelGGL((zero_rows_kernel<T>), grid, dim3(256), 0, stream, static_cast<T*>(a.dwg), a.ld_dwg, a.F, a.K);
   hipLaunchKernelGGL((zero_rows_kernel<T>), grid, dim3(256), 0, stream, static_cast<T*>(a.dwu), a.ld_dwu, a.F, a.K);
   return hipGetLastError();
@@ -789,6 +790,11 @@ size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize) {
   const int64_t pitch = (K * esize + 15) / 16 * 16 / esize;
   const size_t copies = copies_kept(K, esize) ? 2 * area_bytes(F * pitch, esize) + area_bytes(M * pitch, esize) : 0;
   return 256 + area_bytes(M * 2 * Fp, esize) + copies + (x > w ? x : w) * sizeof(float);
+}
+
+double ffn_operand_groups(int64_t M, int64_t K, int64_t F, int esize) {
+  const double chunks = (double)M * padded(F) + (copies_kept(K, esize) ? (2.0 * F + M) * (K + 8.0) : 0.0);
+  return chunks * esize / 16 / 256 + 4;
 }
 
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {

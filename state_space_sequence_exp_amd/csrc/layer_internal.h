@@ -145,6 +145,7 @@ struct FfnArgs {
   void* workspace;
 };
 size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize);
+double ffn_operand_groups(int64_t M, int64_t K, int64_t F, int esize);  // workgroups of its first launch
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream);
 hipError_t launch_ffn_backward(const FfnArgs& a, m3_dtype dtype, hipStream_t stream);
 

@@ -262,7 +262,7 @@ namespace {
 constexpr int64_t kMaxFfnLd = (1 << 22) - 1;
 constexpr double kMaxFfnTiles = 8.0e6;  // of 64 x 64, of up to 512 threads
 
-m3_status check_ffn(const m3_ffn_dims* d, bool backward) {
+m3_status check_ffn(const m3_ffn_dims* d, m3_dtype dtype, bool backward) {
   if (!d) return M3_ERR_INVALID_VALUE;
   if (d->rows < 0 || d->channels < 1 || d->hidden < 1) return M3_ERR_INVALID_VALUE;
   const struct {
@@ -282,6 +282,8 @@ m3_status check_ffn(const m3_ffn_dims* d, bool backward) {
   if (backward && (d->rows > kMaxFfnLd - 63 || d->hidden > kMaxFfnLd / 2 - 63)) return M3_ERR_NOT_SUPPORTED;
   if (d->rows > INT_MAX - 64 || M * F / 2048 > kMaxFfnTiles || M * K / 4096 > kMaxFfnTiles ||
       F * K / 2048 > kMaxFfnTiles)
+    return M3_ERR_NOT_SUPPORTED;
+  if (backward && m3::ffn_operand_groups(d->rows, d->channels, d->hidden, (int)esize_of(dtype)) > kMaxGroups256)
     return M3_ERR_NOT_SUPPORTED;
   return M3_SUCCESS;
 }
@@ -312,7 +314,7 @@ m3_status m3_gated_ffn(const m3_ffn_dims* dims, m3_dtype dtype, const void* x,
                        const void* w_gate, const void* w_up, void* h, float* gate, float* up,
                        void* stream) {
   if (!dtype_ok(&dtype)) return M3_ERR_INVALID_VALUE;
-  const m3_status st = check_ffn(dims, false);
+  const m3_status st = check_ffn(dims, dtype, false);
   if (st != M3_SUCCESS) return st;
   if (dims->rows == 0) return M3_SUCCESS;
   const uintptr_t es = esize_of(dtype);
@@ -335,7 +337,7 @@ m3_status m3_gated_ffn(const m3_ffn_dims* dims, m3_dtype dtype, const void* x,
 }
 
 size_t m3_gated_ffn_backward_workspace_size(const m3_ffn_dims* dims, m3_dtype dtype) {
-  if (!dtype_ok(&dtype) || check_ffn(dims, true) != M3_SUCCESS) return 0;
+  if (!dtype_ok(&dtype) || check_ffn(dims, dtype, true) != M3_SUCCESS) return 0;
   return m3::ffn_backward_workspace(dims->rows, dims->channels, dims->hidden, (int)esize_of(dtype));
 }
 
@@ -345,7 +347,7 @@ m3_status m3_gated_ffn_backward(const m3_ffn_dims* dims, m3_dtype dtype, const v
                                 void* dw_up, void* workspace, size_t workspace_bytes,
                                 void* stream) {
   if (!dtype_ok(&dtype)) return M3_ERR_INVALID_VALUE;
-  const m3_status st = check_ffn(dims, true);
+  const m3_status st = check_ffn(dims, dtype, true);
   if (st != M3_SUCCESS) return st;
   const uintptr_t es = esize_of(dtype);
   if (!maybe(dx, es) || !maybe(dw_gate, es) || !maybe(dw_up, es) ||

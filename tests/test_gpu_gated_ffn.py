@@ -164,6 +164,22 @@ def test_ffn_no_rows():
     assert d["x"].shape == (0, 24) and not d["w_gate"].any() and not d["w_up"].any()
 
 
+def test_ffn_no_rows_wide_weights():
+    """More zeros to write than one launch has threads."""
+    import state_space_sequence_exp_amd as m3
+    F, K = 70000, 61400                                             # > 2^32 elements
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    kept = torch.empty(0, F, device="cuda")
+    wg, wu = new(F, K), new(F, K)
+    dg, du = torch.full_like(wg, float("nan")), torch.full_like(wu, float("nan"))
+    d = m3.gated_ffn_backward(new(0, F), new(0, K), wg, wu, kept, kept, dw_gate=dg, dw_up=du)
+    assert d["w_gate"] is dg
+    for w in (dg, du):
+        assert all(not piece.any() for piece in w.view(torch.int16).split(10000))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M", [3, 100])
 def test_ffn_extremes(dtype, M):

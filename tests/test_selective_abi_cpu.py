@@ -188,6 +188,15 @@ def test_ffn_shapes(lib, bad, code):
     assert lib.m3_gated_ffn_backward_workspace_size(ffn_dims(**bad), 1) == 0
 
 
+def test_ffn_largest_operands(lib):
+    """Copies of rows that are not whole 16-byte chunks: as many as one launch takes."""
+    size = lambda t, **kw: lib.m3_gated_ffn_backward_workspace_size(ffn_dims(hidden=1, **kw), t)
+    big = dict(rows=4190000, ld_x=0, ld_wgate=0, ld_wup=0)
+    assert size(0, channels=7701, **big) == 0 and size(0, channels=7700, **big) > 0
+    assert size(1, channels=7701, **big) > 0 and size(0, channels=3901, **big) > 0
+    assert ffn_bw(lib, dt=0, hidden=1, channels=7701, **big) == UNS
+
+
 def test_ffn_pointers(lib):
     assert ffn(lib, dt=2) == INV and lib.m3_gated_ffn(None, 1, *FFN, None) == INV
     assert ffn(lib, ld_h=95) == INV
