@@ -23,7 +23,7 @@
 //
 // B1 T16384 D4096 N16 bfloat16 with the gate takes 384 us: its scanning waves alone 320,
 // at one a SIMD, which issues an operation in about five cycles, not four; the vector
-// units are busy for 80% of the time.  (With every wave doing both halves' work in turn,
+// units are busy for 85% of the cycles.  (With every wave doing both halves' work in turn,
 // 589 us; the sums by matrix instructions, 586 and more: they wait for their operands
 // and hold up the wave; the sums left to the other half's waves, 703.)  With more
 // waves a state and token takes 0.31 to 0.34 ps (B4 T2048 D4096) instead of 0.36.

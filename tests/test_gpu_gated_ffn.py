@@ -154,6 +154,28 @@ def test_ffn_many_rows(dtype, M, K, F):
     assert all(torch.equal(wide[k], d[k]) and torch.isnan(wide[k]._base[..., :3]).all() for k in wide)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,F", [(2050, 4096), (500, 200), (30, 200)])
+def test_ffn_far_rows(dtype, M, F):
+    """Rows as far apart as is taken, offsets past 32 bits: the results of dense ones."""
+    import state_space_sequence_exp_amd as m3
+    K, ld = 72, 2 ** 22 - 2
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    _, t = inputs([12, M, F], M, K, F, dtype)
+    wide = torch.empty(M, ld, dtype=t["x"].dtype, device="cuda")
+    x, dx, h, dh = wide[:, :K], wide[:, 100:100 + K], wide[:, 1000:1000 + F], wide[:, -F:]
+    x.copy_(t["x"]), dh.copy_(t["dh"])
+    want, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True)
+    got, gf, uf = m3.gated_ffn(x, t["wg"], t["wu"], want_pre=True, h=h)
+    assert got is h and torch.equal(h, want) and torch.equal(gf, g) and torch.equal(uf, u)
+    d = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u)
+    far = m3.gated_ffn_backward(dh, x, t["wg"], t["wu"], g, u, dx=dx)
+    assert far["x"] is dx and all(torch.equal(far[k], d[k]) for k in d)
+    with pytest.raises(Exception):
+        m3.gated_ffn(torch.empty(2, 2 ** 22, dtype=x.dtype, device="cuda")[:, :K], t["wg"], t["wu"])
+
+
 def test_ffn_no_rows():
     import state_space_sequence_exp_amd as m3
     _, t = inputs(5, 4, 24, 32, "f32")
