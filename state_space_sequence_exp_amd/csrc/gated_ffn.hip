@@ -461,7 +461,11 @@ __global__ void __launch_bounds__(256) join_kernel(GemmArgs<T> g) {
 // bfloat16: 61 to 48 us, of 20000 x 64 x 300 120 to 44, float 291 to 75);
 // joining them takes some 6 us and the parts' way through memory, in the unit of the
 // rest: a chip of largest tiles takes 128 bytes of k in 1.6 us, float in 7.4.  No tile
-// takes them in less than 0.3 us, which its loads and barriers need.
+// takes them in less than 0.3 us, which its loads and barriers need.  The two smallest
+// tiles' workgroups, a wave a SIMD, wait less where two share a CU: in float a tile by
+// itself takes 1.3 times its share, and k is cut until there are two (the backward pass
+// of 256 x 2048 x 4096: 167 to 151 us, of 16384 x 256 x 1024: 354 to 331); bfloat16, whose
+// parts take longer to join than their products, gains nothing.
 struct Plan {
   int tile, parts, each;
 };
@@ -476,13 +480,15 @@ Plan plan_gemm(int64_t M, int64_t cols, int64_t K, int esize, bool cut) {
   const int first = esize == 2 ? 0 : 1;  // (the largest gains nothing in float)
   for (int i = first; i < 4; ++i) {
     const int64_t count = (M + tiles[i].m - 1) / tiles[i].m * ((cols + tiles[i].n - 1) / tiles[i].n);
-    int64_t parts = cut ? 256 / count : 1;
+    const bool pairs = esize == 4 && i >= 2;
+    int64_t parts = cut ? (pairs ? 512 : 256) / count : 1;
     if (parts > steps / 8) parts = steps / 8;
     if (parts < 1) parts = 1;
     const int64_t each = (steps + parts - 1) / parts;
     parts = (steps + each - 1) / each;
     const double rate = esize == 2 ? tiles[i].bf16 : tiles[i].f32;
-    double cost = (double)((count * parts + 255) / 256) * tiles[i].m * tiles[i].n / rate;
+    const int64_t rounds = (count * parts + 255) / 256;
+    double cost = (pairs && rounds == 1 ? 1.3 : (double)rounds) * tiles[i].m * tiles[i].n / rate;
     const double alone = esize == 2 ? 12000.0 : 2700.0;
     cost = (cost < alone ? alone : cost) * (double)each;
     if (parts > 1) cost += (6.0 + (double)parts * (double)M * (double)cols * 8.0 / 5.0e6) * (esize == 2 ? 41500.0 : 8900.0);
