@@ -16,9 +16,10 @@
 //
 // Bound by the matrix units at the rate that the chip's power leaves them: 16384 x 2048
 // x 4096 bfloat16 407 us, 1350 TFLOP/s (a product of that size alone, by the library,
-// 1370), the largest tile's waves reading their fragments of the next half tile from
-// the LDS between the matrix instructions of this one; float 145 of 155 TFLOP/s.  A few
-// rows are bound by the weights' bytes (few_kernel).
+// 1370 to 1470), the largest tile's waves reading their fragments of the next half tile
+// from the LDS between the matrix instructions of this one (those of 32 x 32 take as many
+// cycles at a lower clock, 8% more time); float 145 of 155 TFLOP/s.  A few rows are bound
+// by the weights' bytes (few_kernel).
 //
 // (dg and du are rounded to the storage type, as the matrix units take it; g and u
 // are kept in float, or each gradient would carry their rounding as well: 0.0031
