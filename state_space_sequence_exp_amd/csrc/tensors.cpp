@@ -15,6 +15,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/util/SmallVector.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -22,14 +23,22 @@
 
 namespace {
 
-constexpr int kMaxDims = 8;
+using Sizes = c10::SmallVector<int64_t, 8>;  // (more dimensions than that take an allocation)
 
 struct Wanted {
   at::ScalarType type;
-  int64_t sizes[kMaxDims];
-  Py_ssize_t dims;
+  Sizes sizes;
   long device;
 };
+
+// The numbers of a tuple; false with Python's error set.
+bool sizes_of(PyObject* tuple, Sizes& sizes) {
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tuple); ++i) {
+    sizes.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(tuple, i)));
+    if (sizes.back() == -1 && PyErr_Occurred()) return false;
+  }
+  return true;
+}
 
 // The first three arguments.
 bool wanted(PyObject* const* args, Py_ssize_t n, Wanted& w) {
@@ -38,21 +47,13 @@ bool wanted(PyObject* const* args, Py_ssize_t n, Wanted& w) {
     return false;
   }
   w.type = reinterpret_cast<THPDtype*>(args[0])->scalar_type;
-  w.dims = PyTuple_GET_SIZE(args[1]);
-  if (w.dims > kMaxDims) return true;  // (no tensor is found to have it)
-  for (Py_ssize_t i = 0; i < w.dims; ++i) {
-    w.sizes[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], i));
-    if (w.sizes[i] == -1 && PyErr_Occurred()) return false;
-  }
+  if (!sizes_of(args[1], w.sizes)) return false;
   w.device = PyLong_AsLong(args[2]);
   return !(w.device == -1 && PyErr_Occurred());
 }
 
 bool matches(const at::Tensor& t, const Wanted& w) {
-  if (t.scalar_type() != w.type || t.dim() != w.dims || w.dims > kMaxDims || t.layout() != at::kStrided) return false;
-  const at::IntArrayRef sizes = t.sizes();
-  for (Py_ssize_t i = 0; i < w.dims; ++i)
-    if (sizes[i] != w.sizes[i]) return false;
+  if (t.scalar_type() != w.type || t.layout() != at::kStrided || t.sizes() != at::IntArrayRef(w.sizes)) return false;
   return (t.is_cuda() ? (long)t.get_device() : -1) == w.device;
 }
 
@@ -116,19 +117,14 @@ PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
-    if (n != 3 || !THPDtype_Check(args[0]) || !PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) > kMaxDims ||
-        !THPVariable_Check(args[2])) {
-      PyErr_SetString(PyExc_TypeError, "expected (dtype, shape of up to 8 dimensions, tensor)");
+    if (n != 3 || !THPDtype_Check(args[0]) || !PyTuple_Check(args[1]) || !THPVariable_Check(args[2])) {
+      PyErr_SetString(PyExc_TypeError, "expected (dtype, shape, tensor)");
       return nullptr;
     }
-    int64_t sizes[kMaxDims];
-    const Py_ssize_t dims = PyTuple_GET_SIZE(args[1]);
-    for (Py_ssize_t i = 0; i < dims; ++i) {
-      sizes[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], i));
-      if (sizes[i] == -1 && PyErr_Occurred()) return nullptr;
-    }
+    Sizes sizes;
+    if (!sizes_of(args[1], sizes)) return nullptr;
     const auto like = THPVariable_Unpack(args[2]).options();
-    return THPVariable_Wrap(at::empty(at::IntArrayRef(sizes, dims),
+    return THPVariable_Wrap(at::empty(at::IntArrayRef(sizes),
                                       like.dtype(reinterpret_cast<THPDtype*>(args[0])->scalar_type).requires_grad(false)));
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
