@@ -20,6 +20,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <utility>
 
 namespace {
 
@@ -73,46 +74,47 @@ int64_t distance(const at::Tensor& t) {
   return ld;
 }
 
+// A reference to a new object, given up where it is not handed on.
+class Held {
+ public:
+  explicit Held(PyObject* p) : p_(p) {}
+  Held(const Held&) = delete;
+  Held& operator=(const Held&) = delete;
+  ~Held() { Py_XDECREF(p_); }
+  PyObject* get() const { return p_; }
+  PyObject* hand_on() { return std::exchange(p_, nullptr); }
+
+ private:
+  PyObject* p_;
+};
+
 template <bool kRows>
 PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Wanted w;
   if (!wanted(args, n, w)) return nullptr;
   constexpr int kEach = kRows ? 2 : 1;
-  PyObject* out = PyTuple_New((n - 3) * kEach);
-  if (!out) return nullptr;
+  Held out(PyTuple_New((n - 3) * kEach));
+  if (!out.get()) return nullptr;
   for (Py_ssize_t i = 3; i < n; ++i) {
     int64_t ld = 0;
     uintptr_t at = 0;
     if (args[i] != Py_None) {
-      bool good = THPVariable_Check(args[i]);
-      if (good) {
-        const at::Tensor& t = THPVariable_Unpack(args[i]);
-        good = matches(t, w);
-        if (good && kRows) good = (ld = distance(t)) >= 0;
-        if (good && !kRows) good = t.is_contiguous();
-        if (good) at = reinterpret_cast<uintptr_t>(t.data_ptr());
-      }
-      if (!good) {
-        Py_DECREF(out);
-        Py_RETURN_NONE;
-      }
+      if (!THPVariable_Check(args[i])) Py_RETURN_NONE;
+      const at::Tensor& t = THPVariable_Unpack(args[i]);
+      if (!matches(t, w)) Py_RETURN_NONE;
+      if (kRows ? (ld = distance(t)) < 0 : !t.is_contiguous()) Py_RETURN_NONE;
+      at = reinterpret_cast<uintptr_t>(t.data_ptr());
     }
     PyObject* address = PyLong_FromUnsignedLongLong(at);
-    if (!address) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-    PyTuple_SET_ITEM(out, (i - 3) * kEach, address);
+    if (!address) return nullptr;
+    PyTuple_SET_ITEM(out.get(), (i - 3) * kEach, address);
     if (kRows) {
       PyObject* between = PyLong_FromLongLong(ld);
-      if (!between) {
-        Py_DECREF(out);
-        return nullptr;
-      }
-      PyTuple_SET_ITEM(out, (i - 3) * kEach + 1, between);
+      if (!between) return nullptr;
+      PyTuple_SET_ITEM(out.get(), (i - 3) * kEach + 1, between);
     }
   }
-  return out;
+  return out.hand_on();
 }
 
 PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {

@@ -1,5 +1,8 @@
 """CPU checks of the compiled look at a call's tensors: any number of dimensions,
 rows of slices, and what is not an array of rows."""
+import gc
+import sys
+
 import pytest
 import torch
 
@@ -43,3 +46,25 @@ def test_feed_forward_takes_any_leading_axes(dims):
         m3.gated_ffn(torch.zeros(lead[:-1] + (6, 2)).transpose(-1, -2), w, w)
     with pytest.raises(ValueError, match="x: its rows must follow"):
         m3.gated_ffn(torch.zeros(lead[:-2] + (3, 2, 6)).transpose(-2, -3)[..., :2, :], w, w)
+
+
+def test_refused_address_keeps_nothing(look):
+    """Where torch refuses a tensor's address, the call raises and what it had made is
+    given up: a handful of objects for the test itself, not some for every call."""
+    t, grown = torch.empty(3), []
+
+    def f(v):  # a batched tensor, which has none
+        def go():
+            try:
+                look.dense(torch.float32, (3,), -1, t, t, t, t, v)
+            except RuntimeError:
+                return True
+        assert all(go() for _ in range(20))
+        gc.collect()
+        before = sys.getallocatedblocks()
+        for _ in range(500):
+            go()
+        grown.append(sys.getallocatedblocks() - before)
+        return v
+    torch.vmap(f)(torch.empty(2, 3))
+    assert grown[0] < 500
