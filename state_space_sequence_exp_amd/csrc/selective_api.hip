@@ -354,25 +354,25 @@ m3_status m3_gated_ffn_backward(const m3_ffn_dims* dims, m3_dtype dtype, const v
       (dw_gate == nullptr) != (dw_up == nullptr))
     return M3_ERR_INVALID_VALUE;
   m3::FfnArgs a = ffn_args(dims);
-  const Span dxs = rows_of(dx, a.M, a.K, a.ld_dx, es), dwgs = rows_of(dw_gate, a.F, a.K, a.ld_dwg, es);
-  const Span dwus = rows_of(dw_up, a.F, a.K, a.ld_dwu, es);
-  if (dims->rows == 0) {
-    if (!dw_gate) return M3_SUCCESS;
-    if (meet(dwgs, dwus)) return M3_ERR_INVALID_VALUE;
-  } else {
+  size_t bytes = 0;
+  if (dims->rows > 0) {
     if (!need(dh, es) || !need(x, es) || !need(w_gate, es) || !need(w_up, es) || !need(gate, 4) ||
         !need(up, 4))
       return M3_ERR_INVALID_VALUE;
     if (!dx && !dw_gate) return M3_SUCCESS;
-    const size_t bytes = m3_gated_ffn_backward_workspace_size(dims, dtype);
+    bytes = m3_gated_ffn_backward_workspace_size(dims, dtype);
     if (!workspace || workspace_bytes < bytes) return M3_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return M3_ERR_INVALID_VALUE;
-    const Span out[] = {dxs, dwgs, dwus, bytes_of(workspace, bytes)};
-    const Span in[] = {rows_of(x, a.M, a.K, a.ld_x, es),      rows_of(w_gate, a.F, a.K, a.ld_wg, es),
-                       rows_of(w_up, a.F, a.K, a.ld_wu, es),  rows_of(dh, a.M, a.F, a.ld_dh, es),
-                       rows_of(gate, a.M, a.F, a.ld_gate, 4), rows_of(up, a.M, a.F, a.ld_up, 4)};
-    if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
+  } else if (!dw_gate) {
+    return M3_SUCCESS;
   }
+  // (without rows the gradients are still written: not over each other or the weights)
+  const Span out[] = {rows_of(dx, a.M, a.K, a.ld_dx, es), rows_of(dw_gate, a.F, a.K, a.ld_dwg, es),
+                      rows_of(dw_up, a.F, a.K, a.ld_dwu, es), bytes_of(workspace, bytes)};
+  const Span in[] = {rows_of(x, a.M, a.K, a.ld_x, es),      rows_of(w_gate, a.F, a.K, a.ld_wg, es),
+                     rows_of(w_up, a.F, a.K, a.ld_wu, es),  rows_of(dh, a.M, a.F, a.ld_dh, es),
+                     rows_of(gate, a.M, a.F, a.ld_gate, 4), rows_of(up, a.M, a.F, a.ld_up, 4)};
+  if (outputs_meet(out, in)) return M3_ERR_INVALID_VALUE;
   a.dh = dh;
   a.x = x;
   a.wg = w_gate;
