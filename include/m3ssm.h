@@ -729,8 +729,10 @@ m3_status m3_selective_scan_step(const m3_select_dims* dims, m3_dtype dtype, flo
  * Row r of an array is at r ld.  Pointers need element alignment; the products
  * run fastest where every row of x and of the weights starts at a multiple of 4
  * bytes (float rows always do).  Outputs must not overlap an input or each other.
- * K, F and every ld are at most 2^22 - 1 (backward: F at most 2^21 - 64, rows at
- * most 2^22 - 64).
+ * K, F and every ld are at most 2^22 - 1 (backward: F at most 2^21 - 64).  Rows are
+ * limited by launches alone: (rows + 64) (F + 64) and (F + 64) (K + 64) are at most
+ * 1.6e10, (rows + 64) (K + 64) twice that; backward, 2^36 bytes of each of dg and du and
+ * of the copies below.
  */
 typedef struct {
   int64_t rows;     /* (>= 0) */

@@ -257,8 +257,8 @@ m3_status m3_selective_scan_step(const m3_select_dims* dims, m3_dtype dtype, flo
 
 namespace {
 
-// Rows, columns and leading dimensions that a tile's 32-bit indexes hold, and grids
-// of tiles that a launch takes.
+// Leading dimensions whose rows a tile's 32-bit offsets reach (256 of them, in bytes),
+// and grids of tiles that a launch takes.
 constexpr int64_t kMaxFfnLd = (1 << 22) - 1;
 constexpr double kMaxFfnTiles = 8.0e6;  // of 64 x 64, of up to 512 threads
 
@@ -278,8 +278,8 @@ m3_status check_ffn(const m3_ffn_dims* d, m3_dtype dtype, bool backward) {
   for (const auto& a : arrays)
     if (a.here && ld_of(a.ld, a.row) > kMaxFfnLd) return M3_ERR_NOT_SUPPORTED;
   const double M = (double)d->rows + 64, K = (double)d->channels + 64, F = (double)d->hidden + 64;
-  // (backward, dg and du lie side by side, and transposed)
-  if (backward && (d->rows > kMaxFfnLd - 63 || d->hidden > kMaxFfnLd / 2 - 63)) return M3_ERR_NOT_SUPPORTED;
+  // (backward, dg and du lie side by side, whole tiles each)
+  if (backward && d->hidden > kMaxFfnLd / 2 - 63) return M3_ERR_NOT_SUPPORTED;
   if (d->rows > INT_MAX - 64 || M * F / 2048 > kMaxFfnTiles || M * K / 4096 > kMaxFfnTiles ||
       F * K / 2048 > kMaxFfnTiles)
     return M3_ERR_NOT_SUPPORTED;

@@ -2,7 +2,10 @@
 import pytest
 import torch
 
-from test_gpu_gated_ffn import inputs
+from gpu_util import from_gpu
+from layer_util import HALF_STEP, close
+from oracle import selective as O
+from test_gpu_gated_ffn import TYPES, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +26,29 @@ def test_ffn_many_leading_axes():
     e = m3.gated_ffn_backward(t["dh"].view(lead + (F,)), x, t["wg"], t["wu"], got[1], got[2])
     assert e["x"].shape == lead + (K,) and torch.equal(e["x"].view(M, K), d["x"])
     assert all(torch.equal(e[k], d[k]) for k in ("w_gate", "w_up"))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ffn_many_more_rows(dtype):
+    """More than 2^22 rows, forward and backward.  dh is zeros but for some rows, the last
+    ones among them, so that the gradients are those of these rows alone."""
+    import state_space_sequence_exp_amd as m3
+    M, K, F = 2 ** 22 + 4099, 16, 12
+    _, t = inputs([22], 64, K, F, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(M, K, device="cuda", generator=gen).to(t["x"].dtype)
+    rows = torch.cat([torch.arange(0, 20), torch.randint(20, M - 50, (30,)), torch.arange(M - 50, M)]).unique().cuda()
+    dh = torch.zeros(M, F, dtype=x.dtype, device="cuda")
+    dh[rows] = torch.randn(len(rows), F, device="cuda", generator=gen).to(x.dtype)
+    h, g, u = m3.gated_ffn(x, t["wg"], t["wu"], want_pre=True)
+    d = m3.gated_ffn_backward(dh, x, t["wg"], t["wu"], g, u)
+    r = [from_gpu(a) for a in (dh[rows], x[rows], t["wg"], t["wu"])]
+    o = O.gated_ffn(*r[1:])
+    for got, k, kind in ((h, "h", dtype), (g, "g", "f32"), (u, "u", "f32")):
+        close(got[rows], o[k], o["e_" + k], kind, k)
+    w = O.gated_ffn_backward(*r, HALF_STEP[dtype] if dtype == "bf16" else 0.0)
+    close(d["x"][rows], w["dx"], w["e_dx"], dtype, "dx")
+    for k in ("w_gate", "w_up"):
+        close(d[k], w["d" + k], w["e_d" + k], dtype, "d" + k)
+    d["x"][rows] = 0
+    assert not d["x"].any()

@@ -1,6 +1,8 @@
 """More CPU checks of the host's refusals: the short convolution, the selective
 scan and the gated feed-forward projections."""
-from test_selective_abi_cpu import FFN_BW, GOOD, INV, ffn_bw, lib, swap  # noqa: F401
+import pytest
+
+from test_selective_abi_cpu import FFN_BW, GOOD, INV, UNS, ffn_bw, ffn_dims, lib, swap  # noqa: F401
 
 
 def test_ffn_backward_without_rows(lib):  # noqa: F811
@@ -9,3 +11,17 @@ def test_ffn_backward_without_rows(lib):  # noqa: F811
     for o in (7, 8):
         for w in (2, 3):
             assert ffn_bw(lib, swap(FFN_BW, **{"_%d" % o: FFN_BW[w]}), rows=0) == INV
+
+
+@pytest.mark.parametrize("rows,K,F,good", [
+    (1 << 22, 64, 96, True), (100000000, 64, 96, True), (230000000, 1, 1, True), (1 << 23, 1024, 1800, True),
+    (110000000, 64, 96, False), (1 << 28, 1, 1, False), (1 << 23, 1024, 2048, False), (1 << 23, 4000, 64, False)])
+def test_ffn_rows_bounded_by_tiles_alone(lib, rows, K, F, good):  # noqa: F811
+    """Forward and backward take the same rows: as many as the tiles of one launch, rows x units
+    and rows x channels (an unaligned gate tells a call that would be taken)."""
+    kw = dict(rows=rows, channels=K, hidden=F)
+    for dt in (0, 1):
+        size = lib.m3_gated_ffn_backward_workspace_size(ffn_dims(**kw), dt)
+        assert (size > rows * 2 * F * (4 - 2 * dt)) if good else size == 0
+        off = swap(FFN_BW, _5=FFN_BW[5].value + 1)
+        assert ffn_bw(lib, off, dt=dt, **kw) == (INV if good else UNS)
