@@ -731,8 +731,8 @@ m3_status m3_selective_scan_step(const m3_select_dims* dims, m3_dtype dtype, flo
  * bytes (float rows always do).  Outputs must not overlap an input or each other.
  * K, F and every ld are at most 2^22 - 1 (backward: F at most 2^21 - 64).  Rows are
  * limited by launches alone: (rows + 64) (F + 64) and (F + 64) (K + 64) are at most
- * 1.6e10, (rows + 64) (K + 64) twice that; backward, 2^36 bytes of each of dg and du and
- * of the copies below.
+ * 1.6e10, (rows + 64) (K + 64) twice that; backward, dg and the copies below that
+ * the arrays need are together at most 2^36 bytes.
  */
 typedef struct {
   int64_t rows;     /* (>= 0) */
@@ -759,7 +759,9 @@ m3_status m3_gated_ffn(const m3_ffn_dims* dims, m3_dtype dtype, const void* x,
  * together (weights that do not).  rows == 0 writes zeros to dw_gate and dw_up.
  * The workspace (256-byte aligned) holds dg and du, copies of x and the weights for
  * where their rows are not whole 16-byte chunks at multiples of 4 bytes, and the parts
- * of gradients that are summed in parts; it need not be cleared.
+ * of gradients that are summed in parts; it need not be cleared.  Its size holds for
+ * any pointers and distances between rows, so that for bfloat16 it has room for the
+ * copies whether or not a call makes them.
  * Outputs and the workspace must not overlap an input or each other.
  */
 size_t m3_gated_ffn_backward_workspace_size(const m3_ffn_dims* dims, m3_dtype dtype);

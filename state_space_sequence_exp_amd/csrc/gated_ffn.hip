@@ -514,13 +514,14 @@ void launch_gemm_tile(GemmArgs<T> g, bool direct, hipStream_t stream) {
     }
   hipLaunchKernelGGL((gemm_kernel<T, WM, WN, FM, FN, kMode, true>), grid, block, 0, stream, g);
 }
-template <typename T>
-bool rows4(const void* p, int64_t ld) {
-  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * (int64_t)sizeof(T) % 4 == 0;
+bool rows4(const void* p, int64_t ld, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld * es % 4 == 0;
 }
 template <typename T, Mode kMode>
 void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
-  const bool direct = kMode != kDual || (rows4<T>(g.A, g.lda) && rows4<T>(g.B, g.ldb) && rows4<T>(g.B2, g.ldb2));
+  constexpr int es = (int)sizeof(T);
+  const bool direct =
+      kMode != kDual || (rows4(g.A, g.lda, es) && rows4(g.B, g.ldb, es) && rows4(g.B2, g.ldb2, es));
   const Plan plan = plan_gemm(g.M, (kMode == kDual ? 2 : 1) * (int64_t)g.N, g.K, (int)sizeof(T), kMode != kDual);
   g.parts = plan.parts;
   g.each = plan.each;
@@ -674,7 +675,8 @@ __global__ void __launch_bounds__(256) operands_kernel(FfnArgs a, u32x4* zeros, 
 int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
 size_t area_bytes(int64_t n, int es) { return ((size_t)n * es + 255) / 256 * 256; }
 // Whether the workspace has room for copies of x and the weights: where their rows may
-// not be whole 16-byte chunks at multiples of 4 bytes.
+// not be whole 16-byte chunks at multiples of 4 bytes.  (For bfloat16 always: its size
+// is promised for any distances between rows and any pointers, which it is not told.)
 bool copies_kept(int64_t K, int es) { return es == 2 || K % 4 != 0; }
 
 template <typename T>
@@ -724,14 +726,14 @@ hipError_t launch_ffn_backward_t(const FfnArgs& a, hipStream_t stream) {
     o.wg = area((int64_t)a.F * o.pitch);
     o.wu = area((int64_t)a.F * o.pitch);
     o.x = area((int64_t)a.M * o.pitch);
-    const bool chunks = a.K % E == 0;
-    if (a.dx && !(chunks && rows4<T>(a.wg, a.ld_wg) && rows4<T>(a.wu, a.ld_wu))) {
+    const FfnCopies made = ffn_copies(a, es);
+    if (a.dx && made.weights) {
       o.weights = groups(a.F, o.pitch);
       in.wg = o.wg;
       in.wu = o.wu;
       in.ld_wg = in.ld_wu = o.pitch;
     }
-    if (a.dwg && !(chunks && rows4<T>(a.x, a.ld_x))) {
+    if (a.dwg && made.inputs) {
       o.inputs = groups(a.M, o.pitch);
       in.x = o.x;
       in.ld_x = o.pitch;
@@ -799,9 +801,17 @@ size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize) {
   return 256 + area_bytes(M * 2 * Fp, esize) + copies + (x > w ? x : w) * sizeof(float);
 }
 
-double ffn_operand_groups(int64_t M, int64_t K, int64_t F, int esize) {
-  const double chunks = (double)M * padded(F) + (copies_kept(K, esize) ? (2.0 * F + M) * (K + 8.0) : 0.0);
-  return chunks * esize / 16 / 256 + 4;
+FfnCopies ffn_copies(const FfnArgs& a, int esize) {
+  const bool chunks = (int64_t)a.K * esize % 16 == 0;
+  return FfnCopies{!(chunks && rows4(a.wg, a.ld_wg, esize) && rows4(a.wu, a.ld_wu, esize)),
+                   !(chunks && rows4(a.x, a.ld_x, esize))};
+}
+
+double ffn_operand_groups(const FfnArgs& a, int esize) {
+  const FfnCopies made = ffn_copies(a, esize);
+  const double M = a.M, K = a.K + 8.0, F = a.F;
+  const double elements = M * (double)padded(a.F) + (made.weights ? 2.0 * F * K : 0.0) + (made.inputs ? M * K : 0.0);
+  return elements * esize / 16 / 256 + 4;
 }
 
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream) {

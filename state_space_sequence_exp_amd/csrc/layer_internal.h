@@ -145,7 +145,14 @@ struct FfnArgs {
   void* workspace;
 };
 size_t ffn_backward_workspace(int64_t M, int64_t K, int64_t F, int esize);
-double ffn_operand_groups(int64_t M, int64_t K, int64_t F, int esize);  // workgroups of its first launch
+// Which operands' rows are not whole 16-byte chunks at multiples of 4 bytes (a null
+// pointer: by their distance alone), and the workgroups of the first launch, which
+// copies these.
+struct FfnCopies {
+  bool weights, inputs;
+};
+FfnCopies ffn_copies(const FfnArgs& a, int esize);
+double ffn_operand_groups(const FfnArgs& a, int esize);
 hipError_t launch_ffn(const FfnArgs& a, m3_dtype dtype, hipStream_t stream);
 hipError_t launch_ffn_backward(const FfnArgs& a, m3_dtype dtype, hipStream_t stream);
 

@@ -283,8 +283,6 @@ m3_status check_ffn(const m3_ffn_dims* d, m3_dtype dtype, bool backward) {
   if (d->rows > INT_MAX - 64 || M * F / 2048 > kMaxFfnTiles || M * K / 4096 > kMaxFfnTiles ||
       F * K / 2048 > kMaxFfnTiles)
     return M3_ERR_NOT_SUPPORTED;
-  if (backward && m3::ffn_operand_groups(d->rows, d->channels, d->hidden, (int)esize_of(dtype)) > kMaxGroups256)
-    return M3_ERR_NOT_SUPPORTED;
   return M3_SUCCESS;
 }
 
@@ -304,6 +302,19 @@ m3::FfnArgs ffn_args(const m3_ffn_dims* d) {
   a.ld_dwg = ld_of(d->ld_dwgate, d->channels);
   a.ld_dwu = ld_of(d->ld_dwup, d->channels);
   return a;
+}
+
+// The backward's: also whether its first launch holds the copies that have to be made of
+// these arrays, or, of null ones, by their rows' distances alone.
+m3_status check_ffn_backward(const m3_ffn_dims* d, m3_dtype dtype, const void* x, const void* w_gate,
+                             const void* w_up) {
+  const m3_status st = check_ffn(d, dtype, true);
+  if (st != M3_SUCCESS) return st;
+  m3::FfnArgs a = ffn_args(d);
+  a.x = x;
+  a.wg = w_gate;
+  a.wu = w_up;
+  return m3::ffn_operand_groups(a, (int)esize_of(dtype)) > kMaxGroups256 ? M3_ERR_NOT_SUPPORTED : M3_SUCCESS;
 }
 
 }  // namespace
@@ -337,7 +348,7 @@ m3_status m3_gated_ffn(const m3_ffn_dims* dims, m3_dtype dtype, const void* x,
 }
 
 size_t m3_gated_ffn_backward_workspace_size(const m3_ffn_dims* dims, m3_dtype dtype) {
-  if (!dtype_ok(&dtype) || check_ffn(dims, dtype, true) != M3_SUCCESS) return 0;
+  if (!dtype_ok(&dtype) || check_ffn_backward(dims, dtype, nullptr, nullptr, nullptr) != M3_SUCCESS) return 0;
   return m3::ffn_backward_workspace(dims->rows, dims->channels, dims->hidden, (int)esize_of(dtype));
 }
 
@@ -347,7 +358,7 @@ m3_status m3_gated_ffn_backward(const m3_ffn_dims* dims, m3_dtype dtype, const v
                                 void* dw_up, void* workspace, size_t workspace_bytes,
                                 void* stream) {
   if (!dtype_ok(&dtype)) return M3_ERR_INVALID_VALUE;
-  const m3_status st = check_ffn(dims, dtype, true);
+  const m3_status st = check_ffn_backward(dims, dtype, x, w_gate, w_up);
   if (st != M3_SUCCESS) return st;
   const uintptr_t es = esize_of(dtype);
   if (!maybe(dx, es) || !maybe(dw_gate, es) || !maybe(dw_up, es) ||

@@ -6,6 +6,7 @@ from gpu_util import from_gpu
 from layer_util import HALF_STEP, close
 from oracle import selective as O
 from test_gpu_gated_ffn import TYPES, inputs
+from test_gpu_selective import sliced
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,24 @@ def test_ffn_many_more_rows(dtype):
         close(d[k], w["d" + k], w["e_d" + k], dtype, "d" + k)
     d["x"][rows] = 0
     assert not d["x"].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [5, 90])
+@pytest.mark.parametrize("odd", [("x",), ("wg",), ("wu",), ("x", "wg", "wu")])
+def test_ffn_rows_at_odd_elements(dtype, M, odd):
+    """Rows an even number of elements apart that start at odd ones, of one array alone or
+    of all: the results of dense ones, backward in a workspace for dense ones too."""
+    import state_space_sequence_exp_amd as m3
+    K, F = 72, 136
+    _, t = inputs([23, M], M, K, F, dtype)
+    h, g, u = m3.gated_ffn(t["x"], t["wg"], t["wu"], want_pre=True)
+    d = m3.gated_ffn_backward(t["dh"], t["x"], t["wg"], t["wu"], g, u)
+    s = {k: sliced(v, 1, 1) if k in odd else v for k, v in t.items()}
+    assert all(s[k].stride(0) == K + 2 and s[k].data_ptr() % 8 == s[k].element_size() for k in odd)
+    got = m3.gated_ffn(s["x"], s["wg"], s["wu"], want_pre=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, (h, g, u)))
+    need = m3.gated_ffn_backward_workspace_size(M, K, F, t["x"].dtype)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")      # NaN
+    e = m3.gated_ffn_backward(s["dh"], s["x"], s["wg"], s["wu"], g, u, workspace=ws)
+    assert all(torch.equal(e[k], d[k]) for k in d) and (ws[need:] == 255).all()

@@ -25,3 +25,20 @@ def test_ffn_rows_bounded_by_tiles_alone(lib, rows, K, F, good):  # noqa: F811
         assert (size > rows * 2 * F * (4 - 2 * dt)) if good else size == 0
         off = swap(FFN_BW, _5=FFN_BW[5].value + 1)
         assert ffn_bw(lib, off, dt=dt, **kw) == (INV if good else UNS)
+
+
+def test_ffn_backward_counts_the_copies_it_makes(lib):  # noqa: F811
+    """The first launch holds dg and the copies of arrays whose rows are not whole chunks at
+    multiples of 4 bytes: a call of aligned arrays is not refused for copies it does not make."""
+    kw = dict(rows=4190000, channels=7744, hidden=512)
+    assert lib.m3_gated_ffn_backward_workspace_size(ffn_dims(**kw), 1) > 4190000 * (2 * 512 + 7744) * 2
+    off = swap(FFN_BW, _5=FFN_BW[5].value + 1)                     # (tells a call that would be taken)
+    assert ffn_bw(lib, off, **kw) == INV
+    assert ffn_bw(lib, swap(off, _2=FFN_BW[2].value + 2), **kw) == INV    # copies of the weights: few
+    assert ffn_bw(lib, swap(off, _1=FFN_BW[1].value + 2), **kw) == UNS    # of x: 65 GB more to write
+    assert ffn_bw(lib, off, ld_x=7745, **kw) == UNS
+    assert lib.m3_gated_ffn_backward_workspace_size(ffn_dims(ld_x=7745, **kw), 1) == 0
+    assert ffn_bw(lib, off, ld_x=7746, **kw) == INV
+    for less in (dict(kw, channels=7743), dict(kw, channels=7740)):      # rows that are no whole chunks
+        assert ffn_bw(lib, off, **less) == UNS
+        assert lib.m3_gated_ffn_backward_workspace_size(ffn_dims(**less), 1) == 0
