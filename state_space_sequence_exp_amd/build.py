@@ -1,17 +1,20 @@
 """Build libm3ssm.so (HIP for gfx950) in-tree.
 
-    python -m state_space_sequence_exp_amd.build
+    python -m state_space_sequence_exp_amd.build [--library-only] [-v]
 
 compiles every ``csrc/*.hip`` with hipcc for gfx950 (in parallel) and links
-``state_space_sequence_exp_amd/libm3ssm.so``, and builds ``_tensors.so`` beside
-it, through which the binding looks at a call's tensors.  Packed-fp32 VALU instructions
-are disabled for all device code; a few prefill sources take a measured
-instruction-scheduling strategy (SCHED).
+``state_space_sequence_exp_amd/libm3ssm.so``.  The C library needs hipcc alone.
+Where torch is installed, ``_tensors.so`` is built beside it, through which the
+Python binding looks at a call's tensors (g++, torch's and Python's headers);
+``--library-only`` leaves it out.  Packed-fp32 VALU instructions are disabled for
+all device code; a few prefill sources take a measured instruction-scheduling
+strategy (SCHED).
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -66,10 +69,13 @@ def file_flags(src: str):
     return ["-mllvm", "-amdgpu-sched-strategy=" + st] if st else []
 
 
-def build(verbose: bool = False, jobs: int = 8, extra_flags=(), out: str = LIB_PATH) -> str:
+def build(verbose: bool = False, jobs: int = 8, extra_flags=(), out: str = LIB_PATH,
+          binding: bool = True) -> str:
     """Compile every source and link the shared library at `out` (default:
     the in-tree libm3ssm.so).  extra_flags go to every compile line (for
-    instance host-only sanitizer flags, each behind -Xarch_host)."""
+    instance host-only sanitizer flags, each behind -Xarch_host).  With
+    `binding`, _tensors.so is built too, beside the in-tree library, unless
+    torch, without which the binding is of no use, is not installed."""
     hipcc = _hipcc()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     if not srcs:
@@ -97,8 +103,11 @@ def build(verbose: bool = False, jobs: int = 8, extra_flags=(), out: str = LIB_P
         os.replace(out_tmp, out)
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
-    if out == LIB_PATH:
-        build_tensors()
+    if binding and out == LIB_PATH:
+        if importlib.util.find_spec("torch") is None:
+            sys.stderr.write("torch is not installed: _tensors.so, the binding's part, is left out\n")
+        else:
+            build_tensors(verbose)
     return out
 
 
@@ -106,23 +115,29 @@ TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
 TENSORS_PATH = os.path.join(PKG, "_tensors.so")
 
 
-def build_tensors() -> str:
+def build_tensors(verbose: bool = False) -> str:
     """The binding's look at a call's tensors (_tensors.so: host code only,
     against the headers and libraries of the torch that is installed)."""
     import sysconfig
     import torch
+    instead = "(the C library is built without this: --library-only, or build(binding=False))"
+    python = sysconfig.get_paths()["include"]
+    if not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
+        raise RuntimeError("_tensors.so needs g++ and Python.h " + instead)
     base = os.path.dirname(torch.__file__)
     lib = os.path.join(base, "lib")
     out_tmp = TENSORS_PATH + ".tmp%d" % os.getpid()
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
-           "-I", os.path.join(base, "include"),
-           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], TENSORS_SRC, "-o", out_tmp,
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", python, TENSORS_SRC, "-o", out_tmp,
            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (TENSORS_SRC, r.stdout, r.stderr))
+        raise RuntimeError("g++ failed for %s %s:\n%s\n%s" % (TENSORS_SRC, instead, r.stdout, r.stderr))
+    if verbose:
+        sys.stderr.write(r.stderr)
     os.replace(out_tmp, TENSORS_PATH)
     return TENSORS_PATH
 
@@ -143,5 +158,5 @@ def build_probe() -> str:
 
 
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv))
+    print(build(verbose="-v" in sys.argv, binding="--library-only" not in sys.argv))
     print(build_probe())
