@@ -5,7 +5,7 @@ import torch
 from gpu_util import from_gpu
 from layer_util import HALF_STEP, close
 from oracle import selective as O
-from test_gpu_gated_ffn import TYPES, inputs
+from test_gpu_gated_ffn import TYPES, check, inputs
 from test_gpu_selective import sliced
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +74,14 @@ def test_ffn_rows_at_odd_elements(dtype, M, odd):
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")      # NaN
     e = m3.gated_ffn_backward(s["dh"], s["x"], s["wg"], s["wu"], g, u, workspace=ws)
     assert all(torch.equal(e[k], d[k]) for k in d) and (ws[need:] == 255).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F", [(157, 530, 2796), (333, 433, 2806), (687, 185, 3801), (5719, 134, 4503),
+                                   (8301, 136, 2814), (1909, 67, 2233), (1268, 1452, 67), (16830, 70, 33)])
+def test_ffn_other_kernels(dtype, M, K, F):
+    """Sizes that take the kernels that no other size of these tests does: the smallest tile
+    straight into the LDS and through registers, the second one through registers, k cut
+    over the largest tile and, in float, over larger ones, and the second one whole."""
+    r, t = inputs([24, M, K, F], M, K, F, dtype)
+    check(r, t, dtype)
