@@ -132,3 +132,24 @@ def gated_ffn_backward(dh, x, wg, wu, half_step):
     for k, d, e in (("dw_gate", dg, edg), ("dw_up", du, edu)):
         out["e_" + k] = e.T @ ab(x) + (M + 65) * U * ((ab(d) + e).T @ ab(x))
     return out
+
+
+def gated_ffn_backward_stored(dh, x, wg, wu, g, u, store):
+    """Gradients from g and u as they were kept (float32 values, taken as exact), with dg and
+    du rounded by `store` (float64 values to the storage type's) before the products, as
+    the operator defines them; and bounds.  Half a step of dg and du is then no error: what
+    is left of it is the elements that a float evaluation may round to the other side."""
+    M, F = g.shape
+    ab = np.abs
+    sg = sigmoid(g)
+    slope, mag = sg * (1 + g * (1 - sg)), sg * (1 + ab(g) * (1 - sg))
+    du, dg = dh * g * sg, dh * u * slope
+    edu = (delta(g) + 6 * U) * ab(du)
+    edg = ab(dh * u) * (4 * delta(g) + 8 * U) * mag + 4 * U * ab(dg)
+    (dg, edg), (du, edu) = ((store(v), np.maximum(store(v + e) - store(v), store(v) - store(v - e)) + 1e-38)
+                            for v, e in ((dg, edg), (du, edu)))
+    out = dict(dx=dg @ wg + du @ wu, dw_gate=dg.T @ x, dw_up=du.T @ x)
+    out["e_dx"] = (edg @ ab(wg) + edu @ ab(wu)) + (2 * F + 130) * U * ((ab(dg) + edg) @ ab(wg) + (ab(du) + edu) @ ab(wu))
+    for k, d, e in (("dw_gate", dg, edg), ("dw_up", du, edu)):
+        out["e_" + k] = e.T @ ab(x) + (M + 65) * U * ((ab(d) + e).T @ ab(x))
+    return out
