@@ -637,7 +637,8 @@ typedef struct {
 } m3_conv_dims;
 
 /* seqlen == 0 copies the states; batch == 0 enqueues nothing.  At most 2^24 - 1
- * workgroups of 256 vectors by 8 tokens. */
+ * workgroups of 256 items, an item being 16 tokens of a vector of 16 bytes of channels,
+ * or a sequence's kept inputs of one (m3_causal_conv_step: 256 vectors of a row). */
 m3_status m3_causal_conv(const m3_conv_dims* dims, m3_dtype dtype, const void* x,
                          const float* weight, const float* bias, int silu, const void* state_in,
                          const int32_t* lengths, void* y, void* state_out, void* stream);

@@ -2,7 +2,8 @@
 scan and the gated feed-forward projections."""
 import pytest
 
-from test_selective_abi_cpu import FFN_BW, GOOD, INV, UNS, ffn_bw, ffn_dims, lib, swap  # noqa: F401
+from test_selective_abi_cpu import (CONV, CONV_STEP, FFN_BW, GOOD, INV, UNS, conv, conv_step,  # noqa: F401
+                                    ffn_bw, ffn_dims, lib, swap)
 
 
 def test_ffn_backward_without_rows(lib):  # noqa: F811
@@ -42,3 +43,22 @@ def test_ffn_backward_counts_the_copies_it_makes(lib):  # noqa: F811
     for less in (dict(kw, channels=7743), dict(kw, channels=7740)):      # rows that are no whole chunks
         assert ffn_bw(lib, off, **less) == UNS
         assert lib.m3_gated_ffn_backward_workspace_size(ffn_dims(**less), 1) == 0
+
+
+@pytest.mark.parametrize("batch,seqlen,channels,dt,good", [
+    (1 << 20, 4094 * 16, 8, 1, True), (1 << 20, 4095 * 16, 8, 1, False), (1 << 20, 4094 * 16, 9, 1, False),
+    (1 << 20, 2046 * 16, 9, 1, True), (1 << 20, 4094 * 16, 4, 0, True), (1 << 20, 4094 * 16, 5, 0, False),
+    (1, (1 << 31) - 1, 200, 1, True), ((1 << 31) - 256, 1, 8, 1, True), ((1 << 31) - 256, 17, 8, 1, False)])
+def test_conv_largest(lib, batch, seqlen, channels, dt, good):  # noqa: F811
+    """At most 2^24 - 1 workgroups of 256 items: 16 tokens of 16 bytes of channels, or a sequence's
+    kept inputs of these (a misaligned weight tells a call that would be taken)."""
+    off = swap(CONV, _1=CONV[1].value + 1)
+    kw = dict(batch=batch, seqlen=seqlen, channels=channels, ld_x=0, ld_y=0)
+    assert conv(lib, off, dt=dt, **kw) == (INV if good else UNS)
+
+
+@pytest.mark.parametrize("batch,channels,good", [
+    ((1 << 24) - 1, 2048, True), (1 << 24, 2048, False), (1 << 23, 2049, False), ((1 << 23) - 1, 4096, True)])
+def test_conv_step_largest(lib, batch, channels, good):  # noqa: F811
+    off = swap(CONV_STEP, _4=CONV_STEP[4].value + 1)
+    assert conv_step(lib, off, batch=batch, channels=channels, ld_x=0, ld_y=0) == (INV if good else UNS)
