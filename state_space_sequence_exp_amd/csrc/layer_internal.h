@@ -127,9 +127,9 @@ struct SelectArgs {
 };
 // Segments that a scan's tokens are cut into (1: not cut), the workspace that
 // takes, and the workgroups of a launch.
-int select_segments(int64_t B, int64_t T, int64_t D, int N);
+int select_segments(int64_t B, int64_t T, int64_t D);
 size_t select_workspace(int64_t B, int64_t T, int64_t D, int N);
-double select_groups(int64_t B, int64_t T, int64_t D, int N);
+double select_groups(int64_t B, int64_t T, int64_t D);
 double select_step_groups(int64_t B, int64_t D, int N);
 hipError_t launch_select(const SelectArgs& a, m3_dtype dtype, hipStream_t stream);
 hipError_t launch_select_step(const SelectArgs& a, m3_dtype dtype, hipStream_t stream);

@@ -65,7 +65,7 @@ m3_status check_select(const m3_select_dims* d, bool step) {
   if (d->batch > INT_MAX || d->channels > INT_MAX || (!step && d->seqlen > INT_MAX))
     return M3_ERR_NOT_SUPPORTED;
   const double groups = step ? m3::select_step_groups(d->batch, d->channels, (int)d->dstate_n)
-                             : m3::select_groups(d->batch, d->seqlen, d->channels, (int)d->dstate_n);
+                             : m3::select_groups(d->batch, d->seqlen, d->channels);
   return groups > (step ? kMaxGroups256 : kMaxGroups512) ? M3_ERR_NOT_SUPPORTED : M3_SUCCESS;
 }
 

@@ -413,7 +413,7 @@ int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8
 
 template <typename T, int NL>
 void launch_select_n(const SelectArgs& a, hipStream_t stream) {
-  const int tiles = (int)channel_tiles(a.D), segs = select_segments(a.B, a.T, a.D, a.N);
+  const int tiles = (int)channel_tiles(a.D), segs = select_segments(a.B, a.T, a.D);
   const int64_t len = segment_tokens(a.T, segs);
   float* ends = static_cast<float*>(a.workspace);
   float* sums = ends + a.B * (segs - 1) * a.D * a.N;
@@ -452,10 +452,31 @@ hipError_t launch_select_step_t(const SelectArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// A wave holds four channels; with fewer than 512 of them on the 1024 SIMDs the
-// tokens are cut so that there are about 2048, into segments of four tiles at
-// least.  Cutting does two thirds of the work twice.
-int select_segments(int64_t B, int64_t T, int64_t D, int N) {
+// A wave holds four channels; with fewer than 512 of them on the 1024 SIMDs (127 tiles
+// of 16 channels) the tokens are cut so that there are about 2048, into segments of four
+// tiles at least.  Cutting does two thirds of the work twice.  Measured, bfloat16 with the
+// gate, us by the number of segments, * what the rule takes:
+//
+//   T16384 N16   D256:  1: 351   8: 84    16: 48    32: 43*   64: 50
+//                D512:  1: 348   8: 85    16: 72*   32: 72    64: 83
+//                D1024: 1: 346   4: 162    8: 135*  16: 128   32: 130
+//                D1536: 1: 376   3: 310    5*       6: 230     8: 200
+//                D2032: 1: 357   3: 317    4: 269*   8: 252
+//                D2048: 1: 373*  3: 322    4: 272    8: 255
+//                D2560: 1: 404*  2: 496    4: 345    8: 311
+//                D4096: 1: 385*  2: 486    4: 453
+//   T16384 N64   D1024: 1: 1030  4: 453    8: 436*  16: 439
+//                D2032: 1: 1031  3: 952    4: 857*   8: 853
+//                D2560: 1: 1029* 2: 1405   4: 1117   8: 1059
+//   T512         D256:  1: 14.6* 2: 16.0  (fewer than three: not cut)
+//   T768         D256:  1: 20.2  3: 16.1*  6: 11.9
+//   T2048        D64:   1: 46.4  8: 16.1* 16: 12.1
+//
+// So what the rule cuts is worth cutting and what has the chip's 256 CUs full is not; it
+// leaves uncut from 128 tiles on what would still gain in four segments with 16 states
+// (up to 160 tiles; with 64 states not), and segments of two tiles would serve short
+// sequences of few channels better than four.
+int select_segments(int64_t B, int64_t T, int64_t D) {
   const int64_t waves = B * channel_tiles(D) * kWaves;
   if (waves < 1 || waves >= 512) return 1;
   int64_t segs = 2048 / waves;
@@ -466,12 +487,12 @@ int select_segments(int64_t B, int64_t T, int64_t D, int N) {
 }
 
 size_t select_workspace(int64_t B, int64_t T, int64_t D, int N) {
-  const int segs = select_segments(B, T, D, N);
+  const int segs = select_segments(B, T, D);
   return (size_t)B * (segs - 1) * D * (N + 1) * sizeof(float);
 }
 
-double select_groups(int64_t B, int64_t T, int64_t D, int N) {
-  return (double)B * (double)channel_tiles(D) * select_segments(B, T, D, N);
+double select_groups(int64_t B, int64_t T, int64_t D) {
+  return (double)B * (double)channel_tiles(D) * select_segments(B, T, D);
 }
 double select_step_groups(int64_t B, int64_t D, int N) {
   const int each = kThreads / lanes_of(N) * kSteps;
