@@ -13,8 +13,8 @@ constexpr int kPlanRowBytes = 128;  // of k in a tile's row
 // rate that it reaches by itself (8192 x 2048 x 4096, both products, in one tile size
 // each: bfloat16 243, 285, 412 and 547 us; float, whose products take longer than what
 // feeds them, 1.88, 1.86, 1.94 and 2.06 ms).  With 512 rows of those the largest tile
-// would take 42 us where the second takes 22, with 100 rows 41 where the smallest
-// takes 10.  Where a product has few tiles and a long k, its parts fill the CUs
+// would take 42 us where the second takes 23, with 100 rows 41 where the third takes 9,
+// all on inputs that do not change (others come from memory: 31 and 12).  Where a product has few tiles and a long k, its parts fill the CUs
 // instead, of eight tiles of k at least (the backward pass of 256 x 2048 x 4096,
 // bfloat16: 61 to 48 us, of 20000 x 64 x 300 120 to 44, float 291 to 75);
 // joining them takes some 6 us and the parts' way through memory, in the unit of the

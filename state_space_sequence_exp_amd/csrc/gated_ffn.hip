@@ -494,8 +494,9 @@ void launch_gemm(GemmArgs<T> g, hipStream_t stream) {
 
 // ---- few rows ------------------------------------------------------------------
 // Up to 16 FM rows (a decode batch): the weights are read once, straight into the
-// matrix units' layout (4 x 2048 x 4096 bfloat16: 6.9 us, 4.9 TB/s; from 33 rows on the
-// tiles take as long, 10 us).  A workgroup owns 16 hidden units; its eight waves share
+// matrix units' layout (4 x 2048 x 4096 bfloat16: 7 us, 4.8 TB/s, 16 rows 8.0, 32 rows
+// 10.0, on inputs that the caches hold; 33 rows, in tiles, take 8.1, but 40 beside 36 of
+// 4096 x 64 in float).  A workgroup owns 16 hidden units; its eight waves share
 // out k and add their parts in the LDS, in order.
 constexpr int kFewWaves = 8;
 
